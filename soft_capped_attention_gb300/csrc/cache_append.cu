@@ -1,0 +1,128 @@
+// Appending new keys and values to the pages of their sequences.
+//
+// Row r of the new tokens belongs to the sequence b with cu_new[b] <= r <
+// cu_new[b + 1] (row b itself without cu_new) and goes to slot lens[b] -
+// (cu_new[b + 1] - r).  A CTA takes `rows` consecutive rows: one thread a row
+// finds the sequence (binary search), checks slot and page, and leaves the row's
+// place in shared memory; then all threads copy 16-byte vectors, a head's D
+// values being one contiguous run on both sides.
+#include "cache_internal.h"
+
+namespace capattn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxRows = 64;   // rows of a CTA
+constexpr int kVecs = 4;       // vectors a thread has in flight, of K and of V each
+
+struct Place {
+  int32_t b, slot, page;  // page < 0: nothing to write
+  int32_t pos;
+};
+
+__device__ __forceinline__ Place place_of(const CacheParams& p, int r) {
+  Place x;
+  x.page = -1;
+  x.b = r;
+  int end = r + 1;
+  if (p.cu_new) {
+    int lo = 0, hi = p.B;  // the first b with cu_new[b + 1] > r
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (p.cu_new[mid + 1] <= r) lo = mid + 1; else hi = mid;
+    }
+    if (lo >= p.B || p.cu_new[lo] > r) return x;  // behind the last sequence
+    x.b = lo;
+    end = p.cu_new[lo + 1];
+  }
+  const int len = p.lens[x.b];
+  if (len < 0 || len > p.max_len) {
+    atomicOr(p.status, kStatusBadLensBit);
+    return x;
+  }
+  const long long slot = (long long)len - ((long long)end - r);
+  if (slot < 0 || slot >= len) {
+    atomicOr(p.status, kStatusBadNewRowsBit);
+    return x;
+  }
+  x.slot = (int)slot;
+  const int page = p.table[(size_t)x.b * p.max_pages + (x.slot >> p.page_shift)];
+  if (page < 0 || page >= p.num_pages) {
+    atomicOr(p.status, kStatusBadPageBit);
+    return x;
+  }
+  x.page = page;
+  x.pos = p.pos ? p.qpos[x.b] - (end - r - 1) : 0;
+  return x;
+}
+
+// vpr: 16-byte vectors of a row (all heads), vph_shift: log2 of a head's.
+__global__ void __launch_bounds__(kThreads)
+append_kernel(CacheParams p, int rows, int vpr, int vph_shift) {
+  __shared__ Place places[kMaxRows];
+  pdl_trigger();
+  pdl_wait();
+  const int r0 = blockIdx.x * rows;
+  const int n = min(rows, p.n_rows - r0);
+  if (threadIdx.x < n) places[threadIdx.x] = place_of(p, r0 + threadIdx.x);
+  __syncthreads();
+  const uint4* kn = static_cast<const uint4*>(p.k_new);
+  const uint4* vn = static_cast<const uint4*>(p.v_new);
+  uint4* kc = static_cast<uint4*>(p.k);
+  uint4* vc = static_cast<uint4*>(p.v);
+  const int total = n * vpr;
+  for (int i0 = threadIdx.x; i0 < total; i0 += kThreads * kVecs) {
+    uint4 a[kVecs], c[kVecs];
+    long long dst[kVecs];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int i = i0 + u * kThreads;
+      dst[u] = -1;
+      if (i >= total) continue;
+      const int r = i / vpr, w = i - r * vpr;
+      const Place& x = places[r];
+      if (x.page < 0) continue;
+      const int h = w >> vph_shift, at = w & ((1 << vph_shift) - 1);
+      a[u] = __ldcs(kn + (size_t)(r0 + r) * p.k_new_stride + w);
+      c[u] = __ldcs(vn + (size_t)(r0 + r) * p.v_new_stride + w);
+      dst[u] = ((((long long)x.page * p.Hkv + h) << p.page_shift) + (x.slot & (p.page_size - 1)));
+      dst[u] = (dst[u] << vph_shift) + at;
+    }
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      if (dst[u] < 0) continue;
+      kc[dst[u]] = a[u];
+      vc[dst[u]] = c[u];
+    }
+  }
+  if (p.weights || p.pos) {
+    for (int i = threadIdx.x; i < n * p.Hkv; i += kThreads) {
+      const int h = i / n;
+      const Place& x = places[i - h * n];  // neighbouring threads: neighbouring slots
+      if (x.page < 0) continue;
+      const size_t at = ((size_t)x.b * p.Hkv + h) * p.max_len + x.slot;
+      if (p.weights) p.weights[at] = 0.f;
+      if (p.pos) p.pos[at] = x.pos;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const CacheParams& p0, int dtype, cudaStream_t s) {
+  CacheParams p = p0;
+  const int per = dtype == CAPATTN_BF16 ? 8 : 4;  // elements of a vector
+  const int vph = p.D / per;
+  int shift = 0;
+  while ((1 << shift) < vph) ++shift;
+  p.k_new_stride /= per;
+  p.v_new_stride /= per;
+  // Enough rows that every thread has its vectors in flight, but no fewer CTAs
+  // than fill the SMs: a decoding step's rows go one to a CTA.
+  const int vpr = p.Hkv * vph;
+  int rows = (kThreads * kVecs + vpr - 1) / vpr;
+  rows = min(min(rows, kMaxRows), max(1, p.n_rows / (2 * 152)));
+  return launch_pdl(append_kernel, dim3((p.n_rows + rows - 1) / rows), dim3(kThreads), 0, s, p, rows, vpr, shift);
+}
+
+}  // namespace capattn

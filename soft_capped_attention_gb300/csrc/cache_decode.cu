@@ -1,0 +1,345 @@
+// Attention of one new token per sequence over the paged cache: the CUDA-core
+// kernel (fp32), the join of the pieces and the weights pass.
+//
+// Per (sequence b, group of up to 16 query heads of one KV head), over live
+// slots j:  t_j = temp cap(sm_scale <q, k_j>),  m = max t, l = sum e^(t - m),
+// O = sum e^(t - m) v_j, kept as a running triple; o = O / l, lse = m + log l.
+// Pieces (m_i, l_i, O_i) of a split join as M = max m_i, l = sum l_i e^(m_i - M),
+// O likewise.
+#include "cache_internal.h"
+#include "cache_math.cuh"
+#include "cache_sched.cuh"
+#include "cap_math.cuh"
+
+namespace capattn {
+namespace {
+
+constexpr int TK = 32;         // keys of a tile: one a lane
+constexpr int kThreads = 128;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  const int bytes = live ? 16 : 0;  // 0: the 16 bytes are filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f(T x) { return (float)x; }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Dot product of 16 bytes of a key row with q in shared memory.
+__device__ __forceinline__ void dot16(float& acc, const float* k, const float* q) {
+  const float4 a = *reinterpret_cast<const float4*>(k), b = *reinterpret_cast<const float4*>(q);
+  acc = fmaf(a.x, b.x, acc);
+  acc = fmaf(a.y, b.y, acc);
+  acc = fmaf(a.z, b.z, acc);
+  acc = fmaf(a.w, b.w, acc);
+}
+__device__ __forceinline__ void dot16(float& acc, const __nv_bfloat16* k, const float* q) {
+  const uint4 a = *reinterpret_cast<const uint4*>(k);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    acc = fmaf(__uint_as_float(w[e] << 16), q[2 * e], acc);
+    acc = fmaf(__uint_as_float(w[e] & 0xFFFF0000u), q[2 * e + 1], acc);
+  }
+}
+
+template <typename T, int D>
+struct Smem {
+  static constexpr int PER = 16 / sizeof(T);
+  static constexpr int ROW = D + PER;  // a row's stride: 16 bytes of padding against bank conflicts
+  T k[2][TK][ROW];
+  T v[2][TK][ROW];
+  float q[kDecodeHeads][D];
+  float p[kDecodeHeads][TK];
+  float scale[kDecodeHeads];
+  float m[kDecodeHeads], l[kDecodeHeads];
+  float half[kDecodeHeads][64];  // D = 64: outputs of the second half of the threads
+};
+
+// Tiles of 32 keys come in by cp.async, two stages.  Scores: warp w takes heads
+// w, w + 4, .., a lane a key (its row in 16-byte pieces; the padding spreads the
+// lanes over the banks, q is a broadcast).  Outputs: a thread takes a column d
+// (D = 64: and half of the keys) of every head.
+template <typename T, int D, int METHOD, int GM>
+__global__ void __launch_bounds__(kThreads)
+decode_simt_kernel(CacheParams p) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  using S = Smem<T, D>;
+  S& s = *reinterpret_cast<S*>(raw);
+  constexpr int CH = D / S::PER;            // 16-byte pieces of a row
+  constexpr int NH = (GM + 3) / 4;          // heads of a warp
+  constexpr int PARTS = kThreads / D;       // threads of a column
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int d = threadIdx.x % D, part = threadIdx.x / D;
+  const T* kc = static_cast<const T*>(p.k);
+  const T* vc = static_cast<const T*>(p.v);
+  PieceIter<TK> it(p, lane);
+  int b, vh, tile;
+  SeqSpan sp;
+  while (it.next(p, &b, &vh, &tile, &sp)) {
+    const HeadGroup hg = head_group(p, vh);
+    const int n = it.n;
+    for (int i = threadIdx.x; i < kDecodeHeads * D; i += kThreads) {
+      const int g = i / D;
+      s.q[g][i % D] = g < hg.count
+          ? to_f(static_cast<const T*>(p.q)[(size_t)b * p.q_stride + (size_t)(hg.h0 + g) * D + i % D]) : 0.f;
+    }
+    const float temp = p.temp ? p.temp[b] : 1.f;
+    const int qpos = p.pos ? p.qpos[b] : 0;
+    const int32_t* pos = p.pos ? p.pos + ((size_t)b * p.Hkv + hg.g) * p.max_len : nullptr;
+    auto load = [&](int i) {
+      const int st = i & 1, j0 = (tile + i) * TK;
+      for (int c = threadIdx.x; c < TK * CH; c += kThreads) {
+        const int r = c / CH, x = c % CH, j = j0 + r;
+        const bool live = j >= sp.first && j < sp.len;
+        size_t at = 0;
+        if (live) {
+          const size_t row = (((size_t)page_of(p, b, j) * p.Hkv + hg.g) << p.page_shift) + (j & (p.page_size - 1));
+          at = row * D + x * S::PER;
+        }
+        cp_async16(smem_u32(&s.k[st][r][x * S::PER]), kc + at, live);
+        cp_async16(smem_u32(&s.v[st][r][x * S::PER]), vc + at, live);
+      }
+      cp_commit();
+    };
+    float m[NH], l[NH], acc[GM];
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int g = 0; g < GM; ++g) acc[g] = 0.f;
+    load(0);
+    for (int i = 0; i < n; ++i) {
+      const int st = i & 1;
+      if (i + 1 < n) {
+        load(i + 1);
+        cp_wait<1>();
+      } else {
+        cp_wait<0>();
+      }
+      __syncthreads();
+      const int j = (tile + i) * TK + lane;
+      bool live = j >= sp.first && j < sp.len;
+      if (pos && p.window_len > 0 && live && pos[j] <= qpos - p.window_len) {
+        live = false;
+        if (warp == 0)  // a masked row must not reach the sum, whatever it holds
+          for (int x = 0; x < D; ++x) s.v[st][lane][x] = (T)0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < NH; ++u) {
+        const int g = warp + 4 * u;
+        if (g < hg.count) {
+          float dot = 0.f;
+#pragma unroll 8
+          for (int x = 0; x < CH; ++x) dot16(dot, &s.k[st][lane][x * S::PER], &s.q[g][x * S::PER]);
+          float t = exact_cap<METHOD>(dot * p.sm_scale, p.cap) * temp;
+          t = live ? t : -INFINITY;
+          if (p.scores && j < sp.len)
+            p.scores[((size_t)b * p.Hq + hg.h0 + g) * p.max_len + j] = t;
+          float mx = t;
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+          mx = fmaxf(mx, m[u]);
+          const float ref = mx == -INFINITY ? 0.f : mx;
+          const float scale = __expf(m[u] - ref);
+          const float e = __expf(t - ref);
+          float sum = e;
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+          m[u] = mx;
+          l[u] = l[u] * scale + sum;
+          s.p[g][lane] = e;
+          if (lane == 0) s.scale[g] = scale;
+        }
+      }
+      __syncthreads();
+      constexpr int KEYS = TK / PARTS;
+#pragma unroll
+      for (int g = 0; g < GM; ++g)
+        if (g < hg.count) acc[g] *= s.scale[g];
+#pragma unroll 4
+      for (int k4 = 0; k4 < KEYS; k4 += 4) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = to_f(s.v[st][part * KEYS + k4 + e][d]);
+#pragma unroll
+        for (int g = 0; g < GM; ++g) {
+          if (g < hg.count) {
+            const float4 w = *reinterpret_cast<const float4*>(&s.p[g][part * KEYS + k4]);
+            acc[g] = fmaf(w.x, v[0], fmaf(w.y, v[1], fmaf(w.z, v[2], fmaf(w.w, v[3], acc[g]))));
+          }
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < NH; ++u) {
+      const int g = warp + 4 * u;
+      if (lane == 0 && g < hg.count) {
+        s.m[g] = m[u];
+        s.l[g] = l[u];
+      }
+    }
+    if (PARTS > 1 && part == 1) {
+#pragma unroll
+      for (int g = 0; g < GM; ++g) s.half[g][d & 63] = acc[g];
+    }
+    __syncthreads();
+    if (part == 0) {
+#pragma unroll
+      for (int g = 0; g < GM; ++g) {
+        if (g >= hg.count) continue;
+        float o = acc[g];
+        if (PARTS > 1) o += s.half[g][d & 63];
+        if (it.whole) {
+          const float lg = s.l[g];
+          const size_t row = (size_t)b * p.Hq + hg.h0 + g;
+          static_cast<T*>(p.o)[row * D + d] = (T)(s.m[g] == -INFINITY ? 0.f : o / lg);
+          if (d == 0) p.lse[row] = s.m[g] == -INFINITY ? -INFINITY : s.m[g] + logf(lg);
+        } else {
+          p.part_o[((size_t)it.slot * kDecodeHeads + g) * D + d] = o;
+          if (d == 0) p.part_ml[(size_t)it.slot * kDecodeHeads + g] = make_float2(s.m[g], s.l[g]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the pieces of one (sequence, query head): a CTA of four warps, each
+// taking every fourth piece, a lane D / 32 columns.
+template <typename T, int D, int TKEYS>
+__global__ void __launch_bounds__(kThreads)
+decode_join_kernel(CacheParams p) {
+  constexpr int V = D / 32;
+  __shared__ float sl[4], so[4][D];
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x, b = row / p.Hq, h = row % p.Hq;
+  const int g = h / p.G, vh = g * p.HG + (h - g * p.G) / kDecodeHeads;
+  const int in = (h - g * p.G) % kDecodeHeads;
+  // units before this (sequence, group)
+  int all = 0, before = 0;
+  for (int x = lane; x < p.B; x += 32) {
+    const int n = seq_span<TKEYS>(p, x).tiles;
+    all += n;
+    if (x < b) before += n;
+  }
+  all = __reduce_add_sync(0xFFFFFFFFu, all);
+  before = __reduce_add_sync(0xFFFFFFFFu, before);
+  const int tiles = seq_span<TKEYS>(p, b).tiles;
+  const uint32_t share = share_of(p, (uint32_t)all * (uint32_t)p.VH);
+  const uint32_t u0 = (uint32_t)before * p.VH + (uint32_t)vh * tiles, u1 = u0 + tiles;
+  const int c0 = (int)(u0 / share), c1 = (int)((u1 - 1) / share);
+  if (c0 == c1) return;  // written by its CTA
+  auto slot_of = [&](int c) { return 2 * c + (c == c0 && u0 != share * (uint32_t)c ? 1 : 0); };
+  float mx = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, p.part_ml[(size_t)slot_of(c) * kDecodeHeads + in].x);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  float l = 0.f, o[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int c = c0 + warp; c <= c1; c += 4) {
+    const size_t at = (size_t)slot_of(c) * kDecodeHeads + in;
+    const float2 ml = p.part_ml[at];
+    const float w = __expf(ml.x - ref);
+    l = fmaf(ml.y, w, l);
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = fmaf(p.part_o[at * D + lane + 32 * e], w, o[e]);
+  }
+  if (lane == 0) sl[warp] = l;
+#pragma unroll
+  for (int e = 0; e < V; ++e) so[warp][lane + 32 * e] = o[e];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    const float sum = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+    const float x = (so[0][threadIdx.x] + so[1][threadIdx.x]) + (so[2][threadIdx.x] + so[3][threadIdx.x]);
+    static_cast<T*>(p.o)[(size_t)row * D + threadIdx.x] = (T)(mx == -INFINITY ? 0.f : x / sum);
+    if (threadIdx.x == 0) p.lse[row] = mx == -INFINITY ? -INFINITY : mx + logf(sum);
+  }
+}
+
+// weights[b, g, j] += sum over the group's heads of exp(t - lse): a thread a slot.
+__global__ void __launch_bounds__(256)
+decode_weights_kernel(CacheParams p) {
+  pdl_trigger();
+  pdl_wait();
+  const int row = blockIdx.x, b = row / p.Hkv, g = row % p.Hkv;
+  const SeqSpan sp = seq_span<64>(p, b);
+  const float* lse = p.lse + (size_t)b * p.Hq + (size_t)g * p.G;
+  const float* sc = p.scores + ((size_t)b * p.Hq + (size_t)g * p.G) * p.max_len;
+  for (int j = sp.first + blockIdx.y * blockDim.x + threadIdx.x; j < sp.len; j += gridDim.y * blockDim.x) {
+    float sum = 0.f;
+    for (int h = 0; h < p.G; ++h) {
+      const float t = sc[(size_t)h * p.max_len + j];
+      sum += t == -INFINITY ? 0.f : __expf(t - lse[h]);
+    }
+    p.weights[(size_t)row * p.max_len + j] += sum;
+  }
+}
+
+template <typename T, int D, int METHOD, int GM>
+cudaError_t run_simt(const CacheParams& p, cudaStream_t s) {
+  auto* k = decode_simt_kernel<T, D, METHOD, GM>;
+  const int smem = sizeof(Smem<T, D>);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k, dim3(p.ctas), dim3(kThreads), smem, s, p);
+}
+
+template <typename T, int D, int METHOD>
+cudaError_t run_heads(const CacheParams& p, cudaStream_t s) {
+  const int n = p.G < kDecodeHeads ? p.G : kDecodeHeads;
+  if (n <= 1) return run_simt<T, D, METHOD, 1>(p, s);
+  if (n <= 4) return run_simt<T, D, METHOD, 4>(p, s);
+  return run_simt<T, D, METHOD, 16>(p, s);
+}
+
+template <typename T, int D>
+cudaError_t run_cap(const CacheParams& p, cudaStream_t s) {
+  switch (p.method) {
+    case CAPATTN_CAP_TANH: return run_heads<T, D, CAPATTN_CAP_TANH>(p, s);
+    case CAPATTN_CAP_SOFT_SIGN: return run_heads<T, D, CAPATTN_CAP_SOFT_SIGN>(p, s);
+    case CAPATTN_CAP_ALSC: return run_heads<T, D, CAPATTN_CAP_ALSC>(p, s);
+    default: return run_heads<T, D, CAPATTN_CAP_NONE>(p, s);
+  }
+}
+
+template <typename T, int D>
+cudaError_t run_all(const CacheParams& p, cudaStream_t s) {
+  cudaError_t e = run_cap<T, D>(p, s);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(decode_join_kernel<T, D, TK>, dim3(p.B * p.Hq), dim3(kThreads), 0, s, p);
+  if (e != cudaSuccess || !p.scores) return e;
+  const int live = p.window_len > 0 && !p.pos ? min(p.max_len, p.window_len) : p.max_len;
+  const dim3 grid(p.B * p.Hkv, min((live + 255) / 256, 1024));
+  return launch_pdl(decode_weights_kernel, grid, dim3(256), 0, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_decode(const CacheParams& p0, int dtype, cudaStream_t s) {
+  CacheParams p = p0;
+  p.ctas = 152 * 3;
+  p.min_tiles = 2;
+  if (dtype == CAPATTN_BF16)
+    return p.D == 64 ? run_all<__nv_bfloat16, 64>(p, s) : run_all<__nv_bfloat16, 128>(p, s);
+  return p.D == 64 ? run_all<float, 64>(p, s) : run_all<float, 128>(p, s);
+}
+
+}  // namespace capattn

@@ -1,0 +1,92 @@
+// Internal interfaces of the paged cache's calls (capattn_cache.h).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/capattn_cache.h"
+#include "capattn_internal.h"
+
+namespace capattn {
+
+// Status bits of the cache's calls (beside those of status_bits.h).
+constexpr uint32_t kStatusBadLensBit = 32u;     // a length outside [0, max_len]
+constexpr uint32_t kStatusBadPageBit = 64u;     // a page outside [0, num_pages)
+constexpr uint32_t kStatusBadNewRowsBit = 128u; // cu_new decreases, or more new rows than lens
+constexpr uint32_t kStatusBadRowsBit = 256u;    // rows outside 0 <= lo <= hi <= L
+
+// Constants of a cap in the exact form of cache_math.cuh.
+struct ExactCap {
+  float cap, inv_cap;        // tanh, soft_sign
+  float a;                   // alsc: d = a * s
+  float out;                 // alsc: cap / denom
+  float sb, one_minus_sb;    // alsc: sigma(alpha beta) and 1 - sigma
+  float eb, emb;             // alsc: e^(alpha beta), e^(-alpha beta)
+};
+
+struct CacheParams {
+  const void* q;
+  int64_t q_stride;          // elements
+  const void* k_new;
+  const void* v_new;
+  int64_t k_new_stride, v_new_stride;
+  int32_t n_rows;
+  const int32_t* cu_new;
+  void* k;                   // pages
+  void* v;
+  const int32_t* table;
+  const int32_t* lens;
+  const float* temp;
+  int32_t* pos;
+  const int32_t* qpos;
+  float* weights;
+  void* o;
+  float* lse;
+  // eviction
+  int32_t budget, keep_first, keep_last;
+  int32_t* lens_out;
+  float* weights_out;
+  int32_t* pos_out;
+  int32_t* src;
+  // workspace pieces
+  uint32_t* status;
+  float2* part_ml;           // [slots][16] running (max, sum) of a piece's heads
+  float* part_o;             // [slots][16][D] unnormalised outputs
+  float* scores;             // [B, Hq, max_len] scores of the step (decode with weights)
+  int32_t* moves;            // [B, Hkv, max_len] eviction: slots that move, in order
+  int32_t* row_src;          // [B, Hkv, budget] eviction: src when the caller wants none
+  int2* counts;              // [B, Hkv] eviction: (moves, new length)
+  // shapes
+  int32_t B, Hq, Hkv, D, G, page_size, page_shift, max_pages, num_pages, max_len;
+  int32_t HG, VH;            // groups of at most 16 query heads per KV head; VH = Hkv * HG
+  int32_t ctas;              // CTAs of the persistent decode
+  int32_t min_tiles;         // least tiles a decode CTA takes
+  // method
+  float sm_scale;
+  int32_t window_len, method;
+  ExactCap cap;
+};
+
+// Heads a decode CTA handles at once (the rows of one tensor-core tile).
+constexpr int kDecodeHeads = 16;
+// Most CTAs of the persistent decode (bounds its partial results).
+constexpr int kDecodeMaxCtas = 152 * 4;
+
+struct CacheWorkspace {
+  size_t part_ml_off, part_o_off, scores_off, moves_off, row_src_off, counts_off, total;
+};
+
+// Rows of capattn_key_weights beyond what Params holds.
+struct KeyWeightsParams {
+  const int32_t* rows;
+  float* w;
+  int64_t w_stride;
+  ExactCap cap;
+};
+
+cudaError_t launch_cache_append(const CacheParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_cache_decode(const CacheParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_cache_evict(const CacheParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_key_weights(const Params& p, const KeyWeightsParams& w, int dtype, cudaStream_t s);
+
+}  // namespace capattn

@@ -1,0 +1,330 @@
+"""Python binding of the paged key-value cache (argument checks and marshalling only).
+
+The calls mirror include/capattn_cache.h: ``cache_append`` writes new keys and
+values into their sequences' pages, ``cache_decode`` is attention of one new
+token per sequence over its cached tokens with the caps of ``AttnParams``,
+``cache_evict`` keeps the heaviest tokens of each head, and ``key_weights`` gives
+the attention weight that each key of a prompt received, which starts a cache's
+weights.  Lengths (and positions) are the caller's device tensors, taken as they
+are after the new tokens, so that a decoding step is::
+
+    cache.lens += 1
+    cache_append(cache, k, v)
+    o, lse = cache_decode(q, cache, ap)
+
+and can be captured into a CUDA graph.  There is no fallback: if the shared
+library is missing, every call raises.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import capattn as _ca
+from .capattn import AttnParams, CAP_METHODS, DTYPES, PASS_FWD
+
+CALL_APPEND, CALL_DECODE, CALL_DECODE_WEIGHTS, CALL_EVICT = 0, 1, 2, 3
+EXPORTED_SYMBOLS = ("capattn_cache_validate_config", "capattn_cache_workspace_bytes", "capattn_cache_append",
+                    "capattn_cache_decode", "capattn_cache_evict", "capattn_key_weights")
+
+
+class CacheConfig(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("cap_method", ctypes.c_int32),
+                ("cap", ctypes.c_float), ("alpha", ctypes.c_float), ("beta", ctypes.c_float),
+                ("sm_scale", ctypes.c_float), ("window_len", ctypes.c_int32), ("B", ctypes.c_int32),
+                ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+_lib_handle = None
+
+
+def lib() -> ctypes.CDLL:
+    """The loaded library with the cache's signatures; raises if it has not been built."""
+    global _lib_handle
+    if _lib_handle is None:
+        h = _ca.lib()
+        vp, sz, i32, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
+        cfgp = ctypes.POINTER(CacheConfig)
+        h.capattn_cache_validate_config.restype = ctypes.c_int
+        h.capattn_cache_validate_config.argtypes = [cfgp]
+        h.capattn_cache_workspace_bytes.restype = sz
+        h.capattn_cache_workspace_bytes.argtypes = [cfgp, ctypes.c_int]
+        h.capattn_cache_append.restype = ctypes.c_int
+        h.capattn_cache_append.argtypes = [cfgp, vp, vp, i64, i64, i32] + [vp] * 9 + [sz, vp]
+        h.capattn_cache_decode.restype = ctypes.c_int
+        h.capattn_cache_decode.argtypes = [cfgp, vp, i64] + [vp] * 11 + [sz, vp]
+        h.capattn_cache_evict.restype = ctypes.c_int
+        h.capattn_cache_evict.argtypes = [cfgp, i32, i32, i32] + [vp] * 12 + [sz, vp]
+        h.capattn_key_weights.restype = ctypes.c_int
+        h.capattn_key_weights.argtypes = [ctypes.POINTER(_ca.CapattnConfig)] + [vp] * 8 + [i64, vp, sz, vp]
+        _lib_handle = h
+    return _lib_handle
+
+
+def make_cache_config(ap: AttnParams, B: int, Hq: int, Hkv: int, D: int, dtype: torch.dtype,
+                      num_pages: int, page_size: int, max_pages: int) -> CacheConfig:
+    if dtype not in DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if ap.cap_method not in CAP_METHODS:
+        raise ValueError(f"unknown cap method {ap.cap_method!r}")
+    c = CacheConfig()
+    c.struct_size = ctypes.sizeof(CacheConfig)
+    c.cap_method = CAP_METHODS[ap.cap_method]
+    c.cap, c.alpha, c.beta, c.sm_scale = ap.cap, ap.alpha, ap.beta, ap.sm_scale
+    c.window_len = ap.window_len
+    c.B, c.Hq, c.Hkv, c.D, c.dtype = B, Hq, Hkv, D, DTYPES[dtype]
+    c.num_pages, c.page_size, c.max_pages = num_pages, page_size, max_pages
+    return c
+
+
+def cache_workspace_bytes(cfg: CacheConfig, call: int) -> int:
+    return int(lib().capattn_cache_workspace_bytes(ctypes.byref(cfg), call))
+
+
+def _want(t, what, shape, dtype, device):
+    """A contiguous tensor of that shape, type and device, or None."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what}: want a contiguous {dtype} tensor {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _rows(t, what, shape, dtype, device):
+    """Rows of contiguous [heads, D] blocks; returns the row stride in elements."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{what}: want a {dtype} tensor {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    n, heads, D = shape
+    if n and ((D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D)):
+        raise ValueError(f"{what}: the [heads, D] block of a row has to be contiguous, strides are {t.stride()}")
+    return t.stride(0) if n > 1 else heads * D
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """Makes `device` and the call's stream (by default the device's current one) the
+    current ones, so that what a call allocates belongs to its stream; gives the
+    stream's handle."""
+    if stream is None:
+        with torch.cuda.device(device):
+            yield torch.cuda.current_stream(device).cuda_stream
+    else:
+        if stream.device != device:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+
+
+class KVCache:
+    """A paged cache and what its calls share.
+
+    k, v [num_pages, Hkv, page_size, D] (bf16 or fp32); table [B, max_pages]
+    int32; lens [B] int32 (tokens held, at most max_len = max_pages *
+    page_size); optional weights [B, Hkv, max_len] fp32 (attention weight
+    received so far), pos [B, Hkv, max_len] int32 with qpos [B] int32
+    (positions of the cached tokens and of each sequence's newest one).  All of
+    them are the caller's; the cache adds one workspace, which grows to what its
+    calls need.  Calls that may overlap on the GPU (two streams, two captured
+    graphs) need a KVCache each (the tensors may be the same)."""
+
+    def __init__(self, k, v, table, lens, weights=None, pos=None, qpos=None):
+        if k.dim() != 4 or table.dim() != 2:
+            raise ValueError("k is [num_pages, Hkv, page_size, D] and table [B, max_pages]")
+        if k.dtype not in DTYPES:
+            raise ValueError(f"unsupported dtype {k.dtype}")
+        if k.device.type != "cuda":
+            raise ValueError(f"the cache has to be on a GPU, got {k.device}")
+        self.num_pages, self.Hkv, self.page_size, self.D = k.shape
+        self.B, self.max_pages = table.shape
+        self.max_len = self.max_pages * self.page_size
+        self.device, self.dtype = k.device, k.dtype
+        slots = (self.B, self.Hkv, self.max_len)
+        _want(k, "k", k.shape, k.dtype, k.device)
+        _want(v, "v", k.shape, k.dtype, k.device)
+        _want(table, "table", table.shape, torch.int32, k.device)
+        _want(lens, "lens", (self.B,), torch.int32, k.device)
+        _want(weights, "weights", slots, torch.float32, k.device)
+        _want(pos, "pos", slots, torch.int32, k.device)
+        _want(qpos, "qpos", (self.B,), torch.int32, k.device)
+        if pos is not None and qpos is None:
+            raise ValueError("pos needs qpos, the position of each sequence's newest token")
+        self.k, self.v, self.table, self.lens = k, v, table, lens
+        self.weights, self.pos, self.qpos = weights, pos, qpos
+        self._workspaces = []  # the last one is used; earlier ones may live in captured graphs
+
+    def config(self, Hq: int, ap: AttnParams | None = None) -> CacheConfig:
+        cfg = make_cache_config(ap or AttnParams(sm_scale=1.0), self.B, Hq, self.Hkv, self.D, self.dtype,
+                                self.num_pages, self.page_size, self.max_pages)
+        _ca._check(lib().capattn_cache_validate_config(ctypes.byref(cfg)), "KVCache")
+        return cfg
+
+    def workspace(self, cfg: CacheConfig, call: int) -> torch.Tensor:
+        """The cache's workspace, at least as large as `call` needs.  A larger call's
+        first use adds a larger one (so make that call once before a graph is
+        captured); the earlier ones stay, since captured graphs may hold them."""
+        n = cache_workspace_bytes(cfg, call)
+        if not self._workspaces or self._workspaces[-1].numel() < n:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("the cache's workspace would grow during a graph capture: "
+                                   "make the call once before capturing it")
+            new = torch.empty(n, dtype=torch.uint8, device=self.device)
+            new[:256].zero_()  # the status word
+            self._workspaces.append(new)
+        return self._workspaces[-1]
+
+    def status(self, stream=None) -> tuple[int, int]:
+        """Synchronises; returns (status, raw bits) of the calls so far and clears them."""
+        status, raw = 0, 0
+        with _on(self.device, stream) as s:
+            for w in self._workspaces:
+                bits = ctypes.c_uint32(0)
+                st = lib().capattn_device_status(w.data_ptr(), s, ctypes.byref(bits))
+                status, raw = status or int(st), raw | int(bits.value)
+        return status, raw
+
+
+def cache_append(cache: KVCache, k_new, v_new, cu_new=None, stream=None) -> None:
+    """Writes new tokens into the cache.  k_new, v_new [N, Hkv, D] (rows may be
+    strided, as slices of a fused projection are); the rows of sequence b are
+    cu_new[b] .. cu_new[b + 1] - 1 (cu_new [B + 1] int32; None: one row a
+    sequence).  cache.lens (and qpos) already count the new tokens: the n rows of
+    sequence b go to slots lens[b] - n .. lens[b] - 1.  Their weights start at 0."""
+    N = k_new.shape[0]
+    shape = (N, cache.Hkv, cache.D)
+    ks = _rows(k_new, "k_new", shape, cache.dtype, cache.device)
+    vs = _rows(v_new, "v_new", shape, cache.dtype, cache.device)
+    if cu_new is None and N != cache.B:
+        raise ValueError(f"without cu_new there is one new row a sequence: got {N} rows, {cache.B} sequences")
+    _want(cu_new, "cu_new", (cache.B + 1,), torch.int32, cache.device)
+    cfg = cache.config(cache.Hkv)
+    with _on(cache.device, stream) as s:
+        ws = cache.workspace(cfg, CALL_APPEND)
+        st = lib().capattn_cache_append(
+            ctypes.byref(cfg), _ca._ptr(k_new), _ca._ptr(v_new), ks, vs, N, _ca._ptr(cu_new), _ca._ptr(cache.k),
+            _ca._ptr(cache.v), _ca._ptr(cache.table), _ca._ptr(cache.lens), _ca._ptr(cache.weights),
+            _ca._ptr(cache.pos), _ca._ptr(cache.qpos), _ca._ptr(ws), ws.numel(), s)
+    _ca._check(st, "capattn_cache_append")
+
+
+def cache_decode(q, cache: KVCache, ap: AttnParams, temp=None, accumulate=False, out=None, stream=None):
+    """Attention of one new token per sequence over its cached tokens.  q [B, Hq, D]
+    (rows may be strided); temp [B] fp32 optional.  Returns (o [B, Hq, D],
+    lse [B, Hq]); a sequence without live tokens gives o = 0, lse = -inf.  With
+    accumulate, every cached token's share of the group's attention is added to
+    cache.weights.  out: preallocated (o, lse).  ap's z_loss_weight plays no
+    part, and causal none either: the query stands behind every cached token."""
+    if q.dim() != 3:
+        raise ValueError("q is [B, Hq, D]")
+    Hq = q.shape[1]
+    qs = _rows(q, "q", (cache.B, Hq, cache.D), cache.dtype, cache.device)
+    _want(temp, "temp", (cache.B,), torch.float32, cache.device)
+    if accumulate and cache.weights is None:
+        raise ValueError("accumulate needs a cache with weights")
+    cfg = cache.config(Hq, ap)
+    if out is not None:
+        o, lse = out
+        _want(o, "o", (cache.B, Hq, cache.D), cache.dtype, cache.device)
+        _want(lse, "lse", (cache.B, Hq), torch.float32, cache.device)
+    with _on(cache.device, stream) as s:
+        if out is None:
+            o = torch.empty(cache.B, Hq, cache.D, dtype=cache.dtype, device=cache.device)
+            lse = torch.empty(cache.B, Hq, dtype=torch.float32, device=cache.device)
+        ws = cache.workspace(cfg, CALL_DECODE_WEIGHTS if accumulate else CALL_DECODE)
+        st = lib().capattn_cache_decode(
+            ctypes.byref(cfg), _ca._ptr(q), qs, _ca._ptr(cache.k), _ca._ptr(cache.v), _ca._ptr(cache.table),
+            _ca._ptr(cache.lens), _ca._ptr(temp), _ca._ptr(cache.pos), _ca._ptr(cache.qpos), _ca._ptr(o),
+            _ca._ptr(lse), _ca._ptr(cache.weights) if accumulate else None, _ca._ptr(ws), ws.numel(),
+            s)
+    _ca._check(st, "capattn_cache_decode")
+    return o, lse
+
+
+def cache_evict(cache: KVCache, budget: int, keep_first: int = 0, keep_last: int = 0, out=None, want_src=True,
+                stream=None):
+    """Keeps at most `budget` tokens of every (sequence, KV head): the first
+    keep_first and last keep_last positions, then the heaviest (ties: the lower
+    slot).  Kept tokens behind the budget move into the freed slots; lens,
+    weights and pos follow, in place, or into out = (lens, weights, pos) (pos None
+    without positions).  Returns src [B, Hkv, budget] int32, the slot each kept
+    token came from (-1: none), or None without want_src.  Without pos a moved
+    token loses its place in the text: windows and later keep_last then go by
+    slots."""
+    if cache.weights is None:
+        raise ValueError("eviction needs a cache with weights")
+    if out is None:
+        lens_out, weights_out, pos_out = cache.lens, cache.weights, cache.pos
+    else:
+        lens_out, weights_out, pos_out = out
+        _want(lens_out, "lens_out", cache.lens.shape, torch.int32, cache.device)
+        _want(weights_out, "weights_out", cache.weights.shape, torch.float32, cache.device)
+        if (pos_out is None) != (cache.pos is None):
+            raise ValueError("pos_out goes with the cache's pos")
+        _want(pos_out, "pos_out", cache.weights.shape, torch.int32, cache.device)
+    cfg = cache.config(cache.Hkv)
+    if budget < 1 or budget > cache.max_len or keep_first < 0 or keep_last < 0 or keep_first + keep_last > budget:
+        raise ValueError(f"want 1 <= budget <= {cache.max_len} and keep_first + keep_last <= budget, got "
+                         f"{budget}, {keep_first}, {keep_last}")
+    with _on(cache.device, stream) as s:
+        src = torch.empty(cache.B, cache.Hkv, budget, dtype=torch.int32, device=cache.device) if want_src else None
+        ws = cache.workspace(cfg, CALL_EVICT)
+        st = lib().capattn_cache_evict(
+            ctypes.byref(cfg), budget, keep_first, keep_last, _ca._ptr(cache.k), _ca._ptr(cache.v),
+            _ca._ptr(cache.table), _ca._ptr(cache.lens), _ca._ptr(cache.weights), _ca._ptr(cache.pos),
+            _ca._ptr(cache.qpos), _ca._ptr(lens_out), _ca._ptr(weights_out), _ca._ptr(pos_out), _ca._ptr(src),
+            _ca._ptr(ws), ws.numel(), s)
+    _ca._check(st, "capattn_cache_evict")
+    return src
+
+
+def new_key_weights_workspace(q, k, ap: AttnParams) -> torch.Tensor:
+    """Workspace of key_weights for q [B, L, Hq, D] and k [B, Lk, Hkv, D]."""
+    cfg = _ca._config(q, k, ap)
+    n = _ca.workspace_bytes(cfg, PASS_FWD)
+    if n == 0:
+        _ca._check(lib().capattn_validate_config(ctypes.byref(cfg)), "capattn_workspace_bytes")
+    ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+    ws[:256].zero_()  # the status word
+    return ws
+
+
+def key_weights(q, k, lse, ap: AttnParams, temp=None, seg=None, bounds=None, rows=None, out=None, workspace=None,
+                stream=None):
+    """The attention weight that each key received: w[b, g, j] = sum over the query
+    heads of group g and the counted rows i of exp(t_ij - lse_i), with the masks
+    and the lse of capattn_fwd for the same inputs.  rows [B, 2] int32: the
+    counted query rows lo <= i < hi (None: all).  Returns w [B, Hkv, W] fp32, W =
+    Lk, or `out` with W >= Lk (a cache's weights, for instance), of which the
+    entries j < Lk are overwritten."""
+    cfg = _ca._config(q, k, ap)
+    B, L, Hq, D = q.shape
+    Lk, Hkv, dev = k.shape[1], k.shape[2], q.device
+    _want(q, "q", q.shape, q.dtype, dev)
+    _want(k, "k", (B, Lk, Hkv, D), q.dtype, dev)
+    _want(lse, "lse", (B, Hq, L), torch.float32, dev)
+    _want(temp, "temp", (B, L), torch.float32, dev)
+    _want(seg, "seg", (B, L), torch.int32, dev)
+    _want(bounds, "bounds", (B, 4), torch.int32, dev)
+    _want(rows, "rows", (B, 2), torch.int32, dev)
+    if dev.type != "cuda":
+        raise ValueError(f"q has to be on a GPU, got {dev}")
+    if out is not None and (out.dim() != 3 or out.shape[2] < Lk):
+        raise ValueError(f"out is [B, Hkv, W] with W >= {Lk}, got {tuple(out.shape)}")
+    if out is not None:
+        _want(out, "out", (B, Hkv, out.shape[2]), torch.float32, dev)
+    with _on(dev, stream) as s:
+        if workspace is None:
+            workspace = new_key_weights_workspace(q, k, ap)
+        if out is None:
+            out = torch.empty(B, Hkv, Lk, dtype=torch.float32, device=dev)
+        st = lib().capattn_key_weights(
+            ctypes.byref(cfg), _ca._ptr(q), _ca._ptr(k), _ca._ptr(lse), _ca._ptr(temp), _ca._ptr(seg),
+            _ca._ptr(bounds), _ca._ptr(rows), _ca._ptr(out), out.shape[2], _ca._ptr(workspace),
+            workspace.numel(), s)
+    _ca._check(st, "capattn_key_weights")
+    return out
