@@ -69,14 +69,18 @@ typedef struct capattn_cache_config {
 /* Checks a configuration without touching any pointer (same rules as the calls). */
 capattn_status capattn_cache_validate_config(const capattn_cache_config* cfg);
 
+#define CAPATTN_CACHE_HEADER_BYTES 4096
+
 /* Calls that a cache workspace serves. */
 enum { CAPATTN_CACHE_APPEND = 0, CAPATTN_CACHE_DECODE = 1, CAPATTN_CACHE_DECODE_WEIGHTS = 2,
        CAPATTN_CACHE_EVICT = 3 };
 
 /*
  * Bytes of device workspace of a call (CAPATTN_CACHE_*); 0 if cfg is invalid.
- * 256-byte aligned; its first word is the device status, which the caller clears
- * once.  A workspace serves one call at a time: calls (or captured graphs) that
+ * 256-byte aligned.  The caller clears its first CAPATTN_CACHE_HEADER_BYTES once,
+ * before its first use: they hold the device status (the first word) and counters
+ * that every call leaves at zero.  It may serve calls and configurations of any
+ * kind, one after another.  A workspace serves one call at a time: calls (or captured graphs) that
  * may overlap on the GPU need one each.  DECODE_WEIGHTS (a decode with weights)
  * also holds the step's scores, 4 bytes per (query head, slot).
  */

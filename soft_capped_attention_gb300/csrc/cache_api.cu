@@ -56,7 +56,7 @@ ExactCap exact_cap_of(int method, float cap_in, float alpha, float beta, int* ac
 CacheWorkspace layout(const capattn_cache_config& c, int call) {
   CacheWorkspace w;
   memset(&w, 0, sizeof(w));
-  size_t at = 256;  // the status word
+  size_t at = kCacheHeaderBytes;
   const size_t rows = (size_t)c.B * c.Hkv, max_len = max_len_of(c);
   if (call == CAPATTN_CACHE_DECODE || call == CAPATTN_CACHE_DECODE_WEIGHTS) {
     const size_t slots = 2 * (size_t)kDecodeMaxCtas;
@@ -100,6 +100,7 @@ CacheParams params_of(const capattn_cache_config& c, void* ws, int call) {
   const CacheWorkspace w = layout(c, call);
   char* base = static_cast<char*>(ws);
   p.status = reinterpret_cast<uint32_t*>(base);
+  p.counters = reinterpret_cast<uint32_t*>(base + kCountersOff);
   p.part_ml = reinterpret_cast<float2*>(base + w.part_ml_off);
   p.part_o = reinterpret_cast<float*>(base + w.part_o_off);
   p.scores = w.scores_off ? reinterpret_cast<float*>(base + w.scores_off) : nullptr;

@@ -1,5 +1,5 @@
 // Attention of one new token per sequence over the paged cache: the CUDA-core
-// kernel (fp32), the join of the pieces and the weights pass.
+// kernel (fp32) and the weights pass.
 //
 // Per (sequence b, group of up to 16 query heads of one KV head), over live
 // slots j:  t_j = temp cap(sm_scale <q, k_j>),  m = max t, l = sum e^(t - m),
@@ -27,11 +27,6 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <typename T>
-__device__ __forceinline__ float to_f(T x) { return (float)x; }
-template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-
 // Dot product of 16 bytes of a key row with q in shared memory.
 __device__ __forceinline__ void dot16(float& acc, const float* k, const float* q) {
   const float4 a = *reinterpret_cast<const float4*>(k), b = *reinterpret_cast<const float4*>(q);
@@ -40,16 +35,6 @@ __device__ __forceinline__ void dot16(float& acc, const float* k, const float* q
   acc = fmaf(a.z, b.z, acc);
   acc = fmaf(a.w, b.w, acc);
 }
-__device__ __forceinline__ void dot16(float& acc, const __nv_bfloat16* k, const float* q) {
-  const uint4 a = *reinterpret_cast<const uint4*>(k);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    acc = fmaf(__uint_as_float(w[e] << 16), q[2 * e], acc);
-    acc = fmaf(__uint_as_float(w[e] & 0xFFFF0000u), q[2 * e + 1], acc);
-  }
-}
-
 template <typename T, int D>
 struct Smem {
   static constexpr int PER = 16 / sizeof(T);
@@ -61,6 +46,8 @@ struct Smem {
   float scale[kDecodeHeads];
   float m[kDecodeHeads], l[kDecodeHeads];
   float half[kDecodeHeads][64];  // D = 64: outputs of the second half of the threads
+  float join[16][D], lsum[16];
+  int flag;
 };
 
 // Tiles of 32 keys come in by cp.async, two stages.  Scores: warp w takes heads
@@ -91,7 +78,7 @@ decode_simt_kernel(CacheParams p) {
     for (int i = threadIdx.x; i < kDecodeHeads * D; i += kThreads) {
       const int g = i / D;
       s.q[g][i % D] = g < hg.count
-          ? to_f(static_cast<const T*>(p.q)[(size_t)b * p.q_stride + (size_t)(hg.h0 + g) * D + i % D]) : 0.f;
+          ? static_cast<const T*>(p.q)[(size_t)b * p.q_stride + (size_t)(hg.h0 + g) * D + i % D] : 0.f;
     }
     const float temp = p.temp ? p.temp[b] : 1.f;
     const int qpos = p.pos ? p.qpos[b] : 0;
@@ -172,7 +159,7 @@ decode_simt_kernel(CacheParams p) {
       for (int k4 = 0; k4 < KEYS; k4 += 4) {
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = to_f(s.v[st][part * KEYS + k4 + e][d]);
+        for (int e = 0; e < 4; ++e) v[e] = s.v[st][part * KEYS + k4 + e][d];
 #pragma unroll
         for (int g = 0; g < GM; ++g) {
           if (g < hg.count) {
@@ -205,72 +192,16 @@ decode_simt_kernel(CacheParams p) {
         if (it.whole) {
           const float lg = s.l[g];
           const size_t row = (size_t)b * p.Hq + hg.h0 + g;
-          static_cast<T*>(p.o)[row * D + d] = (T)(s.m[g] == -INFINITY ? 0.f : o / lg);
-          if (d == 0) p.lse[row] = s.m[g] == -INFINITY ? -INFINITY : s.m[g] + logf(lg);
+          static_cast<T*>(p.o)[row * D + d] = (T)(lg == 0.f ? 0.f : o / lg);
+          if (d == 0) p.lse[row] = lg == 0.f ? -INFINITY : s.m[g] + logf(lg);
         } else {
           p.part_o[((size_t)it.slot * kDecodeHeads + g) * D + d] = o;
           if (d == 0) p.part_ml[(size_t)it.slot * kDecodeHeads + g] = make_float2(s.m[g], s.l[g]);
         }
       }
     }
+    if (!it.whole) join_pieces<T, D, TK>(p, it, b, hg, threadIdx.x, 1, &s.join[0][0], s.lsum, &s.flag);
     __syncthreads();
-  }
-}
-
-// Joins the pieces of one (sequence, query head): a CTA of four warps, each
-// taking every fourth piece, a lane D / 32 columns.
-template <typename T, int D, int TKEYS>
-__global__ void __launch_bounds__(kThreads)
-decode_join_kernel(CacheParams p) {
-  constexpr int V = D / 32;
-  __shared__ float sl[4], so[4][D];
-  pdl_trigger();
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x, b = row / p.Hq, h = row % p.Hq;
-  const int g = h / p.G, vh = g * p.HG + (h - g * p.G) / kDecodeHeads;
-  const int in = (h - g * p.G) % kDecodeHeads;
-  // units before this (sequence, group)
-  int all = 0, before = 0;
-  for (int x = lane; x < p.B; x += 32) {
-    const int n = seq_span<TKEYS>(p, x).tiles;
-    all += n;
-    if (x < b) before += n;
-  }
-  all = __reduce_add_sync(0xFFFFFFFFu, all);
-  before = __reduce_add_sync(0xFFFFFFFFu, before);
-  const int tiles = seq_span<TKEYS>(p, b).tiles;
-  const uint32_t share = share_of(p, (uint32_t)all * (uint32_t)p.VH);
-  const uint32_t u0 = (uint32_t)before * p.VH + (uint32_t)vh * tiles, u1 = u0 + tiles;
-  const int c0 = (int)(u0 / share), c1 = (int)((u1 - 1) / share);
-  if (c0 == c1) return;  // written by its CTA
-  auto slot_of = [&](int c) { return 2 * c + (c == c0 && u0 != share * (uint32_t)c ? 1 : 0); };
-  float mx = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, p.part_ml[(size_t)slot_of(c) * kDecodeHeads + in].x);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
-  const float ref = mx == -INFINITY ? 0.f : mx;
-  float l = 0.f, o[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) o[e] = 0.f;
-#pragma unroll 4
-  for (int c = c0 + warp; c <= c1; c += 4) {
-    const size_t at = (size_t)slot_of(c) * kDecodeHeads + in;
-    const float2 ml = p.part_ml[at];
-    const float w = __expf(ml.x - ref);
-    l = fmaf(ml.y, w, l);
-#pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = fmaf(p.part_o[at * D + lane + 32 * e], w, o[e]);
-  }
-  if (lane == 0) sl[warp] = l;
-#pragma unroll
-  for (int e = 0; e < V; ++e) so[warp][lane + 32 * e] = o[e];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    const float sum = (sl[0] + sl[1]) + (sl[2] + sl[3]);
-    const float x = (so[0][threadIdx.x] + so[1][threadIdx.x]) + (so[2][threadIdx.x] + so[3][threadIdx.x]);
-    static_cast<T*>(p.o)[(size_t)row * D + threadIdx.x] = (T)(mx == -INFINITY ? 0.f : x / sum);
-    if (threadIdx.x == 0) p.lse[row] = mx == -INFINITY ? -INFINITY : mx + logf(sum);
   }
 }
 
@@ -293,53 +224,51 @@ decode_weights_kernel(CacheParams p) {
   }
 }
 
-template <typename T, int D, int METHOD, int GM>
+template <int D, int METHOD, int GM>
 cudaError_t run_simt(const CacheParams& p, cudaStream_t s) {
-  auto* k = decode_simt_kernel<T, D, METHOD, GM>;
-  const int smem = sizeof(Smem<T, D>);
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto* k = decode_simt_kernel<float, D, METHOD, GM>;
+  static std::atomic<uint64_t> done{0};
+  const int smem = sizeof(Smem<float, D>);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, dim3(p.ctas), dim3(kThreads), smem, s, p);
 }
 
-template <typename T, int D, int METHOD>
+template <int D, int METHOD>
 cudaError_t run_heads(const CacheParams& p, cudaStream_t s) {
   const int n = p.G < kDecodeHeads ? p.G : kDecodeHeads;
-  if (n <= 1) return run_simt<T, D, METHOD, 1>(p, s);
-  if (n <= 4) return run_simt<T, D, METHOD, 4>(p, s);
-  return run_simt<T, D, METHOD, 16>(p, s);
+  if (n <= 1) return run_simt<D, METHOD, 1>(p, s);
+  if (n <= 4) return run_simt<D, METHOD, 4>(p, s);
+  return run_simt<D, METHOD, 16>(p, s);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t run_cap(const CacheParams& p, cudaStream_t s) {
   switch (p.method) {
-    case CAPATTN_CAP_TANH: return run_heads<T, D, CAPATTN_CAP_TANH>(p, s);
-    case CAPATTN_CAP_SOFT_SIGN: return run_heads<T, D, CAPATTN_CAP_SOFT_SIGN>(p, s);
-    case CAPATTN_CAP_ALSC: return run_heads<T, D, CAPATTN_CAP_ALSC>(p, s);
-    default: return run_heads<T, D, CAPATTN_CAP_NONE>(p, s);
+    case CAPATTN_CAP_TANH: return run_heads<D, CAPATTN_CAP_TANH>(p, s);
+    case CAPATTN_CAP_SOFT_SIGN: return run_heads<D, CAPATTN_CAP_SOFT_SIGN>(p, s);
+    case CAPATTN_CAP_ALSC: return run_heads<D, CAPATTN_CAP_ALSC>(p, s);
+    default: return run_heads<D, CAPATTN_CAP_NONE>(p, s);
   }
 }
 
-template <typename T, int D>
-cudaError_t run_all(const CacheParams& p, cudaStream_t s) {
-  cudaError_t e = run_cap<T, D>(p, s);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(decode_join_kernel<T, D, TK>, dim3(p.B * p.Hq), dim3(kThreads), 0, s, p);
-  if (e != cudaSuccess || !p.scores) return e;
-  const int live = p.window_len > 0 && !p.pos ? min(p.max_len, p.window_len) : p.max_len;
-  const dim3 grid(p.B * p.Hkv, min((live + 255) / 256, 1024));
-  return launch_pdl(decode_weights_kernel, grid, dim3(256), 0, s, p);
+cudaError_t launch_decode_fp32(const CacheParams& p0, cudaStream_t s) {
+  CacheParams p = p0;
+  // three CTAs fit an SM; no more than there can be tiles
+  const int64_t most = (int64_t)p.B * p.VH * ((p.max_len + TK - 1) / TK);
+  p.ctas = (int)(most < 152 * 3 ? most : 152 * 3);
+  p.min_tiles = 2;
+  return p.D == 64 ? run_cap<64>(p, s) : run_cap<128>(p, s);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_decode(const CacheParams& p0, int dtype, cudaStream_t s) {
-  CacheParams p = p0;
-  p.ctas = 152 * 3;
-  p.min_tiles = 2;
-  if (dtype == CAPATTN_BF16)
-    return p.D == 64 ? run_all<__nv_bfloat16, 64>(p, s) : run_all<__nv_bfloat16, 128>(p, s);
-  return p.D == 64 ? run_all<float, 64>(p, s) : run_all<float, 128>(p, s);
+cudaError_t launch_cache_decode(const CacheParams& p, int dtype, cudaStream_t s) {
+  const cudaError_t e = dtype == CAPATTN_BF16 ? launch_decode_tc(p, s) : launch_decode_fp32(p, s);
+  if (e != cudaSuccess || !p.scores) return e;
+  const int live = p.window_len > 0 && !p.pos ? min(p.max_len, p.window_len) : p.max_len;
+  const dim3 grid(p.B * p.Hkv, min((live + 255) / 256, 1024));
+  return launch_pdl(decode_weights_kernel, grid, dim3(256), 0, s, p);
 }
 
 }  // namespace capattn

@@ -1,0 +1,412 @@
+// Attention of one new token per sequence over the paged cache, bf16.
+//
+// What bounds it: every cached key and value is read once, 4 D bytes a token and
+// KV head against 4 D G operations, so memory does at any group size G of up to
+// 16; the kernel's task is to keep the loads in flight.  A persistent grid, two
+// CTAs an SM, takes equal shares of 64-key tiles (cache_sched.cuh).  In each CTA
+// one warp fills a ring of shared-memory stages by TMA (a tile's pages are boxes
+// of up to 64 rows x 64 columns in the 128-byte swizzle) and four warps compute,
+// 16 keys of the tile each, with a running (m, l, O) of their own that meets the
+// others' only at a piece's end.
+//
+// Per warp and 16 keys, on mma.m16n8k16 (the rows are the group's query heads,
+// padded to 16: there is one query, so a tcgen05 tile of 128 rows would be
+// empty to 7/8 or more; at 24 bytes a clock and SM the mma pipe is nearly idle
+// either way):
+//   S = Q K^T    Q's fragments stay in registers, K's come by ldmatrix
+//   t = temp cap(sm_scale S), P = e^(t - m)
+//   O += P V     P's accumulators are the A fragment as they stand; V's by
+//                ldmatrix.trans.  P goes in as two bf16 halves (P = hi + lo, 2^-17
+//                of it lost), since the tensor pipe has the room: rounding P to
+//                one bf16 would add half of what rounding o to bf16 does.
+// The reference m moves only when the maximum outgrows it by kSlack (P stays
+// below e^kSlack), which saves the rescaling of O on nearly every step.
+#include <cuda_bf16.h>
+
+#include "cache_internal.h"
+#include "cache_math.cuh"
+#include "cache_sched.cuh"
+#include "cap_math.cuh"
+#include "tma_maps.h"
+
+namespace capattn {
+namespace {
+
+constexpr int TK = 64;                 // keys of a tile
+constexpr int kConsumers = 4;          // warps that compute, 16 keys of a tile each
+constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr float kSlack = 8.f;
+
+template <int D>
+struct Geo {
+  static constexpr int SLABS = D / 64;                // 128-byte wide columns of a row
+  static constexpr int SLAB = TK * 128;
+  static constexpr int HALF = SLABS * SLAB;           // K (or V) of a stage
+  static constexpr int STAGE = 2 * HALF;
+  static constexpr int STAGES = D == 128 ? 3 : 6;     // 96 KB a CTA, two CTAs an SM
+  static constexpr int MERGE = 16 * D * 4;            // 4 warps x 4 heads x D floats
+  static constexpr int SMEM = STAGES * STAGE + MERGE + 1024;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+// Two floats as bf16 pairs hi + lo.
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x, y);
+  lo = pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
+}
+
+// ROWS: 1 when the group has at most 8 query heads (the upper 8 rows of the
+// tensor-core tile are then empty), else 2.
+template <int D, int METHOD, int ROWS>
+__global__ void __launch_bounds__(kThreads, 2)
+decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const CacheParams p) {
+  using G = Geo<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * G::STAGES];
+  __shared__ int abort_flag, join_flag;
+  __shared__ float s_m[kConsumers][16], s_l[kConsumers][16], s_lsum[16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  float* merge = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + G::STAGES * G::STAGE);
+  const uint32_t full = smem_u32(&bars[0]), empty = smem_u32(&bars[G::STAGES]);
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < G::STAGES; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, kConsumers);
+    }
+    fence_mbar_init();
+  }
+  pdl_trigger();
+  pdl_wait();
+  __syncthreads();
+  PieceIter<TK> it(p, lane);
+  int b, vh, tile;
+  SeqSpan sp;
+  uint32_t step = 0;  // tiles so far, over the pieces
+
+  if (warp == kConsumers) {
+    // ------------------------------------------------------------ TMA producer
+    const int rows = min(TK, p.page_size);      // rows of a box
+    const int pages = TK / rows;                // boxes of a tile, one a lane
+    const uint32_t bytes = (uint32_t)rows * D * 2 * 2;
+    if (lane == 0) {
+      tma_prefetch_desc(&mk);
+      tma_prefetch_desc(&mv);
+    }
+    bool ok = true;
+    while (ok && it.next(p, &b, &vh, &tile, &sp)) {
+      const int g = vh / p.HG;
+      // cache row of this lane's box of a tile, or -1: no live slot in it
+      auto row_of = [&](int t) {
+        const int j = t * TK + lane * rows;
+        if (lane >= pages || j >= sp.len || j + rows <= sp.first) return -1;
+        return (page_of(p, b, j) * p.Hkv + g) * p.page_size + (j & (p.page_size - 1));
+      };
+      int row = row_of(tile);
+      for (int i = 0; i < it.n; ++i, ++step) {
+        const int next = i + 1 < it.n ? row_of(tile + i + 1) : -1;  // a tile ahead of its use
+        const uint32_t s = step % G::STAGES, use = step / G::STAGES;
+        if (use > 0 && !mbar_wait_warp(empty + 8 * s, (use - 1) & 1, p.status, &abort_flag)) {
+          ok = false;
+          break;
+        }
+        const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0));
+        if (lane == 0) mbar_expect_tx(full + 8 * s, boxes * bytes);
+        __syncwarp();
+        if (row >= 0) {
+          const uint32_t dst = base + s * G::STAGE + lane * rows * 128;
+#pragma unroll
+          for (int x = 0; x < G::SLABS; ++x) {
+            tma_load_2d(dst + x * G::SLAB, &mk, full + 8 * s, 64 * x, row);
+            tma_load_2d(dst + G::HALF + x * G::SLAB, &mv, full + 8 * s, 64 * x, row);
+          }
+        }
+        __syncwarp();
+        row = next;
+      }
+    }
+    // normally long complete: the consumers waited for every stage
+    for (uint32_t x = step > G::STAGES ? step - G::STAGES : 0; x < step; ++x)
+      drain_wait(full + 8 * (x % G::STAGES), (x / G::STAGES) & 1);
+    return;
+  }
+
+  // ---------------------------------------------------------------- consumers
+  const int tid = threadIdx.x;
+  const int gq = lane >> 2, tq = lane & 3;      // fragment row and column group
+  const uint32_t sw = lane & 7;
+  // this lane's row addresses in a stage's K and V slabs
+  const uint32_t k_row = (uint32_t)(16 * warp + (lane & 7) + ((lane >> 4) << 3)) * 128u, k_add = (lane >> 3) & 1;
+  const uint32_t v_row = (uint32_t)(16 * warp + (lane & 7) + (((lane >> 3) & 1) << 3)) * 128u, v_add = lane >> 4;
+  bool ok = true;
+  while (it.next(p, &b, &vh, &tile, &sp)) {
+    const HeadGroup hg = head_group(p, vh);
+    const float temp = p.temp ? p.temp[b] : 1.f;
+    const bool by_pos = p.pos && p.window_len > 0;
+    const int32_t* pos = p.pos + ((size_t)b * p.Hkv + hg.g) * p.max_len;
+    const int oldest = by_pos ? p.qpos[b] - p.window_len : 0;
+    uint32_t q[D / 16][4];
+    {
+      const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(p.q) + (size_t)b * p.q_stride + (size_t)hg.h0 * D;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = gq + 8 * (e & 1);
+          q[ks][e] = (ROWS == 2 || (e & 1) == 0) && r < hg.count
+              ? *reinterpret_cast<const uint32_t*>(qb + (size_t)r * D + 16 * ks + 8 * (e >> 1) + 2 * tq) : 0u;
+        }
+    }
+    float m[ROWS], l[ROWS], o[D / 8][4];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+#pragma unroll
+    for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[x][e] = 0.f;
+
+    for (int i = 0; i < it.n; ++i, ++step) {
+      const uint32_t s = step % G::STAGES, use = step / G::STAGES;
+      // after a timeout the warp still meets the others at every piece's barriers
+      ok = ok && mbar_wait_warp(full + 8 * s, use & 1, p.status, &abort_flag);
+      if (!ok) break;
+      const int j0 = (tile + i) * TK + 16 * warp;
+      if (j0 < sp.len && j0 + 16 > sp.first) {
+        const uint32_t kb = base + s * G::STAGE + k_row, vb = base + s * G::STAGE + G::HALF + v_row;
+        float c[2][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t kf[4];
+          ldsm4(kb + (ks >> 2) * G::SLAB + (((uint32_t)(2 * (ks & 3)) + k_add) ^ sw) * 16u, kf);
+          mma16816(c[0], q[ks], kf[0], kf[1]);
+          mma16816(c[1], q[ks], kf[2], kf[3]);
+        }
+        // keys of this lane: j0 + 8 n + 2 tq + e
+        const bool all = !by_pos && j0 >= sp.first && j0 + 16 <= sp.len;
+        bool live[2][2] = {{true, true}, {true, true}};
+        if (!all) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int j = j0 + 8 * n + 2 * tq + e;
+              live[n][e] = j >= sp.first && j < sp.len;
+              if (by_pos && live[n][e]) live[n][e] = pos[j] > oldest;
+            }
+        }
+        uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+        bool grow = false;
+        float mx[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float t = exact_cap<METHOD>(c[n][2 * r + e] * p.sm_scale, p.cap) * temp;
+              t = live[n][e] ? t : -INFINITY;
+              c[n][2 * r + e] = t;
+              top = fmaxf(top, t);
+            }
+          if (p.scores && gq + 8 * r < hg.count) {
+            float* sc = p.scores + ((size_t)b * p.Hq + hg.h0 + gq + 8 * r) * p.max_len;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const int j = j0 + 8 * n + 2 * tq;
+              if (j < sp.len) *reinterpret_cast<float2*>(sc + j) = make_float2(c[n][2 * r], c[n][2 * r + 1]);
+            }
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          mx[r] = top;
+          grow = grow || top > m[r] + kSlack;
+        }
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            const float top = fmaxf(m[r], mx[r]);
+            const float scale = top == -INFINITY ? 1.f : __expf(m[r] - top);
+            m[r] = top;
+            l[r] *= scale;
+#pragma unroll
+            for (int x = 0; x < D / 8; ++x) {
+              o[x][2 * r] *= scale;
+              o[x][2 * r + 1] *= scale;
+            }
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          const float ref = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float p0 = __expf(c[n][2 * r] - ref), p1 = __expf(c[n][2 * r + 1] - ref);
+            l[r] += p0 + p1;
+            split_bf16(p0, p1, hi[2 * n + r], lo[2 * n + r]);
+          }
+        }
+        uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (!all) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            keep[n] = (live[n][0] ? 0xFFFFu : 0u) | (live[n][1] ? 0xFFFF0000u : 0u);
+        }
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          uint32_t vf[4];
+          ldsm4_t(vb + (x >> 2) * G::SLAB + (((uint32_t)(2 * (x & 3)) + v_add) ^ sw) * 16u, vf);
+          if (!all) {  // whatever a dead slot holds, NaN too, stays out
+            vf[0] &= keep[0];
+            vf[1] &= keep[1];
+            vf[2] &= keep[0];
+            vf[3] &= keep[1];
+          }
+          mma16816(o[2 * x], hi, vf[0], vf[1]);
+          mma16816(o[2 * x + 1], hi, vf[2], vf[3]);
+          mma16816(o[2 * x], lo, vf[0], vf[1]);
+          mma16816(o[2 * x + 1], lo, vf[2], vf[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * s);
+    }
+    // ---------------------------------------------------------- end of a piece
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
+      if (tq == 0) {
+        s_m[warp][gq + 8 * r] = m[r];
+        s_l[warp][gq + 8 * r] = l[r];
+      }
+    }
+    named_bar_sync(1, kConsumers * 32);
+    float scale[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int h = gq + 8 * r;
+      float top = fmaxf(fmaxf(s_m[0][h], s_m[1][h]), fmaxf(s_m[2][h], s_m[3][h]));
+      scale[r] = m[r] == -INFINITY ? 0.f : __expf(m[r] - top);
+      if (m[r] == -INFINITY && l[r] != 0.f) scale[r] = 1.f;  // nothing but NaN scores: they come through
+    }
+    for (int g0 = 0; g0 < hg.count; g0 += 4) {
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        const int e = gq + 8 * r - g0;
+        if (e >= 0 && e < 4) {
+#pragma unroll
+          for (int x = 0; x < D / 8; ++x)
+            *reinterpret_cast<float2*>(&merge[(warp * 4 + e) * D + 8 * x + 2 * tq]) =
+                make_float2(o[x][2 * r] * scale[r], o[x][2 * r + 1] * scale[r]);
+        }
+      }
+      named_bar_sync(1, kConsumers * 32);
+      for (int x = tid; x < min(4, hg.count - g0) * D; x += kConsumers * 32) {
+        const int e = x / D, d = x % D, h = g0 + e;
+        float top = fmaxf(fmaxf(s_m[0][h], s_m[1][h]), fmaxf(s_m[2][h], s_m[3][h]));
+        float sum = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) {
+          const float mw = s_m[w][h], lw = s_l[w][h];
+          if (lw != 0.f) sum += lw * (mw == -INFINITY ? 1.f : __expf(mw - top));
+          y += merge[(w * 4 + e) * D + d];
+        }
+        if (it.whole) {
+          const size_t row = (size_t)b * p.Hq + hg.h0 + h;
+          static_cast<__nv_bfloat16*>(p.o)[row * D + d] = __float2bfloat16(sum == 0.f ? 0.f : y / sum);
+          if (d == 0) p.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
+        } else {
+          const size_t at = (size_t)it.slot * kDecodeHeads + h;
+          p.part_o[at * D + d] = y;
+          if (d == 0) p.part_ml[at] = make_float2(top, sum);
+        }
+      }
+      named_bar_sync(1, kConsumers * 32);
+    }
+    if (!it.whole) join_pieces<__nv_bfloat16, D, TK>(p, it, b, hg, tid, 1, merge, s_lsum, &join_flag);
+  }
+}
+
+// 2-D map over the cache's rows [num_pages * Hkv * page_size][D]: boxes of 64
+// columns x the rows a tile has of a page, 128-byte swizzle.
+cudaError_t make_rows_map(CUtensorMap* map, const void* base, const CacheParams& p) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  cuuint64_t dims[2] = {(cuuint64_t)p.D, (cuuint64_t)p.num_pages * p.Hkv * p.page_size};
+  cuuint64_t strides[1] = {(cuuint64_t)p.D * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)(p.page_size < TK ? p.page_size : TK)};
+  cuuint32_t es[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D, int METHOD, int ROWS>
+cudaError_t run_tc(const CacheParams& p, cudaStream_t s) {
+  auto* k = decode_tc_kernel<D, METHOD, ROWS>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), Geo<D>::SMEM, done);
+  CUtensorMap mk, mv;
+  if (e == cudaSuccess) e = make_rows_map(&mk, p.k, p);
+  if (e == cudaSuccess) e = make_rows_map(&mv, p.v, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k, dim3(p.ctas), dim3(kThreads), Geo<D>::SMEM, s, mk, mv, p);
+}
+
+template <int D, int METHOD>
+cudaError_t run_rows(const CacheParams& p, cudaStream_t s) {
+  return p.G <= 8 ? run_tc<D, METHOD, 1>(p, s) : run_tc<D, METHOD, 2>(p, s);
+}
+
+template <int D>
+cudaError_t run_cap(const CacheParams& p, cudaStream_t s) {
+  switch (p.method) {
+    case CAPATTN_CAP_TANH: return run_rows<D, CAPATTN_CAP_TANH>(p, s);
+    case CAPATTN_CAP_SOFT_SIGN: return run_rows<D, CAPATTN_CAP_SOFT_SIGN>(p, s);
+    case CAPATTN_CAP_ALSC: return run_rows<D, CAPATTN_CAP_ALSC>(p, s);
+    default: return run_rows<D, CAPATTN_CAP_NONE>(p, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_decode_tc(const CacheParams& p0, cudaStream_t s) {
+  CacheParams p = p0;
+  const int64_t most = (int64_t)p.B * p.VH * ((p.max_len + TK - 1) / TK);
+  p.ctas = (int)(most < 152 * 2 ? most : 152 * 2);
+  p.min_tiles = 2;
+  return p.D == 64 ? run_cap<64>(p, s) : run_cap<128>(p, s);
+}
+
+}  // namespace capattn

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/capattn_cache.h"
 #include "capattn_internal.h"
 
@@ -50,6 +52,7 @@ struct CacheParams {
   int32_t* src;
   // workspace pieces
   uint32_t* status;
+  uint32_t* counters;        // [kDecodeMaxCtas] pieces left so far of the group that starts in a CTA
   float2* part_ml;           // [slots][16] running (max, sum) of a piece's heads
   float* part_o;             // [slots][16][D] unnormalised outputs
   float* scores;             // [B, Hq, max_len] scores of the step (decode with weights)
@@ -72,6 +75,12 @@ constexpr int kDecodeHeads = 16;
 // Most CTAs of the persistent decode (bounds its partial results).
 constexpr int kDecodeMaxCtas = 152 * 4;
 
+// Every cache workspace starts with the status word and the counters, at places
+// that no configuration moves.
+constexpr size_t kCacheHeaderBytes = 4096;
+constexpr size_t kCountersOff = 256;
+static_assert(kCountersOff + kDecodeMaxCtas * sizeof(uint32_t) <= kCacheHeaderBytes, "header too small");
+
 struct CacheWorkspace {
   size_t part_ml_off, part_o_off, scores_off, moves_off, row_src_off, counts_off, total;
 };
@@ -84,8 +93,22 @@ struct KeyWeightsParams {
   ExactCap cap;
 };
 
+// Raises a kernel's dynamic shared memory limit, once per device (`done`: a bit a device).
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 cudaError_t launch_cache_append(const CacheParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_cache_decode(const CacheParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_decode_tc(const CacheParams& p, cudaStream_t s);  // bf16, without the weights pass
 cudaError_t launch_cache_evict(const CacheParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_key_weights(const Params& p, const KeyWeightsParams& w, int dtype, cudaStream_t s);
 

@@ -26,6 +26,7 @@ import torch
 from . import capattn as _ca
 from .capattn import AttnParams, CAP_METHODS, DTYPES, PASS_FWD
 
+HEADER_BYTES = 4096  # of a cache workspace, zero before its first use
 CALL_APPEND, CALL_DECODE, CALL_DECODE_WEIGHTS, CALL_EVICT = 0, 1, 2, 3
 EXPORTED_SYMBOLS = ("capattn_cache_validate_config", "capattn_cache_workspace_bytes", "capattn_cache_append",
                     "capattn_cache_decode", "capattn_cache_evict", "capattn_key_weights")
@@ -174,7 +175,7 @@ class KVCache:
                 raise RuntimeError("the cache's workspace would grow during a graph capture: "
                                    "make the call once before capturing it")
             new = torch.empty(n, dtype=torch.uint8, device=self.device)
-            new[:256].zero_()  # the status word
+            new[:HEADER_BYTES].zero_()  # the status word and the counters
             self._workspaces.append(new)
         return self._workspaces[-1]
 

@@ -77,7 +77,7 @@ def append_args(**kw):
     ({"k_new": None}, 1), ({"v_new": None}, 1), ({"k": None}, 1), ({"v": None}, 1), ({"table": None}, 1),
     ({"lens": None}, 1), ({"n": -1}, 1), ({"n": 3}, 1), ({"ks": 255}, 1), ({"ks": 128}, 1), ({"vs": 260}, 1),
     ({"pos": P}, 1), ({"k_new": ODD}, 1), ({"k": ODD}, 1), ({"weights": ODD}, 1), ({"ws": None}, 5), ({"ws": ODD}, 5),
-    ({"wb": 255}, 5), ({"cfg": cfg(D=96)}, 2), ({"n": 0, "cu": P, "k_new": None, "v_new": None}, 0),
+    ({"wb": 4095}, 5), ({"cfg": cfg(D=96)}, 2), ({"n": 0, "cu": P, "k_new": None, "v_new": None}, 0),
 ], ids=str)
 def test_append_refusals(lib, kw, status):
     assert lib.capattn_cache_append(*append_args(**kw)) == status
