@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include "cache_internal.h"
+#include "softmax_elem.cuh"
 
 namespace capattn {
 namespace {
@@ -35,21 +36,45 @@ capattn_status check_config(const capattn_cache_config* c) {
   return CAPATTN_OK;
 }
 
-ExactCap exact_cap_of(int method, float cap_in, float alpha, float beta, int* active) {
+ExactCap exact_cap_of(int method, float cap_in, float alpha, float beta, float sm_scale, int* active) {
   ExactCap k;
   memset(&k, 0, sizeof(k));
   *active = cap_in > 0.f ? method : CAPATTN_CAP_NONE;
   const double cap = cap_in > 0.f ? (double)cap_in : 1.0;
-  const double ab = (double)alpha * (double)beta;
-  const double sb = 1.0 / (1.0 + exp(-ab));
+  k.sm_scale = sm_scale;
   k.cap = (float)cap;
   k.inv_cap = (float)(1.0 / cap);
-  k.a = (float)((double)alpha / cap);
-  k.out = (float)(cap / (sb * (1.0 - sb) + 1e-12));
-  k.sb = (float)sb;
-  k.one_minus_sb = (float)(1.0 / (1.0 + exp(ab)));
-  k.eb = (float)fmin(exp(ab), (double)FLT_MAX);
-  k.emb = (float)fmin(exp(-ab), (double)FLT_MAX);
+  if (*active == CAPATTN_CAP_TANH) {
+    // cap tanh(in X): the odd polynomial of softmax_elem.cuh with both scales folded in
+    const double in = (double)sm_scale / cap, w = in * in;
+    const double c[5] = {1.0, kTanhC0, kTanhC1, kTanhC2, kTanhC3};
+    double f = cap * in;
+    for (int i = 0; i < 5; ++i, f *= w) k.poly[i] = (float)(c[i] * f);
+    // usable while its last coefficient is a normal number
+    k.xmax = fabsf(k.poly[4]) >= 1e-30f && isfinite(k.poly[4]) ? (float)(kTanhPolyMaxU / fabs(in)) : 0.f;
+  } else if (*active == CAPATTN_CAP_ALSC) {
+    const double ab = (double)alpha * (double)beta;
+    const double sb = 1.0 / (1.0 + exp(-ab));
+    k.a = (float)((double)alpha / cap);
+    k.out = (float)(cap / (sb * (1.0 - sb) + 1e-12));
+    k.sb = (float)sb;
+    k.one_minus_sb = (float)(1.0 / (1.0 + exp(ab)));
+    k.eb = (float)fmin(exp(ab), (double)FLT_MAX);
+    k.emb = (float)fmin(exp(-ab), (double)FLT_MAX);
+    capattn_config c;  // the fit asks for a whole configuration; the shape plays no part
+    memset(&c, 0, sizeof(c));
+    c.struct_size = sizeof(c);
+    c.cap_method = method;
+    c.cap = cap_in; c.alpha = alpha; c.beta = beta; c.sm_scale = sm_scale;
+    c.q_heads_per_kv_head = c.B = c.L = c.Hq = c.Hkv = 1;
+    c.D = 64;
+    bool fine = capattn_debug_alsc_poly(&c, k.poly, &k.xmax) == CAPATTN_OK && isfinite(k.xmax);
+    for (int i = 0; i < 7; ++i) {
+      k.poly[i] *= k.out;
+      fine = fine && isfinite(k.poly[i]) && (fabsf(k.poly[i]) >= 1e-30f || k.poly[i] == 0.f);
+    }
+    if (!fine) k.xmax = 0.f;
+  }
   return k;
 }
 
@@ -96,7 +121,7 @@ CacheParams params_of(const capattn_cache_config& c, void* ws, int call) {
   p.VH = p.Hkv * p.HG;
   p.sm_scale = c.sm_scale;
   p.window_len = c.window_len;
-  p.cap = exact_cap_of(c.cap_method, c.cap, c.alpha, c.beta, &p.method);
+  p.cap = exact_cap_of(c.cap_method, c.cap, c.alpha, c.beta, c.sm_scale, &p.method);
   const CacheWorkspace w = layout(c, call);
   char* base = static_cast<char*>(ws);
   p.status = reinterpret_cast<uint32_t*>(base);
@@ -239,7 +264,7 @@ capattn_status capattn_key_weights(const capattn_config* cfg, const void* q, con
   p.causal = cfg->causal ? 1 : 0;
   p.window_len = cfg->window_len;
   KeyWeightsParams kw;
-  kw.cap = exact_cap_of(cfg->cap_method, cfg->cap, cfg->alpha, cfg->beta, &p.cap.method);
+  kw.cap = exact_cap_of(cfg->cap_method, cfg->cap, cfg->alpha, cfg->beta, cfg->sm_scale, &p.cap.method);
   kw.rows = rows; kw.w = w; kw.w_stride = w_row_stride;
   const WorkspaceLayout l = workspace_layout(*cfg, p.block_q, p.block_kv);
   char* base = static_cast<char*>(workspace);

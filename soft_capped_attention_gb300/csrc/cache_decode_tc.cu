@@ -224,20 +224,35 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             }
         }
         uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
-        bool grow = false;
+        bool grow = false, poly = false;
+        if constexpr (has_poly(METHOD)) {
+          float am = 0.f;
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) am = fmax3_abs(am, c[n][2 * r], c[n][2 * r + 1]);
+          poly = __all_sync(0xFFFFFFFFu, am <= p.cap.xmax && p.cap.xmax > 0.f);
+        }
         float mx[ROWS];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
           float top = -INFINITY;
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < 2; ++n) {
+            float t[2];
+            if (has_poly(METHOD) && poly) {
+              f2_split(poly_cap2<METHOD>(f2(c[n][2 * r], c[n][2 * r + 1]), p.cap), t[0], t[1]);
+            } else {
+              t[0] = any_cap<METHOD>(c[n][2 * r], p.cap);
+              t[1] = any_cap<METHOD>(c[n][2 * r + 1], p.cap);
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float t = exact_cap<METHOD>(c[n][2 * r + e] * p.sm_scale, p.cap) * temp;
-              t = live[n][e] ? t : -INFINITY;
-              c[n][2 * r + e] = t;
-              top = fmaxf(top, t);
+              const float x = live[n][e] ? t[e] * temp : -INFINITY;
+              c[n][2 * r + e] = x;
+              top = fmaxf(top, x);
             }
+          }
           if (p.scores && gq + 8 * r < hg.count) {
             float* sc = p.scores + ((size_t)b * p.Hq + hg.h0 + gq + 8 * r) * p.max_len;
 #pragma unroll

@@ -17,13 +17,18 @@ constexpr uint32_t kStatusBadPageBit = 64u;     // a page outside [0, num_pages)
 constexpr uint32_t kStatusBadNewRowsBit = 128u; // cu_new decreases, or more new rows than lens
 constexpr uint32_t kStatusBadRowsBit = 256u;    // rows outside 0 <= lo <= hi <= L
 
-// Constants of a cap in the exact form of cache_math.cuh.
+// Constants of a cap in the forms of cache_math.cuh, for raw scores X = <q, k>.
 struct ExactCap {
+  float sm_scale;
   float cap, inv_cap;        // tanh, soft_sign
   float a;                   // alsc: d = a * s
   float out;                 // alsc: cap / denom
   float sb, one_minus_sb;    // alsc: sigma(alpha beta) and 1 - sigma
   float eb, emb;             // alsc: e^(alpha beta), e^(-alpha beta)
+  // cap(sm_scale X) as a polynomial for |X| <= xmax (0: none): tanh
+  // X (c0 + z (c1 + z (c2 + z (c3 + z c4)))), z = X^2; alsc X (c0 + X (c1 + .. + X c6))
+  float poly[7];
+  float xmax;
 };
 
 struct CacheParams {
@@ -110,6 +115,7 @@ cudaError_t launch_cache_append(const CacheParams& p, int dtype, cudaStream_t s)
 cudaError_t launch_cache_decode(const CacheParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_decode_tc(const CacheParams& p, cudaStream_t s);  // bf16, without the weights pass
 cudaError_t launch_cache_evict(const CacheParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_key_weights_tc(const Params& p, const KeyWeightsParams& w, cudaStream_t s);  // bf16
 cudaError_t launch_key_weights(const Params& p, const KeyWeightsParams& w, int dtype, cudaStream_t s);
 
 }  // namespace capattn

@@ -1,6 +1,6 @@
 // Attention weight that each key of a prompt received (capattn_key_weights):
 //   w[b, g, j] = sum over heads h of group g, counted rows i of exp(t_ij - lse_i)
-// with t and the masks of the forward.  One CTA per (b, g, 64 keys) walks the
+// with t and the masks of the forward; here the fp32 kernel.  One CTA per (b, g, 64 keys) walks the
 // group's heads and the query tiles that its key tile's visit map names, so the
 // sums need no atomics and keep their order.
 #include "cache_internal.h"
@@ -12,8 +12,8 @@ namespace {
 
 constexpr int kT = 64;   // keys and queries of a step
 
-// CUDA cores: 256 threads, 4 keys x 4 queries each; rows staged as fp32.
-template <typename T, int D, int METHOD>
+// CUDA cores: 256 threads, 4 keys x 4 queries each; rows staged in shared memory.
+template <int D, int METHOD>
 __global__ void __launch_bounds__(256)
 key_weights_simt_kernel(Params p, KeyWeightsParams kw) {
   constexpr int PAD = D + 4;
@@ -38,11 +38,11 @@ key_weights_simt_kernel(Params p, KeyWeightsParams kw) {
       hi = min(hi, p.L);
     }
   }
-  const T* q = static_cast<const T*>(p.q);
-  const T* k = static_cast<const T*>(p.k);
+  const float* q = static_cast<const float*>(p.q);
+  const float* k = static_cast<const float*>(p.k);
   for (int i = threadIdx.x; i < kT * D; i += 256) {
     const int r = i / D, x = i % D;
-    sk[r * PAD + x] = k0 + r < p.Lk ? (float)k[(((size_t)b * p.Lk + k0 + r) * p.Hkv + g) * D + x] : 0.f;
+    sk[r * PAD + x] = k0 + r < p.Lk ? k[(((size_t)b * p.Lk + k0 + r) * p.Hkv + g) * D + x] : 0.f;
   }
   const uint32_t* map = p.kmap + ((size_t)b * p.nk + k0 / p.block_kv) * p.wq;
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -56,7 +56,7 @@ key_weights_simt_kernel(Params p, KeyWeightsParams kw) {
         __syncthreads();
         for (int i = threadIdx.x; i < kT * D; i += 256) {
           const int r = i / D, x = i % D;
-          sq[r * PAD + x] = q0 + r < p.L ? (float)q[(((size_t)b * p.L + q0 + r) * p.Hq + h) * D + x] : 0.f;
+          sq[r * PAD + x] = q0 + r < p.L ? q[(((size_t)b * p.L + q0 + r) * p.Hq + h) * D + x] : 0.f;
         }
         if (threadIdx.x < kT) {
           const int i = q0 + threadIdx.x;
@@ -107,31 +107,31 @@ key_weights_simt_kernel(Params p, KeyWeightsParams kw) {
   }
 }
 
-template <typename T, int D, int METHOD>
+template <int D, int METHOD>
 cudaError_t run_simt(const Params& p, const KeyWeightsParams& kw, cudaStream_t s) {
-  auto* k = key_weights_simt_kernel<T, D, METHOD>;
+  auto* k = key_weights_simt_kernel<D, METHOD>;
+  static std::atomic<uint64_t> done{0};
   const int smem = 2 * kT * (D + 4) * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, dim3((unsigned)p.B * p.Hkv * ((p.Lk + kT - 1) / kT)), dim3(256), smem, s, p, kw);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t run_cap(const Params& p, const KeyWeightsParams& kw, cudaStream_t s) {
   switch (p.cap.method) {
-    case CAPATTN_CAP_TANH: return run_simt<T, D, CAPATTN_CAP_TANH>(p, kw, s);
-    case CAPATTN_CAP_SOFT_SIGN: return run_simt<T, D, CAPATTN_CAP_SOFT_SIGN>(p, kw, s);
-    case CAPATTN_CAP_ALSC: return run_simt<T, D, CAPATTN_CAP_ALSC>(p, kw, s);
-    default: return run_simt<T, D, CAPATTN_CAP_NONE>(p, kw, s);
+    case CAPATTN_CAP_TANH: return run_simt<D, CAPATTN_CAP_TANH>(p, kw, s);
+    case CAPATTN_CAP_SOFT_SIGN: return run_simt<D, CAPATTN_CAP_SOFT_SIGN>(p, kw, s);
+    case CAPATTN_CAP_ALSC: return run_simt<D, CAPATTN_CAP_ALSC>(p, kw, s);
+    default: return run_simt<D, CAPATTN_CAP_NONE>(p, kw, s);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_key_weights(const Params& p, const KeyWeightsParams& kw, int dtype, cudaStream_t s) {
-  if (dtype == CAPATTN_BF16)
-    return p.D == 64 ? run_cap<__nv_bfloat16, 64>(p, kw, s) : run_cap<__nv_bfloat16, 128>(p, kw, s);
-  return p.D == 64 ? run_cap<float, 64>(p, kw, s) : run_cap<float, 128>(p, kw, s);
+  if (dtype == CAPATTN_BF16) return launch_key_weights_tc(p, kw, s);
+  return p.D == 64 ? run_cap<64>(p, kw, s) : run_cap<128>(p, kw, s);
 }
 
 }  // namespace capattn
