@@ -8,13 +8,27 @@
 // it.  Their number is the least that any compaction has to copy, and a copy
 // never reads what another writes (sources lie behind the budget, destinations
 // below it), so all of them run at once.
+//
+// Selection is bound by latency (its 8 bytes a slot are little against the rows
+// that move): a cluster of up to 8 CTAs takes a row, each CTA a run of slots whose
+// keys it reads once and keeps in shared memory.  Three histogram passes (11, 11
+// and 10 bits) find the threshold, each CTA adding up the cluster's histograms by
+// distributed shared memory; three more passes over the keys count and place.
+// The copies are a kernel of their own, over all SMs.
+#include <cooperative_groups.h>
+
 #include "cache_internal.h"
 
 namespace capattn {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kMaxParts = 8;
+constexpr int kBins = 2048;
+constexpr int kCachedKeys = 40 * 1024;  // keys a CTA keeps in shared memory (160 KB)
 
 // Order of a weight as an unsigned key: larger weight, larger key; both zeros
 // equal; NaN lowest.  Protected slots get 0xFFFFFFFF, above +inf's 0xFF800000.
@@ -34,31 +48,55 @@ struct RowKeys {
   }
 };
 
-// Exclusive sum over the block's warps of one count a warp; *total the whole.
-__device__ __forceinline__ int warp_offsets(int mine, int* buf, int warp, int lane, int* total) {
-  __syncthreads();
-  if (lane == 0) buf[warp] = mine;
-  __syncthreads();
-  int x = lane < kSelWarps ? buf[lane] : 0, up = x;
+struct Shared {
+  int hist[3][kBins];
+  int warp_sum[3][kSelWarps];
+  int totals[3];              // of this CTA: equal keys, movers, freed slots
+  uint32_t digit;
+  int above;
+};
+
+// Exclusive sum of x over the block's threads; *total the whole (buf: a word a warp).
+__device__ __forceinline__ int block_scan(int x, int* buf, int warp, int lane, int* total) {
+  int up = x;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int y = __shfl_up_sync(0xFFFFFFFFu, up, d);
     if (lane >= d) up += y;
   }
-  *total = __shfl_sync(0xFFFFFFFFu, up, 31);
-  return __shfl_sync(0xFFFFFFFFu, up - x, warp);
+  if (lane == 31) buf[warp] = up;
+  __syncthreads();
+  const int w = buf[lane];  // 32 warps
+  int all = w;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, all, d);
+    if (lane >= d) all += y;
+  }
+  *total = __shfl_sync(0xFFFFFFFFu, all, 31);
+  return up - x + __shfl_sync(0xFFFFFFFFu, all - w, warp);
 }
 
-__global__ void __launch_bounds__(kSelThreads)
-select_kernel(CacheParams p) {
-  __shared__ int hist[256];
-  __shared__ int buf[kSelWarps];
-  __shared__ uint32_t s_digit;
-  __shared__ int s_above;
+__device__ __forceinline__ int cache_row(const CacheParams& p, int b, int g, int slot) {
+  const int page = p.table[(size_t)b * p.max_pages + (slot >> p.page_shift)];
+  if (page < 0 || page >= p.num_pages) {
+    atomicOr(p.status, kStatusBadPageBit);
+    return -1;
+  }
+  return ((page * p.Hkv + g) << p.page_shift) + (slot & (p.page_size - 1));
+}
+
+__global__ void __launch_bounds__(kSelThreads, 1)
+select_kernel(CacheParams p, int parts) {
+  extern __shared__ uint32_t s_keys[];
+  __shared__ Shared s;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = blockIdx.x % parts, row = blockIdx.x / parts;
+  const int b = row / p.Hkv, g = row % p.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < 3 * kBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
   pdl_trigger();
   pdl_wait();
-  const int row = blockIdx.x, b = row / p.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int n = p.lens[b];
   if (n < 0 || n > p.max_len) {
     if (threadIdx.x == 0) atomicOr(p.status, kStatusBadLensBit);
@@ -73,74 +111,102 @@ select_kernel(CacheParams p) {
   keys.after = (int)max(newest - p.keep_last, -(1ll << 31));
   int32_t* src = p.src + (size_t)row * p.budget;
   int2* moves = reinterpret_cast<int2*>(p.moves + base);
-  if (n <= p.budget) {  // nothing goes
-    for (int j = threadIdx.x; j < p.budget; j += kSelThreads) {
+  if (n <= p.budget) {  // nothing goes (every CTA of the cluster alike)
+    for (int j = rank * kSelThreads + threadIdx.x; j < p.budget; j += parts * kSelThreads) {
       src[j] = j < n ? j : -1;
       if (j < n && p.weights_out != p.weights) p.weights_out[base + j] = keys.w[j];
       if (j < n && p.pos_out && p.pos_out != p.pos) p.pos_out[base + j] = keys.pos[j];
     }
-    if (threadIdx.x == 0) p.counts[row] = make_int2(0, n);
+    if (rank == 0 && threadIdx.x == 0) p.counts[row] = make_int2(0, n);
     return;
   }
-  // the budget-th largest key: its digits from the top, `left` = its rank among
-  // the keys that share the digits so far
+  // this CTA's slots [c0, c1): equal runs of whole groups of 32, a run a warp
+  const int run = (int)(((long long)n + (long long)parts * kSelThreads - 1) / ((long long)parts * kSelThreads)) * 32;
+  const int c0 = (int)min((long long)n, (long long)rank * run * kSelWarps);
+  const int c1 = (int)min((long long)n, (long long)c0 + (long long)run * kSelWarps);
+  const bool cached = run * kSelWarps <= kCachedKeys;
+  __syncthreads();  // the histograms are zero
+  // first digit, with the keys on their way into shared memory
+#pragma unroll 4
+  for (int j = c0 + threadIdx.x; j < c1; j += kSelThreads) {
+    const uint32_t k = keys.at(j);
+    if (cached) s_keys[j - c0] = k;
+    atomicAdd(&s.hist[0][k >> 21], 1);
+  }
+  auto key = [&](int j) { return cached ? s_keys[j - c0] : keys.at(j); };
+  // The budget-th largest key: its digits from the top; `left` is its rank among
+  // the keys that share the digits so far.
   uint32_t prefix = 0;
   int left = p.budget;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    if (threadIdx.x < 256) hist[threadIdx.x] = 0;
-    __syncthreads();
-    for (int j = threadIdx.x; j < n; j += kSelThreads) {
-      const uint32_t k = keys.at(j);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
-    }
-    __syncthreads();
-    if (warp == 0) {
-      // lane l holds digits 255 - 8 l .. 248 - 8 l, from the top
-      int c[8], sum = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        c[e] = hist[255 - 8 * lane - e];
-        sum += c[e];
-      }
-      int up = sum;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xFFFFFFFFu, up, d);
-        if (lane >= d) up += y;
-      }
-      int above = up - sum;
-      if (above < left && left <= up) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (above < left && left <= above + c[e]) {
-            s_digit = (uint32_t)(255 - 8 * lane - e);
-            s_above = above;
-            above = left;  // found
-          } else {
-            above += c[e];
-          }
-        }
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int bins = pass == 2 ? 1024 : kBins;
+    if (pass > 0) {
+      const uint32_t mask = pass == 1 ? 0xFFFFFFFFu << 21 : 0xFFFFFFFFu << 10;
+      for (int j = c0 + threadIdx.x; j < c1; j += kSelThreads) {
+        const uint32_t k = key(j);
+        if ((k & mask) == prefix) atomicAdd(&s.hist[pass][(k >> shift) & (bins - 1)], 1);
       }
     }
+    cluster.sync();  // the cluster's histograms of this pass are whole
+    // a thread holds two bins, from the top
+    int c[2] = {0, 0};
+    const int top = bins - 1 - 2 * (int)threadIdx.x;
+    if (top > 0) {
+      for (int x = 0; x < parts; ++x) {
+        const int* h = cluster.map_shared_rank(&s.hist[pass][0], x);
+        c[0] += h[top];
+        c[1] += h[top - 1];
+      }
+    }
+    int total;
+    const int above = block_scan(c[0] + c[1], s.warp_sum[pass], warp, lane, &total);
+    if (above < left && left <= above + c[0]) {
+      s.digit = (uint32_t)top;
+      s.above = above;
+    } else if (above + c[0] < left && left <= above + c[0] + c[1]) {
+      s.digit = (uint32_t)(top - 1);
+      s.above = above + c[0];
+    }
     __syncthreads();
-    prefix |= s_digit << shift;
-    left -= s_above;
+    prefix |= s.digit << shift;
+    left -= s.above;
+    __syncthreads();
   }
-  // Slots in order: a warp takes a run of consecutive slots (whole groups of 32).
-  const int run = ((n + kSelWarps * 32 - 1) / (kSelWarps * 32)) * 32;
-  const int j0 = min(n, warp * run), j1 = min(n, j0 + run);
-  int equal = 0;
-  for (int j = j0; j < j1; j += 32) {
-    const bool eq = j + lane < j1 && keys.at(j + lane) == prefix;
-    equal += __popc(__ballot_sync(0xFFFFFFFFu, eq));
-  }
-  int total;
-  const int eq0 = warp_offsets(equal, buf, warp, lane, &total);
-  // kept: above the threshold, or among the first `left` equal ones
+  // Places, in the order of the slots: warp by warp, CTA by CTA.
+  const int j0 = min(c1, c0 + warp * run), j1 = min(c1, j0 + run);
   const uint32_t below = (1u << lane) - 1u;
+  int equal = 0;
+  for (int j = j0; j < j1; j += 32) equal += __popc(__ballot_sync(0xFFFFFFFFu, j + lane < j1 && key(j + lane) == prefix));
+  // This warp's start in the cluster's order of one count a warp; *total the cluster's.
+  auto place = [&](int mine, int which, int* total) {
+    if (lane == 0) s.warp_sum[which][warp] = mine;
+    __syncthreads();
+    const int x = s.warp_sum[which][lane];
+    int up = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, up, d);
+      if (lane >= d) up += y;
+    }
+    if (threadIdx.x == 31) s.totals[which] = up;
+    const int start = __shfl_sync(0xFFFFFFFFu, up - x, warp);
+    cluster.sync();
+    int before = 0, all = 0;
+    for (int c = 0; c < parts; ++c) {
+      const int v = *cluster.map_shared_rank(&s.totals[which], c);
+      if (c < rank) before += v;
+      all += v;
+    }
+    *total = all;
+    return before + start;
+  };
+  int total;
+  const int eq0 = place(equal, 0, &total);
+  // kept: above the threshold, or among the first `left` equal ones
   auto kept_of = [&](int j, int& seen) {
-    const uint32_t k = j < j1 ? keys.at(j) : 0u;
+    const uint32_t k = j < j1 ? key(j) : 0u;
     const bool eq = j < j1 && k == prefix;
     const uint32_t eqs = __ballot_sync(0xFFFFFFFFu, eq);
     const bool kept = j < j1 && (k > prefix || (eq && seen + __popc(eqs & below) < left));
@@ -154,10 +220,10 @@ select_kernel(CacheParams p) {
     holes += __popc(__ballot_sync(0xFFFFFFFFu, in && !kept && j + lane < p.budget));
   }
   int n_moves, n_holes;
-  int mover = warp_offsets(movers, buf, warp, lane, &n_moves);
-  int hole = warp_offsets(holes, buf, warp, lane, &n_holes);
-  seen = eq0;
-  if (j1 > p.budget) {
+  int mover = place(movers, 1, &n_moves);
+  int hole = place(holes, 2, &n_holes);
+  if (j1 > p.budget && movers > 0) {
+    seen = eq0;
     for (int j = j0; j < j1; j += 32) {
       const bool moves_it = kept_of(j + lane, seen) && j + lane >= p.budget;
       const uint32_t who = __ballot_sync(0xFFFFFFFFu, moves_it);
@@ -165,18 +231,18 @@ select_kernel(CacheParams p) {
       mover += __popc(who);
     }
   }
-  __syncthreads();
+  cluster.sync();  // the movers' list is whole; nobody reads this CTA's shared memory any more
   seen = eq0;
   for (int j = j0; j < min(j1, p.budget); j += 32) {
     const int x = j + lane;
     const bool kept = kept_of(x, seen), freed = x < j1 && x < p.budget && !kept;
     const uint32_t who = __ballot_sync(0xFFFFFFFFu, freed);
     if (freed) {
-      const int i = hole + __popc(who & below), from = moves[i].y;
-      moves[i].x = x;
+      const int i = hole + __popc(who & below), from = __ldcg(&moves[i].y);
       src[x] = from;
       p.weights_out[base + x] = keys.w[from];
       if (p.pos_out) p.pos_out[base + x] = keys.pos[from];
+      moves[i] = make_int2(cache_row(p, b, g, x), cache_row(p, b, g, from));  // as rows of the cache
     } else if (x < j1 && x < p.budget) {
       src[x] = x;
       if (p.weights_out != p.weights) p.weights_out[base + x] = keys.w[x];
@@ -184,39 +250,42 @@ select_kernel(CacheParams p) {
     }
     hole += __popc(who);
   }
-  if (threadIdx.x == 0) p.counts[row] = make_int2(n_moves, p.budget);
+  if (rank == 0 && threadIdx.x == 0) p.counts[row] = make_int2(n_moves, p.budget);
 }
 
-__device__ __forceinline__ long long cache_row(const CacheParams& p, int b, int g, int slot) {
-  const int page = p.table[(size_t)b * p.max_pages + (slot >> p.page_shift)];
-  if (page < 0 || page >= p.num_pages) {
-    atomicOr(p.status, kStatusBadPageBit);
-    return -1;
-  }
-  return (((long long)page * p.Hkv + g) << p.page_shift) + (slot & (p.page_size - 1));
-}
-
-// Copies the rows that move: a group of vph threads a row, K and V together.
+// Copies the rows that move: a group of vph threads a row, K and V together, two
+// rows in flight a thread.
 constexpr int kMoveThreads = 256;
 __global__ void __launch_bounds__(kMoveThreads)
 move_kernel(CacheParams p, int vph_shift) {
   pdl_trigger();
   pdl_wait();
-  const int row = blockIdx.x, b = row / p.Hkv, g = row % p.Hkv;
+  const int row = blockIdx.x, b = row / p.Hkv;
   const int2 c = p.counts[row];
-  if (g == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.lens_out[b] = c.y;
+  if (row == b * p.Hkv && blockIdx.y == 0 && threadIdx.x == 0) p.lens_out[b] = c.y;
   const int2* moves = reinterpret_cast<const int2*>(p.moves + (size_t)row * p.max_len);
   const int per = kMoveThreads >> vph_shift;
   const int at = threadIdx.x & ((1 << vph_shift) - 1);
   uint4* k = static_cast<uint4*>(p.k);
   uint4* v = static_cast<uint4*>(p.v);
-  for (int i = blockIdx.y * per + (threadIdx.x >> vph_shift); i < c.x; i += gridDim.y * per) {
-    const int2 m = moves[i];
-    const long long to = cache_row(p, b, g, m.x), from = cache_row(p, b, g, m.y);
-    if (to < 0 || from < 0) continue;
-    const uint4 a = k[(from << vph_shift) + at], d = v[(from << vph_shift) + at];
-    k[(to << vph_shift) + at] = a;
-    v[(to << vph_shift) + at] = d;
+  const int stride = gridDim.y * per;
+  for (int i = blockIdx.y * per + (threadIdx.x >> vph_shift); i < c.x; i += 2 * stride) {
+    int2 m[2];
+    uint4 a[2], d[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) m[u] = i + u * stride < c.x ? moves[i + u * stride] : make_int2(-1, -1);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (m[u].x >= 0 && m[u].y >= 0) {
+        a[u] = __ldcs(k + ((size_t)m[u].y << vph_shift) + at);
+        d[u] = __ldcs(v + ((size_t)m[u].y << vph_shift) + at);
+      }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (m[u].x >= 0 && m[u].y >= 0) {
+        k[((size_t)m[u].x << vph_shift) + at] = a[u];
+        v[((size_t)m[u].x << vph_shift) + at] = d[u];
+      }
   }
 }
 
@@ -224,14 +293,34 @@ move_kernel(CacheParams p, int vph_shift) {
 
 cudaError_t launch_cache_evict(const CacheParams& p, int dtype, cudaStream_t s) {
   const int rows = p.B * p.Hkv;
-  cudaError_t e = launch_pdl(select_kernel, dim3(rows), dim3(kSelThreads), 0, s, p);
+  // CTAs of a row: while each still has 2048 slots and the rows leave SMs idle
+  int parts = 1;
+  while (parts < kMaxParts && p.max_len / parts > 2048 && rows * parts * 2 <= 152) parts *= 2;
+  static std::atomic<uint64_t> done{0};
+  const int keys = min((long long)kCachedKeys, ((long long)p.max_len + parts * kSelThreads - 1) / (parts * kSelThreads) * kSelThreads);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(select_kernel), kCachedKeys * 4, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)rows * parts);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = keys * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = parts;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, select_kernel, p, parts);
   if (e != cudaSuccess) return e;
   const int vph = p.D / (dtype == CAPATTN_BF16 ? 8 : 4);
   int shift = 0;
   while ((1 << shift) < vph) ++shift;
   const int per = kMoveThreads >> shift;
   const int most = min(p.budget, max(1, p.max_len - p.budget));  // rows that can move
-  const int y = min(max(1, (152 * 8 + rows - 1) / rows), (most + per - 1) / per);
+  const int y = min(max(1, (152 * 8 + rows - 1) / rows), (most + 2 * per - 1) / (2 * per));
   return launch_pdl(move_kernel, dim3(rows, y), dim3(kMoveThreads), 0, s, p, shift);
 }
 

@@ -87,39 +87,64 @@ def cache_workspace_bytes(cfg: CacheConfig, call: int) -> int:
     return int(lib().capattn_cache_workspace_bytes(ctypes.byref(cfg), call))
 
 
+def _fits(t, shape, dtype, device):
+    return t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()
+
+
 def _want(t, what, shape, dtype, device):
-    """A contiguous tensor of that shape, type and device, or None."""
+    """A contiguous tensor of that shape, type and device, or None; gives its address."""
     if t is None:
-        return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        return None
+    if not _fits(t, shape, dtype, device):
         raise ValueError(f"{what}: want a contiguous {dtype} tensor {tuple(shape)} on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
 
 
 def _rows(t, what, shape, dtype, device):
     """Rows of contiguous [heads, D] blocks; returns the row stride in elements."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+    n, heads, D = shape
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{what}: want a {dtype} tensor {tuple(shape)} on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    n, heads, D = shape
-    if n and ((D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D)):
-        raise ValueError(f"{what}: the [heads, D] block of a row has to be contiguous, strides are {t.stride()}")
-    return t.stride(0) if n > 1 else heads * D
+    if t.is_contiguous():
+        return heads * D
+    stride = t.stride()
+    if n and (stride[2] != 1 or (heads > 1 and stride[1] != D)):
+        raise ValueError(f"{what}: the [heads, D] block of a row has to be contiguous, strides are {stride}")
+    return stride[0] if n > 1 else heads * D
+
+
+def _raw_stream(device, stream):
+    """The handle of the current stream when the call needs no other device or
+    stream than the current ones, else None."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return torch.cuda.current_stream().cuda_stream
+    return None
 
 
 @contextlib.contextmanager
 def _on(device, stream):
     """Makes `device` and the call's stream (by default the device's current one) the
-    current ones, so that what a call allocates belongs to its stream; gives the
-    stream's handle."""
+    current ones, so that what a call allocates belongs to its stream."""
     if stream is None:
         with torch.cuda.device(device):
-            yield torch.cuda.current_stream(device).cuda_stream
+            yield
     else:
         if stream.device != device:
             raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
         with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+            yield
+
+
+class _Plan:
+    """A checked configuration and the workspace bytes of each call."""
+
+    def __init__(self, cfg: CacheConfig):
+        _ca._check(lib().capattn_cache_validate_config(ctypes.byref(cfg)), "KVCache")
+        self.cfg = cfg
+        self.ref = ctypes.byref(cfg)
+        self.bytes = [cache_workspace_bytes(cfg, c) for c in range(4)]
 
 
 class KVCache:
@@ -146,6 +171,7 @@ class KVCache:
         self.max_len = self.max_pages * self.page_size
         self.device, self.dtype = k.device, k.dtype
         slots = (self.B, self.Hkv, self.max_len)
+        self._k_shape = k.shape
         _want(k, "k", k.shape, k.dtype, k.device)
         _want(v, "v", k.shape, k.dtype, k.device)
         _want(table, "table", table.shape, torch.int32, k.device)
@@ -157,19 +183,23 @@ class KVCache:
             raise ValueError("pos needs qpos, the position of each sequence's newest token")
         self.k, self.v, self.table, self.lens = k, v, table, lens
         self.weights, self.pos, self.qpos = weights, pos, qpos
+        self._slots = torch.Size(slots)
+        self._plans = {}       # by (Hq, AttnParams)
         self._workspaces = []  # the last one is used; earlier ones may live in captured graphs
 
-    def config(self, Hq: int, ap: AttnParams | None = None) -> CacheConfig:
-        cfg = make_cache_config(ap or AttnParams(sm_scale=1.0), self.B, Hq, self.Hkv, self.D, self.dtype,
-                                self.num_pages, self.page_size, self.max_pages)
-        _ca._check(lib().capattn_cache_validate_config(ctypes.byref(cfg)), "KVCache")
-        return cfg
+    def plan(self, Hq: int, ap: AttnParams | None = None) -> _Plan:
+        got = self._plans.get((Hq, ap))
+        if got is None:
+            cfg = make_cache_config(ap or AttnParams(sm_scale=1.0), self.B, Hq, self.Hkv, self.D, self.dtype,
+                                    self.num_pages, self.page_size, self.max_pages)
+            got = self._plans[(Hq, ap)] = _Plan(cfg)
+        return got
 
-    def workspace(self, cfg: CacheConfig, call: int) -> torch.Tensor:
+    def workspace(self, plan: _Plan, call: int) -> torch.Tensor:
         """The cache's workspace, at least as large as `call` needs.  A larger call's
         first use adds a larger one (so make that call once before a graph is
         captured); the earlier ones stay, since captured graphs may hold them."""
-        n = cache_workspace_bytes(cfg, call)
+        n = plan.bytes[call]
         if not self._workspaces or self._workspaces[-1].numel() < n:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("the cache's workspace would grow during a graph capture: "
@@ -179,13 +209,30 @@ class KVCache:
             self._workspaces.append(new)
         return self._workspaces[-1]
 
+    def _tensors(self):
+        """Addresses of the cache's own tensors, checked again: they are the caller's
+        to replace."""
+        B, dev = self.B, self.device
+        if not (_fits(self.k, self._k_shape, self.dtype, dev) and _fits(self.v, self._k_shape, self.dtype, dev)):
+            raise ValueError(f"the cache's k and v have to stay {tuple(self._k_shape)} {self.dtype} on {dev}")
+        return (self.k.data_ptr(), self.v.data_ptr(),
+                _want(self.table, "table", (B, self.max_pages), torch.int32, dev), _want(self.lens, "lens", (B,), torch.int32, dev))
+
+    def _positions(self):
+        if self.pos is None:
+            return None, None
+        if self.qpos is None:
+            raise ValueError("pos needs qpos, the position of each sequence's newest token")
+        return (_want(self.pos, "pos", self._slots, torch.int32, self.device),
+                _want(self.qpos, "qpos", (self.B,), torch.int32, self.device))
+
     def status(self, stream=None) -> tuple[int, int]:
         """Synchronises; returns (status, raw bits) of the calls so far and clears them."""
         status, raw = 0, 0
-        with _on(self.device, stream) as s:
+        with _on(self.device, stream):
             for w in self._workspaces:
                 bits = ctypes.c_uint32(0)
-                st = lib().capattn_device_status(w.data_ptr(), s, ctypes.byref(bits))
+                st = lib().capattn_device_status(w.data_ptr(), torch.cuda.current_stream().cuda_stream, ctypes.byref(bits))
                 status, raw = status or int(st), raw | int(bits.value)
         return status, raw
 
@@ -196,20 +243,24 @@ def cache_append(cache: KVCache, k_new, v_new, cu_new=None, stream=None) -> None
     cu_new[b] .. cu_new[b + 1] - 1 (cu_new [B + 1] int32; None: one row a
     sequence).  cache.lens (and qpos) already count the new tokens: the n rows of
     sequence b go to slots lens[b] - n .. lens[b] - 1.  Their weights start at 0."""
+    s = _raw_stream(cache.device, stream)
+    if s is None:
+        with _on(cache.device, stream):
+            return cache_append(cache, k_new, v_new, cu_new)
     N = k_new.shape[0]
     shape = (N, cache.Hkv, cache.D)
     ks = _rows(k_new, "k_new", shape, cache.dtype, cache.device)
     vs = _rows(v_new, "v_new", shape, cache.dtype, cache.device)
     if cu_new is None and N != cache.B:
         raise ValueError(f"without cu_new there is one new row a sequence: got {N} rows, {cache.B} sequences")
-    _want(cu_new, "cu_new", (cache.B + 1,), torch.int32, cache.device)
-    cfg = cache.config(cache.Hkv)
-    with _on(cache.device, stream) as s:
-        ws = cache.workspace(cfg, CALL_APPEND)
-        st = lib().capattn_cache_append(
-            ctypes.byref(cfg), _ca._ptr(k_new), _ca._ptr(v_new), ks, vs, N, _ca._ptr(cu_new), _ca._ptr(cache.k),
-            _ca._ptr(cache.v), _ca._ptr(cache.table), _ca._ptr(cache.lens), _ca._ptr(cache.weights),
-            _ca._ptr(cache.pos), _ca._ptr(cache.qpos), _ca._ptr(ws), ws.numel(), s)
+    cu = _want(cu_new, "cu_new", (cache.B + 1,), torch.int32, cache.device)
+    weights = _want(cache.weights, "weights", cache._slots, torch.float32, cache.device)
+    k, v, table, lens = cache._tensors()
+    pos, qpos = cache._positions()
+    plan = cache.plan(cache.Hkv)
+    ws = cache.workspace(plan, CALL_APPEND)
+    st = _lib_handle.capattn_cache_append(plan.ref, k_new.data_ptr(), v_new.data_ptr(), ks, vs, N, cu, k, v, table,
+                                          lens, weights, pos, qpos, ws.data_ptr(), ws.numel(), s)
     _ca._check(st, "capattn_cache_append")
 
 
@@ -220,28 +271,32 @@ def cache_decode(q, cache: KVCache, ap: AttnParams, temp=None, accumulate=False,
     accumulate, every cached token's share of the group's attention is added to
     cache.weights.  out: preallocated (o, lse).  ap's z_loss_weight plays no
     part, and causal none either: the query stands behind every cached token."""
+    s = _raw_stream(cache.device, stream)
+    if s is None:
+        with _on(cache.device, stream):
+            return cache_decode(q, cache, ap, temp, accumulate, out)
     if q.dim() != 3:
         raise ValueError("q is [B, Hq, D]")
-    Hq = q.shape[1]
-    qs = _rows(q, "q", (cache.B, Hq, cache.D), cache.dtype, cache.device)
-    _want(temp, "temp", (cache.B,), torch.float32, cache.device)
+    Hq, dev = q.shape[1], cache.device
+    shape = (cache.B, Hq, cache.D)
+    qs = _rows(q, "q", shape, cache.dtype, dev)
+    tp = _want(temp, "temp", (cache.B,), torch.float32, dev)
     if accumulate and cache.weights is None:
         raise ValueError("accumulate needs a cache with weights")
-    cfg = cache.config(Hq, ap)
-    if out is not None:
+    weights = _want(cache.weights, "weights", cache._slots, torch.float32, dev) if accumulate else None
+    k, v, table, lens = cache._tensors()
+    pos, qpos = cache._positions()
+    plan = cache.plan(Hq, ap)
+    if out is None:
+        o = q.new_empty(shape)
+        lse = q.new_empty((cache.B, Hq), dtype=torch.float32)
+    else:
         o, lse = out
-        _want(o, "o", (cache.B, Hq, cache.D), cache.dtype, cache.device)
-        _want(lse, "lse", (cache.B, Hq), torch.float32, cache.device)
-    with _on(cache.device, stream) as s:
-        if out is None:
-            o = torch.empty(cache.B, Hq, cache.D, dtype=cache.dtype, device=cache.device)
-            lse = torch.empty(cache.B, Hq, dtype=torch.float32, device=cache.device)
-        ws = cache.workspace(cfg, CALL_DECODE_WEIGHTS if accumulate else CALL_DECODE)
-        st = lib().capattn_cache_decode(
-            ctypes.byref(cfg), _ca._ptr(q), qs, _ca._ptr(cache.k), _ca._ptr(cache.v), _ca._ptr(cache.table),
-            _ca._ptr(cache.lens), _ca._ptr(temp), _ca._ptr(cache.pos), _ca._ptr(cache.qpos), _ca._ptr(o),
-            _ca._ptr(lse), _ca._ptr(cache.weights) if accumulate else None, _ca._ptr(ws), ws.numel(),
-            s)
+        _want(o, "o", shape, cache.dtype, dev)
+        _want(lse, "lse", (cache.B, Hq), torch.float32, dev)
+    ws = cache.workspace(plan, CALL_DECODE_WEIGHTS if accumulate else CALL_DECODE)
+    st = _lib_handle.capattn_cache_decode(plan.ref, q.data_ptr(), qs, k, v, table, lens, tp, pos, qpos, o.data_ptr(),
+                                          lse.data_ptr(), weights, ws.data_ptr(), ws.numel(), s)
     _ca._check(st, "capattn_cache_decode")
     return o, lse
 
@@ -256,29 +311,33 @@ def cache_evict(cache: KVCache, budget: int, keep_first: int = 0, keep_last: int
     token came from (-1: none), or None without want_src.  Without pos a moved
     token loses its place in the text: windows and later keep_last then go by
     slots."""
+    s = _raw_stream(cache.device, stream)
+    if s is None:
+        with _on(cache.device, stream):
+            return cache_evict(cache, budget, keep_first, keep_last, out, want_src)
     if cache.weights is None:
         raise ValueError("eviction needs a cache with weights")
-    if out is None:
-        lens_out, weights_out, pos_out = cache.lens, cache.weights, cache.pos
-    else:
-        lens_out, weights_out, pos_out = out
-        _want(lens_out, "lens_out", cache.lens.shape, torch.int32, cache.device)
-        _want(weights_out, "weights_out", cache.weights.shape, torch.float32, cache.device)
-        if (pos_out is None) != (cache.pos is None):
-            raise ValueError("pos_out goes with the cache's pos")
-        _want(pos_out, "pos_out", cache.weights.shape, torch.int32, cache.device)
-    cfg = cache.config(cache.Hkv)
     if budget < 1 or budget > cache.max_len or keep_first < 0 or keep_last < 0 or keep_first + keep_last > budget:
         raise ValueError(f"want 1 <= budget <= {cache.max_len} and keep_first + keep_last <= budget, got "
                          f"{budget}, {keep_first}, {keep_last}")
-    with _on(cache.device, stream) as s:
-        src = torch.empty(cache.B, cache.Hkv, budget, dtype=torch.int32, device=cache.device) if want_src else None
-        ws = cache.workspace(cfg, CALL_EVICT)
-        st = lib().capattn_cache_evict(
-            ctypes.byref(cfg), budget, keep_first, keep_last, _ca._ptr(cache.k), _ca._ptr(cache.v),
-            _ca._ptr(cache.table), _ca._ptr(cache.lens), _ca._ptr(cache.weights), _ca._ptr(cache.pos),
-            _ca._ptr(cache.qpos), _ca._ptr(lens_out), _ca._ptr(weights_out), _ca._ptr(pos_out), _ca._ptr(src),
-            _ca._ptr(ws), ws.numel(), s)
+    dev = cache.device
+    weights = _want(cache.weights, "weights", cache._slots, torch.float32, dev)
+    k, v, table, lens = cache._tensors()
+    pos, qpos = cache._positions()
+    if out is None:
+        lens_out, weights_out, pos_out = lens, weights, pos
+    else:
+        if (out[2] is None) != (cache.pos is None):
+            raise ValueError("pos_out goes with the cache's pos")
+        lens_out = _want(out[0], "lens_out", (cache.B,), torch.int32, dev)
+        weights_out = _want(out[1], "weights_out", cache._slots, torch.float32, dev)
+        pos_out = _want(out[2], "pos_out", cache._slots, torch.int32, dev)
+    plan = cache.plan(cache.Hkv)
+    src = torch.empty((cache.B, cache.Hkv, budget), dtype=torch.int32, device=dev) if want_src else None
+    ws = cache.workspace(plan, CALL_EVICT)
+    st = _lib_handle.capattn_cache_evict(plan.ref, budget, keep_first, keep_last, k, v, table, lens, weights, pos, qpos,
+                                         lens_out, weights_out, pos_out, None if src is None else src.data_ptr(),
+                                         ws.data_ptr(), ws.numel(), s)
     _ca._check(st, "capattn_cache_evict")
     return src
 
@@ -318,7 +377,7 @@ def key_weights(q, k, lse, ap: AttnParams, temp=None, seg=None, bounds=None, row
         raise ValueError(f"out is [B, Hkv, W] with W >= {Lk}, got {tuple(out.shape)}")
     if out is not None:
         _want(out, "out", (B, Hkv, out.shape[2]), torch.float32, dev)
-    with _on(dev, stream) as s:
+    with _on(dev, stream):
         if workspace is None:
             workspace = new_key_weights_workspace(q, k, ap)
         if out is None:
@@ -326,6 +385,6 @@ def key_weights(q, k, lse, ap: AttnParams, temp=None, seg=None, bounds=None, row
         st = lib().capattn_key_weights(
             ctypes.byref(cfg), _ca._ptr(q), _ca._ptr(k), _ca._ptr(lse), _ca._ptr(temp), _ca._ptr(seg),
             _ca._ptr(bounds), _ca._ptr(rows), _ca._ptr(out), out.shape[2], _ca._ptr(workspace),
-            workspace.numel(), s)
+            workspace.numel(), torch.cuda.current_stream().cuda_stream)
     _ca._check(st, "capattn_key_weights")
     return out
