@@ -45,7 +45,8 @@ struct Geo {
   static constexpr int STAGE = 2 * HALF;
   static constexpr int STAGES = D == 128 ? 3 : 6;     // 96 KB a CTA, two CTAs an SM
   static constexpr int MERGE = 16 * D * 4;            // 4 warps x 4 heads x D floats
-  static constexpr int SMEM = STAGES * STAGE + MERGE + 1024;
+  static constexpr int Q = 16 * D * 2;                // a group's queries
+  static constexpr int SMEM = STAGES * STAGE + MERGE + Q + 1024;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -87,19 +88,23 @@ __global__ void __launch_bounds__(kThreads, 2)
 decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const CacheParams p) {
   using G = Geo<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * G::STAGES];
+  __shared__ __align__(8) uint64_t bars[2 * G::STAGES + 2];
   __shared__ int abort_flag, join_flag;
   __shared__ float s_m[kConsumers][16], s_l[kConsumers][16], s_lsum[16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   float* merge = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + G::STAGES * G::STAGE);
+  const uint32_t s_q = base + G::STAGES * G::STAGE + G::MERGE;
   const uint32_t full = smem_u32(&bars[0]), empty = smem_u32(&bars[G::STAGES]);
+  const uint32_t q_full = smem_u32(&bars[2 * G::STAGES]), q_empty = q_full + 8;
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < G::STAGES; ++s) {
       mbar_init(full + 8 * s, 1);
       mbar_init(empty + 8 * s, kConsumers);
     }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, kConsumers);
     fence_mbar_init();
   }
   pdl_trigger();
@@ -108,7 +113,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   PieceIter<TK> it(p, lane);
   int b, vh, tile;
   SeqSpan sp;
-  uint32_t step = 0;  // tiles so far, over the pieces
+  uint32_t step = 0;   // tiles so far, over the pieces
+  uint32_t piece = 0;  // pieces so far
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------ TMA producer
@@ -129,6 +135,16 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         return (page_of(p, b, j) * p.Hkv + g) * p.page_size + (j & (p.page_size - 1));
       };
       int row = row_of(tile);
+      // the group's queries, as soon as the last piece's are in registers
+      if (piece > 0 && !mbar_wait_warp(q_empty, (piece - 1) & 1, p.status, &abort_flag)) break;
+      if (lane == 0) {
+        const HeadGroup hg = head_group(p, vh);
+        const uint32_t q_bytes = (uint32_t)hg.count * D * 2;
+        mbar_expect_tx(q_full, q_bytes);
+        bulk_load(s_q, static_cast<const __nv_bfloat16*>(p.q) + (size_t)b * p.q_stride + (size_t)hg.h0 * D, q_bytes, q_full);
+      }
+      ++piece;
+      __syncwarp();
       for (int i = 0; i < it.n; ++i, ++step) {
         const int next = i + 1 < it.n ? row_of(tile + i + 1) : -1;  // a tile ahead of its use
         const uint32_t s = step % G::STAGES, use = step / G::STAGES;
@@ -152,6 +168,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
       }
     }
     // normally long complete: the consumers waited for every stage
+    if (piece > 0) drain_wait(q_full, (piece - 1) & 1);
     for (uint32_t x = step > G::STAGES ? step - G::STAGES : 0; x < step; ++x)
       drain_wait(full + 8 * (x % G::STAGES), (x / G::STAGES) & 1);
     return;
@@ -172,17 +189,19 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     const int32_t* pos = p.pos + ((size_t)b * p.Hkv + hg.g) * p.max_len;
     const int oldest = by_pos ? p.qpos[b] - p.window_len : 0;
     uint32_t q[D / 16][4];
-    {
-      const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(p.q) + (size_t)b * p.q_stride + (size_t)hg.h0 * D;
+    ok = ok && mbar_wait_warp(q_full, piece & 1, p.status, &abort_flag);
+    ++piece;
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
+    for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = gq + 8 * (e & 1);
-          q[ks][e] = (ROWS == 2 || (e & 1) == 0) && r < hg.count
-              ? *reinterpret_cast<const uint32_t*>(qb + (size_t)r * D + 16 * ks + 8 * (e >> 1) + 2 * tq) : 0u;
-        }
-    }
+      for (int e = 0; e < 4; ++e) {
+        const int r = gq + 8 * (e & 1);
+        q[ks][e] = 0u;
+        if ((ROWS == 2 || (e & 1) == 0) && r < hg.count)
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(q[ks][e]) : "r"(s_q + r * D * 2 + 32 * ks + 16 * (e >> 1) + 4 * tq) : "memory");
+      }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_empty);
     float m[ROWS], l[ROWS], o[D / 8][4];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {

@@ -2,8 +2,8 @@
 //
 // The live slots of sequence b are cut into tiles of TK keys; a unit of work is
 // one tile of one (sequence, group of query heads).  Units are numbered
-// sequence by sequence, group by group, tile by tile, and CTA c takes units
-// [c q, (c + 1) q): equal shares whatever the lengths.  A CTA's part of one
+// sequence by sequence, group by group, tile by tile, and CTA c of n takes units
+// [U c / n, U (c + 1) / n): equal shares whatever the lengths.  A CTA's part of one
 // (sequence, group) is a piece; a piece that is not the whole leaves (m, l, O) in
 // the CTA's slot 2c (the piece at the start of its range) or 2c + 1 (the one at
 // its end; pieces between the two are whole), and the join adds the pieces up in
@@ -24,10 +24,11 @@ struct SeqSpan {
   int32_t tile0, tiles;  // tiles that hold them (one dead tile when there are none)
 };
 
+// The span of a sequence of length len as read.
 template <int TK>
-__device__ __forceinline__ SeqSpan seq_span(const CacheParams& p, int b) {
+__device__ __forceinline__ SeqSpan span_of(const CacheParams& p, int len) {
   SeqSpan s;
-  s.len = p.lens[b];
+  s.len = len;
   if (s.len < 0 || s.len > p.max_len) {
     atomicOr(p.status, kStatusBadLensBit);
     s.len = s.len < 0 ? 0 : p.max_len;
@@ -37,11 +38,8 @@ __device__ __forceinline__ SeqSpan seq_span(const CacheParams& p, int b) {
   s.tiles = max(1, (s.len + TK - 1) / TK - s.tile0);
   return s;
 }
-
-// A CTA's share in units.
-__device__ __forceinline__ uint32_t share_of(const CacheParams& p, uint32_t units) {
-  return max((uint32_t)p.min_tiles, (units + p.ctas - 1) / (uint32_t)p.ctas);
-}
+template <int TK>
+__device__ __forceinline__ SeqSpan seq_span(const CacheParams& p, int b) { return span_of<TK>(p, p.lens[b]); }
 
 // Inclusive sum over the lanes.
 __device__ __forceinline__ int lane_scan(int x, int lane) {
@@ -56,15 +54,15 @@ __device__ __forceinline__ int lane_scan(int x, int lane) {
 // Walks a CTA's pieces (every lane of a warp alike).
 template <int TK>
 struct PieceIter {
-  uint32_t u, end, begin, share;  // next unit, the CTA's range, its size
+  uint32_t units, ctas;           // all units, the CTAs that share them
+  uint32_t u, end, begin;         // next unit, this CTA's range
   int b, vh, t0;                  // the next piece: sequence, group, first tile of the group
-  SeqSpan sp;
+  int len;                        // lens[b], read ahead of its use
   // of the piece that next() gave
   int n;                   // tiles
   bool whole;
   int slot;                // its partial slot, when not whole
-  int c0, c1;              // the CTAs that share its (sequence, group)
-  bool first_at_begin;     // whether that starts at the begin of c0's range
+  uint32_t s0, s1;         // units [s0, s1) of its (sequence, group)
 
   __device__ PieceIter(const CacheParams& p, int lane) {
     // the first 32 sequences' tiles stay in a register: one read of lens decides
@@ -72,11 +70,11 @@ struct PieceIter {
     const int n0 = lane < p.B ? seq_span<TK>(p, lane).tiles : 0;
     int all = n0;
     for (int x = lane + 32; x < p.B; x += 32) all += seq_span<TK>(p, x).tiles;
-    const uint32_t units = (uint32_t)__reduce_add_sync(0xFFFFFFFFu, all) * (uint32_t)p.VH;
-    share = share_of(p, units);
-    begin = u = min(units, share * blockIdx.x);
-    end = min(units, u + share);
-    b = vh = t0 = 0;
+    units = (uint32_t)__reduce_add_sync(0xFFFFFFFFu, all) * (uint32_t)p.VH;
+    ctas = min((uint32_t)p.ctas, max(1u, units / (uint32_t)p.min_tiles));
+    begin = u = begin_of(blockIdx.x);
+    end = begin_of(blockIdx.x + 1);
+    b = vh = t0 = len = 0;
     if (u >= end) return;
     const int want = (int)(u / (uint32_t)p.VH);  // the tile, counted over the sequences
     int before = 0;
@@ -92,21 +90,29 @@ struct PieceIter {
       }
       before += __shfl_sync(0xFFFFFFFFu, up, 31);
     }
-    sp = seq_span<TK>(p, b);
+    len = p.lens[b];
+    const SeqSpan sp = span_of<TK>(p, len);
     const uint32_t in = u - (uint32_t)before * (uint32_t)p.VH;
     vh = (int)(in / (uint32_t)sp.tiles);
     t0 = (int)(in % (uint32_t)sp.tiles);
   }
+  // First unit of CTA c's range, and the CTA that holds a unit: the largest c with
+  // floor(units c / ctas) <= x.
+  __device__ __forceinline__ uint32_t begin_of(uint32_t c) const {
+    return c >= ctas ? units : (uint32_t)((uint64_t)units * c / ctas);
+  }
+  __device__ __forceinline__ int cta_of(uint32_t x) const {
+    return (int)((((uint64_t)x + 1) * ctas - 1) / units);
+  }
   // Gives the piece (b, vh, tiles [tile, tile + n) of the sequence's span).
   __device__ bool next(const CacheParams& p, int* b_out, int* vh_out, int* tile_out, SeqSpan* sp_out) {
     if (u >= end) return false;
+    const SeqSpan sp = span_of<TK>(p, len);
     n = (int)min((uint32_t)(sp.tiles - t0), end - u);
     whole = t0 == 0 && n == sp.tiles;
     slot = 2 * (int)blockIdx.x + (u == begin ? 0 : 1);
-    const uint32_t s0 = u - (uint32_t)t0;
-    c0 = (int)(s0 / share);
-    c1 = (int)((s0 + (uint32_t)sp.tiles - 1) / share);
-    first_at_begin = s0 == share * (uint32_t)c0;
+    s0 = u - (uint32_t)t0;
+    s1 = s0 + (uint32_t)sp.tiles;
     *b_out = b;
     *vh_out = vh;
     *tile_out = sp.tile0 + t0;
@@ -117,13 +123,23 @@ struct PieceIter {
       if (++vh == p.VH) {
         vh = 0;
         ++b;
-        sp = seq_span<TK>(p, b);
+        len = p.lens[b];  // not looked at before the next call
       }
     }
     return true;
   }
-  // Partial slot of the piece that CTA c (c0 .. c1) has of it.
-  __device__ __forceinline__ int slot_of(int c) const { return 2 * c + (c == c0 && !first_at_begin ? 1 : 0); }
+};
+
+// The pieces of one split (sequence, group): CTAs c0 .. c1, and their slots.
+struct Pieces {
+  int c0, c1, late;  // late: the first one starts inside c0's range
+  template <int TK>
+  __device__ explicit Pieces(const PieceIter<TK>& it) {
+    c0 = it.cta_of(it.s0);
+    c1 = it.cta_of(it.s1 - 1);
+    late = it.s0 != it.begin_of(c0) ? 1 : 0;
+  }
+  __device__ __forceinline__ int slot_of(int c) const { return 2 * c + (c == c0 ? late : 0); }
 };
 
 // First of the query heads of group vh, its count, and the KV head.
@@ -156,12 +172,13 @@ __device__ __forceinline__ int page_of(const CacheParams& p, int b, int slot) {
 template <typename T, int D, int TK>
 __device__ __forceinline__ void join_pieces(const CacheParams& p, const PieceIter<TK>& it, int b, const HeadGroup& hg,
                                             int tid, int bar, float* buf, float* lbuf, int* flag) {
+  const Pieces pc(it);
   __threadfence();
   named_bar_sync(bar, 128);
   if (tid == 0) {
-    const uint32_t left = atomicAdd(&p.counters[it.c0], 1u);
-    const bool last = left == (uint32_t)(it.c1 - it.c0);
-    if (last) p.counters[it.c0] = 0u;
+    const uint32_t left = atomicAdd(&p.counters[pc.c0], 1u);
+    const bool last = left == (uint32_t)(pc.c1 - pc.c0);
+    if (last) p.counters[pc.c0] = 0u;
     __threadfence();
     *flag = last;
   }
@@ -181,37 +198,48 @@ __device__ __forceinline__ void join_pieces(const CacheParams& p, const PieceIte
 #pragma unroll
       for (int x = 0; x < V; ++x) o[e][x] = 0.f;
     }
-    for (int c = it.c0 + lane; c <= it.c1; c += 32)
+    for (int c = pc.c0 + lane; c <= pc.c1; c += 32)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (e < heads) mx[e] = fmaxf(mx[e], __ldcg(&p.part_ml[(size_t)it.slot_of(c) * kDecodeHeads + g0 + e]).x);
+        if (e < heads) mx[e] = fmaxf(mx[e], __ldcg(&p.part_ml[(size_t)pc.slot_of(c) * kDecodeHeads + g0 + e]).x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], x));
       if (mx[e] == -INFINITY) mx[e] = 0.f;
     }
-#pragma unroll 2
-    for (int c = it.c0 + warp; c <= it.c1; c += 4) {
-      const size_t at = (size_t)it.slot_of(c) * kDecodeHeads + g0;
+    // four pieces of four heads in flight a lane
+    for (int c = pc.c0 + warp; c <= pc.c1; c += 16) {
+      float2 ml[4][4];
+      float v[4][4][V];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (e >= heads) continue;
-        const float2 ml = __ldcg(&p.part_ml[at + e]);
-        const float* po = p.part_o + (at + e) * D + lane * V;
-        float v[V];
-        if constexpr (V == 4) {
-          const float4 f = __ldcg(reinterpret_cast<const float4*>(po));
-          v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-        } else {
-          const float2 f = __ldcg(reinterpret_cast<const float2*>(po));
-          v[0] = f.x; v[1] = f.y;
+      for (int y = 0; y < 4; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          ml[y][e] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int x = 0; x < V; ++x) v[y][e][x] = 0.f;
+          if (c + 4 * y > pc.c1 || e >= heads) continue;
+          const size_t at = (size_t)pc.slot_of(c + 4 * y) * kDecodeHeads + g0 + e;
+          ml[y][e] = __ldcg(&p.part_ml[at]);
+          const float* po = p.part_o + at * D + lane * V;
+          if constexpr (V == 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(po));
+            v[y][e][0] = f.x; v[y][e][1] = f.y; v[y][e][2] = f.z; v[y][e][3] = f.w;
+          } else {
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(po));
+            v[y][e][0] = f.x; v[y][e][1] = f.y;
+          }
         }
-        const float w = __expf(ml.x - mx[e]);
-        l[e] = fmaf(ml.y, w, l[e]);
 #pragma unroll
-        for (int x = 0; x < V; ++x) o[e][x] = fmaf(v[x], w, o[e][x]);
-      }
+      for (int y = 0; y < 4; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = __expf(ml[y][e].x - mx[e]);
+          l[e] = fmaf(ml[y][e].y, w, l[e]);
+#pragma unroll
+          for (int x = 0; x < V; ++x) o[e][x] = fmaf(v[y][e][x], w, o[e][x]);
+        }
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {

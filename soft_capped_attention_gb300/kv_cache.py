@@ -119,7 +119,7 @@ def _raw_stream(device, stream):
     """The handle of the current stream when the call needs no other device or
     stream than the current ones, else None."""
     if stream is None and torch.cuda.current_device() == device.index:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device.index)  # the handle alone, without a Stream object
     return None
 
 
