@@ -152,8 +152,11 @@ capattn_status capattn_cache_evict(const capattn_cache_config* cfg, int32_t budg
  * the counted query rows rows[b][0] <= i < rows[b][1] (a padded prompt, or an
  * observation window at its end).  w: row (b, g) at (b * Hkv + g) * w_row_stride
  * floats, w_row_stride >= Lk; entries j < Lk are overwritten.  The weights are summed in
- * a fixed order.  workspace: capattn_workspace_bytes(cfg, CAPATTN_PASS_FWD).
+ * a fixed order.  workspace: capattn_key_weights_workspace_bytes(cfg) bytes, 256-byte
+ * aligned; its first word is the device status.  A capattn_fwd of the same cfg may
+ * use it too (it holds what CAPATTN_PASS_FWD asks for).
  */
+size_t capattn_key_weights_workspace_bytes(const capattn_config* cfg);
 capattn_status capattn_key_weights(const capattn_config* cfg, const void* q, const void* k,
                                    const float* lse, const float* temp, const int32_t* seg,
                                    const int32_t* bounds, const int32_t* rows, float* w,

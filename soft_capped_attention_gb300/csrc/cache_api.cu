@@ -135,6 +135,24 @@ CacheParams params_of(const capattn_cache_config& c, void* ws, int call) {
   return p;
 }
 
+// Workspace of capattn_key_weights: the forward's (spans and visit maps), then
+// what the bf16 kernel adds.
+struct KeyWeightsWorkspace {
+  size_t fwd, steps_off, counters_off, partial_off, total;
+};
+KeyWeightsWorkspace key_weights_layout(const capattn_config& c) {
+  KeyWeightsWorkspace w;
+  w.fwd = capattn_workspace_bytes(&c, CAPATTN_PASS_FWD);
+  int32_t bq = 0, bk = 0;
+  capattn_tile_sizes(&c, &bq, &bk);
+  const size_t nk = ((c.Lk > 0 ? c.Lk : c.L) + bk - 1) / bk;
+  w.steps_off = w.fwd;
+  w.counters_off = up256(w.steps_off + sizeof(int32_t) * c.B * nk);
+  w.partial_off = up256(w.counters_off + sizeof(uint32_t) * kWeightCtas);
+  w.total = up256(w.partial_off + sizeof(float) * 2 * kWeightCtas * 128);
+  return w;
+}
+
 capattn_status of(cudaError_t e) { return e == cudaSuccess ? CAPATTN_OK : CAPATTN_ERR_CUDA; }
 
 // A row stride of [heads, D] rows: whole 16-byte units, no overlap.
@@ -234,6 +252,10 @@ capattn_status capattn_cache_evict(const capattn_cache_config* cfg, int32_t budg
   return of(launch_cache_evict(p, cfg->dtype, stream));
 }
 
+size_t capattn_key_weights_workspace_bytes(const capattn_config* cfg) {
+  return capattn_validate_config(cfg) == CAPATTN_OK ? key_weights_layout(*cfg).total : 0;
+}
+
 capattn_status capattn_key_weights(const capattn_config* cfg, const void* q, const void* k,
                                    const float* lse, const float* temp, const int32_t* seg,
                                    const int32_t* bounds, const int32_t* rows, float* w,
@@ -248,9 +270,8 @@ capattn_status capattn_key_weights(const capattn_config* cfg, const void* q, con
   const void* ptrs[] = {q, k, lse, temp, seg, bounds, rows, w};
   for (const void* ptr : ptrs)
     if (ptr && !aligned(ptr, 16)) return CAPATTN_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < capattn_workspace_bytes(cfg, CAPATTN_PASS_FWD))
-    return CAPATTN_ERR_WORKSPACE;
+  const KeyWeightsWorkspace kl = key_weights_layout(*cfg);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < kl.total) return CAPATTN_ERR_WORKSPACE;
   Params p;
   memset(&p, 0, sizeof(p));
   p.B = cfg->B; p.L = cfg->L; p.Lk = Lk; p.Hq = cfg->Hq; p.Hkv = cfg->Hkv; p.D = cfg->D;
@@ -275,7 +296,11 @@ capattn_status capattn_key_weights(const capattn_config* cfg, const void* q, con
   p.kmap = reinterpret_cast<uint32_t*>(base + l.kmap_off);
   p.qfull = reinterpret_cast<int2*>(base + l.qfull_off);
   p.q = q; p.k = k; p.lse = const_cast<float*>(lse); p.temp = temp; p.seg = seg; p.bounds = bounds;
-  cudaError_t e = launch_prepass(p, true, true, stream);
+  kw.steps = reinterpret_cast<int32_t*>(base + kl.steps_off);
+  kw.counters = reinterpret_cast<uint32_t*>(base + kl.counters_off);
+  kw.partial = reinterpret_cast<float*>(base + kl.partial_off);
+  // bf16 builds its own key-tile map, with the steps it splits
+  cudaError_t e = launch_prepass(p, true, cfg->dtype != CAPATTN_BF16, stream);
   if (e != cudaSuccess) return of(e);
   return of(launch_key_weights(p, kw, cfg->dtype, stream));
 }

@@ -96,7 +96,13 @@ struct KeyWeightsParams {
   float* w;
   int64_t w_stride;
   ExactCap cap;
+  // bf16 (workspace): steps of each (batch, key tile), counters of the split key
+  // tiles, partial sums
+  int32_t* steps;        // [B, nk]
+  uint32_t* counters;    // [kWeightCtas]
+  float* partial;        // [2 kWeightCtas][128]
 };
+constexpr int kWeightCtas = 152;  // CTAs of the persistent bf16 kernel
 
 // Raises a kernel's dynamic shared memory limit, once per device (`done`: a bit a device).
 inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {

@@ -2,25 +2,23 @@
 //
 // w_j = sum over heads h of the group and counted rows i of 2^(x_ij),
 //   x_ij = temp_i log2(e) cap(sm_scale <q_i, k_j>) - log2(e) lse_i.
-// One CTA owns 128 keys of one (batch, KV head): K stays in shared memory, Q tiles
-// of the group's heads stream through a ring by TMA, and tcgen05 forms S^T = K
-// Q^T (128 keys x 128 queries, two TMEM buffers) with a key per TMEM lane, so that
-// the sum over queries is a sum within a thread: no transposition, no atomics.
-// Eight warps (two warpgroups of 64 query columns each) read 32 columns at a
-// time, cap them, exponentiate and add.
+// A unit is 128 keys of one (batch, KV head), a step one query tile of one of the
+// group's heads that the keys' visit map names.  A persistent grid, one CTA an SM,
+// takes equal shares of all steps (as decode does of its tiles, cache_sched.cuh):
+// K stays in shared memory for a unit (two buffers), Q tiles stream through a ring
+// by TMA, and tcgen05 forms S^T = K Q^T (128 keys x 128 queries, four TMEM buffers)
+// with a key per TMEM lane, so that the sum over queries is a sum within a thread:
+// no transposition, no atomics.  Sixteen warps read it (four warpgroups, 32 query
+// columns each), cap, exponentiate and add.  A unit that two CTAs share leaves
+// partial sums, which the last of them adds in order.
 //
 // What bounds it: one exp2 per pair on the MUFU pipe (16 a clock and SM, against
-// about 26 pairs a clock that the tensor cores deliver at D = 128), then the
+// the 32 pairs a clock that the tensor cores could deliver at D = 128), then the
 // issue slots of the cap's polynomial; there is no second product and nothing is
-// stored.  Two CTAs an SM hide each other's waits.  The steps (head x visited
-// query tile) of a key tile are cut into equal parts over a cluster of up to 8
-// CTAs when there are too few key tiles to fill the SMs; the parts are summed
-// through distributed shared memory in rank order.
+// stored.
 //
-// Sums: 32 columns in fp32, then compensated (Kahan) over the chunks: a prompt of
+// Sums: 32 columns in fp32, then compensated (Kahan) over the steps: a prompt of
 // 131072 rows adds as exactly as a short one.
-#include <cooperative_groups.h>
-
 #include "cache_internal.h"
 #include "cache_math.cuh"
 #include "tc_common.cuh"
@@ -29,64 +27,143 @@
 namespace capattn {
 namespace {
 
-namespace cg = cooperative_groups;
-
 constexpr int BT = 128;
 constexpr int SLAB = 128 * 64 * 2;
-constexpr int NSTAGE = 2;
-constexpr int NBUF = 2;
-constexpr int kThreads = 320;  // TMA warp, MMA warp, 8 elementwise warps
+constexpr int NSTAGE = 4;              // Q tiles in flight
+constexpr int NBUF = 4;                // S^T buffers
+constexpr int NK = 2;                  // K buffers
+constexpr int kElem = 16;              // elementwise warps
+constexpr int kThreads = 64 + 32 * kElem;
 template <int HD>
 constexpr int tile_bytes() { return (HD / 64) * SLAB; }
 template <int HD>
-constexpr int smem_bytes() { return (1 + NSTAGE) * tile_bytes<HD>() + 1024; }
+constexpr int smem_bytes() { return (NK + NSTAGE) * tile_bytes<HD>() + 1024; }
 
-// The visited query tiles of a key tile within [qlo, qhi], in order.
-struct MapRow {
-  const uint32_t* map;
-  int qlo, qhi;  // inclusive
-  __device__ __forceinline__ uint32_t word(int w) const {
-    uint32_t x = map[w];
-    if (w == (qlo >> 5)) x &= 0xFFFFFFFFu << (qlo & 31);
-    if (w == (qhi >> 5)) x &= 0xFFFFFFFFu >> (31 - (qhi & 31));
-    return x;
+// Key-tile map (the transpose of the query-tile map, counted rows only) and the
+// steps of each (batch, key tile): a warp each.  The first one clears the counters.
+__global__ void __launch_bounds__(128)
+key_plan_kernel(Params p, KeyWeightsParams kw) {
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t e = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < kWeightCtas; i += 128) kw.counters[i] = 0u;
+  if (e >= (int64_t)p.B * p.nk) return;
+  const int b = (int)(e / p.nk), kt = (int)(e % p.nk);
+  int lo = 0, hi = p.L;
+  if (kw.rows) {
+    lo = kw.rows[2 * b];
+    hi = kw.rows[2 * b + 1];
+    if (!(lo >= 0 && lo <= hi && hi <= p.L)) {
+      if (lane == 0 && kt == 0) atomicOr(p.status, kStatusBadRowsBit);
+      lo = max(lo, 0);
+      hi = min(hi, p.L);
+    }
   }
-  __device__ int count() const {
-    int n = 0;
-    for (int w = qlo >> 5; w <= (qhi >> 5); ++w) n += __popc(word(w));
-    return n;
+  int count = 0;
+  for (int w = 0; w < p.wq; ++w) {
+    const int qt = 32 * w + lane;
+    bool on = qt < p.nq && qt * BT < hi && (qt + 1) * BT > lo && lo < hi;
+    if (on) on = (p.qmap[((size_t)b * p.nq + qt) * p.wk + (kt >> 5)] >> (kt & 31)) & 1u;
+    const uint32_t word = __ballot_sync(0xFFFFFFFFu, on);
+    if (lane == 0) p.kmap[(size_t)e * p.wq + w] = word;
+    count += __popc(word);
+  }
+  if (lane == 0) kw.steps[e] = count * p.G;
+}
+
+// The units' steps, shared out: CTA c of n takes steps [U c / n, U (c + 1) / n) of
+// all U, numbered by (batch, key tile), KV head, step.  A unit counts kUnitCost steps
+// more than it has (its first ones), which is about what starting and ending it
+// costs: the last key tiles of a causal prompt have one step a head.
+constexpr int kUnitCost = 2;
+struct Share {
+  uint64_t total;
+  uint32_t ctas;
+  __device__ __forceinline__ uint64_t begin_of(uint32_t c) const { return c >= ctas ? total : total * c / ctas; }
+  __device__ __forceinline__ int cta_of(uint64_t x) const { return (int)(((x + 1) * ctas - 1) / total); }
+};
+
+struct Start {  // where a CTA's range begins
+  uint64_t total, before;  // all steps; those before entry e
+  int e;
+};
+
+// Walks a CTA's pieces (warp-uniform).
+struct PieceWalk {
+  Share sh;
+  uint64_t u, end, begin;
+  int e, g, t0;
+  // of the piece that next() gave
+  int n;        // its steps (maybe none)
+  int first;    // the first of them within the unit
+  bool whole;
+  int slot;
+  uint64_t s0, s1;
+
+  __device__ PieceWalk(const Params& p, const KeyWeightsParams& kw, const Start& st) {
+    sh.total = st.total;
+    sh.ctas = (uint32_t)min((uint64_t)gridDim.x, st.total);
+    begin = u = sh.begin_of(blockIdx.x);
+    end = sh.begin_of(blockIdx.x + 1);
+    e = st.e;
+    g = t0 = 0;
+    if (u >= end) return;
+    const uint32_t m = (uint32_t)(kw.steps[e] + kUnitCost);
+    const uint64_t in = u - st.before;
+    g = (int)(in / m);
+    t0 = (int)(in % m);
+  }
+  __device__ bool next(const Params& p, const KeyWeightsParams& kw, int* e_out, int* g_out) {
+    if (u >= end) return false;
+    const int m = kw.steps[e] + kUnitCost;
+    const int take = (int)min((uint64_t)(m - t0), end - u);
+    first = max(0, t0 - kUnitCost);
+    n = max(0, t0 + take - kUnitCost) - first;
+    whole = t0 == 0 && take == m;
+    slot = 2 * (int)blockIdx.x + (u == begin ? 0 : 1);
+    s0 = u - (uint64_t)t0;
+    s1 = s0 + (uint64_t)m;
+    *e_out = e;
+    *g_out = g;
+    u += (uint64_t)take;
+    t0 = 0;
+    if (++g == p.Hkv) {
+      g = 0;
+      ++e;
+    }
+    return true;
   }
 };
 
-// Steps [s0, s1) of head-major (head, visited tile).
+// Steps [first, first + n) of a unit, head-major: (head, visited tile).
 struct Steps {
-  MapRow row;
-  int hh, w, left;
+  const uint32_t* map;
+  int words, hh, w, left;
   uint32_t bits;
-  __device__ Steps(const MapRow& r, int ntiles, int s0, int s1) : row(r), left(s1 - s0) {
-    hh = ntiles > 0 ? s0 / ntiles : 0;
-    int skip = s0 - hh * ntiles;
-    w = r.qlo >> 5;
-    bits = left > 0 ? r.word(w) : 0u;
+  __device__ Steps(const uint32_t* m, int wq, int per_head, int first, int n) : map(m), words(wq), left(n) {
+    hh = n > 0 ? first / per_head : 0;
+    int skip = first - hh * per_head;
+    w = 0;
+    bits = n > 0 ? map[0] : 0u;
     while (left > 0) {
       const int c = __popc(bits);
       if (skip < c) break;
       skip -= c;
-      bits = r.word(++w);
+      bits = map[++w];
     }
-    while (skip-- > 0) bits &= bits - 1u;
+    while (left > 0 && skip-- > 0) bits &= bits - 1u;
   }
   __device__ __forceinline__ bool next(int& h, int& qt) {
     if (left <= 0) return false;
     --left;
     while (bits == 0u) {
-      if (w >= (row.qhi >> 5)) {
+      if (++w == words) {
         ++hh;
-        w = row.qlo >> 5;
-      } else {
-        ++w;
+        w = 0;
       }
-      bits = row.word(w);
+      bits = map[w];
     }
     h = hh;
     qt = w * 32 + __ffs(bits) - 1;
@@ -95,80 +172,118 @@ struct Steps {
   }
 };
 
-// A query column's inputs, loaded two steps ahead of use.
-struct ColRaw {
-  float lse, temp;
-  int4 span;
-  int2 full;  // key tiles that the query tile covers whole
+constexpr int NCONST = NBUF;  // column constants go with the S^T buffers
+
+// Per-method constants of the log2-domain logit, kept in registers:
+//   x = log2(e) temp cap(sm_scale X) - log2(e) lse = (temp X) Q(X) + add
+// with Q the cap's polynomial times log2(e) (in z = X^2 for tanh, in X for alsc;
+// the constant sm_scale log2(e) without a cap).
+template <int METHOD>
+struct Poly {
+  static constexpr int N = METHOD == CAPATTN_CAP_TANH ? 5 : METHOD == CAPATTN_CAP_ALSC ? 7 : 1;
+  F2 c[N];
+  __device__ __forceinline__ explicit Poly(const ExactCap& k) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float x = (METHOD == CAPATTN_CAP_NONE ? k.sm_scale : has_poly(METHOD) ? k.poly[i] : 1.f) * kL2E;
+      c[i] = f2(x, x);
+    }
+  }
+  __device__ __forceinline__ F2 eval(F2 X) const {
+    const F2 z = METHOD == CAPATTN_CAP_TANH ? f2_mul(X, X) : X;
+    F2 q = c[N - 1];
+#pragma unroll
+    for (int i = N - 2; i >= 0; --i) q = f2_fma(q, z, c[i]);
+    return q;
+  }
 };
 
-template <int METHOD>
-__device__ __forceinline__ float chunk_sum(const uint32_t (&x)[32], const float4* cc, const int4* spans, int j,
-                                           bool masked, bool poly, const ExactCap& k) {
+// Sum of 2^x over 32 query columns of this thread's key.  fast: every raw score
+// of the warp is in the polynomial's range (or the cap has none to leave).
+// MASK: 0 every pair is live; 1 a column's live keys are [lo, lo + len); 2 and one more.
+template <int METHOD, bool TEMP, int MASK, bool FAST>
+__device__ __forceinline__ float chunk_sum(const uint32_t (&x)[32], const float* add, const float* temp,
+                                           const int2* spans, const int* extra, int j, const Poly<METHOD>& poly, const ExactCap& k) {
   F2 acc = f2(0.f, 0.f);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const float4 c = cc[e];  // mul, mul', add, add'
-    const float X0 = __uint_as_float(x[2 * e]), X1 = __uint_as_float(x[2 * e + 1]);
-    F2 f;
-    if constexpr (METHOD == CAPATTN_CAP_NONE) {
-      f = f2(X0, X1);  // sm_scale is in mul
-    } else if constexpr (has_poly(METHOD)) {
-      f = poly ? poly_cap2<METHOD>(f2(X0, X1), k) : f2(any_cap<METHOD>(X0, k), any_cap<METHOD>(X1, k));
-    } else {
-      f = f2(any_cap<METHOD>(X0, k), any_cap<METHOD>(X1, k));
+  for (int e = 0; e < 32; e += 4) {
+    const float4 ad = *reinterpret_cast<const float4*>(add + e);
+    float4 tp = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (TEMP) tp = *reinterpret_cast<const float4*>(temp + e);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float X0 = __uint_as_float(x[e + 2 * h]), X1 = __uint_as_float(x[e + 2 * h + 1]);
+      const F2 a2 = h == 0 ? f2(ad.x, ad.y) : f2(ad.z, ad.w), t2 = h == 0 ? f2(tp.x, tp.y) : f2(tp.z, tp.w);
+      F2 y;
+      if constexpr (FAST && METHOD != CAPATTN_CAP_SOFT_SIGN) {
+        const F2 X = f2(X0, X1);
+        y = f2_fma(TEMP ? f2_mul(X, t2) : X, poly.eval(X), a2);
+      } else {
+        F2 t = f2_mul(f2(any_cap<METHOD>(X0, k), any_cap<METHOD>(X1, k)), f2(kL2E, kL2E));
+        y = TEMP ? f2_fma(t, t2, a2) : f2_add(t, a2);
+      }
+      float a, b;
+      f2_split(y, a, b);
+      a = ex2_approx(a);
+      b = ex2_approx(b);
+      if (MASK > 0) {
+        const int4 r = *reinterpret_cast<const int4*>(spans + e + 2 * h);  // (lo, len) of two columns
+        bool la = (uint32_t)(j - r.x) < (uint32_t)r.y, lb = (uint32_t)(j - r.z) < (uint32_t)r.w;
+        if (MASK > 1) {
+          la = la || j == extra[e + 2 * h];
+          lb = lb || j == extra[e + 2 * h + 1];
+        }
+        a = la ? a : 0.f;
+        b = lb ? b : 0.f;
+      }
+      acc = f2_add(acc, f2(a, b));
     }
-    float a, b;
-    f2_split(f2_fma(f2(c.x, c.y), f, f2(c.z, c.w)), a, b);
-    a = ex2_approx(a);
-    b = ex2_approx(b);
-    if (masked) {
-      const int4 r0 = spans[2 * e], r1 = spans[2 * e + 1];
-      a = (j >= r0.x && j < r0.y) || j == r0.z ? a : 0.f;
-      b = (j >= r1.x && j < r1.y) || j == r1.z ? b : 0.f;
-    }
-    acc = f2_add(acc, f2(a, b));
   }
   float a, b;
   f2_split(acc, a, b);
   return a + b;
 }
 
-template <int METHOD, int HD>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int METHOD, int HD, bool TEMP>
+__global__ void __launch_bounds__(kThreads, 1)
 key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const Params p,
-                      const KeyWeightsParams kw, const int parts) {
+                      const KeyWeightsParams kw) {
   constexpr int TILE = tile_bytes<HD>();
   constexpr int NSLAB = HD / 64;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[1 + 2 * NSTAGE + 2 * NBUF];
+  __shared__ __align__(8) uint64_t bars[2 * (NK + NSTAGE + NBUF)];
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag;
-  __shared__ __align__(16) float4 colc[2][BT / 2];
-  __shared__ __align__(16) int4 cols[2][BT];
-  __shared__ float s_sum[2][BT], s_out[BT];
+  __shared__ int abort_flag, join_flag;
+  __shared__ __align__(16) float col_add[NCONST][BT], col_temp[TEMP ? NCONST : 1][BT];
+  __shared__ __align__(16) int2 col_span[NCONST][BT];
+  __shared__ int col_extra[NCONST][BT];
+  __shared__ int col_masked[NCONST];
+  __shared__ float s_sum[2][kElem / 4][BT];
+  __shared__ Start s_start;
+  __shared__ uint64_t s_scan[kThreads / 32];
 
-  const int rank = blockIdx.x % parts, unit = blockIdx.x / parts;
-  const int bg = unit % (p.B * p.Hkv), g = bg % p.Hkv, b = bg / p.Hkv;
-  const int kt = unit / (p.B * p.Hkv), k0 = kt * BT;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sK = base, sQ = base + TILE;
-  const uint32_t bar_k = smem_u32(&bars[0]);
-  const uint32_t bar_full = smem_u32(&bars[1]);                        // + 8 s: Q of stage s landed
-  const uint32_t bar_empty = smem_u32(&bars[1 + NSTAGE]);              // + 8 s: its MMAs are done
-  const uint32_t bar_s = smem_u32(&bars[1 + 2 * NSTAGE]);              // + 8 u: S^T in buffer u
-  const uint32_t bar_free = smem_u32(&bars[1 + 2 * NSTAGE + NBUF]);    // + 8 u: buffer u read (8 warps)
+  const uint32_t sK = base, sQ = base + NK * TILE;
+  const uint32_t bar_kfull = smem_u32(&bars[0]);          // + 8 x: K of buffer x landed
+  const uint32_t bar_kempty = bar_kfull + 8 * NK;         // + 8 x: its unit's MMAs are done
+  const uint32_t bar_full = bar_kempty + 8 * NK;          // + 8 s: Q of stage s landed
+  const uint32_t bar_empty = bar_full + 8 * NSTAGE;       // + 8 s: its MMAs are done
+  const uint32_t bar_s = bar_empty + 8 * NSTAGE;          // + 8 u: S^T and constants in buffer u (commit, 32 lanes)
+  const uint32_t bar_free = bar_s + 8 * NBUF;             // + 8 u: buffer u read (all warps)
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    mbar_init(bar_k, 1);
+    for (int x = 0; x < NK; ++x) {
+      mbar_init(bar_kfull + 8 * x, 1);
+      mbar_init(bar_kempty + 8 * x, 1);
+    }
     for (int s = 0; s < NSTAGE; ++s) {
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int u = 0; u < NBUF; ++u) {
-      mbar_init(bar_s + 8 * u, 1);
-      mbar_init(bar_free + 8 * u, 8);
+      mbar_init(bar_s + 8 * u, 33);
+      mbar_init(bar_free + 8 * u, kElem);
     }
     fence_mbar_init();
   }
@@ -178,171 +293,245 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   }
   pdl_trigger();
   pdl_wait();
+  // all steps, and the entry where this CTA's range begins: a thread takes a run of
+  // entries
+  {
+    const int64_t E = (int64_t)p.B * p.nk;
+    const int64_t run = (E + kThreads - 1) / kThreads;
+    const int64_t e0 = min(E, run * (int64_t)threadIdx.x), e1 = min(E, e0 + run);
+    uint64_t mine = 0;
+    for (int64_t e = e0; e < e1; ++e) mine += (uint64_t)(kw.steps[e] + kUnitCost) * p.Hkv;
+    uint64_t up = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, up, d);
+      if (lane >= d) up += y;
+    }
+    if (lane == 31) s_scan[warp] = up;
+    __syncthreads();
+    uint64_t before = up - mine, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += s_scan[w];
+      total += s_scan[w];
+    }
+    Share sh;
+    sh.total = total;
+    sh.ctas = (uint32_t)min((uint64_t)gridDim.x, total);
+    const uint64_t begin = sh.begin_of(blockIdx.x);
+    if (threadIdx.x == 0) s_start.total = total;
+    if (begin >= before && begin < before + mine) {
+      for (int64_t e = e0; e < e1; ++e) {
+        const uint64_t m = (uint64_t)(kw.steps[e] + kUnitCost) * p.Hkv;
+        if (begin < before + m) {
+          s_start.e = (int)e;
+          s_start.before = before;
+          break;
+        }
+        before += m;
+      }
+    } else if (begin >= total && threadIdx.x == 0) {  // an empty range
+      s_start.e = 0;
+      s_start.before = 0;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-
-  int lo = 0, hi = p.L;  // counted rows
-  if (kw.rows) {
-    lo = kw.rows[2 * b];
-    hi = kw.rows[2 * b + 1];
-    if (!(lo >= 0 && lo <= hi && hi <= p.L)) {
-      if (threadIdx.x == 0) atomicOr(p.status, kStatusBadRowsBit);
-      lo = max(lo, 0);
-      hi = min(hi, p.L);
-    }
-  }
-  MapRow row{p.kmap + ((size_t)b * p.nk + kt) * p.wq, lo / BT, (hi - 1) / BT};
-  const int ntiles = lo < hi ? row.count() : 0;
-  const int all = ntiles * p.G;
-  const int s0 = (int)((int64_t)all * rank / parts), s1 = (int)((int64_t)all * (rank + 1) / parts);
-  const int n = s1 - s0;
+  PieceWalk it(p, kw, s_start);
+  int e, g;
+  uint32_t step = 0, unit = 0;  // steps and units with steps so far
 
   if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
-    if (n > 0) {
-      const bool leader = elect_one_sync();
+    // ------------------------------------------- TMA producer and column constants
+    const bool leader = elect_one_sync();
+    bool ok = true;
+    while (ok && it.next(p, kw, &e, &g)) {
+      if (it.n == 0) continue;
+      const int b = e / p.nk, kt = e % p.nk;
+      const int x = unit % NK, ux = unit / NK;
+      if (ux > 0 && !mbar_wait_warp(bar_kempty + 8 * x, (ux - 1) & 1, p.status, &abort_flag)) break;
       if (leader) {
-        mbar_expect_tx(bar_k, TILE);
-        for (int sl = 0; sl < NSLAB; ++sl) tma_load_4d(sK + sl * SLAB, &mk, bar_k, 64 * sl, g, k0, b);
+        mbar_expect_tx(bar_kfull + 8 * x, TILE);
+        for (int sl = 0; sl < NSLAB; ++sl)
+          tma_load_4d(sK + x * TILE + sl * SLAB, &mk, bar_kfull + 8 * x, 64 * sl, g, kt * BT, b);
       }
       __syncwarp();
-      Steps st(row, ntiles, s0, s1);
-      int hh, qt, j = 0;
-      while (st.next(hh, qt)) {
-        const int s = j % NSTAGE, u = j / NSTAGE;
-        if (u > 0 && !mbar_wait_warp(bar_empty + 8 * s, (u - 1) & 1, p.status, &abort_flag)) break;
+      ++unit;
+      const int lo = kw.rows ? max(kw.rows[2 * b], 0) : 0, hi = kw.rows ? min(kw.rows[2 * b + 1], p.L) : p.L;
+      // the raw inputs of a step's columns lane + 32 e, loaded a step ahead
+      float lse[4], temp[4];
+      int4 span[4];
+      int2 full = make_int2(0, 0);
+      auto load = [&](int hh, int qt) {
+        // whole: the tile's rows are all counted
+        full = qt * BT >= lo && (qt + 1) * BT <= hi ? p.qfull[(size_t)b * p.nq + qt] : make_int2(0, 0);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int i = qt * BT + lane + 32 * y;
+          const bool in = i >= lo && i < hi;
+          lse[y] = in ? p.lse[((size_t)b * p.Hq + g * p.G + hh) * p.L + i] : -INFINITY;
+          temp[y] = TEMP && in ? p.temp[(size_t)b * p.L + i] : 1.f;
+          span[y] = in ? p.rowinfo[(size_t)b * p.L + i] : make_int4(0, 0, -1, 0);
+        }
+      };
+      Steps st(p.kmap + (size_t)e * p.wq, p.wq, kw.steps[e] / p.G, it.first, it.n);
+      int hh, qt;
+      bool have = st.next(hh, qt);
+      load(hh, qt);
+      while (have) {
+        const int s = step % NSTAGE, us = step / NSTAGE, c = step % NCONST, uc = step / NCONST;
+        if (us > 0 && !mbar_wait_warp(bar_empty + 8 * s, (us - 1) & 1, p.status, &abort_flag)) {
+          ok = false;
+          break;
+        }
         if (leader) {
           mbar_expect_tx(bar_full + 8 * s, TILE);
           for (int sl = 0; sl < NSLAB; ++sl)
             tma_load_4d(sQ + s * TILE + sl * SLAB, &mq, bar_full + 8 * s, 64 * sl, g * p.G + hh, qt * BT, b);
         }
         __syncwarp();
-        ++j;
+        ++step;
+        if (uc > 0 && !mbar_wait_warp(bar_free + 8 * c, (uc - 1) & 1, p.status, &abort_flag)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int col = lane + 32 * y;
+          col_add[c][col] = lse[y] == -INFINITY ? 0.f : -lse[y] * kL2E;
+          if (TEMP) col_temp[c][col] = temp[y];
+          col_span[c][col] = make_int2(span[y].x, span[y].y - span[y].x);
+          if (p.bounds) col_extra[c][col] = span[y].z;
+        }
+        if (lane == 0) col_masked[c] = !(kt >= full.x && kt < full.y);
+        mbar_arrive(bar_s + 8 * c);
+        have = st.next(hh, qt);
+        if (have) load(hh, qt);
       }
-      if (leader) {
-        drain_wait(bar_k, 0);
-        for (int x = (j > NSTAGE ? j - NSTAGE : 0); x < j; ++x) drain_wait(bar_full + 8 * (x % NSTAGE), (x / NSTAGE) & 1);
-      }
-      __syncwarp();
     }
+    if (leader) {
+      for (uint32_t x = unit > NK ? unit - NK : 0; x < unit; ++x) drain_wait(bar_kfull + 8 * (x % NK), (x / NK) & 1);
+      for (uint32_t x = step > NSTAGE ? step - NSTAGE : 0; x < step; ++x)
+        drain_wait(bar_full + 8 * (x % NSTAGE), (x / NSTAGE) & 1);
+    }
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (n > 0) {
-      const bool leader = elect_one_sync();
-      constexpr uint32_t idesc = idesc_bf16(BT, BT, 0, 0);
-      const uint64_t dK = smem_desc(sK, 16, 1024), dQ = smem_desc(sQ, 16, 1024);
-      bool ok = mbar_wait_warp(bar_k, 0, p.status, &abort_flag);
-      int j = 0;
-      for (; ok && j < n; ++j) {
-        const int s = j % NSTAGE, u = j % NBUF, r = j / NBUF;
+    const bool leader = elect_one_sync();
+    constexpr uint32_t idesc = idesc_bf16(BT, BT, 0, 0);
+    const uint64_t dK = smem_desc(sK, 16, 1024), dQ = smem_desc(sQ, 16, 1024);
+    bool ok = true;
+    while (ok && it.next(p, kw, &e, &g)) {
+      if (it.n == 0) continue;
+      const int x = unit % NK;
+      ok = mbar_wait_warp(bar_kfull + 8 * x, (unit / NK) & 1, p.status, &abort_flag);
+      for (int i = 0; ok && i < it.n; ++i) {
+        const int s = step % NSTAGE, u = step % NBUF, r = step / NBUF;
         if (r > 0) ok = mbar_wait_warp(bar_free + 8 * u, (r - 1) & 1, p.status, &abort_flag);
-        ok = ok && mbar_wait_warp(bar_full + 8 * s, (j / NSTAGE) & 1, p.status, &abort_flag);
+        ok = ok && mbar_wait_warp(bar_full + 8 * s, (step / NSTAGE) & 1, p.status, &abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (leader) {
 #pragma unroll
           for (int ks = 0; ks < HD / 16; ++ks) {
             const uint32_t off = (ks >> 2) * SLAB + (ks & 3) * 32;
-            mma_ss(tmem + u * BT, desc_add(dK, off), desc_add(dQ, s * TILE + off), idesc, ks > 0 ? 1u : 0u);
+            mma_ss(tmem + u * BT, desc_add(dK, x * TILE + off), desc_add(dQ, s * TILE + off), idesc, ks > 0 ? 1u : 0u);
           }
           mma_commit(bar_empty + 8 * s);
           mma_commit(bar_s + 8 * u);
+          if (i == it.n - 1) mma_commit(bar_kempty + 8 * x);
         }
         __syncwarp();
+        ++step;
       }
-      // every MMA has completed before TMEM is freed
-      if (leader)
-        for (int x = (j > NBUF ? j - NBUF : 0); x < j; ++x) mbar_poll(bar_s + 8 * (x % NBUF), (x / NBUF) & 1);
-      __syncwarp();
+      ++unit;
     }
+    // every MMA has completed before TMEM is freed
+    if (leader)
+      for (uint32_t x = step > NSTAGE ? step - NSTAGE : 0; x < step; ++x)
+        mbar_poll(bar_empty + 8 * (x % NSTAGE), (x / NSTAGE) & 1);
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ elementwise
     const int wg = (warp - 2) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;                   // key of the tile
-    const int tid = (warp - 2 - 4 * wg) * 32 + lane;     // within the warpgroup
-    const int j = k0 + r;
-    const uint32_t cols_t = tmem + ((uint32_t)(quarter * 32) << 16) + 64u * wg;
-    const int my_col = 64 * wg + tid;                    // the column whose constants this thread writes (tid < 64)
-    Steps nx(row, ntiles, s0, s1);
-    auto load = [&](bool have, int hh, int qt) {
-      ColRaw c;
-      c.lse = -INFINITY;
-      c.temp = 1.f;
-      c.span = make_int4(0, 0, -1, 0);
-      c.full = make_int2(0, 0);
-      if (!have) return c;
-      // whole: the tile's rows are all counted
-      if (qt * BT >= lo && (qt + 1) * BT <= hi) c.full = p.qfull[(size_t)b * p.nq + qt];
-      const int i = qt * BT + my_col;
-      if (tid < 64 && i >= lo && i < hi) {
-        c.lse = p.lse[((size_t)b * p.Hq + g * p.G + hh) * p.L + i];
-        if (p.temp) c.temp = p.temp[(size_t)b * p.L + i];
-        c.span = p.rowinfo[(size_t)b * p.L + i];
-      }
-      return c;
-    };
-    auto put = [&](int buf, const ColRaw& c) {
-      if (tid < 64) {
-        float* f = reinterpret_cast<float*>(&colc[buf][my_col >> 1]) + (my_col & 1);
-        f[0] = c.temp * kL2E * (METHOD == CAPATTN_CAP_NONE ? p.sm_scale : 1.f);
-        f[2] = c.lse == -INFINITY ? 0.f : -c.lse * kL2E;
-        cols[buf][my_col] = c.span;
-      }
-    };
-    int hh, qt;
-    bool have = nx.next(hh, qt);
-    ColRaw cur = load(have, hh, qt);
-    have = nx.next(hh, qt);
-    ColRaw nxt = load(have, hh, qt);
-    float sum = 0.f, comp = 0.f;
-    put(0, cur);
-    bool ok = true;
-    for (int step = 0; step < n; ++step) {
-      const int cb = step & 1, u = step % NBUF;
-      named_bar_sync(1 + wg, 128);  // this step's constants are written, the last step's read
-      if (step + 1 < n) put(cb ^ 1, nxt);
-      have = nx.next(hh, qt);
-      const ColRaw far = load(have, hh, qt);
-      const bool masked = !(kt >= cur.full.x && kt < cur.full.y);
-      ok = ok && mbar_wait_warp(bar_s + 8 * u, (step / NBUF) & 1, p.status, &abort_flag);
-      if (ok) {
+    const uint32_t cols_t = tmem + ((uint32_t)(quarter * 32) << 16) + 32u * wg;
+    const Poly<METHOD> poly(kw.cap);
+    int parity = 0;
+    bool ok = true;  // after a timeout the warp still meets the others at every unit's barriers
+    while (it.next(p, kw, &e, &g)) {
+      const int b = e / p.nk, k0 = (e % p.nk) * BT, j = k0 + r;
+      float sum = 0.f, comp = 0.f;
+      for (int i = 0; i < it.n; ++i, ++step) {
+        const int u = step % NBUF, c = u;
+        ok = ok && mbar_wait_warp(bar_s + 8 * u, (step / NBUF) & 1, p.status, &abort_flag);
+        if (!ok) break;
         tc_fence_after();
-        uint32_t x[2][32];
-        tmem_ld32(cols_t + u * BT, x[0]);
-        tmem_ld32(cols_t + u * BT + 32, x[1]);
+        const bool masked = col_masked[c] != 0;
+        uint32_t x[32];
+        tmem_ld32(cols_t + u * BT, x);
         tmem_wait_ld();
+        bool fast = true;
+        if constexpr (has_poly(METHOD)) {
+          float am = 0.f;
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) am = fmax3_abs(am, __uint_as_float(x[y]), __uint_as_float(x[y + 1]));
+          fast = __all_sync(0xFFFFFFFFu, am <= kw.cap.xmax && kw.cap.xmax > 0.f);
+        }
+        const float* ad = &col_add[c][32 * wg];
+        const float* tp = &col_temp[TEMP ? c : 0][32 * wg];
+        const int2* sp = &col_span[c][32 * wg];
+        const int* ex = &col_extra[c][32 * wg];
+        float part;
+        if (!masked)
+          part = fast ? chunk_sum<METHOD, TEMP, 0, true>(x, ad, tp, sp, ex, j, poly, kw.cap)
+                      : chunk_sum<METHOD, TEMP, 0, false>(x, ad, tp, sp, ex, j, poly, kw.cap);
+        else if (!p.bounds)
+          part = fast ? chunk_sum<METHOD, TEMP, 1, true>(x, ad, tp, sp, ex, j, poly, kw.cap)
+                      : chunk_sum<METHOD, TEMP, 1, false>(x, ad, tp, sp, ex, j, poly, kw.cap);
+        else
+          part = fast ? chunk_sum<METHOD, TEMP, 2, true>(x, ad, tp, sp, ex, j, poly, kw.cap)
+                      : chunk_sum<METHOD, TEMP, 2, false>(x, ad, tp, sp, ex, j, poly, kw.cap);
+        const float y = part - comp, t = sum + y;
+        comp = (t - sum) - y;
+        sum = t;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_free + 8 * u);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          bool poly = false;
-          if constexpr (has_poly(METHOD)) {
-            float am = 0.f;
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) am = fmax3_abs(am, __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
-            poly = __all_sync(0xFFFFFFFFu, am <= kw.cap.xmax && kw.cap.xmax > 0.f);
-          }
-          const float4* cc = &colc[cb][32 * wg + 16 * c];
-          const int4* sp = &cols[cb][64 * wg + 32 * c];
-          float part;
-          if (masked)
-            part = poly ? chunk_sum<METHOD>(x[c], cc, sp, j, true, true, kw.cap)
-                        : chunk_sum<METHOD>(x[c], cc, sp, j, true, false, kw.cap);
-          else
-            part = poly ? chunk_sum<METHOD>(x[c], cc, sp, j, false, true, kw.cap)
-                        : chunk_sum<METHOD>(x[c], cc, sp, j, false, false, kw.cap);
-          const float y = part - comp, t = sum + y;
-          comp = (t - sum) - y;
-          sum = t;
-        }
       }
-      cur = nxt;
-      nxt = far;
+      // ------------------------------------------------------ end of a piece
+      // The first warpgroup adds the four up and writes; the others go on.  (s_sum
+      // alternates: it is written again only after the next piece's barrier.)
+      float(*sums)[BT] = s_sum[parity];
+      parity ^= 1;
+      sums[wg][r] = sum;
+      named_bar_sync(1, 32 * kElem);
+      if (wg != 0) continue;
+      float* w = kw.w + ((size_t)b * p.Hkv + g) * kw.w_stride + k0;
+      const float mine = (sums[0][r] + sums[1][r]) + (sums[2][r] + sums[3][r]);
+      if (it.whole) {
+        if (j < p.Lk) w[r] = mine;
+        continue;
+      }
+      kw.partial[(size_t)it.slot * BT + r] = mine;
+      __threadfence();
+      named_bar_sync(2, BT);
+      const int c0 = it.sh.cta_of(it.s0), c1 = it.sh.cta_of(it.s1 - 1);
+      if (threadIdx.x == 64) {
+        const bool last = atomicAdd(&kw.counters[c0], 1u) == (uint32_t)(c1 - c0);
+        __threadfence();
+        join_flag = last;
+      }
+      named_bar_sync(2, BT);
+      if (join_flag && j < p.Lk) {
+        const int late = it.s0 != it.sh.begin_of(c0) ? 1 : 0;
+        float x = 0.f;
+        for (int c = c0; c <= c1; ++c) x += __ldcg(&kw.partial[(size_t)(2 * c + (c == c0 ? late : 0)) * BT + r]);
+        w[r] = x;
+      }
+      named_bar_sync(2, BT);  // join_flag is read
     }
-    s_sum[wg][r] = sum;
   }
   __syncwarp();
   tc_fence_before();
@@ -351,49 +540,29 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     tc_fence_after();
     tmem_dealloc(tmem, NBUF * BT);
   }
-  if (threadIdx.x < BT) s_out[threadIdx.x] = s_sum[0][threadIdx.x] + s_sum[1][threadIdx.x];
-  float* w = kw.w + ((size_t)b * p.Hkv + g) * kw.w_stride + k0;
-  if (parts == 1) {
-    if (threadIdx.x < BT && k0 + (int)threadIdx.x < p.Lk) w[threadIdx.x] = s_out[threadIdx.x];
-    return;
-  }
-  cg::cluster_group cluster = cg::this_cluster();
-  cluster.sync();
-  if (rank == 0 && threadIdx.x < BT && k0 + (int)threadIdx.x < p.Lk) {
-    float x = 0.f;
-    for (int c = 0; c < parts; ++c) x += cluster.map_shared_rank(s_out, c)[threadIdx.x];
-    w[threadIdx.x] = x;
-  }
-  cluster.sync();  // no CTA leaves while its sums may be read
 }
 
-template <int METHOD, int HD>
-cudaError_t run(const Params& p, const KeyWeightsParams& kw, cudaStream_t s) {
-  auto* k = key_weights_tc_kernel<METHOD, HD>;
+template <int METHOD, int HD, bool TEMP>
+cudaError_t run_temp(const Params& p, const KeyWeightsParams& kw, cudaStream_t s) {
+  auto* k = key_weights_tc_kernel<METHOD, HD, TEMP>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem_bytes<HD>(), done);
   CUtensorMap mq, mk;
   if (e == cudaSuccess) e = make_bhld_map(&mq, p.q, p.B, p.L, p.Hq, HD, BT);
   if (e == cudaSuccess) e = make_bhld_map(&mk, p.k, p.B, p.Lk, p.Hkv, HD, BT);
   if (e != cudaSuccess) return e;
-  // Parts of a key tile's steps: until two CTAs an SM have several turns each.
-  const int64_t units = (int64_t)p.B * p.Hkv * p.nk;
-  int parts = 1;
-  while (parts < 8 && units * parts < 152 * 2 * 4 && parts * 2 <= p.G * p.nq) parts *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * parts));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<HD>();
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = parts;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k, mq, mk, p, kw, parts);
+  const int64_t entries = (int64_t)p.B * p.nk;
+  e = launch_pdl(key_plan_kernel, dim3((unsigned)((entries + 3) / 4)), dim3(128), 0, s, p, kw);
+  if (e != cudaSuccess) return e;
+  // no more CTAs than there can be steps
+  const int64_t most = entries * p.Hkv * p.nq * p.G;
+  return launch_pdl(k, dim3((unsigned)(most < kWeightCtas ? most : kWeightCtas)), dim3(kThreads), smem_bytes<HD>(), s, mq,
+                    mk, p, kw);
+}
+
+template <int METHOD, int HD>
+cudaError_t run(const Params& p, const KeyWeightsParams& kw, cudaStream_t s) {
+  return p.temp ? run_temp<METHOD, HD, true>(p, kw, s) : run_temp<METHOD, HD, false>(p, kw, s);
 }
 
 template <int HD>

@@ -24,12 +24,13 @@ import ctypes
 import torch
 
 from . import capattn as _ca
-from .capattn import AttnParams, CAP_METHODS, DTYPES, PASS_FWD
+from .capattn import AttnParams, CAP_METHODS, DTYPES
 
 HEADER_BYTES = 4096  # of a cache workspace, zero before its first use
 CALL_APPEND, CALL_DECODE, CALL_DECODE_WEIGHTS, CALL_EVICT = 0, 1, 2, 3
 EXPORTED_SYMBOLS = ("capattn_cache_validate_config", "capattn_cache_workspace_bytes", "capattn_cache_append",
-                    "capattn_cache_decode", "capattn_cache_evict", "capattn_key_weights")
+                    "capattn_cache_decode", "capattn_cache_evict", "capattn_key_weights",
+                    "capattn_key_weights_workspace_bytes")
 
 
 class CacheConfig(ctypes.Structure):
@@ -61,6 +62,8 @@ def lib() -> ctypes.CDLL:
         h.capattn_cache_decode.argtypes = [cfgp, vp, i64] + [vp] * 11 + [sz, vp]
         h.capattn_cache_evict.restype = ctypes.c_int
         h.capattn_cache_evict.argtypes = [cfgp, i32, i32, i32] + [vp] * 12 + [sz, vp]
+        h.capattn_key_weights_workspace_bytes.restype = sz
+        h.capattn_key_weights_workspace_bytes.argtypes = [ctypes.POINTER(_ca.CapattnConfig)]
         h.capattn_key_weights.restype = ctypes.c_int
         h.capattn_key_weights.argtypes = [ctypes.POINTER(_ca.CapattnConfig)] + [vp] * 8 + [i64, vp, sz, vp]
         _lib_handle = h
@@ -288,8 +291,8 @@ def cache_decode(q, cache: KVCache, ap: AttnParams, temp=None, accumulate=False,
     pos, qpos = cache._positions()
     plan = cache.plan(Hq, ap)
     if out is None:
-        o = q.new_empty(shape)
-        lse = q.new_empty((cache.B, Hq), dtype=torch.float32)
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        lse = torch.empty((cache.B, Hq), dtype=torch.float32, device=dev)
     else:
         o, lse = out
         _want(o, "o", shape, cache.dtype, dev)
@@ -345,9 +348,9 @@ def cache_evict(cache: KVCache, budget: int, keep_first: int = 0, keep_last: int
 def new_key_weights_workspace(q, k, ap: AttnParams) -> torch.Tensor:
     """Workspace of key_weights for q [B, L, Hq, D] and k [B, Lk, Hkv, D]."""
     cfg = _ca._config(q, k, ap)
-    n = _ca.workspace_bytes(cfg, PASS_FWD)
+    n = int(lib().capattn_key_weights_workspace_bytes(ctypes.byref(cfg)))
     if n == 0:
-        _ca._check(lib().capattn_validate_config(ctypes.byref(cfg)), "capattn_workspace_bytes")
+        _ca._check(lib().capattn_validate_config(ctypes.byref(cfg)), "capattn_key_weights_workspace_bytes")
     ws = torch.empty(n, dtype=torch.uint8, device=q.device)
     ws[:256].zero_()  # the status word
     return ws
