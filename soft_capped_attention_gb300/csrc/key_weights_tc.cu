@@ -33,7 +33,8 @@ constexpr int NSTAGE = 4;              // Q tiles in flight
 constexpr int NBUF = 4;                // S^T buffers
 constexpr int NK = 2;                  // K buffers
 constexpr int kElem = 16;              // elementwise warps
-constexpr int kThreads = 64 + 32 * kElem;
+constexpr int kConst = 2;              // warps that load the columns' constants, 64 columns each
+constexpr int kThreads = 64 + 32 * (kElem + kConst);
 template <int HD>
 constexpr int tile_bytes() { return (HD / 64) * SLAB; }
 template <int HD>
@@ -269,8 +270,8 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   const uint32_t bar_kempty = bar_kfull + 8 * NK;         // + 8 x: its unit's MMAs are done
   const uint32_t bar_full = bar_kempty + 8 * NK;          // + 8 s: Q of stage s landed
   const uint32_t bar_empty = bar_full + 8 * NSTAGE;       // + 8 s: its MMAs are done
-  const uint32_t bar_s = bar_empty + 8 * NSTAGE;          // + 8 u: S^T and constants in buffer u (commit, 32 lanes)
-  const uint32_t bar_free = bar_s + 8 * NBUF;             // + 8 u: buffer u read (all warps)
+  const uint32_t bar_s = bar_empty + 8 * NSTAGE;          // + 8 u: S^T and constants in buffer u (commit, constants' lanes)
+  const uint32_t bar_free = bar_s + 8 * NBUF;             // + 8 u: buffer u read (elementwise warps)
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int x = 0; x < NK; ++x) {
@@ -282,7 +283,7 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int u = 0; u < NBUF; ++u) {
-      mbar_init(bar_s + 8 * u, 33);
+      mbar_init(bar_s + 8 * u, 1 + 32 * kConst);
       mbar_init(bar_free + 8 * u, kElem);
     }
     fence_mbar_init();
@@ -343,7 +344,7 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   uint32_t step = 0, unit = 0;  // steps and units with steps so far
 
   if (warp == 0) {
-    // ------------------------------------------- TMA producer and column constants
+    // ------------------------------------------------------------ TMA producer
     const bool leader = elect_one_sync();
     bool ok = true;
     while (ok && it.next(p, kw, &e, &g)) {
@@ -358,29 +359,10 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       }
       __syncwarp();
       ++unit;
-      const int lo = kw.rows ? max(kw.rows[2 * b], 0) : 0, hi = kw.rows ? min(kw.rows[2 * b + 1], p.L) : p.L;
-      // the raw inputs of a step's columns lane + 32 e, loaded a step ahead
-      float lse[4], temp[4];
-      int4 span[4];
-      int2 full = make_int2(0, 0);
-      auto load = [&](int hh, int qt) {
-        // whole: the tile's rows are all counted
-        full = qt * BT >= lo && (qt + 1) * BT <= hi ? p.qfull[(size_t)b * p.nq + qt] : make_int2(0, 0);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int i = qt * BT + lane + 32 * y;
-          const bool in = i >= lo && i < hi;
-          lse[y] = in ? p.lse[((size_t)b * p.Hq + g * p.G + hh) * p.L + i] : -INFINITY;
-          temp[y] = TEMP && in ? p.temp[(size_t)b * p.L + i] : 1.f;
-          span[y] = in ? p.rowinfo[(size_t)b * p.L + i] : make_int4(0, 0, -1, 0);
-        }
-      };
       Steps st(p.kmap + (size_t)e * p.wq, p.wq, kw.steps[e] / p.G, it.first, it.n);
       int hh, qt;
-      bool have = st.next(hh, qt);
-      load(hh, qt);
-      while (have) {
-        const int s = step % NSTAGE, us = step / NSTAGE, c = step % NCONST, uc = step / NCONST;
+      while (st.next(hh, qt)) {
+        const int s = step % NSTAGE, us = step / NSTAGE;
         if (us > 0 && !mbar_wait_warp(bar_empty + 8 * s, (us - 1) & 1, p.status, &abort_flag)) {
           ok = false;
           break;
@@ -392,22 +374,6 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         }
         __syncwarp();
         ++step;
-        if (uc > 0 && !mbar_wait_warp(bar_free + 8 * c, (uc - 1) & 1, p.status, &abort_flag)) {
-          ok = false;
-          break;
-        }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int col = lane + 32 * y;
-          col_add[c][col] = lse[y] == -INFINITY ? 0.f : -lse[y] * kL2E;
-          if (TEMP) col_temp[c][col] = temp[y];
-          col_span[c][col] = make_int2(span[y].x, span[y].y - span[y].x);
-          if (p.bounds) col_extra[c][col] = span[y].z;
-        }
-        if (lane == 0) col_masked[c] = !(kt >= full.x && kt < full.y);
-        mbar_arrive(bar_s + 8 * c);
-        have = st.next(hh, qt);
-        if (have) load(hh, qt);
       }
     }
     if (leader) {
@@ -416,6 +382,64 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         drain_wait(bar_full + 8 * (x % NSTAGE), (x / NSTAGE) & 1);
     }
     __syncwarp();
+  } else if (warp >= 2 + kElem) {
+    // ------------------------------------------------------------ column constants
+    const int c0 = 64 * (warp - 2 - kElem) + lane;  // and c0 + 32
+    struct Raw {
+      float lse[2], temp[2];
+      int4 span[2];
+      int2 full;
+    };
+    bool ok = true;
+    while (ok && it.next(p, kw, &e, &g)) {
+      if (it.n == 0) continue;
+      const int b = e / p.nk, kt = e % p.nk;
+      const int lo = kw.rows ? max(kw.rows[2 * b], 0) : 0, hi = kw.rows ? min(kw.rows[2 * b + 1], p.L) : p.L;
+      Steps st(p.kmap + (size_t)e * p.wq, p.wq, kw.steps[e] / p.G, it.first, it.n);
+      // the raw inputs of the next step (unused values when there is none)
+      auto load = [&](bool& have) {
+        Raw v;
+        int hh = 0, qt = 0;
+        have = st.next(hh, qt);
+        // whole: the tile's rows are all counted
+        v.full = have && qt * BT >= lo && (qt + 1) * BT <= hi ? p.qfull[(size_t)b * p.nq + qt] : make_int2(0, 0);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int i = qt * BT + c0 + 32 * y;
+          const bool in = have && i >= lo && i < hi;
+          v.lse[y] = in ? p.lse[((size_t)b * p.Hq + g * p.G + hh) * p.L + i] : -INFINITY;
+          v.temp[y] = TEMP && in ? p.temp[(size_t)b * p.L + i] : 1.f;
+          v.span[y] = in ? p.rowinfo[(size_t)b * p.L + i] : make_int4(0, 0, -1, 0);
+        }
+        return v;
+      };
+      bool have, more;
+      Raw cur = load(have), nxt = load(more);
+      while (have) {
+        bool later;
+        const Raw far = load(later);  // two steps ahead of its use
+        const int c = step % NCONST, uc = step / NCONST;
+        if (uc > 0 && !mbar_wait_warp(bar_free + 8 * c, (uc - 1) & 1, p.status, &abort_flag)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int col = c0 + 32 * y;
+          col_add[c][col] = cur.lse[y] == -INFINITY ? 0.f : -cur.lse[y] * kL2E;
+          if (TEMP) col_temp[c][col] = cur.temp[y];
+          col_span[c][col] = make_int2(cur.span[y].x, cur.span[y].y - cur.span[y].x);
+          if (p.bounds) col_extra[c][col] = cur.span[y].z;
+        }
+        if (c0 == 0) col_masked[c] = !(kt >= cur.full.x && kt < cur.full.y);
+        mbar_arrive(bar_s + 8 * c);
+        ++step;
+        cur = nxt;
+        nxt = far;
+        have = more;
+        more = later;
+      }
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const bool leader = elect_one_sync();
