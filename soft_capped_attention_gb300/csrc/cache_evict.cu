@@ -13,8 +13,11 @@
 // that move): a cluster of up to 8 CTAs takes a row, each CTA a run of slots whose
 // keys it reads once and keeps in shared memory.  Three histogram passes (11, 11
 // and 10 bits) find the threshold, each CTA adding up the cluster's histograms by
-// distributed shared memory; three more passes over the keys count and place.
-// The copies are a kernel of their own, over all SMs.
+// distributed shared memory (four copies of a CTA's first one, since weights share
+// few leading digits and equal bins serialise the atomics); three more passes over
+// the keys count and list the slots.  What follows from the lists (the rows' pages,
+// the copies, the moved tokens' weights and positions) is the second kernel's, over
+// all SMs.
 #include <cooperative_groups.h>
 
 #include "cache_internal.h"
@@ -48,8 +51,9 @@ struct RowKeys {
   }
 };
 
+constexpr int kCopies = 4;  // of the first digit's histogram
 struct Shared {
-  int hist[3][kBins];
+  int hist[kCopies + 2][kBins];  // pass 0 (copies), 1, 2
   int warp_sum[3][kSelWarps];
   int totals[3];              // of this CTA: equal keys, movers, freed slots
   uint32_t digit;
@@ -94,7 +98,7 @@ select_kernel(CacheParams p, int parts) {
   const int rank = blockIdx.x % parts, row = blockIdx.x / parts;
   const int b = row / p.Hkv, g = row % p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < 3 * kBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
+  for (int i = threadIdx.x; i < (kCopies + 2) * kBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
   pdl_trigger();
   pdl_wait();
   int n = p.lens[b];
@@ -131,7 +135,14 @@ select_kernel(CacheParams p, int parts) {
   for (int j = c0 + threadIdx.x; j < c1; j += kSelThreads) {
     const uint32_t k = keys.at(j);
     if (cached) s_keys[j - c0] = k;
-    atomicAdd(&s.hist[0][k >> 21], 1);
+    atomicAdd(&s.hist[threadIdx.x % kCopies][k >> 21], 1);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kSelThreads) {
+    int sum = 0;
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) sum += s.hist[c][i];
+    s.hist[0][i] = sum;
   }
   auto key = [&](int j) { return cached ? s_keys[j - c0] : keys.at(j); };
   // The budget-th largest key: its digits from the top; `left` is its rank among
@@ -141,12 +152,13 @@ select_kernel(CacheParams p, int parts) {
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    int* hist = s.hist[pass == 0 ? 0 : kCopies - 1 + pass];
     const int bins = pass == 2 ? 1024 : kBins;
     if (pass > 0) {
       const uint32_t mask = pass == 1 ? 0xFFFFFFFFu << 21 : 0xFFFFFFFFu << 10;
       for (int j = c0 + threadIdx.x; j < c1; j += kSelThreads) {
         const uint32_t k = key(j);
-        if ((k & mask) == prefix) atomicAdd(&s.hist[pass][(k >> shift) & (bins - 1)], 1);
+        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
       }
     }
     cluster.sync();  // the cluster's histograms of this pass are whole
@@ -155,7 +167,7 @@ select_kernel(CacheParams p, int parts) {
     const int top = bins - 1 - 2 * (int)threadIdx.x;
     if (top > 0) {
       for (int x = 0; x < parts; ++x) {
-        const int* h = cluster.map_shared_rank(&s.hist[pass][0], x);
+        const int* h = cluster.map_shared_rank(hist, x);
         c[0] += h[top];
         c[1] += h[top - 1];
       }
@@ -179,8 +191,9 @@ select_kernel(CacheParams p, int parts) {
   const uint32_t below = (1u << lane) - 1u;
   int equal = 0;
   for (int j = j0; j < j1; j += 32) equal += __popc(__ballot_sync(0xFFFFFFFFu, j + lane < j1 && key(j + lane) == prefix));
-  // This warp's start in the cluster's order of one count a warp; *total the cluster's.
-  auto place = [&](int mine, int which, int* total) {
+  // This warp's start in the cluster's order of one count a warp, after share()
+  // has left it and the cluster has met; *total the cluster's.
+  auto share = [&](int mine, int which) {
     if (lane == 0) s.warp_sum[which][warp] = mine;
     __syncthreads();
     const int x = s.warp_sum[which][lane];
@@ -191,19 +204,22 @@ select_kernel(CacheParams p, int parts) {
       if (lane >= d) up += y;
     }
     if (threadIdx.x == 31) s.totals[which] = up;
-    const int start = __shfl_sync(0xFFFFFFFFu, up - x, warp);
-    cluster.sync();
-    int before = 0, all = 0;
+    return __shfl_sync(0xFFFFFFFFu, up - x, warp);
+  };
+  auto before = [&](int which, int* total) {
+    int sum = 0, all = 0;
     for (int c = 0; c < parts; ++c) {
       const int v = *cluster.map_shared_rank(&s.totals[which], c);
-      if (c < rank) before += v;
+      if (c < rank) sum += v;
       all += v;
     }
     *total = all;
-    return before + start;
+    return sum;
   };
   int total;
-  const int eq0 = place(equal, 0, &total);
+  int eq0 = share(equal, 0);
+  cluster.sync();
+  eq0 += before(0, &total);
   // kept: above the threshold, or among the first `left` equal ones
   auto kept_of = [&](int j, int& seen) {
     const uint32_t k = j < j1 ? key(j) : 0u;
@@ -220,72 +236,76 @@ select_kernel(CacheParams p, int parts) {
     holes += __popc(__ballot_sync(0xFFFFFFFFu, in && !kept && j + lane < p.budget));
   }
   int n_moves, n_holes;
-  int mover = place(movers, 1, &n_moves);
-  int hole = place(holes, 2, &n_holes);
-  if (j1 > p.budget && movers > 0) {
-    seen = eq0;
-    for (int j = j0; j < j1; j += 32) {
-      const bool moves_it = kept_of(j + lane, seen) && j + lane >= p.budget;
-      const uint32_t who = __ballot_sync(0xFFFFFFFFu, moves_it);
-      if (moves_it) moves[mover + __popc(who & below)].y = j + lane;
-      mover += __popc(who);
-    }
-  }
-  cluster.sync();  // the movers' list is whole; nobody reads this CTA's shared memory any more
+  int mover = share(movers, 1), hole = share(holes, 2);
+  cluster.sync();
+  mover += before(1, &n_moves);
+  hole += before(2, &n_holes);
   seen = eq0;
-  for (int j = j0; j < min(j1, p.budget); j += 32) {
+  for (int j = j0; j < j1; j += 32) {
     const int x = j + lane;
-    const bool kept = kept_of(x, seen), freed = x < j1 && x < p.budget && !kept;
-    const uint32_t who = __ballot_sync(0xFFFFFFFFu, freed);
-    if (freed) {
-      const int i = hole + __popc(who & below), from = __ldcg(&moves[i].y);
-      src[x] = from;
-      p.weights_out[base + x] = keys.w[from];
-      if (p.pos_out) p.pos_out[base + x] = keys.pos[from];
-      moves[i] = make_int2(cache_row(p, b, g, x), cache_row(p, b, g, from));  // as rows of the cache
-    } else if (x < j1 && x < p.budget) {
+    const bool kept = kept_of(x, seen);
+    const bool moves_it = kept && x >= p.budget, freed = x < j1 && !kept && x < p.budget;
+    const uint32_t who_moves = __ballot_sync(0xFFFFFFFFu, moves_it), who_goes = __ballot_sync(0xFFFFFFFFu, freed);
+    if (moves_it) moves[mover + __popc(who_moves & below)].y = x;
+    if (freed) moves[hole + __popc(who_goes & below)].x = x;
+    if (kept && x < p.budget) {
       src[x] = x;
       if (p.weights_out != p.weights) p.weights_out[base + x] = keys.w[x];
       if (p.pos_out && p.pos_out != p.pos) p.pos_out[base + x] = keys.pos[x];
     }
-    hole += __popc(who);
+    mover += __popc(who_moves);
+    hole += __popc(who_goes);
   }
   if (rank == 0 && threadIdx.x == 0) p.counts[row] = make_int2(n_moves, p.budget);
+  cluster.sync();  // no CTA leaves while its counts may be read
 }
 
-// Copies the rows that move: a group of vph threads a row, K and V together, two
-// rows in flight a thread.
+// Carries out the moves: a group of vph threads a row, K and V together, two rows in
+// flight a thread; the group's first thread takes the token's weight and position
+// along.  (Moved tokens come from behind the budget and go below it, so none of
+// this reads what another writes, in place too.)
 constexpr int kMoveThreads = 256;
 __global__ void __launch_bounds__(kMoveThreads)
 move_kernel(CacheParams p, int vph_shift) {
   pdl_trigger();
   pdl_wait();
-  const int row = blockIdx.x, b = row / p.Hkv;
+  const int row = blockIdx.x, b = row / p.Hkv, g = row - b * p.Hkv;
   const int2 c = p.counts[row];
-  if (row == b * p.Hkv && blockIdx.y == 0 && threadIdx.x == 0) p.lens_out[b] = c.y;
-  const int2* moves = reinterpret_cast<const int2*>(p.moves + (size_t)row * p.max_len);
+  if (g == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.lens_out[b] = c.y;
+  const size_t base = (size_t)row * p.max_len;
+  const int2* moves = reinterpret_cast<const int2*>(p.moves + base);
+  int32_t* src = p.src + (size_t)row * p.budget;
   const int per = kMoveThreads >> vph_shift;
   const int at = threadIdx.x & ((1 << vph_shift) - 1);
   uint4* k = static_cast<uint4*>(p.k);
   uint4* v = static_cast<uint4*>(p.v);
   const int stride = gridDim.y * per;
   for (int i = blockIdx.y * per + (threadIdx.x >> vph_shift); i < c.x; i += 2 * stride) {
-    int2 m[2];
+    int2 m[2], r[2];
     uint4 a[2], d[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) m[u] = i + u * stride < c.x ? moves[i + u * stride] : make_int2(-1, -1);
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      if (m[u].x >= 0 && m[u].y >= 0) {
-        a[u] = __ldcs(k + ((size_t)m[u].y << vph_shift) + at);
-        d[u] = __ldcs(v + ((size_t)m[u].y << vph_shift) + at);
-      }
+      r[u] = m[u].x >= 0 ? make_int2(cache_row(p, b, g, m[u].x), cache_row(p, b, g, m[u].y)) : make_int2(-1, -1);
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      if (m[u].x >= 0 && m[u].y >= 0) {
-        k[((size_t)m[u].x << vph_shift) + at] = a[u];
-        v[((size_t)m[u].x << vph_shift) + at] = d[u];
+      if (r[u].x >= 0 && r[u].y >= 0) {
+        a[u] = __ldcs(k + ((size_t)r[u].y << vph_shift) + at);
+        d[u] = __ldcs(v + ((size_t)r[u].y << vph_shift) + at);
       }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (at == 0 && m[u].x >= 0) {
+        src[m[u].x] = m[u].y;
+        p.weights_out[base + m[u].x] = p.weights[base + m[u].y];
+        if (p.pos_out) p.pos_out[base + m[u].x] = p.pos[base + m[u].y];
+      }
+      if (r[u].x >= 0 && r[u].y >= 0) {
+        k[((size_t)r[u].x << vph_shift) + at] = a[u];
+        v[((size_t)r[u].x << vph_shift) + at] = d[u];
+      }
+    }
   }
 }
 
