@@ -32,7 +32,7 @@ capattn_status check_config(const capattn_cache_config* c) {
   if ((int64_t)c->max_pages * c->page_size > (1ll << 30)) return CAPATTN_ERR_UNSUPPORTED;
   if ((int64_t)c->num_pages * c->Hkv * c->page_size > (1ll << 31) - 1) return CAPATTN_ERR_UNSUPPORTED;
   // units of work of a decode (64-key tiles) and (sequence, head) rows are 32-bit too
-  if ((int64_t)c->B * c->Hq * (max_len_of(*c) / 32 + 2) > (1ll << 31) - 1) return CAPATTN_ERR_UNSUPPORTED;
+  if ((int64_t)c->B * c->Hq * (max_len_of(*c) / 32 + 4) > (1ll << 31) - 1) return CAPATTN_ERR_UNSUPPORTED;
   return CAPATTN_OK;
 }
 

@@ -9,16 +9,17 @@
 // 16 keys of the tile each, with a running (m, l, O) of their own that meets the
 // others' only at a piece's end.
 //
-// Per warp and 16 keys, on mma.m16n8k16 (the rows are the group's query heads,
-// padded to 16: there is one query, so a tcgen05 tile of 128 rows would be
-// empty to 7/8 or more; at 24 bytes a clock and SM the mma pipe is nearly idle
-// either way):
-//   S = Q K^T    Q's fragments stay in registers, K's come by ldmatrix
+// Per warp and 16 keys, on mma.m16n8k16 (there is one query, so the heads of a
+// group are the only other dimension: 8 columns a tile, two tiles for groups of 9
+// to 16.  A tcgen05 tile of 128 rows would be 7/8 empty with heads as rows, and
+// with keys as rows P would have to go through shared memory; at 24 bytes a clock
+// and SM the mma pipe keeps up):
+//   S^T = K Q^T  keys are the rows: K by ldmatrix, Q's fragments stay in registers
 //   t = temp cap(sm_scale S), P = e^(t - m)
-//   O += P V     P's accumulators are the A fragment as they stand; V's by
-//                ldmatrix.trans.  P goes in as two bf16 halves (P = hi + lo, 2^-17
-//                of it lost), since the tensor pipe has the room: rounding P to
-//                one bf16 would add half of what rounding o to bf16 does.
+//   O^T += V^T P^T  V by ldmatrix.trans, P^T by transposing its accumulators
+//                8 x 8 (movmatrix).  P goes in as two bf16 halves (P = hi + lo,
+//                2^-17 of it lost): rounding P to one bf16 would add half of what
+//                rounding o to bf16 does.
 // The reference m moves only when the maximum outgrows it by kSlack (P stays
 // below e^kSlack), which saves the rescaling of O on nearly every step.
 #include <cuda_bf16.h>
@@ -75,15 +76,20 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
       : "memory");
 }
+// Transposes an 8 x 8 matrix of bf16, a fragment register a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 // Two floats as bf16 pairs hi + lo.
 __device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16x2(x, y);
   lo = pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
 }
 
-// ROWS: 1 when the group has at most 8 query heads (the upper 8 rows of the
-// tensor-core tile are then empty), else 2.
-template <int D, int METHOD, int ROWS>
+// NT: tiles of 8 query heads, 1 for groups of at most 8, else 2.
+template <int D, int METHOD, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
 decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const CacheParams p) {
   using G = Geo<D>;
@@ -178,9 +184,11 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   const int tid = threadIdx.x;
   const int gq = lane >> 2, tq = lane & 3;      // fragment row and column group
   const uint32_t sw = lane & 7;
-  // this lane's row addresses in a stage's K and V slabs
-  const uint32_t k_row = (uint32_t)(16 * warp + (lane & 7) + ((lane >> 4) << 3)) * 128u, k_add = (lane >> 3) & 1;
-  const uint32_t v_row = (uint32_t)(16 * warp + (lane & 7) + (((lane >> 3) & 1) << 3)) * 128u, v_add = lane >> 4;
+  // this lane's row addresses in a stage's K and V slabs: matrices (keys 0-7, d
+  // 0-7), (keys 8-15, d 0-7), (keys 0-7, d 8-15), (keys 8-15, d 8-15) of K, and with
+  // the middle two exchanged of V
+  const uint32_t k_row = (uint32_t)(16 * warp + (lane & 7) + (((lane >> 3) & 1) << 3)) * 128u, k_add = lane >> 4;
+  const uint32_t v_row = (uint32_t)(16 * warp + (lane & 7) + ((lane >> 4) << 3)) * 128u, v_add = (lane >> 3) & 1;
   bool ok = true;
   while (it.next(p, &b, &vh, &tile, &sp)) {
     const HeadGroup hg = head_group(p, vh);
@@ -188,30 +196,35 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     const bool by_pos = p.pos && p.window_len > 0;
     const int32_t* pos = p.pos + ((size_t)b * p.Hkv + hg.g) * p.max_len;
     const int oldest = by_pos ? p.qpos[b] - p.window_len : 0;
-    uint32_t q[D / 16][4];
+    uint32_t q[NT][D / 16][2];
     ok = ok && mbar_wait_warp(q_full, piece & 1, p.status, &abort_flag);
     ++piece;
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = gq + 8 * (e & 1);
-        q[ks][e] = 0u;
-        if ((ROWS == 2 || (e & 1) == 0) && r < hg.count)
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(q[ks][e]) : "r"(s_q + r * D * 2 + 32 * ks + 16 * (e >> 1) + 4 * tq) : "memory");
-      }
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          q[t][ks][e] = 0u;
+          if (gq + 8 * t < hg.count)
+            asm volatile("ld.shared.b32 %0, [%1];"
+                         : "=r"(q[t][ks][e])
+                         : "r"(s_q + (gq + 8 * t) * D * 2 + 32 * ks + 16 * e + 4 * tq)
+                         : "memory");
+        }
     __syncwarp();
     if (lane == 0) mbar_arrive(q_empty);
-    float m[ROWS], l[ROWS], o[D / 8][4];
+    // heads of this lane: 8 t + 2 tq + e; keys: 16 warp + gq + 8 k
+    float m[NT][2], l[NT][2], o[NT][D / 16][4];
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      m[r] = -INFINITY;
-      l[r] = 0.f;
+    for (int t = 0; t < NT; ++t) {
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][x][e] = 0.f;
     }
-#pragma unroll
-    for (int x = 0; x < D / 8; ++x)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[x][e] = 0.f;
 
     for (int i = 0; i < it.n; ++i, ++step) {
       const uint32_t s = step % G::STAGES, use = step / G::STAGES;
@@ -221,99 +234,100 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
       const int j0 = (tile + i) * TK + 16 * warp;
       if (j0 < sp.len && j0 + 16 > sp.first) {
         const uint32_t kb = base + s * G::STAGE + k_row, vb = base + s * G::STAGE + G::HALF + v_row;
-        float c[2][4] = {};
+        float c[NT][4] = {};
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           uint32_t kf[4];
           ldsm4(kb + (ks >> 2) * G::SLAB + (((uint32_t)(2 * (ks & 3)) + k_add) ^ sw) * 16u, kf);
-          mma16816(c[0], q[ks], kf[0], kf[1]);
-          mma16816(c[1], q[ks], kf[2], kf[3]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma16816(c[t], kf, q[t][ks][0], q[t][ks][1]);
         }
-        // keys of this lane: j0 + 8 n + 2 tq + e
+        // live keys: of the scores this lane's j0 + gq + 8 k, of V's fragments the
+        // pairs j0 + 8 k + 2 tq
         const bool all = !by_pos && j0 >= sp.first && j0 + 16 <= sp.len;
-        bool live[2][2] = {{true, true}, {true, true}};
+        bool live[2] = {true, true};
+        uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
         if (!all) {
+          auto is_live = [&](int j) { return j >= sp.first && j < sp.len && (!by_pos || pos[j] > oldest); };
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = j0 + 8 * n + 2 * tq + e;
-              live[n][e] = j >= sp.first && j < sp.len;
-              if (by_pos && live[n][e]) live[n][e] = pos[j] > oldest;
-            }
+          for (int k = 0; k < 2; ++k) {
+            live[k] = is_live(j0 + gq + 8 * k);
+            const int j = j0 + 8 * k + 2 * tq;
+            keep[k] = (is_live(j) ? 0xFFFFu : 0u) | (is_live(j + 1) ? 0xFFFF0000u : 0u);
+          }
         }
-        uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
         bool grow = false, poly = false;
         if constexpr (has_poly(METHOD)) {
           float am = 0.f;
 #pragma unroll
-          for (int r = 0; r < ROWS; ++r)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int n = 0; n < 2; ++n) am = fmax3_abs(am, c[n][2 * r], c[n][2 * r + 1]);
+            for (int k = 0; k < 2; ++k) am = fmax3_abs(am, c[t][2 * k], c[t][2 * k + 1]);
           poly = __all_sync(0xFFFFFFFFu, am <= p.cap.xmax && p.cap.xmax > 0.f);
         }
-        float mx[ROWS];
+        float mx[NT][2];
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          float top = -INFINITY;
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            float t[2];
+          for (int k = 0; k < 2; ++k) {
+            float x[2];
             if (has_poly(METHOD) && poly) {
-              f2_split(poly_cap2<METHOD>(f2(c[n][2 * r], c[n][2 * r + 1]), p.cap), t[0], t[1]);
+              f2_split(poly_cap2<METHOD>(f2(c[t][2 * k], c[t][2 * k + 1]), p.cap), x[0], x[1]);
             } else {
-              t[0] = any_cap<METHOD>(c[n][2 * r], p.cap);
-              t[1] = any_cap<METHOD>(c[n][2 * r + 1], p.cap);
+              x[0] = any_cap<METHOD>(c[t][2 * k], p.cap);
+              x[1] = any_cap<METHOD>(c[t][2 * k + 1], p.cap);
             }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) c[t][2 * k + e] = live[k] ? x[e] * temp : -INFINITY;
+          }
+          if (p.scores) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float x = live[n][e] ? t[e] * temp : -INFINITY;
-              c[n][2 * r + e] = x;
-              top = fmaxf(top, x);
-            }
-          }
-          if (p.scores && gq + 8 * r < hg.count) {
-            float* sc = p.scores + ((size_t)b * p.Hq + hg.h0 + gq + 8 * r) * p.max_len;
+              const int h = 8 * t + 2 * tq + e;
+              float* sc = p.scores + ((size_t)b * p.Hq + hg.h0 + h) * p.max_len + j0 + gq;
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const int j = j0 + 8 * n + 2 * tq;
-              if (j < sp.len) *reinterpret_cast<float2*>(sc + j) = make_float2(c[n][2 * r], c[n][2 * r + 1]);
+              for (int k = 0; k < 2; ++k)
+                if (h < hg.count && j0 + gq + 8 * k < sp.len) sc[8 * k] = c[t][2 * k + e];
             }
           }
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          mx[r] = top;
-          grow = grow || top > m[r] + kSlack;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(c[t][e], c[t][2 + e]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+            mx[t][e] = top;
+            grow = grow || top > m[t][e] + kSlack;
+          }
         }
         if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
-          for (int r = 0; r < ROWS; ++r) {
-            const float top = fmaxf(m[r], mx[r]);
-            const float scale = top == -INFINITY ? 1.f : __expf(m[r] - top);
-            m[r] = top;
-            l[r] *= scale;
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int x = 0; x < D / 8; ++x) {
-              o[x][2 * r] *= scale;
-              o[x][2 * r + 1] *= scale;
+            for (int e = 0; e < 2; ++e) {
+              const float top = fmaxf(m[t][e], mx[t][e]);
+              const float scale = top == -INFINITY ? 1.f : __expf(m[t][e] - top);
+              m[t][e] = top;
+              l[t][e] *= scale;
+#pragma unroll
+              for (int x = 0; x < D / 16; ++x) {
+                o[t][x][e] *= scale;
+                o[t][x][2 + e] *= scale;
+              }
             }
-          }
         }
+        uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          const float ref = m[r] == -INFINITY ? 0.f : m[r];
+        for (int t = 0; t < NT; ++t) {
+          const float r0 = m[t][0] == -INFINITY ? 0.f : m[t][0], r1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float p0 = __expf(c[n][2 * r] - ref), p1 = __expf(c[n][2 * r + 1] - ref);
-            l[r] += p0 + p1;
-            split_bf16(p0, p1, hi[2 * n + r], lo[2 * n + r]);
+          for (int k = 0; k < 2; ++k) {
+            const float p0 = __expf(c[t][2 * k] - r0), p1 = __expf(c[t][2 * k + 1] - r1);
+            l[t][0] += p0;
+            l[t][1] += p1;
+            split_bf16(p0, p1, hi[t][k], lo[t][k]);
+            hi[t][k] = transpose8(hi[t][k]);
+            lo[t][k] = transpose8(lo[t][k]);
           }
-        }
-        uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-        if (!all) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-            keep[n] = (live[n][0] ? 0xFFFFu : 0u) | (live[n][1] ? 0xFFFF0000u : 0u);
         }
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
@@ -321,14 +335,15 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
           ldsm4_t(vb + (x >> 2) * G::SLAB + (((uint32_t)(2 * (x & 3)) + v_add) ^ sw) * 16u, vf);
           if (!all) {  // whatever a dead slot holds, NaN too, stays out
             vf[0] &= keep[0];
-            vf[1] &= keep[1];
-            vf[2] &= keep[0];
+            vf[1] &= keep[0];
+            vf[2] &= keep[1];
             vf[3] &= keep[1];
           }
-          mma16816(o[2 * x], hi, vf[0], vf[1]);
-          mma16816(o[2 * x + 1], hi, vf[2], vf[3]);
-          mma16816(o[2 * x], lo, vf[0], vf[1]);
-          mma16816(o[2 * x + 1], lo, vf[2], vf[3]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma16816(o[t][x], vf, hi[t][0], hi[t][1]);
+            mma16816(o[t][x], vf, lo[t][0], lo[t][1]);
+          }
         }
       }
       __syncwarp();
@@ -336,34 +351,41 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     }
     // ---------------------------------------------------------- end of a piece
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
-      if (tq == 0) {
-        s_m[warp][gq + 8 * r] = m[r];
-        s_l[warp][gq + 8 * r] = l[r];
-      }
-    }
-    named_bar_sync(1, kConsumers * 32);
-    float scale[ROWS];
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const int h = gq + 8 * r;
-      float top = fmaxf(fmaxf(s_m[0][h], s_m[1][h]), fmaxf(s_m[2][h], s_m[3][h]));
-      scale[r] = m[r] == -INFINITY ? 0.f : __expf(m[r] - top);
-      if (m[r] == -INFINITY && l[r] != 0.f) scale[r] = 1.f;  // nothing but NaN scores: they come through
-    }
-    for (int g0 = 0; g0 < hg.count; g0 += 4) {
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        const int e = gq + 8 * r - g0;
-        if (e >= 0 && e < 4) {
-#pragma unroll
-          for (int x = 0; x < D / 8; ++x)
-            *reinterpret_cast<float2*>(&merge[(warp * 4 + e) * D + 8 * x + 2 * tq]) =
-                make_float2(o[x][2 * r] * scale[r], o[x][2 * r + 1] * scale[r]);
+        for (int x = 4; x < 32; x <<= 1) l[t][e] += __shfl_xor_sync(0xFFFFFFFFu, l[t][e], x);
+        if (gq == 0) {
+          s_m[warp][8 * t + 2 * tq + e] = m[t][e];
+          s_l[warp][8 * t + 2 * tq + e] = l[t][e];
         }
       }
+    named_bar_sync(1, kConsumers * 32);
+    float scale[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = 8 * t + 2 * tq + e;
+        const float top = fmaxf(fmaxf(s_m[0][h], s_m[1][h]), fmaxf(s_m[2][h], s_m[3][h]));
+        scale[t][e] = m[t][e] == -INFINITY ? 0.f : __expf(m[t][e] - top);
+        if (m[t][e] == -INFINITY && l[t][e] != 0.f) scale[t][e] = 1.f;  // nothing but NaN scores: they come through
+      }
+    for (int g0 = 0; g0 < hg.count; g0 += 4) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int h = 8 * t + 2 * tq + e - g0;
+          if (h >= 0 && h < 4) {
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+              merge[(warp * 4 + h) * D + 16 * x + gq] = o[t][x][e] * scale[t][e];
+              merge[(warp * 4 + h) * D + 16 * x + gq + 8] = o[t][x][2 + e] * scale[t][e];
+            }
+          }
+        }
       named_bar_sync(1, kConsumers * 32);
       for (int x = tid; x < min(4, hg.count - g0) * D; x += kConsumers * 32) {
         const int e = x / D, d = x % D, h = g0 + e;
@@ -406,9 +428,9 @@ cudaError_t make_rows_map(CUtensorMap* map, const void* base, const CacheParams&
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, int METHOD, int ROWS>
+template <int D, int METHOD, int NT>
 cudaError_t run_tc(const CacheParams& p, cudaStream_t s) {
-  auto* k = decode_tc_kernel<D, METHOD, ROWS>;
+  auto* k = decode_tc_kernel<D, METHOD, NT>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), Geo<D>::SMEM, done);
   CUtensorMap mk, mv;

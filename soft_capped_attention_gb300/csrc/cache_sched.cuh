@@ -3,7 +3,10 @@
 // The live slots of sequence b are cut into tiles of TK keys; a unit of work is
 // one tile of one (sequence, group of query heads).  Units are numbered
 // sequence by sequence, group by group, tile by tile, and CTA c of n takes units
-// [U c / n, U (c + 1) / n): equal shares whatever the lengths.  A CTA's part of one
+// [U c / n, U (c + 1) / n): equal shares whatever the lengths.  A (sequence, group)
+// counts kGroupCost units more than it has tiles (its first ones), about what its
+// end costs (merging the warps, writing, joining): without them the CTAs that get
+// many short sequences finish last.  A CTA's part of one
 // (sequence, group) is a piece; a piece that is not the whole leaves (m, l, O) in
 // the CTA's slot 2c (the piece at the start of its range) or 2c + 1 (the one at
 // its end; pieces between the two are whole), and the join adds the pieces up in
@@ -19,9 +22,12 @@
 
 namespace capattn {
 
+constexpr int kGroupCost = 2;
+
 struct SeqSpan {
   int32_t first, len;    // live slots [first, len) (before the test of pos)
-  int32_t tile0, tiles;  // tiles that hold them (one dead tile when there are none)
+  int32_t tile0, tiles;  // tiles that hold them
+  int32_t units;         // tiles + kGroupCost
 };
 
 // The span of a sequence of length len as read.
@@ -35,7 +41,8 @@ __device__ __forceinline__ SeqSpan span_of(const CacheParams& p, int len) {
   }
   s.first = p.window_len > 0 && !p.pos ? max(0, s.len - p.window_len) : 0;
   s.tile0 = s.first / TK;
-  s.tiles = max(1, (s.len + TK - 1) / TK - s.tile0);
+  s.tiles = (s.len + TK - 1) / TK - s.tile0;
+  s.units = s.tiles + kGroupCost;
   return s;
 }
 template <int TK>
@@ -56,10 +63,10 @@ template <int TK>
 struct PieceIter {
   uint32_t units, ctas;           // all units, the CTAs that share them
   uint32_t u, end, begin;         // next unit, this CTA's range
-  int b, vh, t0;                  // the next piece: sequence, group, first tile of the group
+  int b, vh, t0;                  // the next piece: sequence, group, first unit of the group
   int len;                        // lens[b], read ahead of its use
   // of the piece that next() gave
-  int n;                   // tiles
+  int n;                   // tiles (maybe none)
   bool whole;
   int slot;                // its partial slot, when not whole
   uint32_t s0, s1;         // units [s0, s1) of its (sequence, group)
@@ -67,9 +74,9 @@ struct PieceIter {
   __device__ PieceIter(const CacheParams& p, int lane) {
     // the first 32 sequences' tiles stay in a register: one read of lens decides
     // a small batch
-    const int n0 = lane < p.B ? seq_span<TK>(p, lane).tiles : 0;
+    const int n0 = lane < p.B ? seq_span<TK>(p, lane).units : 0;
     int all = n0;
-    for (int x = lane + 32; x < p.B; x += 32) all += seq_span<TK>(p, x).tiles;
+    for (int x = lane + 32; x < p.B; x += 32) all += seq_span<TK>(p, x).units;
     units = (uint32_t)__reduce_add_sync(0xFFFFFFFFu, all) * (uint32_t)p.VH;
     ctas = min((uint32_t)p.ctas, max(1u, units / (uint32_t)p.min_tiles));
     begin = u = begin_of(blockIdx.x);
@@ -79,7 +86,7 @@ struct PieceIter {
     const int want = (int)(u / (uint32_t)p.VH);  // the tile, counted over the sequences
     int before = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int x = b0 == 0 ? n0 : b0 + lane < p.B ? seq_span<TK>(p, b0 + lane).tiles : 0;
+      const int x = b0 == 0 ? n0 : b0 + lane < p.B ? seq_span<TK>(p, b0 + lane).units : 0;
       const int up = lane_scan(x, lane);
       const uint32_t hit = __ballot_sync(0xFFFFFFFFu, want < before + up);
       if (hit) {
@@ -93,8 +100,8 @@ struct PieceIter {
     len = p.lens[b];
     const SeqSpan sp = span_of<TK>(p, len);
     const uint32_t in = u - (uint32_t)before * (uint32_t)p.VH;
-    vh = (int)(in / (uint32_t)sp.tiles);
-    t0 = (int)(in % (uint32_t)sp.tiles);
+    vh = (int)(in / (uint32_t)sp.units);
+    t0 = (int)(in % (uint32_t)sp.units);
   }
   // First unit of CTA c's range, and the CTA that holds a unit: the largest c with
   // floor(units c / ctas) <= x.
@@ -108,16 +115,18 @@ struct PieceIter {
   __device__ bool next(const CacheParams& p, int* b_out, int* vh_out, int* tile_out, SeqSpan* sp_out) {
     if (u >= end) return false;
     const SeqSpan sp = span_of<TK>(p, len);
-    n = (int)min((uint32_t)(sp.tiles - t0), end - u);
-    whole = t0 == 0 && n == sp.tiles;
+    const int take = (int)min((uint32_t)(sp.units - t0), end - u);
+    const int first = max(0, t0 - kGroupCost);
+    n = max(0, t0 + take - kGroupCost) - first;
+    whole = t0 == 0 && take == sp.units;
     slot = 2 * (int)blockIdx.x + (u == begin ? 0 : 1);
     s0 = u - (uint32_t)t0;
-    s1 = s0 + (uint32_t)sp.tiles;
+    s1 = s0 + (uint32_t)sp.units;
     *b_out = b;
     *vh_out = vh;
-    *tile_out = sp.tile0 + t0;
+    *tile_out = sp.tile0 + first;
     *sp_out = sp;
-    u += (uint32_t)n;
+    u += (uint32_t)take;
     if (u < end) {
       t0 = 0;
       if (++vh == p.VH) {
@@ -173,9 +182,9 @@ template <typename T, int D, int TK>
 __device__ __forceinline__ void join_pieces(const CacheParams& p, const PieceIter<TK>& it, int b, const HeadGroup& hg,
                                             int tid, int bar, float* buf, float* lbuf, int* flag) {
   const Pieces pc(it);
-  __threadfence();
   named_bar_sync(bar, 128);
   if (tid == 0) {
+    __threadfence();  // after the barrier it covers what all 128 threads wrote
     const uint32_t left = atomicAdd(&p.counters[pc.c0], 1u);
     const bool last = left == (uint32_t)(pc.c1 - pc.c0);
     if (last) p.counters[pc.c0] = 0u;
