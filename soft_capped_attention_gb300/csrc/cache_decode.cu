@@ -200,8 +200,14 @@ decode_simt_kernel(CacheParams p) {
         }
       }
     }
-    if (!it.whole) join_pieces<T, D, TK>(p, it, b, hg, threadIdx.x, 1, &s.join[0][0], s.lsum, &s.flag);
     __syncthreads();
+    if (!it.whole) {
+      const Pieces pc(it);
+      if (threadIdx.x == 0) s.flag = count_piece(p, pc);
+      __syncthreads();
+      if (s.flag) join_pieces<T, D, 4>(p, pc, b, hg, warp, lane, 1, &s.join[0][0], s.lsum);
+      __syncthreads();
+    }
   }
 }
 

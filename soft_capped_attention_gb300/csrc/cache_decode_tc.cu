@@ -6,8 +6,10 @@
 // CTAs an SM, takes equal shares of 64-key tiles (cache_sched.cuh).  In each CTA
 // one warp fills a ring of shared-memory stages by TMA (a tile's pages are boxes
 // of up to 64 rows x 64 columns in the 128-byte swizzle) and four warps compute,
-// 16 keys of the tile each, with a running (m, l, O) of their own that meets the
-// others' only at a piece's end.
+// 16 keys of the tile each, with a running (m, l, O) of their own.  At a piece's end
+// they leave those in shared memory and go on with the next piece; a sixth warp adds
+// them up, writes, counts split pieces in and joins them when it comes last (a
+// CTA's last piece: with the four others, which have nothing else to do).
 //
 // Per warp and 16 keys, on mma.m16n8k16 (there is one query, so the heads of a
 // group are the only other dimension: 8 columns a tile, two tiles for groups of 9
@@ -35,7 +37,7 @@ namespace {
 
 constexpr int TK = 64;                 // keys of a tile
 constexpr int kConsumers = 4;          // warps that compute, 16 keys of a tile each
-constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kThreads = (kConsumers + 2) * 32;  // and the TMA warp and the writing one
 constexpr float kSlack = 8.f;
 
 template <int D>
@@ -94,15 +96,16 @@ __global__ void __launch_bounds__(kThreads, 2)
 decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const CacheParams p) {
   using G = Geo<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * G::STAGES + 2];
+  __shared__ __align__(8) uint64_t bars[2 * G::STAGES + 4];
   __shared__ int abort_flag, join_flag;
-  __shared__ float s_m[kConsumers][16], s_l[kConsumers][16], s_lsum[16];
+  __shared__ float s_m[kConsumers][4], s_l[kConsumers][4], s_lsum[16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   float* merge = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + G::STAGES * G::STAGE);
   const uint32_t s_q = base + G::STAGES * G::STAGE + G::MERGE;
   const uint32_t full = smem_u32(&bars[0]), empty = smem_u32(&bars[G::STAGES]);
   const uint32_t q_full = smem_u32(&bars[2 * G::STAGES]), q_empty = q_full + 8;
+  const uint32_t m_full = q_full + 16, m_empty = q_full + 24;  // the warps' results of four heads
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < G::STAGES; ++s) {
@@ -111,6 +114,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, kConsumers);
+    mbar_init(m_full, kConsumers);
+    mbar_init(m_empty, 1);
     fence_mbar_init();
   }
   pdl_trigger();
@@ -180,8 +185,64 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     return;
   }
 
+  uint32_t round = 0;  // groups of four heads handed over so far
+  if (warp == kConsumers + 1) {
+    // ------------------------------------------------------------ writing warp
+    constexpr int V = D / 32;  // columns of a lane
+    while (it.next(p, &b, &vh, &tile, &sp)) {
+      const HeadGroup hg = head_group(p, vh);
+      for (int g0 = 0; g0 < hg.count; g0 += 4, ++round) {
+        mbar_wait_warp(m_full, round & 1, p.status, &abort_flag);  // (after a timeout: whatever is there)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (g0 + e >= hg.count) continue;
+          float top = -INFINITY, sum = 0.f, y[V];
+#pragma unroll
+          for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, s_m[w][e]);
+#pragma unroll
+          for (int x = 0; x < V; ++x) y[x] = 0.f;
+#pragma unroll
+          for (int w = 0; w < kConsumers; ++w) {
+            const float mw = s_m[w][e], lw = s_l[w][e];
+            // a warp without live keys adds nothing; one with nothing but NaN
+            // scores (no maximum, but a sum) comes through
+            const float f = mw != -INFINITY ? __expf(mw - top) : lw != 0.f ? 1.f : 0.f;
+            sum = fmaf(lw, f, sum);
+#pragma unroll
+            for (int x = 0; x < V; ++x) y[x] = fmaf(merge[(w * 4 + e) * D + lane * V + x], f, y[x]);
+          }
+          if (it.whole) {
+            const size_t row = (size_t)b * p.Hq + hg.h0 + g0 + e;
+#pragma unroll
+            for (int x = 0; x < V; x += 2)
+              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + row * D + lane * V + x) =
+                  pack_bf16x2(sum == 0.f ? 0.f : y[x] / sum, sum == 0.f ? 0.f : y[x + 1] / sum);
+            if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
+          } else {
+            const size_t at = (size_t)it.slot * kDecodeHeads + g0 + e;
+#pragma unroll
+            for (int x = 0; x < V; ++x) p.part_o[at * D + lane * V + x] = y[x];
+            if (lane == 0) p.part_ml[at] = make_float2(top, sum);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(m_empty);
+      }
+      if (it.whole) continue;
+      const Pieces pc(it);
+      const bool last = __shfl_sync(0xFFFFFFFFu, lane == 0 ? (int)count_piece(p, pc) : 0, 0) != 0;
+      if (it.u < it.end) {
+        if (last) join_pieces<__nv_bfloat16, D, 1>(p, pc, b, hg, 0, lane, 0, nullptr, nullptr);
+      } else {  // the CTA's last piece: all warps join
+        if (lane == 0) join_flag = last;
+        __syncwarp();
+        named_bar_sync(1, (kConsumers + 1) * 32);
+      }
+    }
+    return;
+  }
+
   // ---------------------------------------------------------------- consumers
-  const int tid = threadIdx.x;
   const int gq = lane >> 2, tq = lane & 3;      // fragment row and column group
   const uint32_t sw = lane & 7;
   // this lane's row addresses in a stage's K and V slabs: matrices (keys 0-7, d
@@ -353,63 +414,35 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[t][e] += __shfl_xor_sync(0xFFFFFFFFu, l[t][e], x);
-        if (gq == 0) {
-          s_m[warp][8 * t + 2 * tq + e] = m[t][e];
-          s_l[warp][8 * t + 2 * tq + e] = l[t][e];
-        }
-      }
-    named_bar_sync(1, kConsumers * 32);
-    float scale[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int h = 8 * t + 2 * tq + e;
-        const float top = fmaxf(fmaxf(s_m[0][h], s_m[1][h]), fmaxf(s_m[2][h], s_m[3][h]));
-        scale[t][e] = m[t][e] == -INFINITY ? 0.f : __expf(m[t][e] - top);
-        if (m[t][e] == -INFINITY && l[t][e] != 0.f) scale[t][e] = 1.f;  // nothing but NaN scores: they come through
-      }
-    for (int g0 = 0; g0 < hg.count; g0 += 4) {
+    for (int g0 = 0; g0 < hg.count; g0 += 4, ++round) {
+      if (round > 0) ok = mbar_wait_warp(m_empty, (round - 1) & 1, p.status, &abort_flag) && ok;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int h = 8 * t + 2 * tq + e - g0;
           if (h >= 0 && h < 4) {
+            if (gq == 0) {
+              s_m[warp][h] = m[t][e];
+              s_l[warp][h] = l[t][e];
+            }
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
-              merge[(warp * 4 + h) * D + 16 * x + gq] = o[t][x][e] * scale[t][e];
-              merge[(warp * 4 + h) * D + 16 * x + gq + 8] = o[t][x][2 + e] * scale[t][e];
+              merge[(warp * 4 + h) * D + 16 * x + gq] = o[t][x][e];
+              merge[(warp * 4 + h) * D + 16 * x + gq + 8] = o[t][x][2 + e];
             }
           }
         }
-      named_bar_sync(1, kConsumers * 32);
-      for (int x = tid; x < min(4, hg.count - g0) * D; x += kConsumers * 32) {
-        const int e = x / D, d = x % D, h = g0 + e;
-        float top = fmaxf(fmaxf(s_m[0][h], s_m[1][h]), fmaxf(s_m[2][h], s_m[3][h]));
-        float sum = 0.f, y = 0.f;
-#pragma unroll
-        for (int w = 0; w < kConsumers; ++w) {
-          const float mw = s_m[w][h], lw = s_l[w][h];
-          if (lw != 0.f) sum += lw * (mw == -INFINITY ? 1.f : __expf(mw - top));
-          y += merge[(w * 4 + e) * D + d];
-        }
-        if (it.whole) {
-          const size_t row = (size_t)b * p.Hq + hg.h0 + h;
-          static_cast<__nv_bfloat16*>(p.o)[row * D + d] = __float2bfloat16(sum == 0.f ? 0.f : y / sum);
-          if (d == 0) p.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
-        } else {
-          const size_t at = (size_t)it.slot * kDecodeHeads + h;
-          p.part_o[at * D + d] = y;
-          if (d == 0) p.part_ml[at] = make_float2(top, sum);
-        }
-      }
-      named_bar_sync(1, kConsumers * 32);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(m_full);
     }
-    if (!it.whole) join_pieces<__nv_bfloat16, D, TK>(p, it, b, hg, tid, 1, merge, s_lsum, &join_flag);
+    if (!it.whole && it.u >= it.end) {
+      named_bar_sync(1, (kConsumers + 1) * 32);
+      if (join_flag) join_pieces<__nv_bfloat16, D, 4>(p, Pieces(it), b, hg, warp, lane, 2, merge, s_lsum);
+    }
   }
 }
 

@@ -174,29 +174,24 @@ __device__ __forceinline__ int page_of(const CacheParams& p, int b, int slot) {
   return page;
 }
 
-// Leaves a piece's last word and, in the CTA that comes last, joins the pieces of
-// (b, group): called by 128 threads after they wrote their part of the partial
-// results; `bar` is a named barrier of those threads, buf 4 x 4 x D floats,
-// flag one int, both shared.  Warp w adds every fourth piece, four heads at a time.
-template <typename T, int D, int TK>
-__device__ __forceinline__ void join_pieces(const CacheParams& p, const PieceIter<TK>& it, int b, const HeadGroup& hg,
-                                            int tid, int bar, float* buf, float* lbuf, int* flag) {
-  const Pieces pc(it);
-  named_bar_sync(bar, 128);
-  if (tid == 0) {
-    __threadfence();  // after the barrier it covers what all 128 threads wrote
-    const uint32_t left = atomicAdd(&p.counters[pc.c0], 1u);
-    const bool last = left == (uint32_t)(pc.c1 - pc.c0);
-    if (last) p.counters[pc.c0] = 0u;
-    __threadfence();
-    *flag = last;
-  }
-  named_bar_sync(bar, 128);
-  const bool last = *flag != 0;
-  named_bar_sync(bar, 128);
-  if (!last) return;
+// Counts a piece in (one thread, after everything of the piece's partial results
+// has been written by threads that it has met at a barrier): whether it is the
+// last one of its (sequence, group).
+__device__ __forceinline__ bool count_piece(const CacheParams& p, const Pieces& pc) {
+  __threadfence();  // after the barrier it covers what the others wrote
+  const bool last = atomicAdd(&p.counters[pc.c0], 1u) == (uint32_t)(pc.c1 - pc.c0);
+  if (last) p.counters[pc.c0] = 0u;
+  __threadfence();
+  return last;
+}
+
+// Adds the pieces of (b, group) up and writes o and lse, by WARPS warps (4 that meet
+// at named barrier `bar`, with buf 4 x 4 x D floats and lbuf 16, both shared; or 1):
+// warp w takes every WARPS-th piece, four heads and four pieces at a time.
+template <typename T, int D, int WARPS>
+__device__ __forceinline__ void join_pieces(const CacheParams& p, const Pieces& pc, int b, const HeadGroup& hg, int warp,
+                                            int lane, int bar, float* buf, float* lbuf) {
   constexpr int V = D / 32;
-  const int warp = tid >> 5, lane = tid & 31;
   for (int g0 = 0; g0 < hg.count; g0 += 4) {
     const int heads = min(4, hg.count - g0);
     float mx[4], l[4], o[4][V];
@@ -217,8 +212,7 @@ __device__ __forceinline__ void join_pieces(const CacheParams& p, const PieceIte
       for (int x = 16; x > 0; x >>= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], x));
       if (mx[e] == -INFINITY) mx[e] = 0.f;
     }
-    // four pieces of four heads in flight a lane
-    for (int c = pc.c0 + warp; c <= pc.c1; c += 16) {
+    for (int c = pc.c0 + warp; c <= pc.c1; c += 4 * WARPS) {
       float2 ml[4][4];
       float v[4][4][V];
 #pragma unroll
@@ -228,8 +222,8 @@ __device__ __forceinline__ void join_pieces(const CacheParams& p, const PieceIte
           ml[y][e] = make_float2(-INFINITY, 0.f);
 #pragma unroll
           for (int x = 0; x < V; ++x) v[y][e][x] = 0.f;
-          if (c + 4 * y > pc.c1 || e >= heads) continue;
-          const size_t at = (size_t)pc.slot_of(c + 4 * y) * kDecodeHeads + g0 + e;
+          if (c + WARPS * y > pc.c1 || e >= heads) continue;
+          const size_t at = (size_t)pc.slot_of(c + WARPS * y) * kDecodeHeads + g0 + e;
           ml[y][e] = __ldcg(&p.part_ml[at]);
           const float* po = p.part_o + at * D + lane * V;
           if constexpr (V == 4) {
@@ -250,22 +244,34 @@ __device__ __forceinline__ void join_pieces(const CacheParams& p, const PieceIte
           for (int x = 0; x < V; ++x) o[e][x] = fmaf(v[y][e][x], w, o[e][x]);
         }
     }
+    if constexpr (WARPS == 1) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 4; ++e) {
+        if (e >= heads) continue;
+        const size_t row = (size_t)b * p.Hq + hg.h0 + g0 + e;
 #pragma unroll
-      for (int x = 0; x < V; ++x) buf[(warp * 4 + e) * D + lane * V + x] = o[e][x];
-      if (lane == 0) lbuf[warp * 4 + e] = l[e];
+        for (int x = 0; x < V; ++x)
+          static_cast<T*>(p.o)[row * D + lane * V + x] = (T)(l[e] == 0.f ? 0.f : o[e][x] / l[e]);
+        if (lane == 0) p.lse[row] = l[e] == 0.f ? -INFINITY : mx[e] + logf(l[e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int x = 0; x < V; ++x) buf[(warp * 4 + e) * D + lane * V + x] = o[e][x];
+        if (lane == 0) lbuf[warp * 4 + e] = l[e];
+      }
+      named_bar_sync(bar, 128);
+      for (int i = warp * 32 + lane; i < heads * D; i += 128) {
+        const int e = i / D, d = i % D;
+        const float sum = (lbuf[e] + lbuf[4 + e]) + (lbuf[8 + e] + lbuf[12 + e]);
+        const float x = (buf[e * D + d] + buf[(4 + e) * D + d]) + (buf[(8 + e) * D + d] + buf[(12 + e) * D + d]);
+        const size_t row = (size_t)b * p.Hq + hg.h0 + g0 + e;
+        static_cast<T*>(p.o)[row * D + d] = (T)(sum == 0.f ? 0.f : x / sum);
+        if (d == 0) p.lse[row] = sum == 0.f ? -INFINITY : (e == 0 ? mx[0] : e == 1 ? mx[1] : e == 2 ? mx[2] : mx[3]) + logf(sum);
+      }
+      named_bar_sync(bar, 128);
     }
-    named_bar_sync(bar, 128);
-    for (int i = tid; i < heads * D; i += 128) {
-      const int e = i / D, d = i % D;
-      const float sum = (lbuf[e] + lbuf[4 + e]) + (lbuf[8 + e] + lbuf[12 + e]);
-      const float x = (buf[e * D + d] + buf[(4 + e) * D + d]) + (buf[(8 + e) * D + d] + buf[(12 + e) * D + d]);
-      const size_t row = (size_t)b * p.Hq + hg.h0 + g0 + e;
-      static_cast<T*>(p.o)[row * D + d] = (T)(sum == 0.f ? 0.f : x / sum);
-      if (d == 0) p.lse[row] = sum == 0.f ? -INFINITY : (e == 0 ? mx[0] : e == 1 ? mx[1] : e == 2 ? mx[2] : mx[3]) + logf(sum);
-    }
-    named_bar_sync(bar, 128);
   }
 }
 
