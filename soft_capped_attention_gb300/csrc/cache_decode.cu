@@ -46,7 +46,7 @@ struct Smem {
   float scale[kDecodeHeads];
   float m[kDecodeHeads], l[kDecodeHeads];
   float half[kDecodeHeads][64];  // D = 64: outputs of the second half of the threads
-  float join[16][D], lsum[16];
+  float join[16][D], lsum[32];
   int flag;
 };
 

@@ -9,7 +9,7 @@
 // 16 keys of the tile each, with a running (m, l, O) of their own.  At a piece's end
 // they leave those in shared memory and go on with the next piece; a sixth warp adds
 // them up, writes, counts split pieces in and joins them when it comes last (a
-// CTA's last piece: with the four others, which have nothing else to do).
+// CTA's last piece they finish themselves: they have nothing else to do).
 //
 // Per warp and 16 keys, on mma.m16n8k16 (there is one query, so the heads of a
 // group are the only other dimension: 8 columns a tile, two tiles for groups of 9
@@ -98,7 +98,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * G::STAGES + 4];
   __shared__ int abort_flag, join_flag;
-  __shared__ float s_m[kConsumers][4], s_l[kConsumers][4], s_lsum[16];
+  __shared__ float s_m[kConsumers * 4], s_l[kConsumers * 4], s_join[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   float* merge = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + G::STAGES * G::STAGE);
@@ -186,58 +186,43 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   }
 
   uint32_t round = 0;  // groups of four heads handed over so far
+  // Head g0 + e of a piece, from what the four warps left: written, or left as a
+  // partial result.
+  auto finish_head = [&](const HeadGroup& hg, int g0, int e) {
+    constexpr int V = D / 32;
+    float y[V], sum, top;
+    merge_warps<D>(merge, s_m, s_l, e, lane, y, &sum, &top);
+    if (it.whole) {
+      const size_t row = (size_t)b * p.Hq + hg.h0 + g0 + e;
+#pragma unroll
+      for (int x = 0; x < V; x += 2)
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + row * D + lane * V + x) =
+            pack_bf16x2(sum == 0.f ? 0.f : y[x] / sum, sum == 0.f ? 0.f : y[x + 1] / sum);
+      if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
+    } else {
+      const size_t at = (size_t)it.slot * kDecodeHeads + g0 + e;
+#pragma unroll
+      for (int x = 0; x < V; ++x) p.part_o[at * D + lane * V + x] = y[x];
+      if (lane == 0) p.part_ml[at] = make_float2(top, sum);
+    }
+  };
   if (warp == kConsumers + 1) {
     // ------------------------------------------------------------ writing warp
-    constexpr int V = D / 32;  // columns of a lane
     while (it.next(p, &b, &vh, &tile, &sp)) {
+      if (it.u >= it.end) break;  // the last piece is the consumers'
       const HeadGroup hg = head_group(p, vh);
       for (int g0 = 0; g0 < hg.count; g0 += 4, ++round) {
         mbar_wait_warp(m_full, round & 1, p.status, &abort_flag);  // (after a timeout: whatever is there)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (g0 + e >= hg.count) continue;
-          float top = -INFINITY, sum = 0.f, y[V];
-#pragma unroll
-          for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, s_m[w][e]);
-#pragma unroll
-          for (int x = 0; x < V; ++x) y[x] = 0.f;
-#pragma unroll
-          for (int w = 0; w < kConsumers; ++w) {
-            const float mw = s_m[w][e], lw = s_l[w][e];
-            // a warp without live keys adds nothing; one with nothing but NaN
-            // scores (no maximum, but a sum) comes through
-            const float f = mw != -INFINITY ? __expf(mw - top) : lw != 0.f ? 1.f : 0.f;
-            sum = fmaf(lw, f, sum);
-#pragma unroll
-            for (int x = 0; x < V; ++x) y[x] = fmaf(merge[(w * 4 + e) * D + lane * V + x], f, y[x]);
-          }
-          if (it.whole) {
-            const size_t row = (size_t)b * p.Hq + hg.h0 + g0 + e;
-#pragma unroll
-            for (int x = 0; x < V; x += 2)
-              *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + row * D + lane * V + x) =
-                  pack_bf16x2(sum == 0.f ? 0.f : y[x] / sum, sum == 0.f ? 0.f : y[x + 1] / sum);
-            if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
-          } else {
-            const size_t at = (size_t)it.slot * kDecodeHeads + g0 + e;
-#pragma unroll
-            for (int x = 0; x < V; ++x) p.part_o[at * D + lane * V + x] = y[x];
-            if (lane == 0) p.part_ml[at] = make_float2(top, sum);
-          }
-        }
+        for (int e = 0; e < 4; ++e)
+          if (g0 + e < hg.count) finish_head(hg, g0, e);
         __syncwarp();
         if (lane == 0) mbar_arrive(m_empty);
       }
       if (it.whole) continue;
       const Pieces pc(it);
       const bool last = __shfl_sync(0xFFFFFFFFu, lane == 0 ? (int)count_piece(p, pc) : 0, 0) != 0;
-      if (it.u < it.end) {
-        if (last) join_pieces<__nv_bfloat16, D, 1>(p, pc, b, hg, 0, lane, 0, nullptr, nullptr);
-      } else {  // the CTA's last piece: all warps join
-        if (lane == 0) join_flag = last;
-        __syncwarp();
-        named_bar_sync(1, (kConsumers + 1) * 32);
-      }
+      if (last) join_pieces<__nv_bfloat16, D, 1>(p, pc, b, hg, 0, lane, 0, nullptr, nullptr);
     }
     return;
   }
@@ -417,8 +402,12 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[t][e] += __shfl_xor_sync(0xFFFFFFFFu, l[t][e], x);
-    for (int g0 = 0; g0 < hg.count; g0 += 4, ++round) {
-      if (round > 0) ok = mbar_wait_warp(m_empty, (round - 1) & 1, p.status, &abort_flag) && ok;
+    const bool final_piece = it.u >= it.end;
+    for (int g0 = 0; g0 < hg.count; g0 += 4) {
+      // the buffer is free: the writing warp took the last round of it (in the last
+      // piece: all of these warps did, at the barrier below)
+      if (round > 0 && (g0 == 0 || !final_piece))
+        ok = mbar_wait_warp(m_empty, (round - 1) & 1, p.status, &abort_flag) && ok;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -426,8 +415,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
           const int h = 8 * t + 2 * tq + e - g0;
           if (h >= 0 && h < 4) {
             if (gq == 0) {
-              s_m[warp][h] = m[t][e];
-              s_l[warp][h] = l[t][e];
+              s_m[4 * warp + h] = m[t][e];
+              s_l[4 * warp + h] = l[t][e];
             }
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
@@ -436,12 +425,21 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             }
           }
         }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(m_full);
+      if (!final_piece) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(m_full);
+        ++round;
+      } else {
+        named_bar_sync(1, kConsumers * 32);
+        if (g0 + warp < hg.count) finish_head(hg, g0, warp);
+        named_bar_sync(1, kConsumers * 32);
+      }
     }
-    if (!it.whole && it.u >= it.end) {
-      named_bar_sync(1, (kConsumers + 1) * 32);
-      if (join_flag) join_pieces<__nv_bfloat16, D, 4>(p, Pieces(it), b, hg, warp, lane, 2, merge, s_lsum);
+    if (final_piece && !it.whole) {
+      const Pieces pc(it);
+      if (threadIdx.x == 0) join_flag = count_piece(p, pc);
+      named_bar_sync(1, kConsumers * 32);
+      if (join_flag) join_pieces<__nv_bfloat16, D, 4>(p, pc, b, hg, warp, lane, 1, merge, s_join);
     }
   }
 }

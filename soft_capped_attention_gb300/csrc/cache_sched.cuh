@@ -22,7 +22,7 @@
 
 namespace capattn {
 
-constexpr int kGroupCost = 2;
+constexpr int kGroupCost = 1;
 
 struct SeqSpan {
   int32_t first, len;    // live slots [first, len) (before the test of pos)
@@ -174,43 +174,61 @@ __device__ __forceinline__ int page_of(const CacheParams& p, int b, int slot) {
   return page;
 }
 
+// Adds up what four warps left of head e of four: results buf [4][4][D], maxima sm
+// and sums sl [4][4], all shared; a lane takes D / 32 columns.
+template <int D>
+__device__ __forceinline__ void merge_warps(const float* buf, const float* sm, const float* sl, int e, int lane,
+                                            float (&y)[D / 32], float* sum_out, float* top_out) {
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = fmaxf(top, sm[4 * w + e]);
+#pragma unroll
+  for (int x = 0; x < D / 32; ++x) y[x] = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float mw = sm[4 * w + e], lw = sl[4 * w + e];
+    // a warp without live keys adds nothing; one with nothing but NaN scores (no
+    // maximum, but a sum) comes through
+    const float f = mw != -INFINITY ? __expf(mw - top) : lw != 0.f ? 1.f : 0.f;
+    sum = fmaf(lw, f, sum);
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) y[x] = fmaf(buf[(w * 4 + e) * D + lane * (D / 32) + x], f, y[x]);
+  }
+  *sum_out = sum;
+  *top_out = top;
+}
+
 // Counts a piece in (one thread, after everything of the piece's partial results
 // has been written by threads that it has met at a barrier): whether it is the
 // last one of its (sequence, group).
 __device__ __forceinline__ bool count_piece(const CacheParams& p, const Pieces& pc) {
-  __threadfence();  // after the barrier it covers what the others wrote
-  const bool last = atomicAdd(&p.counters[pc.c0], 1u) == (uint32_t)(pc.c1 - pc.c0);
+  // release: with the barrier before it, it covers what the others wrote; acquire:
+  // for those that read the other pieces after the next barrier
+  uint32_t before;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(p.counters + pc.c0) : "memory");
+  const bool last = before == (uint32_t)(pc.c1 - pc.c0);
   if (last) p.counters[pc.c0] = 0u;
-  __threadfence();
   return last;
 }
 
 // Adds the pieces of (b, group) up and writes o and lse, by WARPS warps (4 that meet
-// at named barrier `bar`, with buf 4 x 4 x D floats and lbuf 16, both shared; or 1):
-// warp w takes every WARPS-th piece, four heads and four pieces at a time.
+// at named barrier `bar`, with buf 4 x 4 x D floats and sbuf 32, both shared; or 1):
+// warp w takes every WARPS-th piece, four heads and four pieces in flight at a time,
+// with a running maximum, so that nothing is read twice or waits for a first pass.
 template <typename T, int D, int WARPS>
 __device__ __forceinline__ void join_pieces(const CacheParams& p, const Pieces& pc, int b, const HeadGroup& hg, int warp,
-                                            int lane, int bar, float* buf, float* lbuf) {
+                                            int lane, int bar, float* buf, float* sbuf) {
   constexpr int V = D / 32;
   for (int g0 = 0; g0 < hg.count; g0 += 4) {
     const int heads = min(4, hg.count - g0);
-    float mx[4], l[4], o[4][V];
+    float m[4], l[4], o[4][V];  // m: 0 until there is a maximum
+    bool any[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      mx[e] = -INFINITY;
-      l[e] = 0.f;
+      m[e] = l[e] = 0.f;
+      any[e] = false;
 #pragma unroll
       for (int x = 0; x < V; ++x) o[e][x] = 0.f;
-    }
-    for (int c = pc.c0 + lane; c <= pc.c1; c += 32)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < heads) mx[e] = fmaxf(mx[e], __ldcg(&p.part_ml[(size_t)pc.slot_of(c) * kDecodeHeads + g0 + e]).x);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], x));
-      if (mx[e] == -INFINITY) mx[e] = 0.f;
     }
     for (int c = pc.c0 + warp; c <= pc.c1; c += 4 * WARPS) {
       float2 ml[4][4];
@@ -235,14 +253,25 @@ __device__ __forceinline__ void join_pieces(const CacheParams& p, const Pieces& 
           }
         }
 #pragma unroll
-      for (int y = 0; y < 4; ++y)
+      for (int e = 0; e < 4; ++e) {
+        float top = fmaxf(fmaxf(ml[0][e].x, ml[1][e].x), fmaxf(ml[2][e].x, ml[3][e].x));
+        if (top != -INFINITY) {
+          top = any[e] ? fmaxf(top, m[e]) : top;
+          const float scale = any[e] ? __expf(m[e] - top) : 1.f;  // without a maximum l and o are 0 or NaN
+          l[e] *= scale;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float w = __expf(ml[y][e].x - mx[e]);
+          for (int x = 0; x < V; ++x) o[e][x] *= scale;
+          m[e] = top;
+          any[e] = true;
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float w = __expf(ml[y][e].x - m[e]);
           l[e] = fmaf(ml[y][e].y, w, l[e]);
 #pragma unroll
           for (int x = 0; x < V; ++x) o[e][x] = fmaf(v[y][e][x], w, o[e][x]);
         }
+      }
     }
     if constexpr (WARPS == 1) {
 #pragma unroll
@@ -252,23 +281,27 @@ __device__ __forceinline__ void join_pieces(const CacheParams& p, const Pieces& 
 #pragma unroll
         for (int x = 0; x < V; ++x)
           static_cast<T*>(p.o)[row * D + lane * V + x] = (T)(l[e] == 0.f ? 0.f : o[e][x] / l[e]);
-        if (lane == 0) p.lse[row] = l[e] == 0.f ? -INFINITY : mx[e] + logf(l[e]);
+        if (lane == 0) p.lse[row] = l[e] == 0.f ? -INFINITY : m[e] + logf(l[e]);
       }
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
 #pragma unroll
         for (int x = 0; x < V; ++x) buf[(warp * 4 + e) * D + lane * V + x] = o[e][x];
-        if (lane == 0) lbuf[warp * 4 + e] = l[e];
+        if (lane == 0) {
+          sbuf[warp * 4 + e] = any[e] ? m[e] : -INFINITY;
+          sbuf[16 + warp * 4 + e] = l[e];
+        }
       }
       named_bar_sync(bar, 128);
-      for (int i = warp * 32 + lane; i < heads * D; i += 128) {
-        const int e = i / D, d = i % D;
-        const float sum = (lbuf[e] + lbuf[4 + e]) + (lbuf[8 + e] + lbuf[12 + e]);
-        const float x = (buf[e * D + d] + buf[(4 + e) * D + d]) + (buf[(8 + e) * D + d] + buf[(12 + e) * D + d]);
-        const size_t row = (size_t)b * p.Hq + hg.h0 + g0 + e;
-        static_cast<T*>(p.o)[row * D + d] = (T)(sum == 0.f ? 0.f : x / sum);
-        if (d == 0) p.lse[row] = sum == 0.f ? -INFINITY : (e == 0 ? mx[0] : e == 1 ? mx[1] : e == 2 ? mx[2] : mx[3]) + logf(sum);
+      if (warp < heads) {  // a head a warp
+        float y[V], sum, top;
+        merge_warps<D>(buf, sbuf, sbuf + 16, warp, lane, y, &sum, &top);
+        const size_t row = (size_t)b * p.Hq + hg.h0 + g0 + warp;
+#pragma unroll
+        for (int x = 0; x < V; ++x)
+          static_cast<T*>(p.o)[row * D + lane * V + x] = (T)(sum == 0.f ? 0.f : y[x] / sum);
+        if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
       }
       named_bar_sync(bar, 128);
     }
