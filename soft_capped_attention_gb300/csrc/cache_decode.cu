@@ -211,22 +211,38 @@ decode_simt_kernel(CacheParams p) {
   }
 }
 
-// weights[b, g, j] += sum over the group's heads of exp(t - lse): a thread a slot.
-__global__ void __launch_bounds__(256)
+// weights[b, g, j] += sum over the group's heads of exp(t - lse): a thread four
+// consecutive slots (rows are whole 16-byte units: max_len is a multiple of 8).
+__global__ void __launch_bounds__(128)
 decode_weights_kernel(CacheParams p) {
   pdl_trigger();
   pdl_wait();
-  const int row = blockIdx.x, b = row / p.Hkv, g = row % p.Hkv;
+  const int row = blockIdx.x, b = row / p.Hkv, g = row - b * p.Hkv;
   const SeqSpan sp = seq_span<64>(p, b);
   const float* lse = p.lse + (size_t)b * p.Hq + (size_t)g * p.G;
   const float* sc = p.scores + ((size_t)b * p.Hq + (size_t)g * p.G) * p.max_len;
-  for (int j = sp.first + blockIdx.y * blockDim.x + threadIdx.x; j < sp.len; j += gridDim.y * blockDim.x) {
-    float sum = 0.f;
+  float* out = p.weights + (size_t)row * p.max_len;
+  for (int j = (sp.first & ~3) + 4 * (blockIdx.y * 128 + threadIdx.x); j < sp.len; j += gridDim.y * 512) {
+    float4 w = *reinterpret_cast<const float4*>(out + j);
+    float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int h = 0; h < p.G; ++h) {
-      const float t = sc[(size_t)h * p.max_len + j];
-      sum += t == -INFINITY ? 0.f : __expf(t - lse[h]);
+      const float4 t = __ldcs(reinterpret_cast<const float4*>(sc + (size_t)h * p.max_len + j));
+      const float n = lse[h];
+      // a dead score is -inf (and the norm of a head without live keys too)
+      add.x += t.x == -INFINITY ? 0.f : __expf(t.x - n);
+      add.y += t.y == -INFINITY ? 0.f : __expf(t.y - n);
+      add.z += t.z == -INFINITY ? 0.f : __expf(t.z - n);
+      add.w += t.w == -INFINITY ? 0.f : __expf(t.w - n);
     }
-    p.weights[(size_t)row * p.max_len + j] += sum;
+    if (j >= sp.first && j + 4 <= sp.len) {
+      *reinterpret_cast<float4*>(out + j) = make_float4(w.x + add.x, w.y + add.y, w.z + add.z, w.w + add.w);
+    } else {
+      const float a[4] = {w.x + add.x, w.y + add.y, w.z + add.z, w.w + add.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e >= sp.first && j + e < sp.len) out[j + e] = a[e];
+    }
   }
 }
 
@@ -273,8 +289,8 @@ cudaError_t launch_cache_decode(const CacheParams& p, int dtype, cudaStream_t s)
   const cudaError_t e = dtype == CAPATTN_BF16 ? launch_decode_tc(p, s) : launch_decode_fp32(p, s);
   if (e != cudaSuccess || !p.scores) return e;
   const int live = p.window_len > 0 && !p.pos ? min(p.max_len, p.window_len) : p.max_len;
-  const dim3 grid(p.B * p.Hkv, min((live + 255) / 256, 1024));
-  return launch_pdl(decode_weights_kernel, grid, dim3(256), 0, s, p);
+  const dim3 grid(p.B * p.Hkv, min((live + 511) / 512, 1024));
+  return launch_pdl(decode_weights_kernel, grid, dim3(128), 0, s, p);
 }
 
 }  // namespace capattn

@@ -61,6 +61,7 @@ __device__ __forceinline__ int lane_scan(int x, int lane) {
 // Walks a CTA's pieces (every lane of a warp alike).
 template <int TK>
 struct PieceIter {
+  static constexpr int kHeld = 4;
   uint32_t units, ctas;           // all units, the CTAs that share them
   uint32_t u, end, begin;         // next unit, this CTA's range
   int b, vh, t0;                  // the next piece: sequence, group, first unit of the group
@@ -72,11 +73,17 @@ struct PieceIter {
   uint32_t s0, s1;         // units [s0, s1) of its (sequence, group)
 
   __device__ PieceIter(const CacheParams& p, int lane) {
-    // the first 32 sequences' tiles stay in a register: one read of lens decides
-    // a small batch
-    const int n0 = lane < p.B ? seq_span<TK>(p, lane).units : 0;
-    int all = n0;
-    for (int x = lane + 32; x < p.B; x += 32) all += seq_span<TK>(p, x).units;
+    // the lengths of the first 128 sequences stay in registers: one round of loads
+    // decides a batch of that size
+    int raw[kHeld], held[kHeld], all = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) raw[i] = lane + 32 * i < p.B ? p.lens[lane + 32 * i] : 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      held[i] = lane + 32 * i < p.B ? span_of<TK>(p, raw[i]).units : 0;
+      all += held[i];
+    }
+    for (int x = lane + 32 * kHeld; x < p.B; x += 32) all += seq_span<TK>(p, x).units;
     units = (uint32_t)__reduce_add_sync(0xFFFFFFFFu, all) * (uint32_t)p.VH;
     ctas = min((uint32_t)p.ctas, max(1u, units / (uint32_t)p.min_tiles));
     begin = u = begin_of(blockIdx.x);
@@ -85,19 +92,27 @@ struct PieceIter {
     if (u >= end) return;
     const int want = (int)(u / (uint32_t)p.VH);  // the tile, counted over the sequences
     int before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int x = b0 == 0 ? n0 : b0 + lane < p.B ? seq_span<TK>(p, b0 + lane).units : 0;
+    bool found = false;
+    auto look = [&](int b0, int x, int raw_len) {  // in the sequences b0 + lane
       const int up = lane_scan(x, lane);
       const uint32_t hit = __ballot_sync(0xFFFFFFFFu, want < before + up);
+      const int l = hit ? __ffs(hit) - 1 : 31;
       if (hit) {
-        const int l = __ffs(hit) - 1;
+        found = true;
         b = b0 + l;
+        len = __shfl_sync(0xFFFFFFFFu, raw_len, l);
         before += __shfl_sync(0xFFFFFFFFu, up - x, l);
-        break;
+      } else {
+        before += __shfl_sync(0xFFFFFFFFu, up, 31);
       }
-      before += __shfl_sync(0xFFFFFFFFu, up, 31);
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (!found && 32 * i < p.B) look(32 * i, held[i], raw[i]);
+    for (int b0 = 32 * kHeld; !found && b0 < p.B; b0 += 32) {
+      const int r = b0 + lane < p.B ? p.lens[b0 + lane] : 0;
+      look(b0, b0 + lane < p.B ? span_of<TK>(p, r).units : 0, r);
     }
-    len = p.lens[b];
     const SeqSpan sp = span_of<TK>(p, len);
     const uint32_t in = u - (uint32_t)before * (uint32_t)p.VH;
     vh = (int)(in / (uint32_t)sp.units);
