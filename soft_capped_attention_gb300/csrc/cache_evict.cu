@@ -45,15 +45,16 @@ struct RowKeys {
   const float* w;
   const int32_t* pos;
   int first, after;  // protected: position < first or > after
-  __device__ __forceinline__ uint32_t at(int j) const {
-    const int x = pos ? pos[j] : j;
-    return x < first || x > after ? 0xFFFFFFFFu : weight_key(w[j]);
+  __device__ __forceinline__ uint32_t of(float weight, int x) const {
+    return x < first || x > after ? 0xFFFFFFFFu : weight_key(weight);
   }
+  __device__ __forceinline__ uint32_t at(int j) const { return of(w[j], pos ? pos[j] : j); }
 };
 
+constexpr int kBatch = 8;   // slots a thread reads at once
 constexpr int kCopies = 4;  // of the first digit's histogram
 struct Shared {
-  int hist[kCopies + 2][kBins];  // pass 0 (copies), 1, 2
+  __align__(8) int hist[kCopies + 2][kBins];  // pass 0 (copies), 1, 2
   int warp_sum[3][kSelWarps];
   int totals[3];              // of this CTA: equal keys, movers, freed slots
   uint32_t digit;
@@ -95,6 +96,9 @@ select_kernel(CacheParams p, int parts) {
   extern __shared__ uint32_t s_keys[];
   __shared__ Shared s;
   cg::cluster_group cluster = cg::this_cluster();
+  auto meet = [&] {
+    if (parts > 1) cluster.sync(); else __syncthreads();
+  };
   const int rank = blockIdx.x % parts, row = blockIdx.x / parts;
   const int b = row / p.Hkv, g = row % p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -130,12 +134,31 @@ select_kernel(CacheParams p, int parts) {
   const int c1 = (int)min((long long)n, (long long)c0 + (long long)run * kSelWarps);
   const bool cached = run * kSelWarps <= kCachedKeys;
   __syncthreads();  // the histograms are zero
-  // first digit, with the keys on their way into shared memory
-#pragma unroll 4
-  for (int j = c0 + threadIdx.x; j < c1; j += kSelThreads) {
-    const uint32_t k = keys.at(j);
-    if (cached) s_keys[j - c0] = k;
-    atomicAdd(&s.hist[threadIdx.x % kCopies][k >> 21], 1);
+  // First digit, with the keys on their way into shared memory.  Slots below the
+  // budget are written as if they were kept; the moves overwrite those that go.
+  const bool copy_w = p.weights_out != p.weights, copy_pos = p.pos_out && p.pos_out != p.pos;
+  for (int j = c0 + threadIdx.x; j < c1; j += kBatch * kSelThreads) {
+    float w[kBatch];
+    int at[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int x = j + u * kSelThreads;
+      w[u] = x < c1 ? keys.w[x] : 0.f;
+      at[u] = x < c1 && keys.pos ? keys.pos[x] : x;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int x = j + u * kSelThreads;
+      if (x >= c1) break;
+      const uint32_t k = keys.of(w[u], at[u]);
+      if (cached) s_keys[x - c0] = k;
+      atomicAdd(&s.hist[threadIdx.x % kCopies][k >> 21], 1);
+      if (x < p.budget) {
+        src[x] = x;
+        if (copy_w) p.weights_out[base + x] = w[u];
+        if (copy_pos) p.pos_out[base + x] = at[u];
+      }
+    }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < kBins; i += kSelThreads) {
@@ -161,15 +184,25 @@ select_kernel(CacheParams p, int parts) {
         if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
       }
     }
-    cluster.sync();  // the cluster's histograms of this pass are whole
+    meet();  // the cluster's histograms of this pass are whole
     // a thread holds two bins, from the top
     int c[2] = {0, 0};
     const int top = bins - 1 - 2 * (int)threadIdx.x;
     if (top > 0) {
-      for (int x = 0; x < parts; ++x) {
-        const int* h = cluster.map_shared_rank(hist, x);
-        c[0] += h[top];
-        c[1] += h[top - 1];
+      int v[kMaxParts][2];  // all loads on their way before the first sum
+#pragma unroll
+      for (int x = 0; x < kMaxParts; ++x) {
+        v[x][0] = v[x][1] = 0;
+        if (x < parts) {
+          const int2 h = *reinterpret_cast<const int2*>((parts > 1 ? cluster.map_shared_rank(hist, x) : hist) + top - 1);
+          v[x][0] = h.y;
+          v[x][1] = h.x;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kMaxParts; ++x) {
+        c[0] += v[x][0];
+        c[1] += v[x][1];
       }
     }
     int total;
@@ -190,7 +223,8 @@ select_kernel(CacheParams p, int parts) {
   const int j0 = min(c1, c0 + warp * run), j1 = min(c1, j0 + run);
   const uint32_t below = (1u << lane) - 1u;
   int equal = 0;
-  for (int j = j0; j < j1; j += 32) equal += __popc(__ballot_sync(0xFFFFFFFFu, j + lane < j1 && key(j + lane) == prefix));
+  for (int j = j0 + lane; j < j1; j += 32) equal += key(j) == prefix;
+  equal = __reduce_add_sync(0xFFFFFFFFu, equal);
   // This warp's start in the cluster's order of one count a warp, after share()
   // has left it and the cluster has met; *total the cluster's.
   auto share = [&](int mine, int which) {
@@ -207,22 +241,21 @@ select_kernel(CacheParams p, int parts) {
     return __shfl_sync(0xFFFFFFFFu, up - x, warp);
   };
   auto before = [&](int which, int* total) {
-    int sum = 0, all = 0;
-    for (int c = 0; c < parts; ++c) {
-      const int v = *cluster.map_shared_rank(&s.totals[which], c);
-      if (c < rank) sum += v;
-      all += v;
-    }
-    *total = all;
-    return sum;
+    int v = 0;  // a lane a CTA
+    if (lane < parts) v = parts > 1 ? *cluster.map_shared_rank(&s.totals[which], lane) : s.totals[which];
+    *total = __reduce_add_sync(0xFFFFFFFFu, v);
+    return __reduce_add_sync(0xFFFFFFFFu, lane < rank ? v : 0);
   };
   int total;
   int eq0 = share(equal, 0);
-  cluster.sync();
+  meet();
   eq0 += before(0, &total);
-  // kept: above the threshold, or among the first `left` equal ones
+  // Kept: above the threshold, or among the first `left` equal ones.  All equal keys
+  // of a warp are on one side of that, but for one warp of the cluster.
+  const bool all_eq = eq0 + equal <= left, none_eq = eq0 >= left;
   auto kept_of = [&](int j, int& seen) {
     const uint32_t k = j < j1 ? key(j) : 0u;
+    if (all_eq || none_eq) return j < j1 && (all_eq ? k >= prefix : k > prefix);
     const bool eq = j < j1 && k == prefix;
     const uint32_t eqs = __ballot_sync(0xFFFFFFFFu, eq);
     const bool kept = j < j1 && (k > prefix || (eq && seen + __popc(eqs & below) < left));
@@ -231,13 +264,16 @@ select_kernel(CacheParams p, int parts) {
   };
   int movers = 0, holes = 0, seen = eq0;
   for (int j = j0; j < j1; j += 32) {
-    const bool in = j + lane < j1, kept = kept_of(j + lane, seen);
-    movers += __popc(__ballot_sync(0xFFFFFFFFu, kept && j + lane >= p.budget));
-    holes += __popc(__ballot_sync(0xFFFFFFFFu, in && !kept && j + lane < p.budget));
+    const int x = j + lane;
+    const bool kept = kept_of(x, seen);
+    movers += kept && x >= p.budget;
+    holes += x < j1 && !kept && x < p.budget;
   }
+  movers = __reduce_add_sync(0xFFFFFFFFu, movers);
+  holes = __reduce_add_sync(0xFFFFFFFFu, holes);
   int n_moves, n_holes;
   int mover = share(movers, 1), hole = share(holes, 2);
-  cluster.sync();
+  meet();
   mover += before(1, &n_moves);
   hole += before(2, &n_holes);
   seen = eq0;
@@ -248,16 +284,11 @@ select_kernel(CacheParams p, int parts) {
     const uint32_t who_moves = __ballot_sync(0xFFFFFFFFu, moves_it), who_goes = __ballot_sync(0xFFFFFFFFu, freed);
     if (moves_it) moves[mover + __popc(who_moves & below)].y = x;
     if (freed) moves[hole + __popc(who_goes & below)].x = x;
-    if (kept && x < p.budget) {
-      src[x] = x;
-      if (p.weights_out != p.weights) p.weights_out[base + x] = keys.w[x];
-      if (p.pos_out && p.pos_out != p.pos) p.pos_out[base + x] = keys.pos[x];
-    }
     mover += __popc(who_moves);
     hole += __popc(who_goes);
   }
   if (rank == 0 && threadIdx.x == 0) p.counts[row] = make_int2(n_moves, p.budget);
-  cluster.sync();  // no CTA leaves while its counts may be read
+  if (parts > 1) cluster.sync();  // no CTA leaves while its counts may be read
 }
 
 // Carries out the moves: a group of vph threads a row, K and V together, two rows in
