@@ -27,7 +27,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxParts = 8;
 constexpr int kBins = 2048;
@@ -51,33 +51,33 @@ struct RowKeys {
   __device__ __forceinline__ uint32_t at(int j) const { return of(w[j], pos ? pos[j] : j); }
 };
 
-constexpr int kBatch = 8;   // slots a thread reads at once
+constexpr int kBatch = 4;   // vectors of four slots a thread reads at once
 constexpr int kCopies = 4;  // of the first digit's histogram
 struct Shared {
-  __align__(8) int hist[kCopies + 2][kBins];  // pass 0 (copies), 1, 2
+  __align__(16) int hist[kCopies + 2][kBins];  // pass 0 (copies), 1, 2
   int warp_sum[3][kSelWarps];
   int totals[3];              // of this CTA: equal keys, movers, freed slots
   uint32_t digit;
   int above;
 };
 
+// Inclusive sum over the lanes.
+__device__ __forceinline__ int inclusive_sum(int x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
 // Exclusive sum of x over the block's threads; *total the whole (buf: a word a warp).
 __device__ __forceinline__ int block_scan(int x, int* buf, int warp, int lane, int* total) {
-  int up = x;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, up, d);
-    if (lane >= d) up += y;
-  }
+  const int up = inclusive_sum(x, lane);
   if (lane == 31) buf[warp] = up;
   __syncthreads();
-  const int w = buf[lane];  // 32 warps
-  int all = w;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, all, d);
-    if (lane >= d) all += y;
-  }
+  const int w = lane < kSelWarps ? buf[lane] : 0;
+  const int all = inclusive_sum(w, lane);
   *total = __shfl_sync(0xFFFFFFFFu, all, 31);
   return up - x + __shfl_sync(0xFFFFFFFFu, all - w, warp);
 }
@@ -128,35 +128,59 @@ select_kernel(CacheParams p, int parts) {
     if (rank == 0 && threadIdx.x == 0) p.counts[row] = make_int2(0, n);
     return;
   }
-  // this CTA's slots [c0, c1): equal runs of whole groups of 32, a run a warp
-  const int run = (int)(((long long)n + (long long)parts * kSelThreads - 1) / ((long long)parts * kSelThreads)) * 32;
-  const int c0 = (int)min((long long)n, (long long)rank * run * kSelWarps);
-  const int c1 = (int)min((long long)n, (long long)c0 + (long long)run * kSelWarps);
+  // This CTA's slots [c0, c1): equal runs of whole groups of 128, a run a warp, four
+  // consecutive slots a lane (rows of the weights are whole 16-byte units).
+  const uint32_t all_threads = (uint32_t)parts * kSelThreads;  // (n is at most 2^30)
+  const int run = (int)((n + 4 * all_threads - 1) / (4 * all_threads)) * 128;
+  const int c0 = min(n, rank * run * kSelWarps), c1 = min(n, c0 + run * kSelWarps);
+  const int j0 = min(c1, c0 + warp * run), j1 = min(c1, j0 + run);
   const bool cached = run * kSelWarps <= kCachedKeys;
   __syncthreads();  // the histograms are zero
   // First digit, with the keys on their way into shared memory.  Slots below the
   // budget are written as if they were kept; the moves overwrite those that go.
+  // (Vectors may reach behind c1, up to the row's end; those keys are not counted.)
   const bool copy_w = p.weights_out != p.weights, copy_pos = p.pos_out && p.pos_out != p.pos;
-  for (int j = c0 + threadIdx.x; j < c1; j += kBatch * kSelThreads) {
-    float w[kBatch];
-    int at[kBatch];
+  for (int j = j0 + 4 * lane; j < j1; j += 128 * kBatch) {
+    float4 w[kBatch];
+    int4 at[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int x = j + u * kSelThreads;
-      w[u] = x < c1 ? keys.w[x] : 0.f;
-      at[u] = x < c1 && keys.pos ? keys.pos[x] : x;
+      const int x = j + 128 * u;
+      at[u] = make_int4(x, x + 1, x + 2, x + 3);
+      if (x < j1) {
+        w[u] = *reinterpret_cast<const float4*>(keys.w + x);
+        if (keys.pos) at[u] = *reinterpret_cast<const int4*>(keys.pos + x);
+      }
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int x = j + u * kSelThreads;
-      if (x >= c1) break;
-      const uint32_t k = keys.of(w[u], at[u]);
-      if (cached) s_keys[x - c0] = k;
-      atomicAdd(&s.hist[threadIdx.x % kCopies][k >> 21], 1);
-      if (x < p.budget) {
-        src[x] = x;
-        if (copy_w) p.weights_out[base + x] = w[u];
-        if (copy_pos) p.pos_out[base + x] = at[u];
+      const int x = j + 128 * u;
+      if (x >= j1) break;
+      const uint4 k = make_uint4(keys.of(w[u].x, at[u].x), keys.of(w[u].y, at[u].y), keys.of(w[u].z, at[u].z),
+                                 keys.of(w[u].w, at[u].w));
+      if (cached) *reinterpret_cast<uint4*>(s_keys + (x - c0)) = k;
+      int* hist = s.hist[lane % kCopies];
+      atomicAdd(&hist[k.x >> 21], 1);
+      if (x + 1 < j1) atomicAdd(&hist[k.y >> 21], 1);
+      if (x + 2 < j1) atomicAdd(&hist[k.z >> 21], 1);
+      if (x + 3 < j1) atomicAdd(&hist[k.w >> 21], 1);
+      if (x < p.budget) {  // (n is above the budget: all four slots are there)
+        const int some = min(4, p.budget - x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < some) src[x + e] = x + e;
+        if (some == 4) {
+          if (copy_w) *reinterpret_cast<float4*>(p.weights_out + base + x) = w[u];
+          if (copy_pos) *reinterpret_cast<int4*>(p.pos_out + base + x) = at[u];
+        } else {
+          const float ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+          const int as[4] = {at[u].x, at[u].y, at[u].z, at[u].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (e < some && copy_w) p.weights_out[base + x + e] = ws[e];
+            if (e < some && copy_pos) p.pos_out[base + x + e] = as[e];
+          }
+        }
       }
     }
   }
@@ -167,7 +191,14 @@ select_kernel(CacheParams p, int parts) {
     for (int c = 0; c < kCopies; ++c) sum += s.hist[c][i];
     s.hist[0][i] = sum;
   }
-  auto key = [&](int j) { return cached ? s_keys[j - c0] : keys.at(j); };
+  // the keys of slots x .. x + 3 (x < c1)
+  auto keys4 = [&](int x) {
+    if (cached) return *reinterpret_cast<const uint4*>(s_keys + (x - c0));
+    const float4 w = *reinterpret_cast<const float4*>(keys.w + x);
+    int4 at = make_int4(x, x + 1, x + 2, x + 3);
+    if (keys.pos) at = *reinterpret_cast<const int4*>(keys.pos + x);
+    return make_uint4(keys.of(w.x, at.x), keys.of(w.y, at.y), keys.of(w.z, at.z), keys.of(w.w, at.w));
+  };
   // The budget-th largest key: its digits from the top; `left` is its rank among
   // the keys that share the digits so far.
   uint32_t prefix = 0;
@@ -179,40 +210,42 @@ select_kernel(CacheParams p, int parts) {
     const int bins = pass == 2 ? 1024 : kBins;
     if (pass > 0) {
       const uint32_t mask = pass == 1 ? 0xFFFFFFFFu << 21 : 0xFFFFFFFFu << 10;
-      for (int j = c0 + threadIdx.x; j < c1; j += kSelThreads) {
-        const uint32_t k = key(j);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
+      for (int j = j0 + 4 * lane; j < j1; j += 128) {
+        const uint4 k4 = keys4(j);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if ((k[e] & mask) == prefix && j + e < j1) atomicAdd(&hist[(k[e] >> shift) & (bins - 1)], 1);
       }
     }
     meet();  // the cluster's histograms of this pass are whole
-    // a thread holds two bins, from the top
-    int c[2] = {0, 0};
-    const int top = bins - 1 - 2 * (int)threadIdx.x;
+    // a thread holds four bins, from the top
+    static_assert(kBins == 4 * kSelThreads, "bins of a thread");
+    int c[4] = {0, 0, 0, 0};
+    const int top = bins - 1 - 4 * (int)threadIdx.x;
     if (top > 0) {
-      int v[kMaxParts][2];  // all loads on their way before the first sum
+      int4 v[kMaxParts];  // all loads on their way before the first sum
 #pragma unroll
-      for (int x = 0; x < kMaxParts; ++x) {
-        v[x][0] = v[x][1] = 0;
+      for (int x = 0; x < kMaxParts; ++x)
+        if (x < parts) v[x] = *reinterpret_cast<const int4*>((parts > 1 ? cluster.map_shared_rank(hist, x) : hist) + top - 3);
+#pragma unroll
+      for (int x = 0; x < kMaxParts; ++x)
         if (x < parts) {
-          const int2 h = *reinterpret_cast<const int2*>((parts > 1 ? cluster.map_shared_rank(hist, x) : hist) + top - 1);
-          v[x][0] = h.y;
-          v[x][1] = h.x;
+          c[0] += v[x].w;
+          c[1] += v[x].z;
+          c[2] += v[x].y;
+          c[3] += v[x].x;
         }
-      }
-#pragma unroll
-      for (int x = 0; x < kMaxParts; ++x) {
-        c[0] += v[x][0];
-        c[1] += v[x][1];
-      }
     }
     int total;
-    const int above = block_scan(c[0] + c[1], s.warp_sum[pass], warp, lane, &total);
-    if (above < left && left <= above + c[0]) {
-      s.digit = (uint32_t)top;
-      s.above = above;
-    } else if (above + c[0] < left && left <= above + c[0] + c[1]) {
-      s.digit = (uint32_t)(top - 1);
-      s.above = above + c[0];
+    int above = block_scan((c[0] + c[1]) + (c[2] + c[3]), s.warp_sum[pass], warp, lane, &total);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (above < left && left <= above + c[e]) {
+        s.digit = (uint32_t)(top - e);
+        s.above = above;
+      }
+      above += c[e];
     }
     __syncthreads();
     prefix |= s.digit << shift;
@@ -220,23 +253,19 @@ select_kernel(CacheParams p, int parts) {
     __syncthreads();
   }
   // Places, in the order of the slots: warp by warp, CTA by CTA.
-  const int j0 = min(c1, c0 + warp * run), j1 = min(c1, j0 + run);
-  const uint32_t below = (1u << lane) - 1u;
   int equal = 0;
-  for (int j = j0 + lane; j < j1; j += 32) equal += key(j) == prefix;
+  for (int j = j0 + 4 * lane; j < j1; j += 128) {
+    const uint4 k = keys4(j);
+    equal += (k.x == prefix) + (j + 1 < j1 && k.y == prefix) + (j + 2 < j1 && k.z == prefix) + (j + 3 < j1 && k.w == prefix);
+  }
   equal = __reduce_add_sync(0xFFFFFFFFu, equal);
   // This warp's start in the cluster's order of one count a warp, after share()
   // has left it and the cluster has met; *total the cluster's.
   auto share = [&](int mine, int which) {
     if (lane == 0) s.warp_sum[which][warp] = mine;
     __syncthreads();
-    const int x = s.warp_sum[which][lane];
-    int up = x;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, up, d);
-      if (lane >= d) up += y;
-    }
+    const int x = lane < kSelWarps ? s.warp_sum[which][lane] : 0;
+    const int up = inclusive_sum(x, lane);
     if (threadIdx.x == 31) s.totals[which] = up;
     return __shfl_sync(0xFFFFFFFFu, up - x, warp);
   };
@@ -253,21 +282,44 @@ select_kernel(CacheParams p, int parts) {
   // Kept: above the threshold, or among the first `left` equal ones.  All equal keys
   // of a warp are on one side of that, but for one warp of the cluster.
   const bool all_eq = eq0 + equal <= left, none_eq = eq0 >= left;
-  auto kept_of = [&](int j, int& seen) {
-    const uint32_t k = j < j1 ? key(j) : 0u;
-    if (all_eq || none_eq) return j < j1 && (all_eq ? k >= prefix : k > prefix);
-    const bool eq = j < j1 && k == prefix;
-    const uint32_t eqs = __ballot_sync(0xFFFFFFFFu, eq);
-    const bool kept = j < j1 && (k > prefix || (eq && seen + __popc(eqs & below) < left));
-    seen += __popc(eqs);
-    return kept;
+  // Bits 0 .. 3: which of the slots x .. x + 3 are kept (warp-collective).
+  auto kept_of = [&](int x, int& seen) {
+    uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
+    if (x < j1) k4 = keys4(x);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+    const uint32_t in = x + 4 <= j1 ? 15u : x < j1 ? (1u << (j1 - x)) - 1u : 0u;
+    uint32_t over = 0, same = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      over |= (k[e] > prefix ? 1u : 0u) << e;
+      same |= (k[e] == prefix ? 1u : 0u) << e;
+    }
+    over &= in;
+    same &= in;
+    if (none_eq) return over;
+    if (all_eq) return over | same;
+    int at = __popc(same), mine = at;  // equal keys up to this lane's
+    at = inclusive_sum(at, lane);
+    const int first = seen + at - mine;
+    seen += __shfl_sync(0xFFFFFFFFu, at, 31);
+    int room = max(0, left - first);  // of this lane's equal keys, the lowest `room` are kept
+    uint32_t take = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if ((same >> e) & 1u) {
+        if (room > 0) take |= 1u << e;
+        --room;
+      }
+    return over | take;
   };
+  // bits of the slots x .. x + 3 that lie below the budget / below j1
+  auto below_of = [&](int x, int end) { return x + 4 <= end ? 15u : x < end ? (1u << (end - x)) - 1u : 0u; };
   int movers = 0, holes = 0, seen = eq0;
-  for (int j = j0; j < j1; j += 32) {
-    const int x = j + lane;
-    const bool kept = kept_of(x, seen);
-    movers += kept && x >= p.budget;
-    holes += x < j1 && !kept && x < p.budget;
+  for (int j = j0; j < j1; j += 128) {
+    const int x = j + 4 * lane;
+    const uint32_t kept = kept_of(x, seen), low = below_of(x, p.budget), in = below_of(x, j1);
+    movers += __popc(kept & ~low);
+    holes += __popc(in & low & ~kept);
   }
   movers = __reduce_add_sync(0xFFFFFFFFu, movers);
   holes = __reduce_add_sync(0xFFFFFFFFu, holes);
@@ -277,15 +329,21 @@ select_kernel(CacheParams p, int parts) {
   mover += before(1, &n_moves);
   hole += before(2, &n_holes);
   seen = eq0;
-  for (int j = j0; j < j1; j += 32) {
-    const int x = j + lane;
-    const bool kept = kept_of(x, seen);
-    const bool moves_it = kept && x >= p.budget, freed = x < j1 && !kept && x < p.budget;
-    const uint32_t who_moves = __ballot_sync(0xFFFFFFFFu, moves_it), who_goes = __ballot_sync(0xFFFFFFFFu, freed);
-    if (moves_it) moves[mover + __popc(who_moves & below)].y = x;
-    if (freed) moves[hole + __popc(who_goes & below)].x = x;
-    mover += __popc(who_moves);
-    hole += __popc(who_goes);
+  for (int j = j0; j < j1; j += 128) {
+    const int x = j + 4 * lane;
+    const uint32_t kept = kept_of(x, seen), low = below_of(x, p.budget), in = below_of(x, j1);
+    const uint32_t moves_it = kept & ~low, freed = in & low & ~kept;
+    // both counts in one sum over the lanes: at most 128 of each
+    const int mine = __popc(moves_it) | __popc(freed) << 16;
+    const int up = inclusive_sum(mine, lane), all = __shfl_sync(0xFFFFFFFFu, up, 31);
+    int m = mover + ((up - mine) & 0xFFFF), h = hole + ((up - mine) >> 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if ((moves_it >> e) & 1u) moves[m++].y = x + e;
+      if ((freed >> e) & 1u) moves[h++].x = x + e;
+    }
+    mover += all & 0xFFFF;
+    hole += all >> 16;
   }
   if (rank == 0 && threadIdx.x == 0) p.counts[row] = make_int2(n_moves, p.budget);
   if (parts > 1) cluster.sync();  // no CTA leaves while its counts may be read
@@ -348,7 +406,8 @@ cudaError_t launch_cache_evict(const CacheParams& p, int dtype, cudaStream_t s) 
   int parts = 1;
   while (parts < kMaxParts && p.max_len / parts > 2048 && rows * parts * 2 <= 152) parts *= 2;
   static std::atomic<uint64_t> done{0};
-  const int keys = min((long long)kCachedKeys, ((long long)p.max_len + parts * kSelThreads - 1) / (parts * kSelThreads) * kSelThreads);
+  const int64_t per_cta = (int64_t)4 * kSelThreads;
+  const int keys = (int)min((int64_t)kCachedKeys, (p.max_len + parts * per_cta - 1) / (parts * per_cta) * per_cta);
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(select_kernel), kCachedKeys * 4, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
