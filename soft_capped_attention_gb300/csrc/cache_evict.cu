@@ -11,11 +11,11 @@
 //
 // Selection is bound by latency (its 8 bytes a slot are little against the rows
 // that move): a cluster of up to 8 CTAs takes a row, each CTA a run of slots whose
-// keys it reads once and keeps in shared memory.  Three histogram passes (11, 11
-// and 10 bits) find the threshold, each CTA adding up the cluster's histograms by
-// distributed shared memory (four copies of a CTA's first one, since weights share
-// few leading digits and equal bins serialise the atomics); three more passes over
-// the keys count and list the slots.  What follows from the lists (the rows' pages,
+// keys it reads once and keeps in shared memory.  Four histogram passes of 8 bits
+// find the threshold, each CTA adding up the cluster's histograms by distributed
+// shared memory (of 11 bits, three passes: reading 8 KB from each of 8 CTAs took 7000
+// cycles a pass, more than a pass of 8 bits altogether); three more passes over the
+// keys count and list the slots.  What follows from the lists (the rows' pages,
 // the copies, the moved tokens' weights and positions) is the second kernel's, over
 // all SMs.
 #include <cooperative_groups.h>
@@ -30,7 +30,7 @@ namespace cg = cooperative_groups;
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxParts = 8;
-constexpr int kBins = 2048;
+constexpr int kBins = 256;
 constexpr int kCachedKeys = 40 * 1024;  // keys a CTA keeps in shared memory (160 KB)
 
 // Order of a weight as an unsigned key: larger weight, larger key; both zeros
@@ -48,17 +48,14 @@ struct RowKeys {
   __device__ __forceinline__ uint32_t of(float weight, int x) const {
     return x < first || x > after ? 0xFFFFFFFFu : weight_key(weight);
   }
-  __device__ __forceinline__ uint32_t at(int j) const { return of(w[j], pos ? pos[j] : j); }
 };
 
 constexpr int kBatch = 4;   // vectors of four slots a thread reads at once
-constexpr int kCopies = 4;  // of the first digit's histogram
 struct Shared {
-  __align__(16) int hist[kCopies + 2][kBins];  // pass 0 (copies), 1, 2
+  __align__(16) int hist[4][kBins];  // of each pass
+  __align__(16) int sum[2][kBins];   // the cluster's (two, for passes in turn)
   int warp_sum[3][kSelWarps];
   int totals[3];              // of this CTA: equal keys, movers, freed slots
-  uint32_t digit;
-  int above;
 };
 
 // Inclusive sum over the lanes.
@@ -69,17 +66,6 @@ __device__ __forceinline__ int inclusive_sum(int x, int lane) {
     if (lane >= d) x += y;
   }
   return x;
-}
-
-// Exclusive sum of x over the block's threads; *total the whole (buf: a word a warp).
-__device__ __forceinline__ int block_scan(int x, int* buf, int warp, int lane, int* total) {
-  const int up = inclusive_sum(x, lane);
-  if (lane == 31) buf[warp] = up;
-  __syncthreads();
-  const int w = lane < kSelWarps ? buf[lane] : 0;
-  const int all = inclusive_sum(w, lane);
-  *total = __shfl_sync(0xFFFFFFFFu, all, 31);
-  return up - x + __shfl_sync(0xFFFFFFFFu, all - w, warp);
 }
 
 __device__ __forceinline__ int cache_row(const CacheParams& p, int b, int g, int slot) {
@@ -102,7 +88,7 @@ select_kernel(CacheParams p, int parts) {
   const int rank = blockIdx.x % parts, row = blockIdx.x / parts;
   const int b = row / p.Hkv, g = row % p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < (kCopies + 2) * kBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
+  for (int i = threadIdx.x; i < 4 * kBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
   pdl_trigger();
   pdl_wait();
   int n = p.lens[b];
@@ -159,11 +145,10 @@ select_kernel(CacheParams p, int parts) {
       const uint4 k = make_uint4(keys.of(w[u].x, at[u].x), keys.of(w[u].y, at[u].y), keys.of(w[u].z, at[u].z),
                                  keys.of(w[u].w, at[u].w));
       if (cached) *reinterpret_cast<uint4*>(s_keys + (x - c0)) = k;
-      int* hist = s.hist[lane % kCopies];
-      atomicAdd(&hist[k.x >> 21], 1);
-      if (x + 1 < j1) atomicAdd(&hist[k.y >> 21], 1);
-      if (x + 2 < j1) atomicAdd(&hist[k.z >> 21], 1);
-      if (x + 3 < j1) atomicAdd(&hist[k.w >> 21], 1);
+      atomicAdd(&s.hist[0][k.x >> 24], 1);
+      if (x + 1 < j1) atomicAdd(&s.hist[0][k.y >> 24], 1);
+      if (x + 2 < j1) atomicAdd(&s.hist[0][k.z >> 24], 1);
+      if (x + 3 < j1) atomicAdd(&s.hist[0][k.w >> 24], 1);
       if (x < p.budget) {  // (n is above the budget: all four slots are there)
         const int some = min(4, p.budget - x);
 #pragma unroll
@@ -184,13 +169,6 @@ select_kernel(CacheParams p, int parts) {
       }
     }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kBins; i += kSelThreads) {
-    int sum = 0;
-#pragma unroll
-    for (int c = 0; c < kCopies; ++c) sum += s.hist[c][i];
-    s.hist[0][i] = sum;
-  }
   // the keys of slots x .. x + 3 (x < c1)
   auto keys4 = [&](int x) {
     if (cached) return *reinterpret_cast<const uint4*>(s_keys + (x - c0));
@@ -204,53 +182,53 @@ select_kernel(CacheParams p, int parts) {
   uint32_t prefix = 0;
   int left = p.budget;
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    int* hist = s.hist[pass == 0 ? 0 : kCopies - 1 + pass];
-    const int bins = pass == 2 ? 1024 : kBins;
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    int* hist = s.hist[pass];
     if (pass > 0) {
-      const uint32_t mask = pass == 1 ? 0xFFFFFFFFu << 21 : 0xFFFFFFFFu << 10;
+      const uint32_t mask = 0xFFFFFFFFu << (shift + 8);
       for (int j = j0 + 4 * lane; j < j1; j += 128) {
         const uint4 k4 = keys4(j);
         const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if ((k[e] & mask) == prefix && j + e < j1) atomicAdd(&hist[(k[e] >> shift) & (bins - 1)], 1);
+          if ((k[e] & mask) == prefix && j + e < j1) atomicAdd(&hist[(k[e] >> shift) & (kBins - 1)], 1);
       }
     }
     meet();  // the cluster's histograms of this pass are whole
-    // a thread holds four bins, from the top
-    static_assert(kBins == 4 * kSelThreads, "bins of a thread");
-    int c[4] = {0, 0, 0, 0};
-    const int top = bins - 1 - 4 * (int)threadIdx.x;
-    if (top > 0) {
-      int4 v[kMaxParts];  // all loads on their way before the first sum
+    if (parts > 1) {
+      if (threadIdx.x < kBins) {
+        int v[kMaxParts], sum = 0;  // all loads on their way before the first sum
 #pragma unroll
-      for (int x = 0; x < kMaxParts; ++x)
-        if (x < parts) v[x] = *reinterpret_cast<const int4*>((parts > 1 ? cluster.map_shared_rank(hist, x) : hist) + top - 3);
+        for (int x = 0; x < kMaxParts; ++x) v[x] = x < parts ? cluster.map_shared_rank(hist, x)[threadIdx.x] : 0;
 #pragma unroll
-      for (int x = 0; x < kMaxParts; ++x)
-        if (x < parts) {
-          c[0] += v[x].w;
-          c[1] += v[x].z;
-          c[2] += v[x].y;
-          c[3] += v[x].x;
-        }
+        for (int x = 0; x < kMaxParts; ++x) sum += v[x];
+        s.sum[pass & 1][threadIdx.x] = sum;
+      }
+      __syncthreads();
     }
-    int total;
-    int above = block_scan((c[0] + c[1]) + (c[2] + c[3]), s.warp_sum[pass], warp, lane, &total);
+    // every warp finds the digit: a lane holds eight bins, from the top
+    const int* all = parts > 1 ? s.sum[pass & 1] : hist;
+    const int top = kBins - 1 - 8 * lane;
+    const int4 c0123 = *reinterpret_cast<const int4*>(all + top - 3), c4567 = *reinterpret_cast<const int4*>(all + top - 7);
+    const int c[8] = {c0123.w, c0123.z, c0123.y, c0123.x, c4567.w, c4567.z, c4567.y, c4567.x};
+    int mine = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 8; ++e) mine += c[e];
+    const int up = inclusive_sum(mine, lane);
+    int above = up - mine, digit = 0, before = 0;
+    const bool here = above < left && left <= up;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
       if (above < left && left <= above + c[e]) {
-        s.digit = (uint32_t)(top - e);
-        s.above = above;
+        digit = top - e;
+        before = above;
       }
       above += c[e];
     }
-    __syncthreads();
-    prefix |= s.digit << shift;
-    left -= s.above;
-    __syncthreads();
+    const int from = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
+    prefix |= (uint32_t)__shfl_sync(0xFFFFFFFFu, digit, from) << shift;
+    left -= __shfl_sync(0xFFFFFFFFu, before, from);
   }
   // Places, in the order of the slots: warp by warp, CTA by CTA.
   int equal = 0;
