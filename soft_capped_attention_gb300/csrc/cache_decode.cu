@@ -35,19 +35,22 @@ __device__ __forceinline__ void dot16(float& acc, const float* k, const float* q
   acc = fmaf(a.z, b.z, acc);
   acc = fmaf(a.w, b.w, acc);
 }
-template <typename T, int D>
+template <typename T, int D, int GM>
 struct Smem {
   static constexpr int PER = 16 / sizeof(T);
   static constexpr int ROW = D + PER;  // a row's stride: 16 bytes of padding against bank conflicts
+  static constexpr int PARTS = kThreads / D;
   T k[2][TK][ROW];
   T v[2][TK][ROW];
-  float q[kDecodeHeads][D];
-  float p[kDecodeHeads][TK];
-  float scale[kDecodeHeads];
-  float m[kDecodeHeads], l[kDecodeHeads];
-  float half[kDecodeHeads][64];  // D = 64: outputs of the second half of the threads
-  float join[16][D], lsum[32];
+  float q[GM][D];
+  float p[GM][TK];
+  float scale[GM], m[GM], l[GM];
+  float half[PARTS > 1 ? GM : 1][64];  // D = 64: outputs of the second half of the threads
+  float lsum[32];
   int flag;
+  // the join's 4 x 4 x D floats: no tile is in flight at a piece's end
+  __device__ float* join() { return reinterpret_cast<float*>(&k[0][0][0]); }
+  static_assert(2 * TK * ROW * sizeof(T) >= 16 * D * sizeof(float), "the join's buffer");
 };
 
 // Tiles of 32 keys come in by cp.async, two stages.  Scores: warp w takes heads
@@ -58,7 +61,7 @@ template <typename T, int D, int METHOD, int GM>
 __global__ void __launch_bounds__(kThreads)
 decode_simt_kernel(CacheParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
-  using S = Smem<T, D>;
+  using S = Smem<T, D, GM>;
   S& s = *reinterpret_cast<S*>(raw);
   constexpr int CH = D / S::PER;            // 16-byte pieces of a row
   constexpr int NH = (GM + 3) / 4;          // heads of a warp
@@ -75,7 +78,7 @@ decode_simt_kernel(CacheParams p) {
   while (it.next(p, &b, &vh, &tile, &sp)) {
     const HeadGroup hg = head_group(p, vh);
     const int n = it.n;
-    for (int i = threadIdx.x; i < kDecodeHeads * D; i += kThreads) {
+    for (int i = threadIdx.x; i < GM * D; i += kThreads) {
       const int g = i / D;
       s.q[g][i % D] = g < hg.count
           ? static_cast<const T*>(p.q)[(size_t)b * p.q_stride + (size_t)(hg.h0 + g) * D + i % D] : 0.f;
@@ -205,7 +208,7 @@ decode_simt_kernel(CacheParams p) {
       const Pieces pc(it);
       if (threadIdx.x == 0) s.flag = count_piece(p, pc);
       __syncthreads();
-      if (s.flag) join_pieces<T, D, 4>(p, pc, b, hg, warp, lane, 1, &s.join[0][0], s.lsum);
+      if (s.flag) join_pieces<T, D, 4>(p, pc, b, hg, warp, lane, 1, s.join(), s.lsum);
       __syncthreads();
     }
   }
@@ -247,12 +250,19 @@ decode_weights_kernel(CacheParams p) {
 }
 
 template <int D, int METHOD, int GM>
-cudaError_t run_simt(const CacheParams& p, cudaStream_t s) {
+cudaError_t run_simt(const CacheParams& p0, cudaStream_t s) {
   auto* k = decode_simt_kernel<float, D, METHOD, GM>;
   static std::atomic<uint64_t> done{0};
-  const int smem = sizeof(Smem<float, D>);
+  const int smem = sizeof(Smem<float, D, GM>);
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem, done);
   if (e != cudaSuccess) return e;
+  // as many CTAs as the SMs hold at once (three by their registers), no more than
+  // there can be tiles
+  CacheParams p = p0;
+  const int per_sm = 227 * 1024 / (smem + 1024) < 3 ? 227 * 1024 / (smem + 1024) : 3;
+  const int64_t most = (int64_t)p.B * p.VH * ((p.max_len + TK - 1) / TK);
+  p.ctas = (int)(most < 152 * per_sm ? most : 152 * per_sm);
+  p.min_tiles = 2;
   return launch_pdl(k, dim3(p.ctas), dim3(kThreads), smem, s, p);
 }
 
@@ -274,12 +284,7 @@ cudaError_t run_cap(const CacheParams& p, cudaStream_t s) {
   }
 }
 
-cudaError_t launch_decode_fp32(const CacheParams& p0, cudaStream_t s) {
-  CacheParams p = p0;
-  // three CTAs fit an SM; no more than there can be tiles
-  const int64_t most = (int64_t)p.B * p.VH * ((p.max_len + TK - 1) / TK);
-  p.ctas = (int)(most < 152 * 3 ? most : 152 * 3);
-  p.min_tiles = 2;
+cudaError_t launch_decode_fp32(const CacheParams& p, cudaStream_t s) {
   return p.D == 64 ? run_cap<64>(p, s) : run_cap<128>(p, s);
 }
 
