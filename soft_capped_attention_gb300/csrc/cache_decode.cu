@@ -72,7 +72,8 @@ decode_simt_kernel(CacheParams p) {
   const int d = threadIdx.x % D, part = threadIdx.x / D;
   const T* kc = static_cast<const T*>(p.k);
   const T* vc = static_cast<const T*>(p.v);
-  PieceIter<TK> it(p, lane);
+  __shared__ int s_sums[kSchedSums];
+  PieceIter<TK> it(p, warp, lane, kThreads / 32, s_sums);
   int b, vh, tile;
   SeqSpan sp;
   while (it.next(p, &b, &vh, &tile, &sp)) {

@@ -5,8 +5,8 @@
 // 16; the kernel's task is to keep the loads in flight.  A persistent grid, two
 // CTAs an SM, takes equal shares of 64-key tiles (cache_sched.cuh).  In each CTA
 // one warp fills a ring of shared-memory stages by TMA (a tile's pages are boxes
-// of up to 64 rows x 64 columns in the 128-byte swizzle) and four warps compute,
-// 16 keys of the tile each, with a running (m, l, O) of their own.  At a piece's end
+// of up to a tile's rows x 64 columns in the 128-byte swizzle) and four warps compute,
+// every fourth 16 keys of the tile each, with a running (m, l, O) of their own.  At a piece's end
 // they leave those in shared memory and go on with the next piece; a sixth warp adds
 // them up, writes, counts split pieces in and joins them when it comes last (a
 // CTA's last piece they finish themselves: they have nothing else to do).
@@ -25,6 +25,7 @@
 // The reference m moves only when the maximum outgrows it by kSlack (P stays
 // below e^kSlack), which saves the rescaling of O on nearly every step.
 #include <cuda_bf16.h>
+#include <limits.h>
 
 #include "cache_internal.h"
 #include "cache_math.cuh"
@@ -35,21 +36,29 @@
 namespace capattn {
 namespace {
 
-constexpr int TK = 64;                 // keys of a tile
 constexpr int kConsumers = 4;          // warps that compute, 16 keys of a tile each
 constexpr int kThreads = (kConsumers + 2) * 32;  // and the TMA warp and the writing one
 constexpr float kSlack = 8.f;
 
+// Keys of a tile: 32 KB of keys and values, 64 keys (D = 128) or 128.
 template <int D>
+constexpr int tile_keys() { return 8192 / D; }
+template <int D, int NT>
 struct Geo {
+  static constexpr int TK = tile_keys<D>();
+  static constexpr int GROUPS = TK / 64;              // groups of 16 keys of a warp
   static constexpr int SLABS = D / 64;                // 128-byte wide columns of a row
   static constexpr int SLAB = TK * 128;
   static constexpr int HALF = SLABS * SLAB;           // K (or V) of a stage
   static constexpr int STAGE = 2 * HALF;
-  static constexpr int STAGES = D == 128 ? 3 : 6;     // 96 KB a CTA, two CTAs an SM
+  static constexpr int STAGES = 3;                    // 96 KB a CTA, two CTAs an SM
   static constexpr int MERGE = 16 * D * 4;            // 4 warps x 4 heads x D floats
-  static constexpr int Q = 16 * D * 2;                // a group's queries
-  static constexpr int SMEM = STAGES * STAGE + MERGE + Q + 1024;
+  // A group's queries, of as many pieces as there are stages where that fits (with
+  // one slot a piece's tiles could not be asked for before the last piece's queries
+  // are in registers, which left short sequences waiting for memory)
+  static constexpr int Q = 8 * NT * D * 2;
+  static constexpr int QSLOTS = D == 128 && NT == 2 ? 1 : 3;
+  static constexpr int SMEM = STAGES * STAGE + MERGE + QSLOTS * Q + 1024;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -94,9 +103,10 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint3
 template <int D, int METHOD, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
 decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const CacheParams p) {
-  using G = Geo<D>;
+  using G = Geo<D, NT>;
+  constexpr int TK = G::TK;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * G::STAGES + 4];
+  __shared__ __align__(8) uint64_t bars[2 * G::STAGES + 2 * G::QSLOTS + 2];
   __shared__ int abort_flag, join_flag;
   __shared__ float s_m[kConsumers * 4], s_l[kConsumers * 4], s_join[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -104,16 +114,18 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   float* merge = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + G::STAGES * G::STAGE);
   const uint32_t s_q = base + G::STAGES * G::STAGE + G::MERGE;
   const uint32_t full = smem_u32(&bars[0]), empty = smem_u32(&bars[G::STAGES]);
-  const uint32_t q_full = smem_u32(&bars[2 * G::STAGES]), q_empty = q_full + 8;
-  const uint32_t m_full = q_full + 16, m_empty = q_full + 24;  // the warps' results of four heads
+  const uint32_t q_full = smem_u32(&bars[2 * G::STAGES]), q_empty = q_full + 8 * G::QSLOTS;  // + 8 x: slot x
+  const uint32_t m_full = q_empty + 8 * G::QSLOTS, m_empty = m_full + 8;  // the warps' results of four heads
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < G::STAGES; ++s) {
       mbar_init(full + 8 * s, 1);
       mbar_init(empty + 8 * s, kConsumers);
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, kConsumers);
+    for (int x = 0; x < G::QSLOTS; ++x) {
+      mbar_init(q_full + 8 * x, 1);
+      mbar_init(q_empty + 8 * x, kConsumers);
+    }
     mbar_init(m_full, kConsumers);
     mbar_init(m_empty, 1);
     fence_mbar_init();
@@ -121,7 +133,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   pdl_trigger();
   pdl_wait();
   __syncthreads();
-  PieceIter<TK> it(p, lane);
+  PieceIter<TK> it(p, warp, lane, kThreads / 32, reinterpret_cast<int*>(merge));
   int b, vh, tile;
   SeqSpan sp;
   uint32_t step = 0;   // tiles so far, over the pieces
@@ -139,34 +151,43 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     bool ok = true;
     while (ok && it.next(p, &b, &vh, &tile, &sp)) {
       const int g = vh / p.HG;
-      // cache row of this lane's box of a tile, or -1: no live slot in it
-      auto row_of = [&](int t) {
+      // The page of this lane's box of a tile, as read (kNoBox: no live slot in it);
+      // looked at a tile later, so that the read is not waited for.
+      constexpr int kNoBox = INT_MIN;
+      const int32_t* table = p.table + (size_t)b * p.max_pages;
+      auto page_at = [&](int t) {
         const int j = t * TK + lane * rows;
-        if (lane >= pages || j >= sp.len || j + rows <= sp.first) return -1;
-        return (page_of(p, b, j) * p.Hkv + g) * p.page_size + (j & (p.page_size - 1));
+        return lane >= pages || j >= sp.len || j + rows <= sp.first ? kNoBox : table[j >> p.page_shift];
       };
-      int row = row_of(tile);
-      // the group's queries, as soon as the last piece's are in registers
-      if (piece > 0 && !mbar_wait_warp(q_empty, (piece - 1) & 1, p.status, &abort_flag)) break;
+      int page = page_at(tile);
+      // the group's queries
+      const uint32_t qs = piece % G::QSLOTS, q_use = piece / G::QSLOTS;
+      if (q_use > 0 && !mbar_wait_warp(q_empty + 8 * qs, (q_use - 1) & 1, p.status, &abort_flag)) break;
       if (lane == 0) {
         const HeadGroup hg = head_group(p, vh);
         const uint32_t q_bytes = (uint32_t)hg.count * D * 2;
-        mbar_expect_tx(q_full, q_bytes);
-        bulk_load(s_q, static_cast<const __nv_bfloat16*>(p.q) + (size_t)b * p.q_stride + (size_t)hg.h0 * D, q_bytes, q_full);
+        mbar_expect_tx(q_full + 8 * qs, q_bytes);
+        bulk_load(s_q + qs * G::Q, static_cast<const __nv_bfloat16*>(p.q) + (size_t)b * p.q_stride + (size_t)hg.h0 * D,
+                  q_bytes, q_full + 8 * qs);
       }
       ++piece;
       __syncwarp();
       for (int i = 0; i < it.n; ++i, ++step) {
-        const int next = i + 1 < it.n ? row_of(tile + i + 1) : -1;  // a tile ahead of its use
+        const int next = i + 1 < it.n ? page_at(tile + i + 1) : kNoBox;
         const uint32_t s = step % G::STAGES, use = step / G::STAGES;
         if (use > 0 && !mbar_wait_warp(empty + 8 * s, (use - 1) & 1, p.status, &abort_flag)) {
           ok = false;
           break;
         }
-        const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0));
+        const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, page != kNoBox));
         if (lane == 0) mbar_expect_tx(full + 8 * s, boxes * bytes);
         __syncwarp();
-        if (row >= 0) {
+        if (page != kNoBox) {
+          if (page < 0 || page >= p.num_pages) {  // flagged, and read as page 0
+            atomicOr(p.status, kStatusBadPageBit);
+            page = 0;
+          }
+          const int row = (page * p.Hkv + g) * p.page_size + (((tile + i) * TK + lane * rows) & (p.page_size - 1));
           const uint32_t dst = base + s * G::STAGE + lane * rows * 128;
 #pragma unroll
           for (int x = 0; x < G::SLABS; ++x) {
@@ -175,11 +196,12 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
           }
         }
         __syncwarp();
-        row = next;
+        page = next;
       }
     }
     // normally long complete: the consumers waited for every stage
-    if (piece > 0) drain_wait(q_full, (piece - 1) & 1);
+    for (uint32_t x = piece > G::QSLOTS ? piece - G::QSLOTS : 0; x < piece; ++x)
+      drain_wait(q_full + 8 * (x % G::QSLOTS), (x / G::QSLOTS) & 1);
     for (uint32_t x = step > G::STAGES ? step - G::STAGES : 0; x < step; ++x)
       drain_wait(full + 8 * (x % G::STAGES), (x / G::STAGES) & 1);
     return;
@@ -194,10 +216,11 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     merge_warps<D>(merge, s_m, s_l, e, lane, y, &sum, &top);
     if (it.whole) {
       const size_t row = (size_t)b * p.Hq + hg.h0 + g0 + e;
+      const float inv = sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
       for (int x = 0; x < V; x += 2)
         *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + row * D + lane * V + x) =
-            pack_bf16x2(sum == 0.f ? 0.f : y[x] / sum, sum == 0.f ? 0.f : y[x + 1] / sum);
+            pack_bf16x2(y[x] * inv, y[x + 1] * inv);
       if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
     } else {
       const size_t at = (size_t)it.slot * kDecodeHeads + g0 + e;
@@ -243,7 +266,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     const int32_t* pos = p.pos + ((size_t)b * p.Hkv + hg.g) * p.max_len;
     const int oldest = by_pos ? p.qpos[b] - p.window_len : 0;
     uint32_t q[NT][D / 16][2];
-    ok = ok && mbar_wait_warp(q_full, piece & 1, p.status, &abort_flag);
+    const uint32_t qs = piece % G::QSLOTS;
+    ok = ok && mbar_wait_warp(q_full + 8 * qs, (piece / G::QSLOTS) & 1, p.status, &abort_flag);
     ++piece;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -255,11 +279,11 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
           if (gq + 8 * t < hg.count)
             asm volatile("ld.shared.b32 %0, [%1];"
                          : "=r"(q[t][ks][e])
-                         : "r"(s_q + (gq + 8 * t) * D * 2 + 32 * ks + 16 * e + 4 * tq)
+                         : "r"(s_q + qs * G::Q + (gq + 8 * t) * D * 2 + 32 * ks + 16 * e + 4 * tq)
                          : "memory");
         }
     __syncwarp();
-    if (lane == 0) mbar_arrive(q_empty);
+    if (lane == 0) mbar_arrive(q_empty + 8 * qs);
     // heads of this lane: 8 t + 2 tq + e; keys: 16 warp + gq + 8 k
     float m[NT][2], l[NT][2], o[NT][D / 16][4];
 #pragma unroll
@@ -277,9 +301,12 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
       // after a timeout the warp still meets the others at every piece's barriers
       ok = ok && mbar_wait_warp(full + 8 * s, use & 1, p.status, &abort_flag);
       if (!ok) break;
-      const int j0 = (tile + i) * TK + 16 * warp;
-      if (j0 < sp.len && j0 + 16 > sp.first) {
-        const uint32_t kb = base + s * G::STAGE + k_row, vb = base + s * G::STAGE + G::HALF + v_row;
+#pragma unroll
+      for (int group = 0; group < G::GROUPS; ++group) {
+        const int j0 = (tile + i) * TK + 64 * group + 16 * warp;
+        if (j0 >= sp.len || j0 + 16 <= sp.first) continue;
+        const uint32_t kb = base + s * G::STAGE + 64 * 128 * group + k_row;
+        const uint32_t vb = base + s * G::STAGE + G::HALF + 64 * 128 * group + v_row;
         float c[NT][4] = {};
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -446,12 +473,12 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 
 // 2-D map over the cache's rows [num_pages * Hkv * page_size][D]: boxes of 64
 // columns x the rows a tile has of a page, 128-byte swizzle.
-cudaError_t make_rows_map(CUtensorMap* map, const void* base, const CacheParams& p) {
+cudaError_t make_rows_map(CUtensorMap* map, const void* base, const CacheParams& p, int tile) {
   auto enc = tensor_map_encoder();
   if (!enc) return cudaErrorNotSupported;
   cuuint64_t dims[2] = {(cuuint64_t)p.D, (cuuint64_t)p.num_pages * p.Hkv * p.page_size};
   cuuint64_t strides[1] = {(cuuint64_t)p.D * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)(p.page_size < TK ? p.page_size : TK)};
+  cuuint32_t box[2] = {64, (cuuint32_t)(p.page_size < tile ? p.page_size : tile)};
   cuuint32_t es[2] = {1, 1};
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -463,12 +490,12 @@ template <int D, int METHOD, int NT>
 cudaError_t run_tc(const CacheParams& p, cudaStream_t s) {
   auto* k = decode_tc_kernel<D, METHOD, NT>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), Geo<D>::SMEM, done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), (Geo<D, NT>::SMEM), done);
   CUtensorMap mk, mv;
-  if (e == cudaSuccess) e = make_rows_map(&mk, p.k, p);
-  if (e == cudaSuccess) e = make_rows_map(&mv, p.v, p);
+  if (e == cudaSuccess) e = make_rows_map(&mk, p.k, p, tile_keys<D>());
+  if (e == cudaSuccess) e = make_rows_map(&mv, p.v, p, tile_keys<D>());
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3(p.ctas), dim3(kThreads), Geo<D>::SMEM, s, mk, mv, p);
+  return launch_pdl(k, dim3(p.ctas), dim3(kThreads), (Geo<D, NT>::SMEM), s, mk, mv, p);
 }
 
 template <int D, int METHOD>
@@ -490,7 +517,8 @@ cudaError_t run_cap(const CacheParams& p, cudaStream_t s) {
 
 cudaError_t launch_decode_tc(const CacheParams& p0, cudaStream_t s) {
   CacheParams p = p0;
-  const int64_t most = (int64_t)p.B * p.VH * ((p.max_len + TK - 1) / TK);
+  const int tk = 8192 / p.D;
+  const int64_t most = (int64_t)p.B * p.VH * ((p.max_len + tk - 1) / tk);
   p.ctas = (int)(most < 152 * 2 ? most : 152 * 2);
   p.min_tiles = 2;
   return p.D == 64 ? run_cap<64>(p, s) : run_cap<128>(p, s);

@@ -58,10 +58,60 @@ __device__ __forceinline__ int lane_scan(int x, int lane) {
   return x;
 }
 
+constexpr int kSchedSums = 256;
+
+// Batches of more than 64: sums over runs of whole groups of 32 sequences, at most
+// kSchedSums of them, in shared memory (built by all threads of the CTA); returns
+// the units of all sequences.
+__device__ __forceinline__ int run_groups(const CacheParams& p) {
+  return ((p.B + 31) / 32 + kSchedSums - 1) / kSchedSums;
+}
+template <int TK>
+__device__ __noinline__ int sum_large(const CacheParams& p, int warp, int lane, int warps, int* s_sums) {
+  const int run = run_groups(p) * 32, runs = (p.B + run - 1) / run;
+#pragma unroll 4
+  for (int r = warp; r < runs; r += warps) {
+    int sum = 0;
+    for (int x = r * run + lane; x < min(p.B, (r + 1) * run); x += 32) sum += seq_span<TK>(p, x).units;
+    sum = __reduce_add_sync(0xFFFFFFFFu, sum);
+    if (lane == 0) s_sums[r] = sum;
+  }
+  __syncthreads();
+  int all = 0;
+  for (int r = lane; r < runs; r += 32) all += s_sums[r];
+  return __reduce_add_sync(0xFFFFFFFFu, all);
+}
+// The sequence that holds unit `want`, its length as read and the units before it.
+template <int TK>
+__device__ __noinline__ int3 find_large(const CacheParams& p, int lane, const int* s_sums, int want) {
+  const int run = run_groups(p) * 32, runs = (p.B + run - 1) / run;
+  int before = 0, from = 0;
+  for (int r0 = 0; r0 < runs; r0 += 32) {
+    const int x = r0 + lane < runs ? s_sums[r0 + lane] : 0, up = lane_scan(x, lane);
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, want < before + up);
+    if (mask) {
+      from = (r0 + __ffs(mask) - 1) * run;
+      before += __shfl_sync(0xFFFFFFFFu, up - x, __ffs(mask) - 1);
+      break;
+    }
+    before += __shfl_sync(0xFFFFFFFFu, up, 31);
+  }
+  for (int b0 = from; b0 < p.B; b0 += 32) {
+    const int r = b0 + lane < p.B ? p.lens[b0 + lane] : 0;
+    const int x = b0 + lane < p.B ? span_of<TK>(p, r).units : 0, up = lane_scan(x, lane);
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, want < before + up);
+    if (mask) {
+      const int l = __ffs(mask) - 1;
+      return make_int3(b0 + l, __shfl_sync(0xFFFFFFFFu, r, l), before + __shfl_sync(0xFFFFFFFFu, up - x, l));
+    }
+    before += __shfl_sync(0xFFFFFFFFu, up, 31);
+  }
+  return make_int3(p.B - 1, 0, before);
+}
+
 // Walks a CTA's pieces (every lane of a warp alike).
 template <int TK>
 struct PieceIter {
-  static constexpr int kHeld = 4;
   uint32_t units, ctas;           // all units, the CTAs that share them
   uint32_t u, end, begin;         // next unit, this CTA's range
   int b, vh, t0;                  // the next piece: sequence, group, first unit of the group
@@ -72,46 +122,46 @@ struct PieceIter {
   int slot;                // its partial slot, when not whole
   uint32_t s0, s1;         // units [s0, s1) of its (sequence, group)
 
-  __device__ PieceIter(const CacheParams& p, int lane) {
-    // the lengths of the first 128 sequences stay in registers: one round of loads
-    // decides a batch of that size
-    int raw[kHeld], held[kHeld], all = 0;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) raw[i] = lane + 32 * i < p.B ? p.lens[lane + 32 * i] : 0;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      held[i] = lane + 32 * i < p.B ? span_of<TK>(p, raw[i]).units : 0;
-      all += held[i];
+  // All threads of the CTA (whole warps) build it together; s_sums: kSchedSums ints
+  // of shared memory, written by this alone.
+  __device__ PieceIter(const CacheParams& p, int warp, int lane, int warps, int* s_sums) {
+    b = vh = t0 = len = 0;
+    // A batch of 64 stays in registers: one read of lens decides it, in little code
+    // (which every launch fetches anew: unrolled over more sequences, or with the
+    // large batch's path inline, this cost a launch 1 to 3 us).
+    int raw0 = 0, raw1 = 0, n0 = 0, n1 = 0, sum0 = 0, all;
+    const bool small = p.B <= 64;
+    if (small) {
+      if (lane < p.B) raw0 = p.lens[lane];
+      if (lane + 32 < p.B) raw1 = p.lens[lane + 32];
+      if (lane < p.B) n0 = span_of<TK>(p, raw0).units;
+      if (lane + 32 < p.B) n1 = span_of<TK>(p, raw1).units;
+      sum0 = __reduce_add_sync(0xFFFFFFFFu, n0);
+      all = sum0 + __reduce_add_sync(0xFFFFFFFFu, n1);
+    } else {
+      all = sum_large<TK>(p, warp, lane, warps, s_sums);
     }
-    for (int x = lane + 32 * kHeld; x < p.B; x += 32) all += seq_span<TK>(p, x).units;
-    units = (uint32_t)__reduce_add_sync(0xFFFFFFFFu, all) * (uint32_t)p.VH;
+    units = (uint32_t)all * (uint32_t)p.VH;
     ctas = min((uint32_t)p.ctas, max(1u, units / (uint32_t)p.min_tiles));
     begin = u = begin_of(blockIdx.x);
     end = begin_of(blockIdx.x + 1);
-    b = vh = t0 = len = 0;
     if (u >= end) return;
-    const int want = (int)(u / (uint32_t)p.VH);  // the tile, counted over the sequences
-    int before = 0;
-    bool found = false;
-    auto look = [&](int b0, int x, int raw_len) {  // in the sequences b0 + lane
+    const int want = (int)(u / (uint32_t)p.VH);  // counted over the sequences
+    int before;
+    if (small) {
+      const bool low = want < sum0;
+      const int x = low ? n0 : n1;
+      before = low ? 0 : sum0;
       const int up = lane_scan(x, lane);
-      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, want < before + up);
-      const int l = hit ? __ffs(hit) - 1 : 31;
-      if (hit) {
-        found = true;
-        b = b0 + l;
-        len = __shfl_sync(0xFFFFFFFFu, raw_len, l);
-        before += __shfl_sync(0xFFFFFFFFu, up - x, l);
-      } else {
-        before += __shfl_sync(0xFFFFFFFFu, up, 31);
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (!found && 32 * i < p.B) look(32 * i, held[i], raw[i]);
-    for (int b0 = 32 * kHeld; !found && b0 < p.B; b0 += 32) {
-      const int r = b0 + lane < p.B ? p.lens[b0 + lane] : 0;
-      look(b0, b0 + lane < p.B ? span_of<TK>(p, r).units : 0, r);
+      const int hit = __ffs(__ballot_sync(0xFFFFFFFFu, want < before + up)) - 1;
+      before += __shfl_sync(0xFFFFFFFFu, up - x, hit);
+      len = __shfl_sync(0xFFFFFFFFu, low ? raw0 : raw1, hit);
+      b = low ? hit : hit + 32;
+    } else {
+      const int3 f = find_large<TK>(p, lane, s_sums, want);
+      b = f.x;
+      len = f.y;
+      before = f.z;
     }
     const SeqSpan sp = span_of<TK>(p, len);
     const uint32_t in = u - (uint32_t)before * (uint32_t)p.VH;
