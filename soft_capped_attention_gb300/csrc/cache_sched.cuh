@@ -2,19 +2,19 @@
 //
 // The live slots of sequence b are cut into tiles of TK keys; a unit of work is
 // one tile of one (sequence, group of query heads).  Units are numbered
-// sequence by sequence, group by group, tile by tile, and CTA c of n takes units
-// [U c / n, U (c + 1) / n): equal shares whatever the lengths.  A (sequence, group)
-// counts kGroupCost units more than it has tiles (its first ones), about what its
-// end costs (merging the warps, writing, joining): without them the CTAs that get
-// many short sequences finish last.  A CTA's part of one
-// (sequence, group) is a piece; a piece that is not the whole leaves (m, l, O) in
-// the CTA's slot 2c (the piece at the start of its range) or 2c + 1 (the one at
-// its end; pieces between the two are whole), and the join adds the pieces up in
-// order: the CTA that leaves the last piece of a (sequence, group) does it, found
-// by a counter per split group, which belongs to the CTA where the group starts
-// (at most one split group starts in a CTA) and returns to zero.  Pieces are
-// added in the order of their CTAs, whichever comes last.  Every role computes the split from lens by itself, so the lengths stay
-// on the device.
+// sequence by sequence, group by group, tile by tile, and each CTA takes an equal
+// run of them, to one unit, whatever the lengths.  A (sequence, group) counts
+// kGroupCost units more than it has tiles (its first ones) for what its end costs,
+// so that a CTA with many short sequences does not finish last.
+//
+// A CTA's part of one (sequence, group) is a piece; a piece that is not the whole
+// leaves (m, l, O) in the CTA's slot 2c (the piece at the start of its range) or
+// 2c + 1 (the one at its end; pieces between the two are whole).  The CTA that
+// leaves the last piece of a (sequence, group) joins them, in the order of their
+// CTAs whichever came last; it is found by a counter that belongs to the CTA where
+// the group starts (at most one split group starts in a CTA) and returns to zero.
+// Every warp computes the split from lens by itself, so the lengths stay on the
+// device.
 #pragma once
 
 #include "cache_internal.h"
@@ -113,6 +113,7 @@ __device__ __noinline__ int3 find_large(const CacheParams& p, int lane, const in
 template <int TK>
 struct PieceIter {
   uint32_t units, ctas;           // all units, the CTAs that share them
+  uint32_t q, more;               // units / ctas, units % ctas
   uint32_t u, end, begin;         // next unit, this CTA's range
   int b, vh, t0;                  // the next piece: sequence, group, first unit of the group
   int len;                        // lens[b], read ahead of its use
@@ -143,6 +144,8 @@ struct PieceIter {
     }
     units = (uint32_t)all * (uint32_t)p.VH;
     ctas = min((uint32_t)p.ctas, max(1u, units / (uint32_t)p.min_tiles));
+    q = units / ctas;
+    more = units - q * ctas;
     begin = u = begin_of(blockIdx.x);
     end = begin_of(blockIdx.x + 1);
     if (u >= end) return;
@@ -168,13 +171,12 @@ struct PieceIter {
     vh = (int)(in / (uint32_t)sp.units);
     t0 = (int)(in % (uint32_t)sp.units);
   }
-  // First unit of CTA c's range, and the CTA that holds a unit: the largest c with
-  // floor(units c / ctas) <= x.
-  __device__ __forceinline__ uint32_t begin_of(uint32_t c) const {
-    return c >= ctas ? units : (uint32_t)((uint64_t)units * c / ctas);
-  }
+  // First unit of CTA c's range, and the CTA that holds a unit: the first `more` of
+  // them take q + 1 units, the others q.
+  __device__ __forceinline__ uint32_t begin_of(uint32_t c) const { return c >= ctas ? units : q * c + min(c, more); }
   __device__ __forceinline__ int cta_of(uint32_t x) const {
-    return (int)((((uint64_t)x + 1) * ctas - 1) / units);
+    const uint32_t cut = (q + 1) * more;
+    return (int)(x < cut ? x / (q + 1) : more + (x - cut) / q);
   }
   // Gives the piece (b, vh, tiles [tile, tile + n) of the sequence's span).
   __device__ bool next(const CacheParams& p, int* b_out, int* vh_out, int* tile_out, SeqSpan* sp_out) {

@@ -76,6 +76,34 @@ DECODE = [
 ]
 
 
+# batches whose split takes several groups of sequences (and runs of groups)
+LARGE = [(300, 70, 4, 2, 128, BF16), (9000, 20, 2, 1, 64, BF16), (700, 40, 3, 1, 64, FP32)]
+
+
+@pytest.mark.parametrize("B,longest,Hq,Hkv,D,dtype", LARGE, ids=str)
+def test_decode_of_large_batches(B, longest, Hq, Hkv, D, dtype):
+    """Against fp32 on the GPU, every sequence: o within the types' roundings and the
+    terms of check_decode for at most 70 keys (t below 40)."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, longest + 1, (B,), generator=g).tolist()
+    pool = Pool(lens, Hkv, D, 16, dtype, B)
+    q = torch.randn(B, Hq, D, generator=g).to(dtype)
+    ap = params("tanh", D)
+    cache = pool.cuda()
+    o, lse = kv().cache_decode(q.cuda(), cache, ap)
+    n = pool.max_pages * 16
+    gather = lambda x: torch.nan_to_num(x[cache.table.clamp(min=0).long()].transpose(1, 2).reshape(B, Hkv, n, D).double())  # noqa: E731
+    s = torch.einsum("bhgd,bhnd->bhgn", q.cuda().double().reshape(B, Hkv, -1, D), gather(cache.k)) * ap.sm_scale
+    t = ap.cap * torch.tanh(s / ap.cap)
+    live = torch.arange(n, device="cuda") < cache.lens[:, None]
+    t = t.masked_fill(~live[:, None, None], -math.inf)
+    want = torch.einsum("bhgn,bhnd->bhgd", torch.nan_to_num(torch.softmax(t, -1)), gather(cache.v)).reshape(B, Hq, D)
+    half = torch.finfo(dtype).eps / 2
+    assert ((o.double() - want).abs() <= 1.0001 * half * want.abs() + 5 * 2.0 ** -13).all()
+    assert torch.equal(torch.isneginf(lse), torch.isneginf(torch.logsumexp(t, -1).reshape(B, Hq)))
+    assert cache.status() == (0, 0)
+
+
 @pytest.mark.parametrize("acc", [False, True], ids=["plain", "weights"])
 @pytest.mark.parametrize("case", DECODE, ids=lambda c: "-".join(str(x)[:24] for x in c))
 def test_decode(case, acc):
@@ -272,6 +300,26 @@ def test_evict(case, in_place):
     assert torch.equal(bits(cache.k.cpu()), bits(want_k)) and torch.equal(bits(cache.v.cpu()), bits(want_v))
 
 
+def test_evict_past_the_keys_that_fit_shared_memory():
+    """400,000 slots, of which a cluster's shared memory holds fewer; in place."""
+    n, page, budget = 399_990, 1024, 150_001
+    pool = Pool([n], 1, 64, page, BF16, 8)
+    w = (torch.randn(1, 1, pool.max_pages * page, generator=pool.gen) * 3).round()  # many ties
+    cache = pool.cuda(weights=w)
+    before = cache.k.clone()
+    src = kv().cache_evict(cache, budget, 3, 1000).cpu()[0, 0]
+    want = torch.tensor(evict_row(w[0, 0].tolist(), None, n - 1, n, budget, 3, 1000), dtype=torch.int32)
+    assert torch.equal(src, want)
+    assert cache.lens.tolist() == [budget]
+    assert torch.equal(cache.weights[0, 0, :budget].cpu(), w[0, 0][want.long()])
+    table = cache.table[0].long()
+    at = lambda j: (table[j // page], j % page)  # noqa: E731
+    new, old = torch.arange(budget, device="cuda"), want.long().cuda()
+    (p0, s0), (p1, s1) = at(new), at(old)
+    assert torch.equal(cache.k[p0, 0, s0].view(torch.int16), before[p1, 0, s1].view(torch.int16))
+    assert cache.status() == (0, 0)
+
+
 WEIGHTS = [
     # B, L, Lk, Hq, Hkv, D, dtype, cap, causal, window, temp, mask, rows
     (1, 1, 1, 1, 1, 128, BF16, "none", True, 0, False, None, None),
@@ -282,6 +330,8 @@ WEIGHTS = [
     (1, 100, 333, 4, 4, 128, BF16, "alsc", False, 0, False, None, None),
     (1, 333, 100, 4, 2, 128, BF16, "none", True, 30, False, None, None),
     (1, 700, 700, 2, 1, 128, BF16, "tanh", True, 0, True, "seg", None),
+    (1, 2500, 2500, 4, 2, 64, BF16, "alsc", True, 0, False, None, [[100, 2400]]),
+    (3, 640, 640, 6, 3, 128, BF16, "none", True, 200, True, None, [[0, 640], [639, 640], [128, 512]]),
     (2, 150, 150, 4, 2, 64, FP32, "tanh", True, 0, True, None, [[1, 2], [0, 150]]),
     (1, 129, 129, 2, 2, 128, FP32, "alsc", False, 0, False, "ranker", None),
     (1, 65, 200, 2, 2, 64, FP32, "soft_sign", False, 9, False, None, None),
@@ -509,6 +559,52 @@ def test_calls_on_a_given_stream():
     side.synchronize()
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     assert cache.status(stream=side) == (0, 0)
+
+
+def test_two_caches_over_the_same_tensors_on_two_streams():
+    """Calls that overlap need a KVCache each; the tensors may be the same."""
+    pool = Pool([5000, 3100], 2, 128, 16, BF16, 21)
+    ap = params("tanh", 128)
+    q = [torch.randn(2, 8, 128).to(BF16).cuda() for _ in range(2)]
+    one = pool.cuda()
+    two = kv().KVCache(one.k, one.v, one.table, one.lens)
+    want = [kv().cache_decode(x, one, ap) for x in q]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, cache in enumerate((one, two)):
+            got[i].append(kv().cache_decode(q[i], cache, ap, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1]) for o, lse in got[i])
+
+
+def test_a_graph_outlives_a_larger_workspace():
+    """A graph captured before the cache's workspace grew still replays, and a growth
+    during a capture is refused."""
+    pool = Pool([900, 333], 2, 128, 16, BF16, 22)
+    ap = params("alsc", 128)
+    q = torch.randn(2, 4, 128).to(BF16).cuda()
+    cache = pool.cuda(weights=torch.zeros(2, 2, pool.max_pages * 16))
+    want, _ = kv().cache_decode(q, cache, ap)
+    out = (torch.zeros_like(want), torch.zeros(2, 4, device="cuda"))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kv().cache_decode(q, cache, ap, out=out)
+    with pytest.raises(RuntimeError, match="grow"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            kv().cache_decode(q, cache, ap, accumulate=True, out=out)
+    torch.cuda.synchronize()
+    kv().cache_decode(q, cache, ap, accumulate=True)
+    filler = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    out[0].zero_()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], want) and len(filler) == 64
+    total = cache.weights[0, 0, :900].sum().item()  # two query heads a group, one step
+    assert abs(total - 2.0) < 1e-4 and cache.status() == (0, 0)
 
 
 def test_empty_batch_of_rows_appends_nothing():

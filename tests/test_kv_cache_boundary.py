@@ -5,6 +5,8 @@ before it launches anything."""
 import ctypes
 import os
 import re
+import shutil
+import subprocess
 
 import pytest
 import torch
@@ -42,6 +44,18 @@ def test_header_and_library_agree(lib):
     assert names == set(kv.EXPORTED_SYMBOLS)
     for n in names:
         assert hasattr(lib, n), n
+
+
+def test_the_header_is_plain_c(tmp_path):
+    gcc, cuda = shutil.which("gcc"), "/usr/local/cuda/include"
+    if gcc is None or not os.path.exists(os.path.join(cuda, "cuda_runtime_api.h")):
+        pytest.skip("gcc or the CUDA headers are not available")
+    src = tmp_path / "c.c"
+    src.write_text('#include "capattn_cache.h"\nint main(void) { capattn_cache_config c = {0};'
+                   ' return (int)sizeof(c) - 60 + (int)capattn_cache_validate_config(0); }\n')
+    subprocess.run([gcc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-fsyntax-only", "-I", os.path.join(ROOT, "include"),
+                    "-isystem", cuda, str(src)], check=True)
+    assert ctypes.sizeof(kv.CacheConfig) == 60
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -136,6 +150,16 @@ def weights_args(**kw):
 ], ids=str)
 def test_key_weights_refusals(lib, kw, status):
     assert lib.capattn_key_weights(*weights_args(**kw)) == status
+
+
+def test_key_weights_workspace_holds_the_forwards(lib):
+    for dtype in (torch.bfloat16, torch.float32):
+        c = ca.make_config(ca.AttnParams(sm_scale=0.1), 3, 1000, 4, 2, 64, dtype)
+        n = lib.capattn_key_weights_workspace_bytes(ctypes.byref(c))
+        assert n > lib.capattn_workspace_bytes(ctypes.byref(c), ca.PASS_FWD)
+        assert lib.capattn_key_weights(*weights_args(wb=lib.capattn_workspace_bytes(ctypes.byref(c), 0))) == 5
+    c.D = 96
+    assert lib.capattn_key_weights_workspace_bytes(ctypes.byref(c)) == 0
 
 
 def test_python_refuses_a_cache_off_the_gpu():
