@@ -8,8 +8,9 @@
 // K stays in shared memory for a unit (two buffers), Q tiles stream through a ring
 // by TMA, and tcgen05 forms S^T = K Q^T (128 keys x 128 queries, four TMEM buffers)
 // with a key per TMEM lane, so that the sum over queries is a sum within a thread:
-// no transposition, no atomics.  Sixteen warps read it (four warpgroups, 32 query
-// columns each), cap, exponentiate and add.  A unit that two CTAs share leaves
+// no transposition, no atomics.  Sixteen warps read it, cap, exponentiate and add:
+// four warpgroups, two for the even steps and two for the odd ones, 64 query columns
+// each.  A unit that two CTAs share leaves
 // partial sums, which the last of them adds in order.
 //
 // What bounds it: one exp2 per pair on the MUFU pipe (16 a clock and SM, against
@@ -17,8 +18,10 @@
 // issue slots of the cap's polynomial; there is no second product and nothing is
 // stored.
 //
-// Sums: 32 columns in fp32, then compensated (Kahan) over the steps: a prompt of
+// Sums: 32 columns in fp32, then compensated (Kahan) over those: a prompt of
 // 131072 rows adds as exactly as a short one.
+#include <limits.h>
+
 #include "cache_internal.h"
 #include "cache_math.cuh"
 #include "tc_common.cuh"
@@ -258,7 +261,10 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   __shared__ __align__(16) float col_add[NCONST][BT], col_temp[TEMP ? NCONST : 1][BT];
   __shared__ __align__(16) int2 col_span[NCONST][BT];
   __shared__ int col_extra[NCONST][BT];
-  __shared__ int col_masked[NCONST];
+  // (least and largest lo, least and largest hi) over the live spans of 32 columns;
+  // a column without live keys makes the largest lo and the least hi impossible
+  __shared__ __align__(16) int4 col_range[NCONST][BT / 32];
+  __shared__ int col_masked[NCONST];  // whether any pair of the step is dead
   __shared__ float s_sum[2][kElem / 4][BT];
   __shared__ Start s_start;
   __shared__ uint64_t s_scan[kThreads / 32];
@@ -284,7 +290,7 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     }
     for (int u = 0; u < NBUF; ++u) {
       mbar_init(bar_s + 8 * u, 1 + 32 * kConst);
-      mbar_init(bar_free + 8 * u, kElem);
+      mbar_init(bar_free + 8 * u, kElem / 2);
     }
     fence_mbar_init();
   }
@@ -423,15 +429,24 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           ok = false;
           break;
         }
+        const bool step_masked = !(kt >= cur.full.x && kt < cur.full.y);
+        if (c0 == 0) col_masked[c] = step_masked;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const int col = c0 + 32 * y;
           col_add[c][col] = cur.lse[y] == -INFINITY ? 0.f : -cur.lse[y] * kL2E;
           if (TEMP) col_temp[c][col] = cur.temp[y];
           col_span[c][col] = make_int2(cur.span[y].x, cur.span[y].y - cur.span[y].x);
+          if (!step_masked) continue;
           if (p.bounds) col_extra[c][col] = cur.span[y].z;
+          const bool some = cur.span[y].y > cur.span[y].x;
+          int4 range;
+          range.x = __reduce_min_sync(0xFFFFFFFFu, some ? cur.span[y].x : INT_MAX);
+          range.y = __reduce_max_sync(0xFFFFFFFFu, some ? cur.span[y].x : INT_MAX);
+          range.z = __reduce_min_sync(0xFFFFFFFFu, some ? cur.span[y].y : INT_MIN);
+          range.w = __reduce_max_sync(0xFFFFFFFFu, some ? cur.span[y].y : INT_MIN);
+          if (lane == 0) col_range[c][col >> 5] = range;
         }
-        if (c0 == 0) col_masked[c] = !(kt >= cur.full.x && kt < cur.full.y);
         mbar_arrive(bar_s + 8 * c);
         ++step;
         cur = nxt;
@@ -480,50 +495,66 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     // ------------------------------------------------------------ elementwise
     const int wg = (warp - 2) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;                   // key of the tile
-    const uint32_t cols_t = tmem + ((uint32_t)(quarter * 32) << 16) + 32u * wg;
+    const uint32_t mine = wg >> 1;                       // the steps it takes: even or odd ones
+    const int half = 64 * (wg & 1);                      // its columns of them
+    const uint32_t cols_t = tmem + ((uint32_t)(quarter * 32) << 16) + half;
     const Poly<METHOD> poly(kw.cap);
     int parity = 0;
     bool ok = true;  // after a timeout the warp still meets the others at every unit's barriers
     while (it.next(p, kw, &e, &g)) {
       const int b = e / p.nk, k0 = (e % p.nk) * BT, j = k0 + r;
       float sum = 0.f, comp = 0.f;
-      for (int i = 0; i < it.n; ++i, ++step) {
-        const int u = step % NBUF, c = u;
+      const uint32_t end = step + it.n;
+      for (step += (step & 1) ^ mine; step < end; step += 2) {
+        const int u = step % NBUF;
         ok = ok && mbar_wait_warp(bar_s + 8 * u, (step / NBUF) & 1, p.status, &abort_flag);
         if (!ok) break;
         tc_fence_after();
-        const bool masked = col_masked[c] != 0;
-        uint32_t x[32];
-        tmem_ld32(cols_t + u * BT, x);
-        tmem_wait_ld();
-        bool fast = true;
-        if constexpr (has_poly(METHOD)) {
-          float am = 0.f;
+        const bool step_masked = col_masked[u] != 0;
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 32) {
+          bool masked = step_masked;
+          if (step_masked) {
+            // this warp's keys [j - lane, j - lane + 32) against the columns' spans: all
+            // live, none (skipped), or a test a pair
+            const int4 range = col_range[u][(half + c) >> 5];
+            const int first = j - lane;
+            if (!p.bounds && (first + 31 < range.x || first >= range.w)) continue;
+            masked = first < range.y || first + 32 > range.z;
+          }
+          uint32_t x[32];
+          tmem_ld32(cols_t + u * BT + c, x);
+          tmem_wait_ld();
+          bool fast = true;
+          if constexpr (has_poly(METHOD)) {
+            float am = 0.f;
 #pragma unroll
-          for (int y = 0; y < 32; y += 2) am = fmax3_abs(am, __uint_as_float(x[y]), __uint_as_float(x[y + 1]));
-          fast = __all_sync(0xFFFFFFFFu, am <= kw.cap.xmax && kw.cap.xmax > 0.f);
+            for (int y = 0; y < 32; y += 2) am = fmax3_abs(am, __uint_as_float(x[y]), __uint_as_float(x[y + 1]));
+            fast = __all_sync(0xFFFFFFFFu, am <= kw.cap.xmax && kw.cap.xmax > 0.f);
+          }
+          const float* ad = &col_add[u][half + c];
+          const float* tp = &col_temp[TEMP ? u : 0][half + c];
+          const int2* sp = &col_span[u][half + c];
+          const int* ex = &col_extra[u][half + c];
+          float part;
+          if (!masked)
+            part = fast ? chunk_sum<METHOD, TEMP, 0, true>(x, ad, tp, sp, ex, j, poly, kw.cap)
+                        : chunk_sum<METHOD, TEMP, 0, false>(x, ad, tp, sp, ex, j, poly, kw.cap);
+          else if (!p.bounds)
+            part = fast ? chunk_sum<METHOD, TEMP, 1, true>(x, ad, tp, sp, ex, j, poly, kw.cap)
+                        : chunk_sum<METHOD, TEMP, 1, false>(x, ad, tp, sp, ex, j, poly, kw.cap);
+          else
+            part = fast ? chunk_sum<METHOD, TEMP, 2, true>(x, ad, tp, sp, ex, j, poly, kw.cap)
+                        : chunk_sum<METHOD, TEMP, 2, false>(x, ad, tp, sp, ex, j, poly, kw.cap);
+          const float y = part - comp, t = sum + y;
+          comp = (t - sum) - y;
+          sum = t;
         }
-        const float* ad = &col_add[c][32 * wg];
-        const float* tp = &col_temp[TEMP ? c : 0][32 * wg];
-        const int2* sp = &col_span[c][32 * wg];
-        const int* ex = &col_extra[c][32 * wg];
-        float part;
-        if (!masked)
-          part = fast ? chunk_sum<METHOD, TEMP, 0, true>(x, ad, tp, sp, ex, j, poly, kw.cap)
-                      : chunk_sum<METHOD, TEMP, 0, false>(x, ad, tp, sp, ex, j, poly, kw.cap);
-        else if (!p.bounds)
-          part = fast ? chunk_sum<METHOD, TEMP, 1, true>(x, ad, tp, sp, ex, j, poly, kw.cap)
-                      : chunk_sum<METHOD, TEMP, 1, false>(x, ad, tp, sp, ex, j, poly, kw.cap);
-        else
-          part = fast ? chunk_sum<METHOD, TEMP, 2, true>(x, ad, tp, sp, ex, j, poly, kw.cap)
-                      : chunk_sum<METHOD, TEMP, 2, false>(x, ad, tp, sp, ex, j, poly, kw.cap);
-        const float y = part - comp, t = sum + y;
-        comp = (t - sum) - y;
-        sum = t;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_free + 8 * u);
       }
+      step = end;
       // ------------------------------------------------------ end of a piece
       // The first warpgroup adds the four up and writes; the others go on.  (s_sum
       // alternates: it is written again only after the next piece's barrier.)
@@ -533,12 +564,12 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       named_bar_sync(1, 32 * kElem);
       if (wg != 0) continue;
       float* w = kw.w + ((size_t)b * p.Hkv + g) * kw.w_stride + k0;
-      const float mine = (sums[0][r] + sums[1][r]) + (sums[2][r] + sums[3][r]);
+      const float all = (sums[0][r] + sums[1][r]) + (sums[2][r] + sums[3][r]);
       if (it.whole) {
-        if (j < p.Lk) w[r] = mine;
+        if (j < p.Lk) w[r] = all;
         continue;
       }
-      kw.partial[(size_t)it.slot * BT + r] = mine;
+      kw.partial[(size_t)it.slot * BT + r] = all;
       __threadfence();
       named_bar_sync(2, BT);
       const int c0 = it.sh.cta_of(it.s0), c1 = it.sh.cta_of(it.s1 - 1);
