@@ -86,7 +86,7 @@ select_kernel(CacheParams p, int parts) {
     if (parts > 1) cluster.sync(); else __syncthreads();
   };
   const int rank = blockIdx.x % parts, row = blockIdx.x / parts;
-  const int b = row / p.Hkv, g = row % p.Hkv;
+  const int b = row / p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < 4 * kBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
   pdl_trigger();
@@ -347,30 +347,41 @@ move_kernel(CacheParams p, int vph_shift) {
   uint4* k = static_cast<uint4*>(p.k);
   uint4* v = static_cast<uint4*>(p.v);
   const int stride = gridDim.y * per;
-  for (int i = blockIdx.y * per + (threadIdx.x >> vph_shift); i < c.x; i += 2 * stride) {
-    int2 m[2], r[2];
-    uint4 a[2], d[2];
+  constexpr int N = 2;
+  for (int i = blockIdx.y * per + (threadIdx.x >> vph_shift); i < c.x; i += N * stride) {
+    int2 m[N];
+    int to[N], from[N], x[N];
+    float w[N];
+    uint4 a[N], d[N];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) m[u] = i + u * stride < c.x ? moves[i + u * stride] : make_int2(-1, -1);
+    for (int u = 0; u < N; ++u) m[u] = i + u * stride < c.x ? moves[i + u * stride] : make_int2(-1, -1);
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-      r[u] = m[u].x >= 0 ? make_int2(cache_row(p, b, g, m[u].x), cache_row(p, b, g, m[u].y)) : make_int2(-1, -1);
+    for (int u = 0; u < N; ++u) {
+      to[u] = from[u] = -1;
+      if (m[u].x < 0) continue;
+      to[u] = cache_row(p, b, g, m[u].x);
+      from[u] = cache_row(p, b, g, m[u].y);
+      if (at == 0) {
+        w[u] = p.weights[base + m[u].y];
+        if (p.pos_out) x[u] = p.pos[base + m[u].y];
+      }
+    }
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-      if (r[u].x >= 0 && r[u].y >= 0) {
-        a[u] = __ldcs(k + ((size_t)r[u].y << vph_shift) + at);
-        d[u] = __ldcs(v + ((size_t)r[u].y << vph_shift) + at);
+    for (int u = 0; u < N; ++u)
+      if (to[u] >= 0 && from[u] >= 0) {
+        a[u] = __ldcs(k + ((size_t)from[u] << vph_shift) + at);
+        d[u] = __ldcs(v + ((size_t)from[u] << vph_shift) + at);
       }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < N; ++u) {
       if (at == 0 && m[u].x >= 0) {
         src[m[u].x] = m[u].y;
-        p.weights_out[base + m[u].x] = p.weights[base + m[u].y];
-        if (p.pos_out) p.pos_out[base + m[u].x] = p.pos[base + m[u].y];
+        p.weights_out[base + m[u].x] = w[u];
+        if (p.pos_out) p.pos_out[base + m[u].x] = x[u];
       }
-      if (r[u].x >= 0 && r[u].y >= 0) {
-        k[((size_t)r[u].x << vph_shift) + at] = a[u];
-        v[((size_t)r[u].x << vph_shift) + at] = d[u];
+      if (to[u] >= 0 && from[u] >= 0) {
+        k[((size_t)to[u] << vph_shift) + at] = a[u];
+        v[((size_t)to[u] << vph_shift) + at] = d[u];
       }
     }
   }
@@ -408,7 +419,8 @@ cudaError_t launch_cache_evict(const CacheParams& p, int dtype, cudaStream_t s) 
   while ((1 << shift) < vph) ++shift;
   const int per = kMoveThreads >> shift;
   const int most = min(p.budget, max(1, p.max_len - p.budget));  // rows that can move
-  const int y = min(max(1, (152 * 8 + rows - 1) / rows), (most + 2 * per - 1) / (2 * per));
+  // eight CTAs an SM, no more than there can be moves
+  const int y = min(max(1, 152 * 8 / rows), (most + 2 * per - 1) / (2 * per));
   return launch_pdl(move_kernel, dim3(rows, y), dim3(kMoveThreads), 0, s, p, shift);
 }
 
