@@ -187,6 +187,7 @@ class KVCache:
         self.k, self.v, self.table, self.lens = k, v, table, lens
         self.weights, self.pos, self.qpos = weights, pos, qpos
         self._slots = torch.Size(slots)
+        self._seen = (k, v, table, lens)  # checked above
         self._plans = {}       # by (Hq, AttnParams)
         self._workspaces = []  # the last one is used; earlier ones may live in captured graphs
 
@@ -213,13 +214,18 @@ class KVCache:
         return self._workspaces[-1]
 
     def _tensors(self):
-        """Addresses of the cache's own tensors, checked again: they are the caller's
-        to replace."""
-        B, dev = self.B, self.device
-        if not (_fits(self.k, self._k_shape, self.dtype, dev) and _fits(self.v, self._k_shape, self.dtype, dev)):
-            raise ValueError(f"the cache's k and v have to stay {tuple(self._k_shape)} {self.dtype} on {dev}")
-        return (self.k.data_ptr(), self.v.data_ptr(),
-                _want(self.table, "table", (B, self.max_pages), torch.int32, dev), _want(self.lens, "lens", (B,), torch.int32, dev))
+        """Addresses of the cache's own tensors.  They are the caller's to replace: a
+        new one is checked as the first was."""
+        k, v, table, lens = now = (self.k, self.v, self.table, self.lens)
+        seen = self._seen
+        if k is not seen[0] or v is not seen[1] or table is not seen[2] or lens is not seen[3]:
+            B, dev = self.B, self.device
+            if not (_fits(k, self._k_shape, self.dtype, dev) and _fits(v, self._k_shape, self.dtype, dev)):
+                raise ValueError(f"the cache's k and v have to stay {tuple(self._k_shape)} {self.dtype} on {dev}")
+            _want(table, "table", (B, self.max_pages), torch.int32, dev)
+            _want(lens, "lens", (B,), torch.int32, dev)
+            self._seen = now
+        return k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr()
 
     def _positions(self):
         if self.pos is None:
@@ -291,7 +297,7 @@ def cache_decode(q, cache: KVCache, ap: AttnParams, temp=None, accumulate=False,
     pos, qpos = cache._positions()
     plan = cache.plan(Hq, ap)
     if out is None:
-        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        o = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=q.dtype, device=dev)
         lse = torch.empty((cache.B, Hq), dtype=torch.float32, device=dev)
     else:
         o, lse = out

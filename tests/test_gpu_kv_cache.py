@@ -442,6 +442,13 @@ def test_refusals_of_the_binding():
     ]:
         with pytest.raises(ValueError, match=match):
             call()
+    good, cache.lens = cache.lens, cache.lens.long()  # a replaced tensor is checked too
+    with pytest.raises(ValueError, match="lens: want"):
+        kv().cache_decode(q, cache, ap)
+    cache.lens, cache.k = good, cache.k[:-1]
+    with pytest.raises(ValueError, match="k and v"):
+        kv().cache_append(cache, new, new)
+    cache.k = cache.v.clone()
     with pytest.raises(ca.CapattnError, match="invalid argument"):
         kv().cache_decode(torch.zeros(2, 5, 128, dtype=BF16, device="cuda"), cache, ap)
     cache = pool.cuda(weights=torch.zeros(2, 2, 112))
