@@ -6,6 +6,9 @@
 // O = sum e^(t - m) v_j, kept as a running triple; o = O / l, lse = m + log l.
 // Pieces (m_i, l_i, O_i) of a split join as M = max m_i, l = sum l_i e^(m_i - M),
 // O likewise.
+//   fp32 stays on the CUDA cores (a TF32 product keeps 11 bits of q and k).  Memory
+// bounds a group of one head (4 sequences of 16,000 keys x 8 heads, D = 128, 524 MB:
+// 97 us, 5.4 TB/s), the products a larger one (4 heads: 125 us, 16 heads: 385 us).
 #include "cache_internal.h"
 #include "cache_math.cuh"
 #include "cache_sched.cuh"

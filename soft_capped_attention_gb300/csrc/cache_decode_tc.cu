@@ -2,7 +2,11 @@
 //
 // What bounds it: every cached key and value is read once, 4 D bytes a token and
 // KV head against 4 D G operations, so memory does at any group size G of up to
-// 16; the kernel's task is to keep the loads in flight.  A persistent grid, two
+// 16; the kernel's task is to keep the loads in flight.  Measured: 130,977 keys of 8
+// heads (D = 128, 537 MB) in 85 us, 6.3 TB/s, 93 % of the measured copy rate; 32 users
+// of 1024 to 3968 keys (82 MB) in 16 us, 5.1 TB/s; 64 sequences in a window of 1024
+// (240 MB) in 45 us, 5.3 TB/s (of a consumer warp's 80,000 cycles 34,000 compute,
+// 32,000 wait for memory and 14,000 are the starts, ends and joins of its pieces).  The CUDA-core form of the fp32 kernel took 230, 47 and 120 us.  A persistent grid, two
 // CTAs an SM, takes equal shares of 64-key tiles (cache_sched.cuh).  In each CTA
 // one warp fills a ring of shared-memory stages by TMA (a tile's pages are boxes
 // of up to a tile's rows x 64 columns in the 128-byte swizzle) and four warps compute,
@@ -19,7 +23,9 @@
 //   S^T = K Q^T  keys are the rows: K by ldmatrix, Q's fragments stay in registers
 //   t = temp cap(sm_scale S), P = e^(t - m)
 //   O^T += V^T P^T  V by ldmatrix.trans, P^T by transposing its accumulators
-//                8 x 8 (movmatrix).  P goes in as two bf16 halves (P = hi + lo,
+//                8 x 8 (movmatrix).  (With the heads as rows, half of them empty for
+//                groups of 8, the mma pipe was 79 % busy: 60 us for the windowed
+//                batch against 50.)  P goes in as two bf16 halves (P = hi + lo,
 //                2^-17 of it lost): rounding P to one bf16 would add half of what
 //                rounding o to bf16 does.
 // The reference m moves only when the maximum outgrows it by kSlack (P stays

@@ -23,6 +23,7 @@
 namespace capattn {
 
 constexpr int kGroupCost = 1;
+static_assert(kGroupCost >= 1, "an empty sequence has to belong to a CTA too");
 
 struct SeqSpan {
   int32_t first, len;    // live slots [first, len) (before the test of pos)

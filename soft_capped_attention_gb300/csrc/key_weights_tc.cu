@@ -13,10 +13,20 @@
 // each.  A unit that two CTAs share leaves
 // partial sums, which the last of them adds in order.
 //
-// What bounds it: one exp2 per pair on the MUFU pipe (16 a clock and SM, against
-// the 32 pairs a clock that the tensor cores could deliver at D = 128), then the
-// issue slots of the cap's polynomial; there is no second product and nothing is
-// stored.
+// What bounds it: the elementwise pass.  There is no second product and nothing is
+// stored; the tensor cores need 260 cycles for a step of 128 x 128 pairs, the exp2s
+// 512 on the MUFU pipe (32 a clock and SM), the cap's polynomial and the sums 900
+// (tanh; 7 products a pair at 128 a clock) to 1150 (alsc with temperatures).  Measured
+// are about 1800 cycles a step on a long prompt (8192 rows, 32 heads: 412 us, 667
+// TFLOP/s at 2 D a live pair), the issue slots 52 % used, and about
+// 12 us of launches and first loads (two prompts of 2048 x 16 heads: 37 us in all;
+// 4096 rows x 32 heads in a window of 1024 with alsc and temperatures: 74 us).
+//   Tried: the steps of a key tile cut over clusters of up to 8 CTAs instead of the
+// persistent shares (58 us for the two prompts: two steps a CTA, mostly prologue);
+// constants loaded by the TMA warp (40 us: the MMAs waited for it); one step for all
+// sixteen warps, 32 columns each (38 -> 40 us: the waits are paid per 32 columns);
+// 16-column chunks (41 us); both chunks of a step unrolled (42 us: more code than the
+// instruction caches like).
 //
 // Sums: 32 columns in fp32, then compensated (Kahan) over those: a prompt of
 // 131072 rows adds as exactly as a short one.
@@ -79,9 +89,11 @@ key_plan_kernel(Params p, KeyWeightsParams kw) {
 
 // The units' steps, shared out: CTA c of n takes steps [U c / n, U (c + 1) / n) of
 // all U, numbered by (batch, key tile), KV head, step.  A unit counts kUnitCost steps
-// more than it has (its first ones), which is about what starting and ending it
-// costs: the last key tiles of a causal prompt have one step a head.
-constexpr int kUnitCost = 2;
+// more than it has (its first ones), about what starting and ending it costs: the
+// last key tiles of a causal prompt have one step a head (two prompts of 2048: 37 us
+// with 1, 39 with 2, 40 with 4).  At least 1: a unit without steps has zeros to write.
+constexpr int kUnitCost = 1;
+static_assert(kUnitCost >= 1, "every unit has to belong to a CTA");
 struct Share {
   uint64_t total;
   uint32_t ctas;
