@@ -166,6 +166,7 @@ struct PieceIter {
       b = f.x;
       len = f.y;
       before = f.z;
+      __syncthreads();  // every warp has read s_sums (all of them get here: the range is the CTA's)
     }
     const SeqSpan sp = span_of<TK>(p, len);
     const uint32_t in = u - (uint32_t)before * (uint32_t)p.VH;

@@ -160,7 +160,9 @@ class KVCache:
     (positions of the cached tokens and of each sequence's newest one).  All of
     them are the caller's; the cache adds one workspace, which grows to what its
     calls need.  Calls that may overlap on the GPU (two streams, two captured
-    graphs) need a KVCache each (the tensors may be the same)."""
+    graphs) need a KVCache each (the tensors may be the same); keep a KVCache until
+    the work that it enqueued on other streams has finished.  The calls are for
+    serving: they record no gradients."""
 
     def __init__(self, k, v, table, lens, weights=None, pos=None, qpos=None):
         if k.dim() != 4 or table.dim() != 2:
