@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -353,12 +354,20 @@ def cache_evict(cache: KVCache, budget: int, keep_first: int = 0, keep_last: int
     return src
 
 
-def new_key_weights_workspace(q, k, ap: AttnParams) -> torch.Tensor:
-    """Workspace of key_weights for q [B, L, Hq, D] and k [B, Lk, Hkv, D]."""
-    cfg = _ca._config(q, k, ap)
+@functools.lru_cache(maxsize=64)
+def _prompt_plan(ap: AttnParams, B: int, L: int, Hq: int, Hkv: int, D: int, dtype: torch.dtype, Lk: int):
+    """A checked configuration of key_weights, its reference and workspace bytes."""
+    cfg = _ca.make_config(ap, B, L, Hq, Hkv, D, dtype, Lk=Lk)
     n = int(lib().capattn_key_weights_workspace_bytes(ctypes.byref(cfg)))
     if n == 0:
         _ca._check(lib().capattn_validate_config(ctypes.byref(cfg)), "capattn_key_weights_workspace_bytes")
+    return cfg, ctypes.byref(cfg), n
+
+
+def new_key_weights_workspace(q, k, ap: AttnParams) -> torch.Tensor:
+    """Workspace of key_weights for q [B, L, Hq, D] and k [B, Lk, Hkv, D]."""
+    B, L, Hq, D = q.shape
+    n = _prompt_plan(ap, B, L, Hq, k.shape[2], D, q.dtype, k.shape[1])[2]
     ws = torch.empty(n, dtype=torch.uint8, device=q.device)
     ws[:256].zero_()  # the status word
     return ws
@@ -372,30 +381,33 @@ def key_weights(q, k, lse, ap: AttnParams, temp=None, seg=None, bounds=None, row
     counted query rows lo <= i < hi (None: all).  Returns w [B, Hkv, W] fp32, W =
     Lk, or `out` with W >= Lk (a cache's weights, for instance), of which the
     entries j < Lk are overwritten."""
-    cfg = _ca._config(q, k, ap)
-    B, L, Hq, D = q.shape
-    Lk, Hkv, dev = k.shape[1], k.shape[2], q.device
-    _want(q, "q", q.shape, q.dtype, dev)
-    _want(k, "k", (B, Lk, Hkv, D), q.dtype, dev)
-    _want(lse, "lse", (B, Hq, L), torch.float32, dev)
-    _want(temp, "temp", (B, L), torch.float32, dev)
-    _want(seg, "seg", (B, L), torch.int32, dev)
-    _want(bounds, "bounds", (B, 4), torch.int32, dev)
-    _want(rows, "rows", (B, 2), torch.int32, dev)
+    dev = q.device
     if dev.type != "cuda":
         raise ValueError(f"q has to be on a GPU, got {dev}")
-    if out is not None and (out.dim() != 3 or out.shape[2] < Lk):
+    s = _raw_stream(dev, stream)
+    if s is None:
+        with _on(dev, stream):
+            return key_weights(q, k, lse, ap, temp, seg, bounds, rows, out, workspace)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q is [B, L, Hq, D] and k [B, Lk, Hkv, D]")
+    B, L, Hq, D = q.shape
+    Lk, Hkv = k.shape[1], k.shape[2]
+    qp = _want(q, "q", q.shape, q.dtype, dev)
+    kp = _want(k, "k", (B, Lk, Hkv, D), q.dtype, dev)
+    lp = _want(lse, "lse", (B, Hq, L), torch.float32, dev)
+    tp = _want(temp, "temp", (B, L), torch.float32, dev)
+    sp = _want(seg, "seg", (B, L), torch.int32, dev)
+    bp = _want(bounds, "bounds", (B, 4), torch.int32, dev)
+    rp = _want(rows, "rows", (B, 2), torch.int32, dev)
+    cfg, ref, _ = _prompt_plan(ap, B, L, Hq, Hkv, D, q.dtype, Lk)
+    if out is None:
+        out = torch.empty((B, Hkv, Lk), dtype=torch.float32, device=dev)
+    elif out.dim() != 3 or out.shape[2] < Lk:
         raise ValueError(f"out is [B, Hkv, W] with W >= {Lk}, got {tuple(out.shape)}")
-    if out is not None:
-        _want(out, "out", (B, Hkv, out.shape[2]), torch.float32, dev)
-    with _on(dev, stream):
-        if workspace is None:
-            workspace = new_key_weights_workspace(q, k, ap)
-        if out is None:
-            out = torch.empty(B, Hkv, Lk, dtype=torch.float32, device=dev)
-        st = lib().capattn_key_weights(
-            ctypes.byref(cfg), _ca._ptr(q), _ca._ptr(k), _ca._ptr(lse), _ca._ptr(temp), _ca._ptr(seg),
-            _ca._ptr(bounds), _ca._ptr(rows), _ca._ptr(out), out.shape[2], _ca._ptr(workspace),
-            workspace.numel(), torch.cuda.current_stream().cuda_stream)
+    W = out.shape[2]
+    op = _want(out, "out", (B, Hkv, W), torch.float32, dev)
+    if workspace is None:
+        workspace = new_key_weights_workspace(q, k, ap)
+    st = lib().capattn_key_weights(ref, qp, kp, lp, tp, sp, bp, rp, op, W, workspace.data_ptr(), workspace.numel(), s)
     _ca._check(st, "capattn_key_weights")
     return out

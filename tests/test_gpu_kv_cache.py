@@ -171,6 +171,16 @@ def test_decode_reads_pages_past_32_bit_offsets():
     o64, lse64, add64, et = decode64(q, pool.k, pool.v, pool.table, [201], ap)
     o, lse = kv().cache_decode(q.cuda(), cache, ap)
     check_decode((o, lse), (o64, lse64, add64), et, 5.0, BF16, 201)
+    w = torch.rand(1, 2, 256)
+    cache.weights = w.cuda()
+    before = big[last].cpu()  # the sequence's four pages
+    src = kv().cache_evict(cache, 90, 2, 20).cpu()
+    after = big[last].cpu()
+    for h in range(2):
+        want = evict_row(w[0, h].tolist(), None, 200, 201, 90, 2, 20)
+        assert src[0, h].tolist() == want
+        for dst, old in enumerate(want):
+            assert torch.equal(after[dst // 64, h, dst % 64], before[old // 64, h, old % 64])
     assert cache.status() == (0, 0)
 
 
