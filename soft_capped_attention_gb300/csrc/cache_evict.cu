@@ -81,6 +81,9 @@ __device__ __forceinline__ int cache_row(const CacheParams& p, int b, int g, int
   return ((page * p.Hkv + g) << p.page_shift) + (slot & (p.page_size - 1));
 }
 
+// CACHED: a CTA's keys fit its shared memory (else they are computed anew in every
+// pass).
+template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads, 1)
 select_kernel(CacheParams p, int parts) {
   extern __shared__ uint32_t s_keys[];
@@ -124,7 +127,6 @@ select_kernel(CacheParams p, int parts) {
   const int run = (int)((n + 4 * all_threads - 1) / (4 * all_threads)) * 128;
   const int c0 = min(n, rank * run * kSelWarps), c1 = min(n, c0 + run * kSelWarps);
   const int j0 = min(c1, c0 + warp * run), j1 = min(c1, j0 + run);
-  const bool cached = run * kSelWarps <= kCachedKeys;
   __syncthreads();  // the histograms are zero
   // First digit, with the keys on their way into shared memory.  Slots below the
   // budget are written as if they were kept; the moves overwrite those that go.
@@ -148,7 +150,7 @@ select_kernel(CacheParams p, int parts) {
       if (x >= j1) break;
       const uint4 k = make_uint4(keys.of(w[u].x, at[u].x), keys.of(w[u].y, at[u].y), keys.of(w[u].z, at[u].z),
                                  keys.of(w[u].w, at[u].w));
-      if (cached) *reinterpret_cast<uint4*>(s_keys + (x - c0)) = k;
+      if (CACHED) *reinterpret_cast<uint4*>(s_keys + (x - c0)) = k;
       atomicAdd(&s.hist[0][k.x >> 24], 1);
       if (x + 1 < j1) atomicAdd(&s.hist[0][k.y >> 24], 1);
       if (x + 2 < j1) atomicAdd(&s.hist[0][k.z >> 24], 1);
@@ -175,7 +177,7 @@ select_kernel(CacheParams p, int parts) {
   }
   // the keys of slots x .. x + 3 (x < c1)
   auto keys4 = [&](int x) {
-    if (cached) return *reinterpret_cast<const uint4*>(s_keys + (x - c0));
+    if (CACHED) return *reinterpret_cast<const uint4*>(s_keys + (x - c0));
     const float4 w = *reinterpret_cast<const float4*>(keys.w + x);
     int4 at = make_int4(x, x + 1, x + 2, x + 3);
     if (keys.pos) at = *reinterpret_cast<const int4*>(keys.pos + x);
@@ -191,6 +193,7 @@ select_kernel(CacheParams p, int parts) {
     int* hist = s.hist[pass];
     if (pass > 0) {
       const uint32_t mask = 0xFFFFFFFFu << (shift + 8);
+#pragma unroll 4
       for (int j = j0 + 4 * lane; j < j1; j += 128) {
         const uint4 k4 = keys4(j);
         const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
@@ -236,6 +239,7 @@ select_kernel(CacheParams p, int parts) {
   }
   // Places, in the order of the slots: warp by warp, CTA by CTA.
   int equal = 0;
+#pragma unroll 4
   for (int j = j0 + 4 * lane; j < j1; j += 128) {
     const uint4 k = keys4(j);
     equal += (k.x == prefix) + (j + 1 < j1 && k.y == prefix) + (j + 2 < j1 && k.z == prefix) + (j + 3 < j1 && k.w == prefix);
@@ -297,6 +301,7 @@ select_kernel(CacheParams p, int parts) {
   // bits of the slots x .. x + 3 that lie below the budget / below j1
   auto below_of = [&](int x, int end) { return x + 4 <= end ? 15u : x < end ? (1u << (end - x)) - 1u : 0u; };
   int movers = 0, holes = 0, seen = eq0;
+#pragma unroll 4
   for (int j = j0; j < j1; j += 128) {
     const int x = j + 4 * lane;
     const uint32_t kept = kept_of(x, seen), low = below_of(x, p.budget), in = below_of(x, j1);
@@ -400,13 +405,14 @@ cudaError_t launch_cache_evict(const CacheParams& p, int dtype, cudaStream_t s) 
   while (parts < kMaxParts && p.max_len / parts > 2048 && rows * parts * 2 <= 152) parts *= 2;
   static std::atomic<uint64_t> done{0};
   const int64_t per_cta = (int64_t)4 * kSelThreads;
-  const int keys = (int)min((int64_t)kCachedKeys, (p.max_len + parts * per_cta - 1) / (parts * per_cta) * per_cta);
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(select_kernel), kCachedKeys * 4, done);
+  const int64_t keys = (p.max_len + parts * per_cta - 1) / (parts * per_cta) * per_cta;
+  const bool cached = keys <= kCachedKeys;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(select_kernel<true>), kCachedKeys * 4, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)rows * parts);
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = keys * 4;
+  cfg.dynamicSmemBytes = cached ? keys * 4 : 0;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -416,7 +422,7 @@ cudaError_t launch_cache_evict(const CacheParams& p, int dtype, cudaStream_t s) 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, select_kernel, p, parts);
+  e = cached ? cudaLaunchKernelEx(&cfg, select_kernel<true>, p, parts) : cudaLaunchKernelEx(&cfg, select_kernel<false>, p, parts);
   if (e != cudaSuccess) return e;
   const int vph = p.D / (dtype == CAPATTN_BF16 ? 8 : 4);
   int shift = 0;
