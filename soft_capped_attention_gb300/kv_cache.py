@@ -192,6 +192,7 @@ class KVCache:
         self._slots = torch.Size(slots)
         self._seen = (k, v, table, lens)  # checked above
         self._plans = {}       # by (Hq, AttnParams)
+        self._workspace_bytes = 0
         self._workspaces = []  # the last one is used; earlier ones may live in captured graphs
 
     def plan(self, Hq: int, ap: AttnParams | None = None) -> _Plan:
@@ -207,13 +208,14 @@ class KVCache:
         first use adds a larger one (so make that call once before a graph is
         captured); the earlier ones stay, since captured graphs may hold them."""
         n = plan.bytes[call]
-        if not self._workspaces or self._workspaces[-1].numel() < n:
+        if self._workspace_bytes < n:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("the cache's workspace would grow during a graph capture: "
                                    "make the call once before capturing it")
             new = torch.empty(n, dtype=torch.uint8, device=self.device)
             new[:HEADER_BYTES].zero_()  # the status word and the counters
             self._workspaces.append(new)
+            self._workspace_bytes = n
         return self._workspaces[-1]
 
     def _tensors(self):
@@ -291,16 +293,23 @@ def cache_decode(q, cache: KVCache, ap: AttnParams, temp=None, accumulate=False,
         raise ValueError("q is [B, Hq, D]")
     Hq, dev = q.shape[1], cache.device
     shape = (cache.B, Hq, cache.D)
-    qs = _rows(q, "q", shape, cache.dtype, dev)
-    tp = _want(temp, "temp", (cache.B,), torch.float32, dev)
-    if accumulate and cache.weights is None:
-        raise ValueError("accumulate needs a cache with weights")
-    weights = _want(cache.weights, "weights", cache._slots, torch.float32, dev) if accumulate else None
+    flat = q.is_contiguous()
+    if flat and q.shape == shape and q.dtype is cache.dtype and q.device == dev:
+        qs = Hq * cache.D
+    else:
+        qs = _rows(q, "q", shape, cache.dtype, dev)
+    tp = None if temp is None else _want(temp, "temp", (cache.B,), torch.float32, dev)
+    weights = pos = qpos = None
+    if accumulate:
+        if cache.weights is None:
+            raise ValueError("accumulate needs a cache with weights")
+        weights = _want(cache.weights, "weights", cache._slots, torch.float32, dev)
     k, v, table, lens = cache._tensors()
-    pos, qpos = cache._positions()
-    plan = cache.plan(Hq, ap)
+    if cache.pos is not None:
+        pos, qpos = cache._positions()
+    plan = cache._plans.get((Hq, ap)) or cache.plan(Hq, ap)
     if out is None:
-        o = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=q.dtype, device=dev)
+        o = torch.empty_like(q) if flat else torch.empty(shape, dtype=q.dtype, device=dev)
         lse = torch.empty((cache.B, Hq), dtype=torch.float32, device=dev)
     else:
         o, lse = out
@@ -309,7 +318,8 @@ def cache_decode(q, cache: KVCache, ap: AttnParams, temp=None, accumulate=False,
     ws = cache.workspace(plan, CALL_DECODE_WEIGHTS if accumulate else CALL_DECODE)
     st = _lib_handle.capattn_cache_decode(plan.ref, q.data_ptr(), qs, k, v, table, lens, tp, pos, qpos, o.data_ptr(),
                                           lse.data_ptr(), weights, ws.data_ptr(), ws.numel(), s)
-    _ca._check(st, "capattn_cache_decode")
+    if st:
+        _ca._check(st, "capattn_cache_decode")
     return o, lse
 
 
