@@ -12,7 +12,6 @@
 #include "cache_internal.h"
 #include "cache_math.cuh"
 #include "cache_sched.cuh"
-#include "cap_math.cuh"
 
 namespace capattn {
 namespace {
@@ -75,7 +74,7 @@ decode_simt_kernel(CacheParams p) {
   const int d = threadIdx.x % D, part = threadIdx.x / D;
   const T* kc = static_cast<const T*>(p.k);
   const T* vc = static_cast<const T*>(p.v);
-  __shared__ int s_sums[kSchedSums];
+  __shared__ int s_sums[kSchedSums + 32];
   PieceIter<TK> it(p, warp, lane, kThreads / 32, s_sums);
   int b, vh, tile;
   SeqSpan sp;

@@ -36,7 +36,6 @@
 #include "cache_internal.h"
 #include "cache_math.cuh"
 #include "cache_sched.cuh"
-#include "cap_math.cuh"
 #include "tma_maps.h"
 
 namespace capattn {

@@ -18,7 +18,7 @@
 // keys count and list the slots.  What follows from the lists (the rows' pages,
 // the copies, the moved tokens' weights and positions) is the second kernel's, over
 // all SMs.
-//   Measured: 8 rows of 130,977 tokens cut to 16,384 take 46 us (about 23 of them
+//   Measured: 8 rows of 130,977 tokens cut to 16,384 take 44.6 us (about 22 of them
 // selection, 20 the 117 MB of rows that move), 128 rows of 2049 to 4096 cut to 2048
 // take 25 us.  Clusters of 16 CTAs take 59 us for the first (a GPC places few of them
 // at once); one CTA a row took 640 us.

@@ -7,6 +7,12 @@
 // kGroupCost units more than it has tiles (its first ones) for what its end costs,
 // so that a CTA with many short sequences does not finish last.
 //
+// Where no sequence has more than kWholeTiles tiles (twice as many when there are
+// groups enough for half of the CTAs), the units are whole (sequence, group)s instead:
+// joining the parts of so short a one takes longer than reading it (100 keys of 8
+// heads: 5.4 us against 8.9; 32 sequences of 50 to 300 keys, 8 heads: 8.3 against
+// 11.1; one of 500 keys, 8 heads, is faster split: 9.5 against 10.1).
+//
 // A CTA's part of one (sequence, group) is a piece; a piece that is not the whole
 // leaves (m, l, O) in the CTA's slot 2c (the piece at the start of its range) or
 // 2c + 1 (the one at its end; pieces between the two are whole).  The CTA that
@@ -23,6 +29,7 @@
 namespace capattn {
 
 constexpr int kGroupCost = 1;
+constexpr int kWholeTiles = 4;
 static_assert(kGroupCost >= 1, "an empty sequence has to belong to a CTA too");
 
 struct SeqSpan {
@@ -67,19 +74,28 @@ constexpr int kSchedSums = 256;
 __device__ __forceinline__ int run_groups(const CacheParams& p) {
   return ((p.B + 31) / 32 + kSchedSums - 1) / kSchedSums;
 }
+// (and the longest sequence's, in s_sums[kSchedSums .. kSchedSums + warps)).
 template <int TK>
-__device__ __noinline__ int sum_large(const CacheParams& p, int warp, int lane, int warps, int* s_sums) {
+__device__ __noinline__ int sum_large(const CacheParams& p, int warp, int lane, int warps, int* s_sums, int* longest) {
   const int run = run_groups(p) * 32, runs = (p.B + run - 1) / run;
+  int top = 0;
 #pragma unroll 4
   for (int r = warp; r < runs; r += warps) {
     int sum = 0;
-    for (int x = r * run + lane; x < min(p.B, (r + 1) * run); x += 32) sum += seq_span<TK>(p, x).units;
+    for (int x = r * run + lane; x < min(p.B, (r + 1) * run); x += 32) {
+      const int n = seq_span<TK>(p, x).units;
+      sum += n;
+      top = max(top, n);
+    }
     sum = __reduce_add_sync(0xFFFFFFFFu, sum);
     if (lane == 0) s_sums[r] = sum;
   }
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if (lane == 0) s_sums[kSchedSums + warp] = top;
   __syncthreads();
   int all = 0;
   for (int r = lane; r < runs; r += 32) all += s_sums[r];
+  *longest = __reduce_max_sync(0xFFFFFFFFu, lane < warps ? s_sums[kSchedSums + lane] : 0);
   return __reduce_add_sync(0xFFFFFFFFu, all);
 }
 // The sequence that holds unit `want`, its length as read and the units before it.
@@ -124,14 +140,16 @@ struct PieceIter {
   int slot;                // its partial slot, when not whole
   uint32_t s0, s1;         // units [s0, s1) of its (sequence, group)
 
-  // All threads of the CTA (whole warps) build it together; s_sums: kSchedSums ints
-  // of shared memory, written by this alone.
+  bool groups;             // the units are whole (sequence, group)s: none is split
+
+  // All threads of the CTA (whole warps) build it together; s_sums: kSchedSums + 32
+  // ints of shared memory, written by this alone.
   __device__ PieceIter(const CacheParams& p, int warp, int lane, int warps, int* s_sums) {
     b = vh = t0 = len = 0;
     // A batch of 64 stays in registers: one read of lens decides it, in little code
     // (which every launch fetches anew: unrolled over more sequences, or with the
     // large batch's path inline, this cost a launch 1 to 3 us).
-    int raw0 = 0, raw1 = 0, n0 = 0, n1 = 0, sum0 = 0, all;
+    int raw0 = 0, raw1 = 0, n0 = 0, n1 = 0, sum0 = 0, all, longest;
     const bool small = p.B <= 64;
     if (small) {
       if (lane < p.B) raw0 = p.lens[lane];
@@ -140,11 +158,13 @@ struct PieceIter {
       if (lane + 32 < p.B) n1 = span_of<TK>(p, raw1).units;
       sum0 = __reduce_add_sync(0xFFFFFFFFu, n0);
       all = sum0 + __reduce_add_sync(0xFFFFFFFFu, n1);
+      longest = __reduce_max_sync(0xFFFFFFFFu, max(n0, n1));
     } else {
-      all = sum_large<TK>(p, warp, lane, warps, s_sums);
+      all = sum_large<TK>(p, warp, lane, warps, s_sums, &longest);
     }
-    units = (uint32_t)all * (uint32_t)p.VH;
-    ctas = min((uint32_t)p.ctas, max(1u, units / (uint32_t)p.min_tiles));
+    groups = longest <= (2 * p.B * p.VH >= p.ctas ? 2 : 1) * kWholeTiles + kGroupCost;
+    units = (uint32_t)(groups ? p.B : all) * (uint32_t)p.VH;
+    ctas = min((uint32_t)p.ctas, max(1u, units / (uint32_t)(groups ? 1 : p.min_tiles)));
     q = units / ctas;
     more = units - q * ctas;
     begin = u = begin_of(blockIdx.x);
@@ -152,6 +172,13 @@ struct PieceIter {
     if (u >= end) return;
     const int want = (int)(u / (uint32_t)p.VH);  // counted over the sequences
     int before;
+    if (groups) {
+      b = want;
+      vh = (int)(u - (uint32_t)want * (uint32_t)p.VH);
+      len = p.lens[b];
+      if (!small) __syncthreads();
+      return;
+    }
     if (small) {
       const bool low = want < sum0;
       const int x = low ? n0 : n1;
@@ -184,10 +211,10 @@ struct PieceIter {
   __device__ bool next(const CacheParams& p, int* b_out, int* vh_out, int* tile_out, SeqSpan* sp_out) {
     if (u >= end) return false;
     const SeqSpan sp = span_of<TK>(p, len);
-    const int take = (int)min((uint32_t)(sp.units - t0), end - u);
+    const int take = groups ? 1 : (int)min((uint32_t)(sp.units - t0), end - u);
     const int first = max(0, t0 - kGroupCost);
-    n = max(0, t0 + take - kGroupCost) - first;
-    whole = t0 == 0 && take == sp.units;
+    n = groups ? sp.tiles : max(0, t0 + take - kGroupCost) - first;
+    whole = groups || (t0 == 0 && take == sp.units);
     slot = 2 * (int)blockIdx.x + (u == begin ? 0 : 1);
     s0 = u - (uint32_t)t0;
     s1 = s0 + (uint32_t)sp.units;

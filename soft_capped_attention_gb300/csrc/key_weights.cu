@@ -5,7 +5,6 @@
 // sums need no atomics and keep their order.
 #include "cache_internal.h"
 #include "cache_math.cuh"
-#include "cap_math.cuh"
 
 namespace capattn {
 namespace {
@@ -45,7 +44,7 @@ key_weights_simt_kernel(Params p, KeyWeightsParams kw) {
     sk[r * PAD + x] = k0 + r < p.Lk ? k[(((size_t)b * p.Lk + k0 + r) * p.Hkv + g) * D + x] : 0.f;
   }
   const uint32_t* map = p.kmap + ((size_t)b * p.nk + k0 / p.block_kv) * p.wq;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  float sum[4] = {0.f, 0.f, 0.f, 0.f}, comp[4] = {0.f, 0.f, 0.f, 0.f};  // compensated (Kahan)
   for (int hh = 0; hh < p.G; ++hh) {
     const int h = g * p.G + hh;
     TileIter it(map, p.wq);
@@ -81,6 +80,7 @@ key_weights_simt_kernel(Params p, KeyWeightsParams kw) {
             for (int f = 0; f < 4; ++f)
               acc[e][f] = fmaf(a[e].x, c[f].x, fmaf(a[e].y, c[f].y, fmaf(a[e].z, c[f].z, fmaf(a[e].w, c[f].w, acc[e][f]))));
         }
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
           const int4 r = s_row[ty + 16 * f];
@@ -90,8 +90,14 @@ key_weights_simt_kernel(Params p, KeyWeightsParams kw) {
             const int j = k0 + tx + 16 * e;
             const bool live = (j >= r.x && j < r.y) || j == r.z;
             const float t = exact_cap<METHOD>(acc[e][f] * p.sm_scale, kw.cap) * temp;
-            sum[e] += live ? __expf(t - lse) : 0.f;
+            part[e] += live ? __expf(t - lse) : 0.f;
           }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float y = part[e] - comp[e], t = sum[e] + y;
+          comp[e] = (t - sum[e]) - y;
+          sum[e] = t;
         }
       }
     }

@@ -67,6 +67,9 @@ DECODE = [
     ([5000], 16, 1, 128, 16, BF16, "tanh", 0, False, False),
     ([20000], 4, 1, 128, 64, BF16, "alsc", 0, False, False),
     ([40] * 70, 8, 2, 64, 16, BF16, "none", 0, False, False),
+    ([250, 0, 256, 3], 4, 2, 128, 16, BF16, "tanh", 0, True, False),      # whole groups
+    ([500, 130] * 40, 4, 2, 128, 32, BF16, "soft_sign", 0, False, False),  # whole groups, many
+    ([520, 130] * 40, 4, 2, 128, 32, BF16, "soft_sign", 0, False, False),  # the same, split
     ([1], 1, 1, 64, 8, FP32, "tanh", 0, False, False),
     ([100, 0, 33], 4, 2, 64, 16, FP32, "alsc", 0, True, False),
     ([1000, 31], 5, 1, 128, 32, FP32, "tanh", 100, False, False),
