@@ -36,6 +36,26 @@ capattn_status check_config(const capattn_cache_config* c) {
   return CAPATTN_OK;
 }
 
+// tanh(u) = u (a0 + a1 w + a2 w^2), w = u^2, for |u| <= kNearTanh: tanh(u) / u
+// interpolated at the three Chebyshev nodes of w in [0, kNearTanh^2] (error 3e-8 of
+// tanh(u) / u), then with both scales folded in: cap tanh(in X) = X (c0 + z (c1 + z c2)),
+// z = X^2.
+constexpr double kNearTanh = 0.2;
+void near_tanh_fit(double cap, double in, float c[3]) {
+  const double pi = 3.14159265358979323846, half = 0.5 * kNearTanh * kNearTanh;
+  double w[3], f[3];
+  for (int i = 0; i < 3; ++i) {
+    w[i] = half * (1.0 + cos((2 * i + 1) * pi / 6.0));
+    f[i] = tanh(sqrt(w[i])) / sqrt(w[i]);
+  }
+  // Newton's divided differences, multiplied out
+  const double d01 = (f[1] - f[0]) / (w[1] - w[0]), d12 = (f[2] - f[1]) / (w[2] - w[1]);
+  const double d012 = (d12 - d01) / (w[2] - w[0]);
+  const double a[3] = {f[0] - d01 * w[0] + d012 * w[0] * w[1], d01 - d012 * (w[0] + w[1]), d012};
+  double s = cap * in;
+  for (int i = 0; i < 3; ++i, s *= in * in) c[i] = (float)(a[i] * s);
+}
+
 ExactCap exact_cap_of(int method, float cap_in, float alpha, float beta, float sm_scale, int* active) {
   ExactCap k;
   memset(&k, 0, sizeof(k));
@@ -50,17 +70,19 @@ ExactCap exact_cap_of(int method, float cap_in, float alpha, float beta, float s
     const double c[5] = {1.0, kTanhC0, kTanhC1, kTanhC2, kTanhC3};
     double f = cap * in;
     for (int i = 0; i < 5; ++i, f *= w) k.poly[i] = (float)(c[i] * f);
-    // usable while its last coefficient is a normal number
+    near_tanh_fit(cap, in, k.near.c);
+    // usable while the last coefficient is a normal number
+    k.near.xmax = fabsf(k.near.c[2]) >= 1e-30f && isfinite(k.near.c[2]) ? (float)(kNearTanh / fabs(in)) : 0.f;
     k.xmax = fabsf(k.poly[4]) >= 1e-30f && isfinite(k.poly[4]) ? (float)(kTanhPolyMaxU / fabs(in)) : 0.f;
   } else if (*active == CAPATTN_CAP_ALSC) {
     const double ab = (double)alpha * (double)beta;
     const double sb = 1.0 / (1.0 + exp(-ab));
-    k.a = (float)((double)alpha / cap);
-    k.out = (float)(cap / (sb * (1.0 - sb) + 1e-12));
-    k.sb = (float)sb;
-    k.one_minus_sb = (float)(1.0 / (1.0 + exp(ab)));
-    k.eb = (float)fmin(exp(ab), (double)FLT_MAX);
-    k.emb = (float)fmin(exp(-ab), (double)FLT_MAX);
+    k.alsc.a = (float)((double)alpha / cap);
+    k.alsc.out = (float)(cap / (sb * (1.0 - sb) + 1e-12));
+    k.alsc.sb = (float)sb;
+    k.alsc.one_minus_sb = (float)(1.0 / (1.0 + exp(ab)));
+    k.alsc.eb = (float)fmin(exp(ab), (double)FLT_MAX);
+    k.alsc.emb = (float)fmin(exp(-ab), (double)FLT_MAX);
     capattn_config c;  // the fit asks for a whole configuration; the shape plays no part
     memset(&c, 0, sizeof(c));
     c.struct_size = sizeof(c);
@@ -70,7 +92,7 @@ ExactCap exact_cap_of(int method, float cap_in, float alpha, float beta, float s
     c.D = 64;
     bool fine = capattn_debug_alsc_poly(&c, k.poly, &k.xmax) == CAPATTN_OK && isfinite(k.xmax);
     for (int i = 0; i < 7; ++i) {
-      k.poly[i] *= k.out;
+      k.poly[i] *= k.alsc.out;
       fine = fine && isfinite(k.poly[i]) && (fabsf(k.poly[i]) >= 1e-30f || k.poly[i] == 0.f);
     }
     if (!fine) k.xmax = 0.f;

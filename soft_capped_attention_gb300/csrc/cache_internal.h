@@ -18,13 +18,24 @@ constexpr uint32_t kStatusBadNewRowsBit = 128u; // cu_new decreases, or more new
 constexpr uint32_t kStatusBadRowsBit = 256u;    // rows outside 0 <= lo <= hi <= L
 
 // Constants of a cap in the forms of cache_math.cuh, for raw scores X = <q, k>.
+struct AlscCap {
+  float a;                   // d = a * s
+  float out;                 // cap / denom
+  float sb, one_minus_sb;    // sigma(alpha beta) and 1 - sigma
+  float eb, emb;             // e^(alpha beta), e^(-alpha beta)
+};
+// cap tanh(in X) = X (c[0] + z (c[1] + z c[2])), z = X^2, for |X| <= xmax (0: none)
+struct NearTanh {
+  float c[3];
+  float xmax;
+};
 struct ExactCap {
   float sm_scale;
   float cap, inv_cap;        // tanh, soft_sign
-  float a;                   // alsc: d = a * s
-  float out;                 // alsc: cap / denom
-  float sb, one_minus_sb;    // alsc: sigma(alpha beta) and 1 - sigma
-  float eb, emb;             // alsc: e^(alpha beta), e^(-alpha beta)
+  union {
+    AlscCap alsc;
+    NearTanh near;
+  };
   // cap(sm_scale X) as a polynomial for |X| <= xmax (0: none): tanh
   // X (c0 + z (c1 + z (c2 + z (c3 + z c4)))), z = X^2; alsc X (c0 + X (c1 + .. + X c6))
   float poly[7];

@@ -30,12 +30,12 @@ __device__ __forceinline__ float exact_cap(float s, const ExactCap& k) {
   } else if constexpr (METHOD == CAPATTN_CAP_SOFT_SIGN) {
     return s / (1.0f + fabsf(s) * k.inv_cap);
   } else if constexpr (METHOD == CAPATTN_CAP_ALSC) {
-    const float d = s * k.a;
+    const float d = s * k.alsc.a;
     const float e = expm1f(-fabsf(d));
     const bool up = d >= 0.f;
-    const float num = up ? -k.one_minus_sb : k.sb;
-    const float den = up ? k.emb : k.eb;
-    return k.out * (e * num / fmaf(den, 1.0f + e, 1.0f));
+    const float num = up ? -k.alsc.one_minus_sb : k.alsc.sb;
+    const float den = up ? k.alsc.emb : k.alsc.eb;
+    return k.alsc.out * (e * num / fmaf(den, 1.0f + e, 1.0f));
   } else {
     return s;
   }
@@ -75,10 +75,10 @@ __device__ __forceinline__ float any_cap(float X, const ExactCap& k) {
       const float e = ex2_approx(fabsf(s) * (k.inv_cap * 2.0f * kL2E));
       far = copysignf(k.cap * (1.0f - 2.0f * rcp_approx(1.0f + e)), s);
     } else {
-      const float d = s * k.a;
+      const float d = s * k.alsc.a;
       const float x = ex2_approx(-fabsf(d) * kL2E);
       const bool up = d >= 0.f;
-      far = k.out * ((1.0f - x) * (up ? k.one_minus_sb : -k.sb)) * rcp_approx(fmaf(up ? k.emb : k.eb, x, 1.0f));
+      far = k.alsc.out * ((1.0f - x) * (up ? k.alsc.one_minus_sb : -k.alsc.sb)) * rcp_approx(fmaf(up ? k.alsc.emb : k.alsc.eb, x, 1.0f));
     }
     return fabsf(X) <= k.xmax ? near : far;
   } else if constexpr (METHOD == CAPATTN_CAP_SOFT_SIGN) {

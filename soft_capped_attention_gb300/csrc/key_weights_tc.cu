@@ -15,12 +15,13 @@
 //
 // What bounds it: the elementwise pass.  There is no second product and nothing is
 // stored; the tensor cores need 260 cycles for a step of 128 x 128 pairs, the exp2s
-// 512 on the MUFU pipe (32 a clock and SM), the cap's polynomial and the sums 900
-// (tanh; 7 products a pair at 128 a clock) to 1150 (alsc with temperatures).  Measured
-// are about 1800 cycles a step on a long prompt (8192 rows, 32 heads: 412 us, 667
-// TFLOP/s at 2 D a live pair), the issue slots 52 % used, and about
-// 12 us of launches and first loads (two prompts of 2048 x 16 heads: 37 us in all;
-// 4096 rows x 32 heads in a window of 1024 with alsc and temperatures: 74 us).
+// 512 on the MUFU pipe (32 a clock and SM), the cap's polynomial and the sums 640
+// (tanh near zero; 5 products a pair at 128 a clock) to 1150 (alsc with
+// temperatures).  Measured are about 1600 cycles a step on a long prompt (8192 rows,
+// 32 heads, tanh: 370 us, 743 TFLOP/s at 2 D a live pair), about half of the issue
+// slots used, and about 12 us of launches and first loads (two prompts of 2048 x 16
+// heads: 34.4 us in all; 4096 rows x 32 heads in a window of 1024 with alsc and
+// temperatures: 74 us).
 //   Tried: the steps of a key tile cut over clusters of up to 8 CTAs instead of the
 // persistent shares (58 us for the two prompts: two steps a CTA, mostly prologue);
 // constants loaded by the TMA warp (40 us: the MMAs waited for it); one step for all
@@ -190,19 +191,24 @@ struct Steps {
 
 constexpr int NCONST = NBUF;  // column constants go with the S^T buffers
 
-// Per-method constants of the log2-domain logit, kept in registers:
+// Per-method constants of the log2-domain logit:
 //   x = log2(e) temp cap(sm_scale X) - log2(e) lse = (temp X) Q(X) + add
 // with Q the cap's polynomial times log2(e) (in z = X^2 for tanh, in X for alsc;
-// the constant sm_scale log2(e) without a cap).
-template <int METHOD>
+// the constant sm_scale log2(e) without a cap).  tanh has one of three terms for
+// scores near zero, kept in registers (two products a pair less: 34.4 us for the two
+// prompts against 36.8), and one of five.
+template <int METHOD, bool WIDE>
 struct Poly {
-  static constexpr int N = METHOD == CAPATTN_CAP_TANH ? 5 : METHOD == CAPATTN_CAP_ALSC ? 7 : 1;
+  static constexpr int N = METHOD == CAPATTN_CAP_TANH ? (WIDE ? 5 : 3) : METHOD == CAPATTN_CAP_ALSC ? 7 : 1;
   F2 c[N];
   __device__ __forceinline__ explicit Poly(const ExactCap& k) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float x = (METHOD == CAPATTN_CAP_NONE ? k.sm_scale : has_poly(METHOD) ? k.poly[i] : 1.f) * kL2E;
-      c[i] = f2(x, x);
+      float x = 1.f;
+      if (METHOD == CAPATTN_CAP_NONE) x = k.sm_scale;
+      else if (METHOD == CAPATTN_CAP_TANH && !WIDE) x = k.near.c[i];
+      else if (has_poly(METHOD)) x = k.poly[i];
+      c[i] = f2(x * kL2E, x * kL2E);
     }
   }
   __device__ __forceinline__ F2 eval(F2 X) const {
@@ -213,13 +219,16 @@ struct Poly {
     return q;
   }
 };
+// How a chunk's scores are capped: by the polynomial in registers, by tanh's longer
+// one, one by one.
+enum { kNear, kWide, kOneByOne };
 
-// Sum of 2^x over 32 query columns of this thread's key.  fast: every raw score
-// of the warp is in the polynomial's range (or the cap has none to leave).
+// Sum of 2^x over 32 query columns of this thread's key.  LEVEL: every raw score of
+// the warp is in that polynomial's range (or the cap has none to leave).
 // MASK: 0 every pair is live; 1 a column's live keys are [lo, lo + len); 2 and one more.
-template <int METHOD, bool TEMP, int MASK, bool FAST>
+template <int METHOD, bool TEMP, int MASK, int LEVEL, class P>
 __device__ __forceinline__ float chunk_sum(const uint32_t (&x)[32], const float* add, const float* temp,
-                                           const int2* spans, const int* extra, int j, const Poly<METHOD>& poly, const ExactCap& k) {
+                                           const int2* spans, const int* extra, int j, const P& poly, const ExactCap& k) {
   F2 acc = f2(0.f, 0.f);
 #pragma unroll
   for (int e = 0; e < 32; e += 4) {
@@ -231,7 +240,7 @@ __device__ __forceinline__ float chunk_sum(const uint32_t (&x)[32], const float*
       const float X0 = __uint_as_float(x[e + 2 * h]), X1 = __uint_as_float(x[e + 2 * h + 1]);
       const F2 a2 = h == 0 ? f2(ad.x, ad.y) : f2(ad.z, ad.w), t2 = h == 0 ? f2(tp.x, tp.y) : f2(tp.z, tp.w);
       F2 y;
-      if constexpr (FAST && METHOD != CAPATTN_CAP_SOFT_SIGN) {
+      if constexpr (LEVEL != kOneByOne && METHOD != CAPATTN_CAP_SOFT_SIGN) {
         const F2 X = f2(X0, X1);
         y = f2_fma(TEMP ? f2_mul(X, t2) : X, poly.eval(X), a2);
       } else {
@@ -510,7 +519,7 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     const uint32_t mine = wg >> 1;                       // the steps it takes: even or odd ones
     const int half = 64 * (wg & 1);                      // its columns of them
     const uint32_t cols_t = tmem + ((uint32_t)(quarter * 32) << 16) + half;
-    const Poly<METHOD> poly(kw.cap);
+    const Poly<METHOD, false> near(kw.cap);
     int parity = 0;
     bool ok = true;  // after a timeout the warp still meets the others at every unit's barriers
     while (it.next(p, kw, &e, &g)) {
@@ -537,27 +546,41 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           uint32_t x[32];
           tmem_ld32(cols_t + u * BT + c, x);
           tmem_wait_ld();
-          bool fast = true;
+          int level = kNear;
           if constexpr (has_poly(METHOD)) {
             float am = 0.f;
 #pragma unroll
             for (int y = 0; y < 32; y += 2) am = fmax3_abs(am, __uint_as_float(x[y]), __uint_as_float(x[y + 1]));
-            fast = __all_sync(0xFFFFFFFFu, am <= kw.cap.xmax && kw.cap.xmax > 0.f);
+            const bool wide = __all_sync(0xFFFFFFFFu, am <= kw.cap.xmax && kw.cap.xmax > 0.f);
+            if constexpr (METHOD == CAPATTN_CAP_TANH) {
+              const bool close = __all_sync(0xFFFFFFFFu, am <= kw.cap.near.xmax && kw.cap.near.xmax > 0.f);
+              level = close ? kNear : wide ? kWide : kOneByOne;
+            } else {
+              level = wide ? kNear : kOneByOne;
+            }
           }
           const float* ad = &col_add[u][half + c];
           const float* tp = &col_temp[TEMP ? u : 0][half + c];
           const int2* sp = &col_span[u][half + c];
           const int* ex = &col_extra[u][half + c];
           float part;
-          if (!masked)
-            part = fast ? chunk_sum<METHOD, TEMP, 0, true>(x, ad, tp, sp, ex, j, poly, kw.cap)
-                        : chunk_sum<METHOD, TEMP, 0, false>(x, ad, tp, sp, ex, j, poly, kw.cap);
-          else if (!p.bounds)
-            part = fast ? chunk_sum<METHOD, TEMP, 1, true>(x, ad, tp, sp, ex, j, poly, kw.cap)
-                        : chunk_sum<METHOD, TEMP, 1, false>(x, ad, tp, sp, ex, j, poly, kw.cap);
-          else
-            part = fast ? chunk_sum<METHOD, TEMP, 2, true>(x, ad, tp, sp, ex, j, poly, kw.cap)
-                        : chunk_sum<METHOD, TEMP, 2, false>(x, ad, tp, sp, ex, j, poly, kw.cap);
+#define CAPATTN_CHUNK(MASK)                                                                              \
+  if (level == kNear) {                                                                                  \
+    part = chunk_sum<METHOD, TEMP, MASK, kNear>(x, ad, tp, sp, ex, j, near, kw.cap);                     \
+  } else if (METHOD == CAPATTN_CAP_TANH && level == kWide) {                                             \
+    const Poly<METHOD, true> wide(kw.cap);                                                               \
+    part = chunk_sum<METHOD, TEMP, MASK, METHOD == CAPATTN_CAP_TANH ? kWide : kNear>(x, ad, tp, sp, ex, j, wide, kw.cap); \
+  } else {                                                                                               \
+    part = chunk_sum<METHOD, TEMP, MASK, kOneByOne>(x, ad, tp, sp, ex, j, near, kw.cap);                 \
+  }
+          if (!masked) {
+            CAPATTN_CHUNK(0)
+          } else if (!p.bounds) {
+            CAPATTN_CHUNK(1)
+          } else {
+            CAPATTN_CHUNK(2)
+          }
+#undef CAPATTN_CHUNK
           const float y = part - comp, t = sum + y;
           comp = (t - sum) - y;
           sum = t;

@@ -6,7 +6,14 @@ import math
 import torch
 
 EPS32 = 2.0 ** -24          # half a step of fp32, relative
-CAPS = {"none": (0.0, 0.0, 0.0), "tanh": (5.0, 0.0, 0.0), "soft_sign": (3.0, 0.0, 0.0), "alsc": (4.0, 2.0, 0.5)}
+# tight caps bend most scores (the kernels' one-by-one forms), wide ones few (their
+# polynomials), the one between takes both and tanh's longer polynomial
+CAPS = {"none": (0.0, 0.0, 0.0), "tanh": (5.0, 0.0, 0.0), "soft_sign": (3.0, 0.0, 0.0), "alsc": (4.0, 2.0, 0.5),
+        "tanh15": (15.0, 0.0, 0.0), "tanh50": (50.0, 0.0, 0.0), "alsc30": (30.0, 2.0, 0.5), "alsc90": (90.0, 2.0, 0.5)}
+
+
+def method_of(cap):
+    return cap.rstrip("0123456789")
 
 
 def cap64(x, method, cap, alpha, beta):

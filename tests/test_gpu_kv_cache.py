@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from kv_cache_utils import CAPS, EPS32, Pool, decode64, evict_row, key_weights64, live_mask
+from kv_cache_utils import CAPS, EPS32, Pool, decode64, evict_row, key_weights64, live_mask, method_of
 from parity_utils import Guarded
 from soft_capped_attention_gb300 import capattn as ca
 
@@ -22,7 +22,7 @@ def kv():
 
 def params(cap, D, window=0, scale=None):
     c, a, b = CAPS[cap]
-    return ca.AttnParams(sm_scale=scale or 1 / math.sqrt(D), cap_method=cap, cap=c, alpha=a, beta=b, causal=True,
+    return ca.AttnParams(sm_scale=scale or 1 / math.sqrt(D), cap_method=method_of(cap), cap=c, alpha=a, beta=b, causal=True,
                          window_len=window)
 
 
@@ -70,6 +70,10 @@ DECODE = [
     ([250, 0, 256, 3], 4, 2, 128, 16, BF16, "tanh", 0, True, False),      # whole groups
     ([500, 130] * 40, 4, 2, 128, 32, BF16, "soft_sign", 0, False, False),  # whole groups, many
     ([520, 130] * 40, 4, 2, 128, 32, BF16, "soft_sign", 0, False, False),  # the same, split
+    ([800, 90], 8, 2, 128, 16, BF16, "tanh50", 0, True, False),
+    ([800, 90], 24, 2, 64, 16, BF16, "tanh15", 0, False, False),
+    ([800, 90], 4, 4, 128, 16, BF16, "alsc90", 0, False, False),
+    ([800, 90], 16, 1, 64, 32, BF16, "alsc30", 300, True, False),
     ([1], 1, 1, 64, 8, FP32, "tanh", 0, False, False),
     ([100, 0, 33], 4, 2, 64, 16, FP32, "alsc", 0, True, False),
     ([1000, 31], 5, 1, 128, 32, FP32, "tanh", 100, False, False),
@@ -345,6 +349,10 @@ WEIGHTS = [
     (1, 700, 700, 2, 1, 128, BF16, "tanh", True, 0, True, "seg", None),
     (1, 2500, 2500, 4, 2, 64, BF16, "alsc", True, 0, False, None, [[100, 2400]]),
     (3, 640, 640, 6, 3, 128, BF16, "none", True, 200, True, None, [[0, 640], [639, 640], [128, 512]]),
+    (2, 400, 400, 4, 2, 128, BF16, "tanh50", True, 0, True, None, None),
+    (1, 400, 400, 4, 4, 64, BF16, "tanh15", True, 90, False, None, None),
+    (1, 400, 400, 4, 2, 128, BF16, "alsc30", True, 0, True, None, None),
+    (1, 400, 400, 2, 2, 64, BF16, "alsc90", False, 0, False, "ranker", None),
     (2, 150, 150, 4, 2, 64, FP32, "tanh", True, 0, True, None, [[1, 2], [0, 150]]),
     (1, 129, 129, 2, 2, 128, FP32, "alsc", False, 0, False, "ranker", None),
     (1, 65, 200, 2, 2, 64, FP32, "soft_sign", False, 9, False, None, None),
@@ -363,7 +371,8 @@ def test_key_weights(case):
     elif mask == "ranker":
         bounds = torch.tensor([[3 * b, 60 + b, 60 + b, 90 + b] for b in range(B)], dtype=torch.int32)
     c, a, be = CAPS[cap]
-    ap = ca.AttnParams(sm_scale=1 / math.sqrt(D), cap_method=cap, cap=c, alpha=a, beta=be, causal=causal, window_len=window)
+    ap = ca.AttnParams(sm_scale=1 / math.sqrt(D), cap_method=method_of(cap), cap=c, alpha=a, beta=be, causal=causal,
+                         window_len=window)
     live = live_mask(B, L, Lk, causal, window, seg, bounds)
     d = lambda x: None if x is None else x.cuda()  # noqa: E731
     _, lse, _, _ = ca.capattn_fwd(q.cuda(), k.cuda(), k.cuda().clone(), ap, d(temp), d(seg), d(bounds))
