@@ -54,12 +54,21 @@ struct RowKeys {
   }
 };
 
-constexpr int kBatch = 4;   // vectors of four slots a thread reads at once
+constexpr int kBatch = 4;       // vectors of four slots a thread reads at once
+constexpr int kListed = 2048;   // keys of the first two digits' bin that a CTA lists
+// Kept slots of a warp or CTA: keys above the threshold and equal to it, of its slots
+// below the budget (lo) and behind it (hi).
+struct Counts {
+  int over_lo, equal_lo, over_hi, equal_hi;
+};
 struct Shared {
   __align__(16) int hist[4][kBins];  // of each pass
   __align__(16) int sum[2][kBins];   // the cluster's (two, for passes in turn)
-  int warp_sum[3][kSelWarps];
-  int totals[3];              // of this CTA: equal keys, movers, freed slots
+  __align__(16) int4 warp_counts[kSelWarps];
+  int4 counts;                // of this CTA
+  int edge_equal;             // of rank 0: equal keys of the slots in the budget's vector, below it
+  int listed;
+  uint32_t list[kListed];
 };
 
 // Inclusive sum over the lanes.
@@ -86,7 +95,7 @@ __device__ __forceinline__ int cache_row(const CacheParams& p, int b, int g, int
 template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads, 1)
 select_kernel(CacheParams p, int parts) {
-  extern __shared__ uint32_t s_keys[];
+  extern __shared__ __align__(16) uint32_t s_keys[];
   __shared__ Shared s;
   cg::cluster_group cluster = cg::this_cluster();
   auto meet = [&] {
@@ -96,6 +105,7 @@ select_kernel(CacheParams p, int parts) {
   const int b = row / p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < 4 * kBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
+  if (threadIdx.x == 0) s.listed = s.edge_equal = 0;
   pdl_trigger();
   pdl_wait();
   int n = p.lens[b];
@@ -121,67 +131,83 @@ select_kernel(CacheParams p, int parts) {
     if (rank == 0 && threadIdx.x == 0) p.counts[row] = make_int2(0, n);
     return;
   }
-  // This CTA's slots [c0, c1): equal runs of whole groups of 128, a run a warp, four
-  // consecutive slots a lane (rows of the weights are whole 16-byte units).
-  const uint32_t all_threads = (uint32_t)parts * kSelThreads;  // (n is at most 2^30)
-  const int run = (int)((n + 4 * all_threads - 1) / (4 * all_threads)) * 128;
-  const int c0 = min(n, rank * run * kSelWarps), c1 = min(n, c0 + run * kSelWarps);
-  const int j0 = min(c1, c0 + warp * run), j1 = min(c1, j0 + run);
+  // The slots below the budget (whole vectors of four) and those behind it are shared out
+  // apart, so that no CTA has all that go or all that come: a run of each a warp, in
+  // order, in steps of four consecutive slots a lane (rows of the weights are whole
+  // 16-byte units).
+  const int edge = p.budget & ~3;  // slots [edge, budget) belong to the second part
+  const int all_warps = parts * kSelWarps, at_warp = rank * kSelWarps + warp;  // (n is at most 2^30)
+  const int run_lo = (edge + 128 * all_warps - 1) / (128 * all_warps) * 128;
+  const int run_hi = (n - edge + 128 * all_warps - 1) / (128 * all_warps) * 128;
+  const int lo0 = min(edge, at_warp * run_lo), lo1 = min(edge, lo0 + run_lo);
+  const int hi0 = edge + min(n - edge, at_warp * run_hi), hi1 = min(n, hi0 + run_hi);
+  const int steps_lo = (lo1 - lo0 + 127) / 128, steps = steps_lo + (hi1 - hi0 + 127) / 128;
+  uint32_t* const cached = s_keys + warp * (run_lo + run_hi) + 4 * lane;
+  // this lane's first slot of a step, and the end of its run
+  auto slot_of = [&](int i) { return (i < steps_lo ? lo0 + 128 * i : hi0 + 128 * (i - steps_lo)) + 4 * lane; };
+  auto end_of = [&](int i) { return i < steps_lo ? lo1 : hi1; };
   __syncthreads();  // the histograms are zero
-  // First digit, with the keys on their way into shared memory.  Slots below the
-  // budget are written as if they were kept; the moves overwrite those that go.
-  // (Vectors may reach behind c1, up to the row's end; those keys are not counted.)
+  // First digit, with the keys on their way into shared memory.  Lanes behind the end
+  // of a run have keys 0, the lowest: more of those change no digit of the budget-th
+  // largest key.  (A run ends inside a vector only at n, and rows are whole vectors.)
+  // Tokens below the budget are written as if they were kept; the moves overwrite
+  // those that go.
   const bool copy_w = p.weights_out != p.weights, copy_pos = p.pos_out && p.pos_out != p.pos;
-  for (int j = j0 + 4 * lane; j < j1; j += 128 * kBatch) {
+  auto make_keys = [&](int x, int end, const float4& w, const int4& at) {
+    return make_uint4(keys.of(w.x, at.x), x + 1 < end ? keys.of(w.y, at.y) : 0u, x + 2 < end ? keys.of(w.z, at.z) : 0u,
+                      x + 3 < end ? keys.of(w.w, at.w) : 0u);
+  };
+  for (int i = 0; i < steps; i += kBatch) {
     float4 w[kBatch];
     int4 at[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int x = j + 128 * u;
+      if (i + u >= steps) break;
+      const int x = slot_of(i + u);
       at[u] = make_int4(x, x + 1, x + 2, x + 3);
-      if (x < j1) {
+      if (x < end_of(i + u)) {
         w[u] = *reinterpret_cast<const float4*>(keys.w + x);
         if (keys.pos) at[u] = *reinterpret_cast<const int4*>(keys.pos + x);
       }
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int x = j + 128 * u;
-      if (x >= j1) break;
-      const uint4 k = make_uint4(keys.of(w[u].x, at[u].x), keys.of(w[u].y, at[u].y), keys.of(w[u].z, at[u].z),
-                                 keys.of(w[u].w, at[u].w));
-      if (CACHED) *reinterpret_cast<uint4*>(s_keys + (x - c0)) = k;
-      atomicAdd(&s.hist[0][k.x >> 24], 1);
-      if (x + 1 < j1) atomicAdd(&s.hist[0][k.y >> 24], 1);
-      if (x + 2 < j1) atomicAdd(&s.hist[0][k.z >> 24], 1);
-      if (x + 3 < j1) atomicAdd(&s.hist[0][k.w >> 24], 1);
-      if (x < p.budget) {  // (n is above the budget: all four slots are there)
-        const int some = min(4, p.budget - x);
+      if (i + u >= steps) break;
+      const int x = slot_of(i + u), end = end_of(i + u);
+      uint4 k = make_uint4(0u, 0u, 0u, 0u);
+      if (x < end) {
+        k = make_keys(x, end, w[u], at[u]);
+        atomicAdd(&s.hist[0][k.x >> 24], 1);
+        atomicAdd(&s.hist[0][k.y >> 24], 1);
+        atomicAdd(&s.hist[0][k.z >> 24], 1);
+        atomicAdd(&s.hist[0][k.w >> 24], 1);
+        if (x < p.budget) {
+          if (x < edge) {
+            if (copy_w) *reinterpret_cast<float4*>(p.weights_out + base + x) = w[u];
+            if (copy_pos) *reinterpret_cast<int4*>(p.pos_out + base + x) = at[u];
+          } else {
+            const float ws[3] = {w[u].x, w[u].y, w[u].z};
+            const int as[3] = {at[u].x, at[u].y, at[u].z};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < some) src[x + e] = x + e;
-        if (some == 4) {
-          if (copy_w) *reinterpret_cast<float4*>(p.weights_out + base + x) = w[u];
-          if (copy_pos) *reinterpret_cast<int4*>(p.pos_out + base + x) = at[u];
-        } else {
-          const float ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-          const int as[4] = {at[u].x, at[u].y, at[u].z, at[u].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (e < some && copy_w) p.weights_out[base + x + e] = ws[e];
-            if (e < some && copy_pos) p.pos_out[base + x + e] = as[e];
+            for (int e = 0; e < 3; ++e) {
+              if (x + e < p.budget && copy_w) p.weights_out[base + x + e] = ws[e];
+              if (x + e < p.budget && copy_pos) p.pos_out[base + x + e] = as[e];
+            }
           }
         }
       }
+      if (CACHED) *reinterpret_cast<uint4*>(cached + 128 * (i + u)) = k;
     }
   }
-  // the keys of slots x .. x + 3 (x < c1)
-  auto keys4 = [&](int x) {
-    if (CACHED) return *reinterpret_cast<const uint4*>(s_keys + (x - c0));
+  // this lane's keys of a step (0 behind the run's end)
+  auto keys4 = [&](int i) {
+    if (CACHED) return *reinterpret_cast<const uint4*>(cached + 128 * i);
+    const int x = slot_of(i), end = end_of(i);
+    if (x >= end) return make_uint4(0u, 0u, 0u, 0u);
     const float4 w = *reinterpret_cast<const float4*>(keys.w + x);
     int4 at = make_int4(x, x + 1, x + 2, x + 3);
     if (keys.pos) at = *reinterpret_cast<const int4*>(keys.pos + x);
-    return make_uint4(keys.of(w.x, at.x), keys.of(w.y, at.y), keys.of(w.z, at.z), keys.of(w.w, at.w));
+    return make_keys(x, end, w, at);
   };
   // The budget-th largest key: its digits from the top; `left` is its rank among
   // the keys that share the digits so far.
@@ -192,14 +218,29 @@ select_kernel(CacheParams p, int parts) {
     const int shift = 24 - 8 * pass;
     int* hist = s.hist[pass];
     if (pass > 0) {
+      // The keys that share two digits are few as a rule: the third pass lists them
+      // for the fourth.
       const uint32_t mask = 0xFFFFFFFFu << (shift + 8);
+      if (pass == 3 && s.listed <= kListed) {
+        for (int x = threadIdx.x; x < s.listed; x += kSelThreads) {
+          const uint32_t k = s.list[x];
+          if ((k & mask) == prefix) atomicAdd(&hist[k & (kBins - 1)], 1);
+        }
+      } else {
 #pragma unroll 4
-      for (int j = j0 + 4 * lane; j < j1; j += 128) {
-        const uint4 k4 = keys4(j);
-        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        for (int i = 0; i < steps; ++i) {
+          const uint4 k4 = keys4(i);
+          const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if ((k[e] & mask) == prefix && j + e < j1) atomicAdd(&hist[(k[e] >> shift) & (kBins - 1)], 1);
+          for (int e = 0; e < 4; ++e)
+            if ((k[e] & mask) == prefix) {
+              atomicAdd(&hist[(k[e] >> shift) & (kBins - 1)], 1);
+              if (pass == 2) {
+                const int x = atomicAdd(&s.listed, 1);
+                if (x < kListed) s.list[x] = k[e];
+              }
+            }
+        }
       }
     }
     meet();  // the cluster's histograms of this pass are whole
@@ -237,103 +278,106 @@ select_kernel(CacheParams p, int parts) {
     prefix |= (uint32_t)__shfl_sync(0xFFFFFFFFu, digit, from) << shift;
     left -= __shfl_sync(0xFFFFFFFFu, before, from);
   }
-  // Places, in the order of the slots: warp by warp, CTA by CTA.
-  int equal = 0;
-#pragma unroll 4
-  for (int j = j0 + 4 * lane; j < j1; j += 128) {
-    const uint4 k = keys4(j);
-    equal += (k.x == prefix) + (j + 1 < j1 && k.y == prefix) + (j + 2 < j1 && k.z == prefix) + (j + 3 < j1 && k.w == prefix);
-  }
-  equal = __reduce_add_sync(0xFFFFFFFFu, equal);
-  // This warp's start in the cluster's order of one count a warp, after share()
-  // has left it and the cluster has met; *total the cluster's.
-  auto share = [&](int mine, int which) {
-    if (lane == 0) s.warp_sum[which][warp] = mine;
-    __syncthreads();
-    const int x = lane < kSelWarps ? s.warp_sum[which][lane] : 0;
-    const int up = inclusive_sum(x, lane);
-    if (threadIdx.x == 31) s.totals[which] = up;
-    return __shfl_sync(0xFFFFFFFFu, up - x, warp);
-  };
-  auto before = [&](int which, int* total) {
-    int v = 0;  // a lane a CTA
-    if (lane < parts) v = parts > 1 ? *cluster.map_shared_rank(&s.totals[which], lane) : s.totals[which];
-    *total = __reduce_add_sync(0xFFFFFFFFu, v);
-    return __reduce_add_sync(0xFFFFFFFFu, lane < rank ? v : 0);
-  };
-  int total;
-  int eq0 = share(equal, 0);
-  meet();
-  eq0 += before(0, &total);
-  // Kept: above the threshold, or among the first `left` equal ones.  All equal keys
-  // of a warp are on one side of that, but for one warp of the cluster.
-  const bool all_eq = eq0 + equal <= left, none_eq = eq0 >= left;
-  // Bits 0 .. 3: which of the slots x .. x + 3 are kept (warp-collective).
-  auto kept_of = [&](int x, int& seen) {
-    uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
-    if (x < j1) k4 = keys4(x);
+  // Places, in the order of the slots.  Kept are the keys above the threshold and the
+  // first `left` equal ones, so that of `e` equal ones in a row from the first on
+  // min(e, left) are: one round of counts gives every warp the number of freed slots
+  // and of movers before it.
+  auto in_of = [&](int x, int end) { return x + 4 <= end ? 15u : x < end ? (1u << (end - x)) - 1u : 0u; };
+  // bits of the slots x .. x + 3 above and equal to the threshold
+  auto compare = [&](int i, int x, uint32_t* over, uint32_t* same) {
+    const uint4 k4 = keys4(i);
     const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-    const uint32_t in = x + 4 <= j1 ? 15u : x < j1 ? (1u << (j1 - x)) - 1u : 0u;
-    uint32_t over = 0, same = 0;
+    *over = *same = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      over |= (k[e] > prefix ? 1u : 0u) << e;
-      same |= (k[e] == prefix ? 1u : 0u) << e;
+      *over |= (k[e] > prefix ? 1u : 0u) << e;
+      *same |= (k[e] == prefix ? 1u : 0u) << e;
     }
-    over &= in;
-    same &= in;
-    if (none_eq) return over;
-    if (all_eq) return over | same;
-    int at = __popc(same), mine = at;  // equal keys up to this lane's
-    at = inclusive_sum(at, lane);
-    const int first = seen + at - mine;
-    seen += __shfl_sync(0xFFFFFFFFu, at, 31);
-    int room = max(0, left - first);  // of this lane's equal keys, the lowest `room` are kept
-    uint32_t take = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if ((same >> e) & 1u) {
-        if (room > 0) take |= 1u << e;
-        --room;
-      }
-    return over | take;
+    if (prefix == 0) *same &= in_of(x, end_of(i));  // (over is never true of key 0)
   };
-  // bits of the slots x .. x + 3 that lie below the budget / below j1
-  auto below_of = [&](int x, int end) { return x + 4 <= end ? 15u : x < end ? (1u << (end - x)) - 1u : 0u; };
-  int movers = 0, holes = 0, seen = eq0;
+  Counts mine = {0, 0, 0, 0};
 #pragma unroll 4
-  for (int j = j0; j < j1; j += 128) {
-    const int x = j + 4 * lane;
-    const uint32_t kept = kept_of(x, seen), low = below_of(x, p.budget), in = below_of(x, j1);
-    movers += __popc(kept & ~low);
-    holes += __popc(in & low & ~kept);
+  for (int i = 0; i < steps; ++i) {
+    const int x = slot_of(i);
+    uint32_t over, same;
+    compare(i, x, &over, &same);
+    if (i < steps_lo) {
+      mine.over_lo += __popc(over);
+      mine.equal_lo += __popc(same);
+    } else {
+      uint32_t low = 0;
+      if (i == steps_lo && hi0 == edge) low = in_of(x, p.budget);  // the budget's vector
+      if (same & low) s.edge_equal = __popc(same & low);           // (one lane of the cluster)
+      mine.over_hi += __popc(over & ~low);
+      mine.equal_hi += __popc(same & ~low);
+    }
   }
-  movers = __reduce_add_sync(0xFFFFFFFFu, movers);
-  holes = __reduce_add_sync(0xFFFFFFFFu, holes);
-  int n_moves, n_holes;
-  int mover = share(movers, 1), hole = share(holes, 2);
+  auto sum4 = [&](const int4& v, bool on) {
+    return Counts{__reduce_add_sync(0xFFFFFFFFu, on ? v.x : 0), __reduce_add_sync(0xFFFFFFFFu, on ? v.y : 0),
+                  __reduce_add_sync(0xFFFFFFFFu, on ? v.z : 0), __reduce_add_sync(0xFFFFFFFFu, on ? v.w : 0)};
+  };
+  mine = sum4(make_int4(mine.over_lo, mine.equal_lo, mine.over_hi, mine.equal_hi), true);
+  if (lane == 0) s.warp_counts[warp] = make_int4(mine.over_lo, mine.equal_lo, mine.over_hi, mine.equal_hi);
+  __syncthreads();
+  const int4 of_warp = s.warp_counts[lane % kSelWarps];
+  const Counts in_cta = sum4(of_warp, lane < warp);
+  if (warp == 0) {
+    const Counts c = sum4(of_warp, lane < kSelWarps);
+    if (lane == 0) s.counts = make_int4(c.over_lo, c.equal_lo, c.over_hi, c.equal_hi);
+  }
   meet();
-  mover += before(1, &n_moves);
-  hole += before(2, &n_holes);
-  seen = eq0;
-  for (int j = j0; j < j1; j += 128) {
-    const int x = j + 4 * lane;
-    const uint32_t kept = kept_of(x, seen), low = below_of(x, p.budget), in = below_of(x, j1);
-    const uint32_t moves_it = kept & ~low, freed = in & low & ~kept;
+  int4 of_cta = make_int4(0, 0, 0, 0);  // a lane a CTA
+  if (lane < parts) of_cta = parts > 1 ? *cluster.map_shared_rank(&s.counts, lane) : s.counts;
+  const int edge_equal = parts > 1 ? *cluster.map_shared_rank(&s.edge_equal, 0) : s.edge_equal;
+  const Counts in_cluster = sum4(of_cta, lane < rank), all = sum4(of_cta, true);
+  // the cluster's counts are read: a CTA may leave once all have come here
+  if (parts > 1) cluster.barrier_arrive();
+  const int equal_lo = all.equal_lo + edge_equal;  // below the budget
+  const int taken_lo = min(left, equal_lo);
+  // equal keys before this warp's runs
+  const int seen_lo = in_cluster.equal_lo + in_cta.equal_lo;
+  const int seen_hi = hi0 == edge ? all.equal_lo : equal_lo + in_cluster.equal_hi + in_cta.equal_hi;
+  int hole = lo0 - (in_cluster.over_lo + in_cta.over_lo) - min(left, seen_lo);  // freed slots before
+  int mover = in_cluster.over_hi + in_cta.over_hi + max(0, min(left, seen_hi) - taken_lo);
+  const int n_moves = all.over_hi + min(left, equal_lo + all.equal_hi) - taken_lo;
+  int seen = seen_lo;
+  for (int i = 0; i < steps; ++i) {
+    const int x = slot_of(i);
+    if (i == steps_lo) {
+      seen = seen_hi;
+      hole = edge - all.over_lo - min(left, all.equal_lo);  // (of the budget's vector alone)
+    }
+    uint32_t over, same;
+    compare(i, x, &over, &same);
+    uint32_t kept = over;
+    if (__any_sync(0xFFFFFFFFu, same != 0)) {
+      const int mine = __popc(same), up = inclusive_sum(mine, lane);
+      int room = left - (seen + up - mine);  // of this lane's equal keys, the lowest `room` are kept
+      seen += __shfl_sync(0xFFFFFFFFu, up, 31);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((same >> e) & 1u) {
+          if (room > 0) kept |= 1u << e;
+          --room;
+        }
+    }
+    const uint32_t low = in_of(x, p.budget);
+    const uint32_t moves_it = kept & ~low, freed = in_of(x, end_of(i)) & low & ~kept;
     // both counts in one sum over the lanes: at most 128 of each
-    const int mine = __popc(moves_it) | __popc(freed) << 16;
-    const int up = inclusive_sum(mine, lane), all = __shfl_sync(0xFFFFFFFFu, up, 31);
-    int m = mover + ((up - mine) & 0xFFFF), h = hole + ((up - mine) >> 16);
+    const int both = __popc(moves_it) | __popc(freed) << 16;
+    const int up = inclusive_sum(both, lane), sum = __shfl_sync(0xFFFFFFFFu, up, 31);
+    int m = mover + ((up - both) & 0xFFFF), h = hole + ((up - both) >> 16);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if ((moves_it >> e) & 1u) moves[m++].y = x + e;
       if ((freed >> e) & 1u) moves[h++].x = x + e;
     }
-    mover += all & 0xFFFF;
-    hole += all >> 16;
+    mover += sum & 0xFFFF;
+    hole += sum >> 16;
   }
   if (rank == 0 && threadIdx.x == 0) p.counts[row] = make_int2(n_moves, p.budget);
-  if (parts > 1) cluster.sync();  // no CTA leaves while its counts may be read
+  for (int j = rank * kSelThreads + threadIdx.x; j < p.budget; j += parts * kSelThreads) src[j] = j;
+  if (parts > 1) cluster.barrier_wait();
 }
 
 // Carries out the moves: a group of vph threads a row, K and V together, two rows in
@@ -405,7 +449,7 @@ cudaError_t launch_cache_evict(const CacheParams& p, int dtype, cudaStream_t s) 
   while (parts < kMaxParts && p.max_len / parts > 2048 && rows * parts * 2 <= 152) parts *= 2;
   static std::atomic<uint64_t> done{0};
   const int64_t per_cta = (int64_t)4 * kSelThreads;
-  const int64_t keys = (p.max_len + parts * per_cta - 1) / (parts * per_cta) * per_cta;
+  const int64_t keys = ((p.max_len + parts * per_cta - 1) / (parts * per_cta) + 1) * per_cta;  // (two runs a warp)
   const bool cached = keys <= kCachedKeys;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(select_kernel<true>), kCachedKeys * 4, done);
   if (e != cudaSuccess) return e;
