@@ -55,20 +55,24 @@ struct RowKeys {
 };
 
 constexpr int kBatch = 4;       // vectors of four slots a thread reads at once
-constexpr int kListed = 2048;   // keys of the first two digits' bin that a CTA lists
-// Kept slots of a warp or CTA: keys above the threshold and equal to it, of its slots
-// below the budget (lo) and behind it (hi).
+// The keys that share two digits are few as a rule: of a CTA's this many are listed.
+constexpr int kListed = 2048;
+constexpr int kFew = 256;       // so few are ranked against one another instead
+// Slots of a warp or CTA with keys above and equal to the threshold, of those below
+// the budget (lo) and behind it (hi).
 struct Counts {
   int over_lo, equal_lo, over_hi, equal_hi;
 };
 struct Shared {
   __align__(16) int hist[4][kBins];  // of each pass
   __align__(16) int sum[2][kBins];   // the cluster's (two, for passes in turn)
-  __align__(16) int4 warp_counts[kSelWarps];
-  int4 counts;                // of this CTA
-  int edge_equal;             // of rank 0: equal keys of the slots in the budget's vector, below it
+  __align__(16) int warp_counts[kSelWarps][4];  // Counts
+  __align__(16) uint32_t list[kListed];         // keys
+  uint8_t list_of[kListed];   // and whose: 2 warp + (1: behind the budget)
   int listed;
-  uint32_t list[kListed];
+  int4 counts;                // Counts of this CTA
+  uint32_t threshold;
+  int left;
 };
 
 // Inclusive sum over the lanes.
@@ -105,7 +109,7 @@ select_kernel(CacheParams p, int parts) {
   const int b = row / p.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < 4 * kBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
-  if (threadIdx.x == 0) s.listed = s.edge_equal = 0;
+  if (threadIdx.x == 0) s.listed = 0;
   pdl_trigger();
   pdl_wait();
   int n = p.lens[b];
@@ -135,27 +139,30 @@ select_kernel(CacheParams p, int parts) {
   // apart, so that no CTA has all that go or all that come: a run of each a warp, in
   // order, in steps of four consecutive slots a lane (rows of the weights are whole
   // 16-byte units).
-  const int edge = p.budget & ~3;  // slots [edge, budget) belong to the second part
+  const int edge = p.budget & ~3;  // the vector at the edge of both is in both, each with its slots
   const int all_warps = parts * kSelWarps, at_warp = rank * kSelWarps + warp;  // (n is at most 2^30)
-  const int run_lo = (edge + 128 * all_warps - 1) / (128 * all_warps) * 128;
+  const int run_lo = (p.budget + 128 * all_warps - 1) / (128 * all_warps) * 128;
   const int run_hi = (n - edge + 128 * all_warps - 1) / (128 * all_warps) * 128;
-  const int lo0 = min(edge, at_warp * run_lo), lo1 = min(edge, lo0 + run_lo);
+  const int lo0 = min(p.budget, at_warp * run_lo), lo1 = min(p.budget, lo0 + run_lo);
   const int hi0 = edge + min(n - edge, at_warp * run_hi), hi1 = min(n, hi0 + run_hi);
   const int steps_lo = (lo1 - lo0 + 127) / 128, steps = steps_lo + (hi1 - hi0 + 127) / 128;
   uint32_t* const cached = s_keys + warp * (run_lo + run_hi) + 4 * lane;
   // this lane's first slot of a step, and the end of its run
   auto slot_of = [&](int i) { return (i < steps_lo ? lo0 + 128 * i : hi0 + 128 * (i - steps_lo)) + 4 * lane; };
   auto end_of = [&](int i) { return i < steps_lo ? lo1 : hi1; };
+  auto begin_of = [&](int i) { return i < steps_lo ? 0 : p.budget; };
   __syncthreads();  // the histograms are zero
-  // First digit, with the keys on their way into shared memory.  Lanes behind the end
-  // of a run have keys 0, the lowest: more of those change no digit of the budget-th
-  // largest key.  (A run ends inside a vector only at n, and rows are whole vectors.)
-  // Tokens below the budget are written as if they were kept; the moves overwrite
+  // First digit, with the keys on their way into shared memory.  Slots outside a run
+  // have keys 0, the lowest: more of those change no digit of the budget-th largest
+  // key.  Tokens below the budget are written as if they were kept; the moves overwrite
   // those that go.
   const bool copy_w = p.weights_out != p.weights, copy_pos = p.pos_out && p.pos_out != p.pos;
-  auto make_keys = [&](int x, int end, const float4& w, const int4& at) {
-    return make_uint4(keys.of(w.x, at.x), x + 1 < end ? keys.of(w.y, at.y) : 0u, x + 2 < end ? keys.of(w.z, at.z) : 0u,
-                      x + 3 < end ? keys.of(w.w, at.w) : 0u);
+  auto make_keys = [&](int i, int x, const float4& w, const int4& at) {
+    const int begin = begin_of(i), end = end_of(i);
+    auto key = [&](int e, float weight, int place) {
+      return x + e >= begin && x + e < end ? keys.of(weight, place) : 0u;
+    };
+    return make_uint4(key(0, w.x, at.x), key(1, w.y, at.y), key(2, w.z, at.z), key(3, w.w, at.w));
   };
   for (int i = 0; i < steps; i += kBatch) {
     float4 w[kBatch];
@@ -173,15 +180,15 @@ select_kernel(CacheParams p, int parts) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       if (i + u >= steps) break;
-      const int x = slot_of(i + u), end = end_of(i + u);
+      const int x = slot_of(i + u);
       uint4 k = make_uint4(0u, 0u, 0u, 0u);
-      if (x < end) {
-        k = make_keys(x, end, w[u], at[u]);
+      if (x < end_of(i + u)) {
+        k = make_keys(i + u, x, w[u], at[u]);
         atomicAdd(&s.hist[0][k.x >> 24], 1);
         atomicAdd(&s.hist[0][k.y >> 24], 1);
         atomicAdd(&s.hist[0][k.z >> 24], 1);
         atomicAdd(&s.hist[0][k.w >> 24], 1);
-        if (x < p.budget) {
+        if (i + u < steps_lo) {
           if (x < edge) {
             if (copy_w) *reinterpret_cast<float4*>(p.weights_out + base + x) = w[u];
             if (copy_pos) *reinterpret_cast<int4*>(p.pos_out + base + x) = at[u];
@@ -199,15 +206,15 @@ select_kernel(CacheParams p, int parts) {
       if (CACHED) *reinterpret_cast<uint4*>(cached + 128 * (i + u)) = k;
     }
   }
-  // this lane's keys of a step (0 behind the run's end)
+  // this lane's keys of a step
   auto keys4 = [&](int i) {
     if (CACHED) return *reinterpret_cast<const uint4*>(cached + 128 * i);
-    const int x = slot_of(i), end = end_of(i);
-    if (x >= end) return make_uint4(0u, 0u, 0u, 0u);
+    const int x = slot_of(i);
+    if (x >= end_of(i)) return make_uint4(0u, 0u, 0u, 0u);
     const float4 w = *reinterpret_cast<const float4*>(keys.w + x);
     int4 at = make_int4(x, x + 1, x + 2, x + 3);
     if (keys.pos) at = *reinterpret_cast<const int4*>(keys.pos + x);
-    return make_keys(x, end, w, at);
+    return make_keys(i, x, w, at);
   };
   // The budget-th largest key: its digits from the top; `left` is its rank among
   // the keys that share the digits so far.
@@ -217,29 +224,67 @@ select_kernel(CacheParams p, int parts) {
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
     int* hist = s.hist[pass];
-    if (pass > 0) {
-      // The keys that share two digits are few as a rule: the third pass lists them
-      // for the fourth.
-      const uint32_t mask = 0xFFFFFFFFu << (shift + 8);
-      if (pass == 3 && s.listed <= kListed) {
-        for (int x = threadIdx.x; x < s.listed; x += kSelThreads) {
-          const uint32_t k = s.list[x];
-          if ((k & mask) == prefix) atomicAdd(&hist[k & (kBins - 1)], 1);
-        }
-      } else {
+    const uint32_t mask = pass > 0 ? 0xFFFFFFFFu << (shift + 8) : 0u;
+    if (pass == 3 && s.listed <= kListed) {
+      for (int x = threadIdx.x; x < s.listed; x += kSelThreads) {
+        const uint32_t k = s.list[x];
+        if ((k & mask) == prefix) atomicAdd(&hist[k & (kBins - 1)], 1);
+      }
+    } else if (pass > 0) {
+      int over = 0, over_lo = 0;  // keys above these digits
 #pragma unroll 4
-        for (int i = 0; i < steps; ++i) {
-          const uint4 k4 = keys4(i);
-          const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+      for (int i = 0; i < steps; ++i) {
+        if (i == steps_lo) {
+          over_lo = over;
+          over = 0;
+        }
+        const uint4 k4 = keys4(i);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if ((k[e] & mask) == prefix) {
-              atomicAdd(&hist[(k[e] >> shift) & (kBins - 1)], 1);
-              if (pass == 2) {
-                const int x = atomicAdd(&s.listed, 1);
-                if (x < kListed) s.list[x] = k[e];
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t digits = k[e] & mask;
+          over += digits > prefix;
+          if (digits == prefix) {
+            atomicAdd(&hist[(k[e] >> shift) & (kBins - 1)], 1);
+            if (pass == 2) {
+              const int x = atomicAdd(&s.listed, 1);
+              if (x < kListed) {
+                s.list[x] = k[e];
+                s.list_of[x] = (uint8_t)(2 * warp + (i < steps_lo ? 0 : 1));
               }
             }
+          }
+        }
+      }
+      if (pass == 2) {
+        if (steps == steps_lo) {
+          over_lo = over;
+          over = 0;
+        }
+        over_lo = __reduce_add_sync(0xFFFFFFFFu, over_lo);
+        over = __reduce_add_sync(0xFFFFFFFFu, over);
+        if (lane == 0) *reinterpret_cast<int4*>(s.warp_counts[warp]) = make_int4(over_lo, 0, over, 0);
+        if (parts == 1) {
+          __syncthreads();
+          const int listed = s.listed;
+          if (listed <= kFew) {
+            if (threadIdx.x < listed) {
+              const uint32_t k = s.list[threadIdx.x];
+              int above = 0, same = 0;
+              for (int x = 0; x < listed; ++x) {
+                above += s.list[x] > k;
+                same += s.list[x] == k;
+              }
+              if (above < left && left <= above + same) {
+                s.threshold = k;
+                s.left = left - above;
+              }
+            }
+            __syncthreads();
+            prefix = s.threshold;
+            left = s.left;
+            break;
+          }
         }
       }
     }
@@ -279,11 +324,13 @@ select_kernel(CacheParams p, int parts) {
     left -= __shfl_sync(0xFFFFFFFFu, before, from);
   }
   // Places, in the order of the slots.  Kept are the keys above the threshold and the
-  // first `left` equal ones, so that of `e` equal ones in a row from the first on
-  // min(e, left) are: one round of counts gives every warp the number of freed slots
-  // and of movers before it.
+  // first `left` equal ones, so that of the first e equal ones min(e, left) are: one
+  // round of counts gives every warp the number of freed slots and of movers before it.
+  // The counts of the third pass lack the keys that share its digits.
   auto in_of = [&](int x, int end) { return x + 4 <= end ? 15u : x < end ? (1u << (end - x)) - 1u : 0u; };
-  // bits of the slots x .. x + 3 above and equal to the threshold
+  // bits of a step's slots x .. x + 3 that are this lane's
+  auto mine_of = [&](int i, int x) { return in_of(x, end_of(i)) & ~in_of(x, begin_of(i)); };
+  // bits of the slots above and equal to the threshold (key 0 is above none)
   auto compare = [&](int i, int x, uint32_t* over, uint32_t* same) {
     const uint4 k4 = keys4(i);
     const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
@@ -293,33 +340,37 @@ select_kernel(CacheParams p, int parts) {
       *over |= (k[e] > prefix ? 1u : 0u) << e;
       *same |= (k[e] == prefix ? 1u : 0u) << e;
     }
-    if (prefix == 0) *same &= in_of(x, end_of(i));  // (over is never true of key 0)
+    if (prefix == 0) *same &= mine_of(i, x);
   };
-  Counts mine = {0, 0, 0, 0};
-#pragma unroll 4
-  for (int i = 0; i < steps; ++i) {
-    const int x = slot_of(i);
-    uint32_t over, same;
-    compare(i, x, &over, &same);
-    if (i < steps_lo) {
-      mine.over_lo += __popc(over);
-      mine.equal_lo += __popc(same);
-    } else {
-      uint32_t low = 0;
-      if (i == steps_lo && hi0 == edge) low = in_of(x, p.budget);  // the budget's vector
-      if (same & low) s.edge_equal = __popc(same & low);           // (one lane of the cluster)
-      mine.over_hi += __popc(over & ~low);
-      mine.equal_hi += __popc(same & ~low);
+  if (prefix != 0 && s.listed <= kListed) {
+    for (int x = threadIdx.x; x < s.listed; x += kSelThreads)
+      if (s.list[x] >= prefix) {
+        const int of = s.list_of[x];
+        atomicAdd(&s.warp_counts[of >> 1][2 * (of & 1) + (s.list[x] == prefix)], 1);
+      }
+  } else {
+    int4 c = make_int4(0, 0, 0, 0);
+    for (int i = 0; i < steps; ++i) {
+      uint32_t over, same;
+      compare(i, slot_of(i), &over, &same);
+      if (i < steps_lo) {
+        c.x += __popc(over);
+        c.y += __popc(same);
+      } else {
+        c.z += __popc(over);
+        c.w += __popc(same);
+      }
     }
+    c = make_int4(__reduce_add_sync(0xFFFFFFFFu, c.x), __reduce_add_sync(0xFFFFFFFFu, c.y),
+                  __reduce_add_sync(0xFFFFFFFFu, c.z), __reduce_add_sync(0xFFFFFFFFu, c.w));
+    if (lane == 0) *reinterpret_cast<int4*>(s.warp_counts[warp]) = c;
   }
+  __syncthreads();
   auto sum4 = [&](const int4& v, bool on) {
     return Counts{__reduce_add_sync(0xFFFFFFFFu, on ? v.x : 0), __reduce_add_sync(0xFFFFFFFFu, on ? v.y : 0),
                   __reduce_add_sync(0xFFFFFFFFu, on ? v.z : 0), __reduce_add_sync(0xFFFFFFFFu, on ? v.w : 0)};
   };
-  mine = sum4(make_int4(mine.over_lo, mine.equal_lo, mine.over_hi, mine.equal_hi), true);
-  if (lane == 0) s.warp_counts[warp] = make_int4(mine.over_lo, mine.equal_lo, mine.over_hi, mine.equal_hi);
-  __syncthreads();
-  const int4 of_warp = s.warp_counts[lane % kSelWarps];
+  const int4 of_warp = *reinterpret_cast<const int4*>(s.warp_counts[lane % kSelWarps]);
   const Counts in_cta = sum4(of_warp, lane < warp);
   if (warp == 0) {
     const Counts c = sum4(of_warp, lane < kSelWarps);
@@ -328,31 +379,24 @@ select_kernel(CacheParams p, int parts) {
   meet();
   int4 of_cta = make_int4(0, 0, 0, 0);  // a lane a CTA
   if (lane < parts) of_cta = parts > 1 ? *cluster.map_shared_rank(&s.counts, lane) : s.counts;
-  const int edge_equal = parts > 1 ? *cluster.map_shared_rank(&s.edge_equal, 0) : s.edge_equal;
   const Counts in_cluster = sum4(of_cta, lane < rank), all = sum4(of_cta, true);
   // the cluster's counts are read: a CTA may leave once all have come here
   if (parts > 1) cluster.barrier_arrive();
-  const int equal_lo = all.equal_lo + edge_equal;  // below the budget
-  const int taken_lo = min(left, equal_lo);
-  // equal keys before this warp's runs
-  const int seen_lo = in_cluster.equal_lo + in_cta.equal_lo;
-  const int seen_hi = hi0 == edge ? all.equal_lo : equal_lo + in_cluster.equal_hi + in_cta.equal_hi;
-  int hole = lo0 - (in_cluster.over_lo + in_cta.over_lo) - min(left, seen_lo);  // freed slots before
-  int mover = in_cluster.over_hi + in_cta.over_hi + max(0, min(left, seen_hi) - taken_lo);
-  const int n_moves = all.over_hi + min(left, equal_lo + all.equal_hi) - taken_lo;
-  int seen = seen_lo;
+  // equal keys before this warp's runs, freed slots, movers
+  const int taken_lo = min(left, all.equal_lo);
+  const int seen_hi = all.equal_lo + in_cluster.equal_hi + in_cta.equal_hi;
+  int seen = in_cluster.equal_lo + in_cta.equal_lo;
+  int hole = lo0 - (in_cluster.over_lo + in_cta.over_lo) - min(left, seen);
+  int mover = in_cluster.over_hi + in_cta.over_hi + min(left, seen_hi) - taken_lo;
   for (int i = 0; i < steps; ++i) {
     const int x = slot_of(i);
-    if (i == steps_lo) {
-      seen = seen_hi;
-      hole = edge - all.over_lo - min(left, all.equal_lo);  // (of the budget's vector alone)
-    }
+    if (i == steps_lo) seen = seen_hi;
     uint32_t over, same;
     compare(i, x, &over, &same);
     uint32_t kept = over;
     if (__any_sync(0xFFFFFFFFu, same != 0)) {
-      const int mine = __popc(same), up = inclusive_sum(mine, lane);
-      int room = left - (seen + up - mine);  // of this lane's equal keys, the lowest `room` are kept
+      const int equal = __popc(same), up = inclusive_sum(equal, lane);
+      int room = left - (seen + up - equal);  // of this lane's equal keys, the lowest `room` are kept
       seen += __shfl_sync(0xFFFFFFFFu, up, 31);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -361,21 +405,23 @@ select_kernel(CacheParams p, int parts) {
           --room;
         }
     }
-    const uint32_t low = in_of(x, p.budget);
-    const uint32_t moves_it = kept & ~low, freed = in_of(x, end_of(i)) & low & ~kept;
-    // both counts in one sum over the lanes: at most 128 of each
-    const int both = __popc(moves_it) | __popc(freed) << 16;
-    const int up = inclusive_sum(both, lane), sum = __shfl_sync(0xFFFFFFFFu, up, 31);
-    int m = mover + ((up - both) & 0xFFFF), h = hole + ((up - both) >> 16);
+    // the slots that are listed: freed ones below the budget, movers behind it
+    const bool lo = i < steps_lo;
+    const uint32_t out = lo ? mine_of(i, x) & ~kept : kept;
+    const int count = __popc(out), up = inclusive_sum(count, lane);
+    int* to = reinterpret_cast<int*>(moves) + (lo ? 2 * (hole + up - count) : 2 * (mover + up - count) + 1);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if ((moves_it >> e) & 1u) moves[m++].y = x + e;
-      if ((freed >> e) & 1u) moves[h++].x = x + e;
-    }
-    mover += sum & 0xFFFF;
-    hole += sum >> 16;
+    for (int e = 0; e < 4; ++e)
+      if ((out >> e) & 1u) {
+        *to = x + e;
+        to += 2;
+      }
+    const int sum = __shfl_sync(0xFFFFFFFFu, up, 31);
+    if (lo) hole += sum;
+    else mover += sum;
   }
-  if (rank == 0 && threadIdx.x == 0) p.counts[row] = make_int2(n_moves, p.budget);
+  if (rank == 0 && threadIdx.x == 0)
+    p.counts[row] = make_int2(all.over_hi + min(left, all.equal_lo + all.equal_hi) - taken_lo, p.budget);
   for (int j = rank * kSelThreads + threadIdx.x; j < p.budget; j += parts * kSelThreads) src[j] = j;
   if (parts > 1) cluster.barrier_wait();
 }
@@ -449,7 +495,8 @@ cudaError_t launch_cache_evict(const CacheParams& p, int dtype, cudaStream_t s) 
   while (parts < kMaxParts && p.max_len / parts > 2048 && rows * parts * 2 <= 152) parts *= 2;
   static std::atomic<uint64_t> done{0};
   const int64_t per_cta = (int64_t)4 * kSelThreads;
-  const int64_t keys = ((p.max_len + parts * per_cta - 1) / (parts * per_cta) + 1) * per_cta;  // (two runs a warp)
+  // two runs a warp, of one vector more than the row
+  const int64_t keys = ((p.max_len + 3 + parts * per_cta - 1) / (parts * per_cta) + 1) * per_cta;
   const bool cached = keys <= kCachedKeys;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(select_kernel<true>), kCachedKeys * 4, done);
   if (e != cudaSuccess) return e;
