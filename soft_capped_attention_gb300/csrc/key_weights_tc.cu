@@ -219,6 +219,23 @@ struct Poly {
     return q;
   }
 };
+// 32 lanes x 32 bits, 32 consecutive columns per thread, and the largest |x| of them
+// (NaN apart) by the same load.
+__device__ __forceinline__ float tmem_ld32_absmax(uint32_t taddr, uint32_t (&r)[32]) {
+  float top;
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.abs.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(top)
+      : "r"(taddr)
+      : "memory");
+  return top;
+}
+
 // How a chunk's scores are capped: by the polynomial in registers, by tanh's longer
 // one, one by one.
 enum { kNear, kWide, kOneByOne };
@@ -544,13 +561,13 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             masked = first < range.y || first + 32 > range.z;
           }
           uint32_t x[32];
-          tmem_ld32(cols_t + u * BT + c, x);
-          tmem_wait_ld();
           int level = kNear;
-          if constexpr (has_poly(METHOD)) {
-            float am = 0.f;
-#pragma unroll
-            for (int y = 0; y < 32; y += 2) am = fmax3_abs(am, __uint_as_float(x[y]), __uint_as_float(x[y + 1]));
+          if constexpr (!has_poly(METHOD)) {
+            tmem_ld32(cols_t + u * BT + c, x);
+            tmem_wait_ld();
+          } else {
+            float am = tmem_ld32_absmax(cols_t + u * BT + c, x);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(am)::"memory");
             const bool wide = __all_sync(0xFFFFFFFFu, am <= kw.cap.xmax && kw.cap.xmax > 0.f);
             if constexpr (METHOD == CAPATTN_CAP_TANH) {
               const bool close = __all_sync(0xFFFFFFFFu, am <= kw.cap.near.xmax && kw.cap.near.xmax > 0.f);
