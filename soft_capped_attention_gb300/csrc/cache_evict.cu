@@ -14,14 +14,19 @@
 // keys it reads once and keeps in shared memory.  Four histogram passes of 8 bits
 // find the threshold, each CTA adding up the cluster's histograms by distributed
 // shared memory (of 11 bits, three passes: reading 8 KB from each of 8 CTAs took 7000
-// cycles a pass, more than a pass of 8 bits altogether); three more passes over the
-// keys count and list the slots.  What follows from the lists (the rows' pages,
+// cycles a pass, more than a pass of 8 bits altogether).  The third pass lists the few
+// keys that share two digits, which is all the fourth has to look at, and counts the
+// keys above them, so that one exchange of counts gives every warp its places; the
+// last pass over the keys lists the slots.  What follows from the lists (the rows' pages,
 // the copies, the moved tokens' weights and positions) is the second kernel's, over
 // all SMs.
-//   Measured: 8 rows of 130,977 tokens cut to 16,384 take 44.6 us (about 22 of them
+//   Measured: 8 rows of 130,977 tokens cut to 16,384 take 38.4 us (about 17 of them
 // selection, 20 the 117 MB of rows that move), 128 rows of 2049 to 4096 cut to 2048
-// take 25 us.  Clusters of 16 CTAs take 59 us for the first (a GPC places few of them
-// at once); one CTA a row took 640 us.
+// take 24.6 us.  With the slots shared out in one run a CTA instead of two, the CTA
+// below the budget had all the freed ones to list (and 44.6 us, with three exchanges
+// of counts).  Clusters of 16 CTAs took 59 us against 46 (a GPC places few of them at
+// once), one CTA a row 640 us.  1024 threads a CTA, copies of the first histogram and
+// twice the loads in flight changed nothing.
 #include <cooperative_groups.h>
 
 #include "cache_internal.h"

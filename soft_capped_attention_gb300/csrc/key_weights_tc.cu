@@ -17,17 +17,18 @@
 // stored; the tensor cores need 260 cycles for a step of 128 x 128 pairs, the exp2s
 // 512 on the MUFU pipe (32 a clock and SM), the cap's polynomial and the sums 640
 // (tanh near zero; 5 products a pair at 128 a clock) to 1150 (alsc with
-// temperatures).  Measured are about 1600 cycles a step on a long prompt (8192 rows,
-// 32 heads, tanh: 370 us, 743 TFLOP/s at 2 D a live pair), about half of the issue
+// temperatures).  Measured are about 1400 cycles a step on a long prompt (8192 rows,
+// 32 heads, tanh: 322 us, 854 TFLOP/s at 2 D a live pair), about half of the issue
 // slots used, and about 12 us of launches and first loads (two prompts of 2048 x 16
-// heads: 34.4 us in all; 4096 rows x 32 heads in a window of 1024 with alsc and
-// temperatures: 74 us).
+// heads: 32.1 us in all; 4096 rows x 32 heads in a window of 1024 with alsc and
+// temperatures: 70.3 us).
 //   Tried: the steps of a key tile cut over clusters of up to 8 CTAs instead of the
 // persistent shares (58 us for the two prompts: two steps a CTA, mostly prologue);
 // constants loaded by the TMA warp (40 us: the MMAs waited for it); one step for all
 // sixteen warps, 32 columns each (38 -> 40 us: the waits are paid per 32 columns);
 // 16-column chunks (41 us); both chunks of a step unrolled (42 us: more code than the
-// instruction caches like).
+// instruction caches like); a piece's sums written by the TMA warp between its loads
+// (37.5 us against 32.1).
 //
 // Sums: 32 columns in fp32, then compensated (Kahan) over those: a prompt of
 // 131072 rows adds as exactly as a short one.

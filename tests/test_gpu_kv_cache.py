@@ -337,6 +337,39 @@ def test_evict_past_the_keys_that_fit_shared_memory():
     assert cache.status() == (0, 0)
 
 
+@pytest.mark.parametrize("n, heads, budget, first, last", [
+    (700, 2, 203, 0, 0), (2048, 80, 2047, 3, 3), (4095, 80, 1026, 5, 2), (9000, 2, 4097, 0, 17), (70_001, 1, 33_335, 2, 1),
+    (400_000, 1, 7, 3, 4), (400_000, 1, 399_999, 0, 0),
+])
+@pytest.mark.parametrize("kind", ["equal", "zeros", "nan", "lowest", "close", "two"])
+def test_evict_of_keys_alike(n, heads, budget, first, last, kind):
+    """Weights whose leading digits are the same for few, many or all slots, budgets off
+    whole vectors, one to eight CTAs a row with and without the keys in shared memory."""
+    page = 1024 if n > 10_000 else 64
+    pool = Pool([n], heads, 64, page, BF16, n + budget)
+    shape = (1, heads, pool.max_pages * page)
+    if kind == "close":  # within 2^-13 of one another, most of them different
+        w = 1 + torch.randint(0, 1000, shape, generator=pool.gen) * 2.0**-23
+    elif kind == "two":  # 1 in 20 of another value
+        w = torch.where(torch.randint(0, 20, shape, generator=pool.gen) == 0, 0.75, 0.5)
+    else:
+        w = torch.full(shape, {"equal": 0.3, "zeros": 0.0, "nan": math.nan, "lowest": -math.inf}[kind])
+    w = w.float()
+    cache = pool.cuda(weights=w)
+    before = cache.k.clone()
+    src = kv().cache_evict(cache, budget, first, last).cpu()
+    assert cache.status() == (0, 0) and cache.lens.tolist() == [budget]
+    table = cache.table[0].long()
+    new = torch.arange(budget, device="cuda")
+    for h in range(heads):
+        want = torch.tensor(evict_row(w[0, h].tolist(), None, n - 1, n, budget, first, last), dtype=torch.int32)
+        assert torch.equal(src[0, h], want)
+        assert torch.equal(cache.weights[0, h, :budget].cpu().view(torch.int32), w[0, h][want.long()].view(torch.int32))
+        old = want.long().cuda()
+        assert torch.equal(cache.k[table[new // page], h, new % page].view(torch.int16),
+                           before[table[old // page], h, old % page].view(torch.int16))
+
+
 WEIGHTS = [
     # B, L, Lk, Hq, Hkv, D, dtype, cap, causal, window, temp, mask, rows
     (1, 1, 1, 1, 1, 128, BF16, "none", True, 0, False, None, None),
