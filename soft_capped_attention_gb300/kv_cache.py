@@ -122,7 +122,7 @@ def _rows(t, what, shape, dtype, device):
 def _raw_stream(device, stream):
     """The handle of the current stream when the call needs no other device or
     stream than the current ones, else None."""
-    if stream is None and torch.cuda.current_device() == device.index:
+    if stream is None and torch._C._cuda_getDevice() == device.index:  # (CUDA is up: the tensors are there)
         return torch._C._cuda_getCurrentRawStream(device.index)  # the handle alone, without a Stream object
     return None
 
@@ -149,6 +149,7 @@ class _Plan:
         self.cfg = cfg
         self.ref = ctypes.byref(cfg)
         self.bytes = [cache_workspace_bytes(cfg, c) for c in range(4)]
+        self.lse_like = None  # a tensor of lse's shape, which new ones are made like
 
 
 class KVCache:
@@ -191,20 +192,21 @@ class KVCache:
         self.weights, self.pos, self.qpos = weights, pos, qpos
         self._slots = torch.Size(slots)
         self._seen = (k, v, table, lens)  # checked above
-        self._plans = {}       # by (Hq, AttnParams)
-        self._workspace_bytes = 0
+        self._plans = {}       # by Hq and the parameters that count
+        self._workspace_at = self._workspace_bytes = 0
         self._workspaces = []  # the last one is used; earlier ones may live in captured graphs
 
     def plan(self, Hq: int, ap: AttnParams | None = None) -> _Plan:
-        got = self._plans.get((Hq, ap))
+        key = (Hq,) if ap is None else (Hq, ap.sm_scale, ap.cap_method, ap.cap, ap.alpha, ap.beta, ap.window_len)
+        got = self._plans.get(key)
         if got is None:
             cfg = make_cache_config(ap or AttnParams(sm_scale=1.0), self.B, Hq, self.Hkv, self.D, self.dtype,
                                     self.num_pages, self.page_size, self.max_pages)
-            got = self._plans[(Hq, ap)] = _Plan(cfg)
+            got = self._plans[key] = _Plan(cfg)
         return got
 
-    def workspace(self, plan: _Plan, call: int) -> torch.Tensor:
-        """The cache's workspace, at least as large as `call` needs.  A larger call's
+    def workspace(self, plan: _Plan, call: int) -> tuple[int, int]:
+        """The cache's workspace (its address and bytes), at least as large as `call` needs.  A larger call's
         first use adds a larger one (so make that call once before a graph is
         captured); the earlier ones stay, since captured graphs may hold them."""
         n = plan.bytes[call]
@@ -215,8 +217,8 @@ class KVCache:
             new = torch.empty(n, dtype=torch.uint8, device=self.device)
             new[:HEADER_BYTES].zero_()  # the status word and the counters
             self._workspaces.append(new)
-            self._workspace_bytes = n
-        return self._workspaces[-1]
+            self._workspace_at, self._workspace_bytes = new.data_ptr(), n
+        return self._workspace_at, self._workspace_bytes
 
     def _tensors(self):
         """Addresses of the cache's own tensors.  They are the caller's to replace: a
@@ -272,9 +274,9 @@ def cache_append(cache: KVCache, k_new, v_new, cu_new=None, stream=None) -> None
     k, v, table, lens = cache._tensors()
     pos, qpos = cache._positions()
     plan = cache.plan(cache.Hkv)
-    ws = cache.workspace(plan, CALL_APPEND)
+    ws, ws_bytes = cache.workspace(plan, CALL_APPEND)
     st = _lib_handle.capattn_cache_append(plan.ref, k_new.data_ptr(), v_new.data_ptr(), ks, vs, N, cu, k, v, table,
-                                          lens, weights, pos, qpos, ws.data_ptr(), ws.numel(), s)
+                                          lens, weights, pos, qpos, ws, ws_bytes, s)
     _ca._check(st, "capattn_cache_append")
 
 
@@ -307,17 +309,19 @@ def cache_decode(q, cache: KVCache, ap: AttnParams, temp=None, accumulate=False,
     k, v, table, lens = cache._tensors()
     if cache.pos is not None:
         pos, qpos = cache._positions()
-    plan = cache._plans.get((Hq, ap)) or cache.plan(Hq, ap)
+    plan = cache.plan(Hq, ap)
     if out is None:
         o = torch.empty_like(q) if flat else torch.empty(shape, dtype=q.dtype, device=dev)
-        lse = torch.empty((cache.B, Hq), dtype=torch.float32, device=dev)
+        if plan.lse_like is None:
+            plan.lse_like = torch.empty((cache.B, Hq), dtype=torch.float32, device=dev)
+        lse = torch.empty_like(plan.lse_like)  # (half the time of naming shape, type and device)
     else:
         o, lse = out
         _want(o, "o", shape, cache.dtype, dev)
         _want(lse, "lse", (cache.B, Hq), torch.float32, dev)
-    ws = cache.workspace(plan, CALL_DECODE_WEIGHTS if accumulate else CALL_DECODE)
+    ws, ws_bytes = cache.workspace(plan, CALL_DECODE_WEIGHTS if accumulate else CALL_DECODE)
     st = _lib_handle.capattn_cache_decode(plan.ref, q.data_ptr(), qs, k, v, table, lens, tp, pos, qpos, o.data_ptr(),
-                                          lse.data_ptr(), weights, ws.data_ptr(), ws.numel(), s)
+                                          lse.data_ptr(), weights, ws, ws_bytes, s)
     if st:
         _ca._check(st, "capattn_cache_decode")
     return o, lse
@@ -356,10 +360,10 @@ def cache_evict(cache: KVCache, budget: int, keep_first: int = 0, keep_last: int
         pos_out = _want(out[2], "pos_out", cache._slots, torch.int32, dev)
     plan = cache.plan(cache.Hkv)
     src = torch.empty((cache.B, cache.Hkv, budget), dtype=torch.int32, device=dev) if want_src else None
-    ws = cache.workspace(plan, CALL_EVICT)
+    ws, ws_bytes = cache.workspace(plan, CALL_EVICT)
     st = _lib_handle.capattn_cache_evict(plan.ref, budget, keep_first, keep_last, k, v, table, lens, weights, pos, qpos,
                                          lens_out, weights_out, pos_out, None if src is None else src.data_ptr(),
-                                         ws.data_ptr(), ws.numel(), s)
+                                         ws, ws_bytes, s)
     _ca._check(st, "capattn_cache_evict")
     return src
 
