@@ -258,8 +258,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
       }
       if (it.whole) continue;
       const Pieces pc(it);
-      const bool last = __shfl_sync(0xFFFFFFFFu, lane == 0 ? (int)count_piece(p, pc) : 0, 0) != 0;
-      if (last) join_pieces<__nv_bfloat16, D, 1>(p, pc, b, hg, 0, lane, 0, nullptr, nullptr);
+      if (count_piece_warp(p, pc, lane)) join_pieces<__nv_bfloat16, D, 1>(p, pc, b, hg, 0, lane, 0, nullptr, nullptr);
     }
     return;
   }

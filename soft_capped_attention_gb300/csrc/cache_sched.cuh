@@ -238,6 +238,7 @@ struct PieceIter {
 // The pieces of one split (sequence, group): CTAs c0 .. c1, and their slots.
 struct Pieces {
   int c0, c1, late;  // late: the first one starts inside c0's range
+  __device__ Pieces(int first, int last, int starts_late) : c0(first), c1(last), late(starts_late) {}
   template <int TK>
   __device__ explicit Pieces(const PieceIter<TK>& it) {
     c0 = it.cta_of(it.s0);
@@ -305,6 +306,16 @@ __device__ __forceinline__ bool count_piece(const CacheParams& p, const Pieces& 
   const bool last = before == (uint32_t)(pc.c1 - pc.c0);
   if (last) p.counters[pc.c0] = 0u;
   return last;
+}
+// The same for a piece that one whole warp has left (every lane gets the answer): the
+// lanes meet before lane 0 counts, and after it, since a shuffle alone orders no memory
+// and the last piece's lanes go on to read what other CTAs wrote.
+__device__ __forceinline__ bool count_piece_warp(const CacheParams& p, const Pieces& pc, int lane) {
+  int last = 0;
+  __syncwarp();
+  if (lane == 0) last = count_piece(p, pc);
+  __syncwarp();
+  return __shfl_sync(0xFFFFFFFFu, last, 0) != 0;
 }
 
 // Adds the pieces of (b, group) up and writes o and lse, by WARPS warps (4 that meet
