@@ -16,8 +16,8 @@
 // A CTA's part of one (sequence, group) is a piece; a piece that is not the whole
 // leaves (m, l, O) in the CTA's slot 2c (the piece at the start of its range) or
 // 2c + 1 (the one at its end; pieces between the two are whole).  The CTA that
-// leaves the last piece of a (sequence, group) joins them, in the order of their
-// CTAs whichever came last; it is found by a counter that belongs to the CTA where
+// leaves the last piece of a (sequence, group) joins them, in an order that their CTAs'
+// numbers alone decide (join_pieces); it is found by a counter that belongs to the CTA where
 // the group starts (at most one split group starts in a CTA) and returns to zero.
 // Every warp computes the split from lens by itself, so the lengths stay on the
 // device.
@@ -271,28 +271,44 @@ __device__ __forceinline__ int page_of(const CacheParams& p, int b, int slot) {
   return page;
 }
 
-// Adds up what four warps left of head e of four: results buf [4][4][D], maxima sm
+// Adds up four parts of a head: maxima m (-inf: no live keys), sums l and this lane's
+// columns of O.
+template <int V>
+__device__ __forceinline__ void merge_parts(const float (&m)[4], const float (&l)[4], const float (&o)[4][V],
+                                            float (&y)[V], float* sum_out, float* top_out) {
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = fmaxf(top, m[w]);
+#pragma unroll
+  for (int x = 0; x < V; ++x) y[x] = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    // a part without live keys adds nothing; one with nothing but NaN scores (no
+    // maximum, but a sum) comes through
+    const float f = m[w] != -INFINITY ? __expf(m[w] - top) : l[w] != 0.f ? 1.f : 0.f;
+    sum = fmaf(l[w], f, sum);
+#pragma unroll
+    for (int x = 0; x < V; ++x) y[x] = fmaf(o[w][x], f, y[x]);
+  }
+  *sum_out = sum;
+  *top_out = top;
+}
+
+// The same for what four warps left of head e of four: results buf [4][4][D], maxima sm
 // and sums sl [4][4], all shared; a lane takes D / 32 columns.
 template <int D>
 __device__ __forceinline__ void merge_warps(const float* buf, const float* sm, const float* sl, int e, int lane,
                                             float (&y)[D / 32], float* sum_out, float* top_out) {
-  float top = -INFINITY, sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, sm[4 * w + e]);
-#pragma unroll
-  for (int x = 0; x < D / 32; ++x) y[x] = 0.f;
+  constexpr int V = D / 32;
+  float m[4], l[4], o[4][V];
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const float mw = sm[4 * w + e], lw = sl[4 * w + e];
-    // a warp without live keys adds nothing; one with nothing but NaN scores (no
-    // maximum, but a sum) comes through
-    const float f = mw != -INFINITY ? __expf(mw - top) : lw != 0.f ? 1.f : 0.f;
-    sum = fmaf(lw, f, sum);
+    m[w] = sm[4 * w + e];
+    l[w] = sl[4 * w + e];
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) y[x] = fmaf(buf[(w * 4 + e) * D + lane * (D / 32) + x], f, y[x]);
+    for (int x = 0; x < V; ++x) o[w][x] = buf[(w * 4 + e) * D + lane * V + x];
   }
-  *sum_out = sum;
-  *top_out = top;
+  merge_parts<V>(m, l, o, y, sum_out, top_out);
 }
 
 // Counts a piece in (one thread, after everything of the piece's partial results
@@ -318,97 +334,161 @@ __device__ __forceinline__ bool count_piece_warp(const CacheParams& p, const Pie
   return __shfl_sync(0xFFFFFFFFu, last, 0) != 0;
 }
 
+// A running sum over some of a head's pieces: maximum m (0 until there is one), sum and
+// this lane's V columns of O.
+template <int V>
+struct Chain {
+  float m, l, o[V];
+  bool any;
+  __device__ __forceinline__ Chain() : m(0.f), l(0.f), any(false) {
+#pragma unroll
+    for (int x = 0; x < V; ++x) o[x] = 0.f;
+  }
+  // N pieces in order (one that is not there: maximum -inf, zeros).  Fewer than four give
+  // what four would whose last ones are not there, but for the sign of a zero.
+  template <int N>
+  __device__ __forceinline__ void add(const float2 (&ml)[N], const float (&v)[N][V]) {
+    float top = ml[0].x;
+#pragma unroll
+    for (int y = 1; y < N; ++y) top = fmaxf(top, ml[y].x);
+    if (top != -INFINITY) {
+      top = any ? fmaxf(top, m) : top;
+      const float scale = any ? __expf(m - top) : 1.f;  // without a maximum l and o are 0 or NaN
+      l *= scale;
+#pragma unroll
+      for (int x = 0; x < V; ++x) o[x] *= scale;
+      m = top;
+      any = true;
+    }
+#pragma unroll
+    for (int y = 0; y < N; ++y) {
+      const float w = __expf(ml[y].x - m);
+      l = fmaf(ml[y].y, w, l);
+#pragma unroll
+      for (int x = 0; x < V; ++x) o[x] = fmaf(v[y][x], w, o[x]);
+    }
+  }
+};
+
+// Piece c of a head: its (m, l) and this lane's columns; not there when !in.
+template <int D>
+__device__ __forceinline__ void load_piece(const CacheParams& p, const Pieces& pc, int c, int head, int lane, bool in,
+                                           float2& ml, float (&v)[D / 32]) {
+  constexpr int V = D / 32;
+  ml = make_float2(-INFINITY, 0.f);
+#pragma unroll
+  for (int x = 0; x < V; ++x) v[x] = 0.f;
+  if (!in) return;
+  const size_t at = (size_t)pc.slot_of(c) * kDecodeHeads + head;
+  ml = __ldcg(&p.part_ml[at]);
+  const float* po = p.part_o + at * D + lane * V;
+  if constexpr (V == 4) {
+    const float4 f = __ldcg(reinterpret_cast<const float4*>(po));
+    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+  } else {
+    const float2 f = __ldcg(reinterpret_cast<const float2*>(po));
+    v[0] = f.x; v[1] = f.y;
+  }
+}
+
+// Writes row `row` of o and lse from the sum of its pieces.
+template <typename T, int V>
+__device__ __forceinline__ void write_row(const CacheParams& p, size_t row, int lane, const float (&y)[V], float sum,
+                                          float top) {
+#pragma unroll
+  for (int x = 0; x < V; ++x) static_cast<T*>(p.o)[row * (32 * V) + lane * V + x] = (T)(sum == 0.f ? 0.f : y[x] / sum);
+  if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
+}
+
+// The join by one warp: four chains of HEADS heads at a time, 4 / HEADS pieces of each in
+// flight (with more than one head: all that there are).
+template <typename T, int D, int HEADS>
+__device__ __forceinline__ void join_by_warp(const CacheParams& p, const Pieces& pc, int b, const HeadGroup& hg, int lane) {
+  constexpr int V = D / 32, N = 4 / HEADS;
+  for (int h0 = 0; h0 < hg.count; h0 += HEADS) {
+    Chain<V> chains[HEADS][4];
+    for (int c = pc.c0; c <= pc.c1; c += 4 * N) {
+      float2 ml[HEADS][4][N];
+      float v[HEADS][4][N][V];
+#pragma unroll
+      for (int e = 0; e < HEADS; ++e)
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+          for (int y = 0; y < N; ++y)
+            load_piece<D>(p, pc, c + w + 4 * y, h0 + e, lane, c + w + 4 * y <= pc.c1 && h0 + e < hg.count, ml[e][w][y],
+                          v[e][w][y]);
+#pragma unroll
+      for (int e = 0; e < HEADS; ++e)
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (c + w <= pc.c1) chains[e][w].template add<N>(ml[e][w], v[e][w]);
+      if (HEADS > 1) break;
+    }
+#pragma unroll
+    for (int e = 0; e < HEADS; ++e) {
+      if (h0 + e >= hg.count) break;
+      float m[4], l[4], o[4][V], y[V], sum, top;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        m[w] = chains[e][w].any ? chains[e][w].m : -INFINITY;
+        l[w] = chains[e][w].l;
+#pragma unroll
+        for (int x = 0; x < V; ++x) o[w][x] = chains[e][w].o[x];
+      }
+      merge_parts<V>(m, l, o, y, &sum, &top);
+      write_row<T, V>(p, (size_t)b * p.Hq + hg.h0 + h0 + e, lane, y, sum, top);
+    }
+  }
+}
+
 // Adds the pieces of (b, group) up and writes o and lse, by WARPS warps (4 that meet
-// at named barrier `bar`, with buf 4 x 4 x D floats and sbuf 32, both shared; or 1):
-// warp w takes every WARPS-th piece, four heads and four pieces in flight at a time,
-// with a running maximum, so that nothing is read twice or waits for a first pass.
+// at named barrier `bar`, with buf 4 x 4 x D floats and sbuf 32, both shared; or 1).
+// Either way four chains take every fourth piece each, four pieces at a time with a
+// running maximum, so that nothing is read twice or waits for a first pass, and are then
+// added in order: the result does not depend on which CTA came last.  Four warps take a
+// chain each, of four heads at a time; one warp all four, of as many heads at a time as
+// its registers hold (a head at a time whatever the pieces: 32 users of 1024 to 3968
+// keys a pass of 25 us against 23).
 template <typename T, int D, int WARPS>
 __device__ __forceinline__ void join_pieces(const CacheParams& p, const Pieces& pc, int b, const HeadGroup& hg, int warp,
                                             int lane, int bar, float* buf, float* sbuf) {
+  static_assert(WARPS == 1 || WARPS == 4, "four chains, by one warp or four");
   constexpr int V = D / 32;
-  for (int g0 = 0; g0 < hg.count; g0 += 4) {
-    const int heads = min(4, hg.count - g0);
-    float m[4], l[4], o[4][V];  // m: 0 until there is a maximum
-    bool any[4];
+  if constexpr (WARPS == 1) {
+    const int n = pc.c1 - pc.c0 + 1;
+    if (n <= 4) join_by_warp<T, D, 4>(p, pc, b, hg, lane);
+    else if (n <= 8) join_by_warp<T, D, 2>(p, pc, b, hg, lane);
+    else join_by_warp<T, D, 1>(p, pc, b, hg, lane);
+  } else {
+    for (int g0 = 0; g0 < hg.count; g0 += 4) {
+      const int heads = min(4, hg.count - g0);
+      Chain<V> chains[4];  // of the four heads
+      for (int c = pc.c0 + warp; c <= pc.c1; c += 16) {
+        float2 ml[4][4];
+        float v[4][4][V];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      m[e] = l[e] = 0.f;
-      any[e] = false;
+        for (int y = 0; y < 4; ++y)
 #pragma unroll
-      for (int x = 0; x < V; ++x) o[e][x] = 0.f;
-    }
-    for (int c = pc.c0 + warp; c <= pc.c1; c += 4 * WARPS) {
-      float2 ml[4][4];
-      float v[4][4][V];
+          for (int e = 0; e < 4; ++e)
+            load_piece<D>(p, pc, c + 4 * y, g0 + e, lane, c + 4 * y <= pc.c1 && e < heads, ml[e][y], v[e][y]);
 #pragma unroll
-      for (int y = 0; y < 4; ++y)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          ml[y][e] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-          for (int x = 0; x < V; ++x) v[y][e][x] = 0.f;
-          if (c + WARPS * y > pc.c1 || e >= heads) continue;
-          const size_t at = (size_t)pc.slot_of(c + WARPS * y) * kDecodeHeads + g0 + e;
-          ml[y][e] = __ldcg(&p.part_ml[at]);
-          const float* po = p.part_o + at * D + lane * V;
-          if constexpr (V == 4) {
-            const float4 f = __ldcg(reinterpret_cast<const float4*>(po));
-            v[y][e][0] = f.x; v[y][e][1] = f.y; v[y][e][2] = f.z; v[y][e][3] = f.w;
-          } else {
-            const float2 f = __ldcg(reinterpret_cast<const float2*>(po));
-            v[y][e][0] = f.x; v[y][e][1] = f.y;
-          }
-        }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float top = fmaxf(fmaxf(ml[0][e].x, ml[1][e].x), fmaxf(ml[2][e].x, ml[3][e].x));
-        if (top != -INFINITY) {
-          top = any[e] ? fmaxf(top, m[e]) : top;
-          const float scale = any[e] ? __expf(m[e] - top) : 1.f;  // without a maximum l and o are 0 or NaN
-          l[e] *= scale;
-#pragma unroll
-          for (int x = 0; x < V; ++x) o[e][x] *= scale;
-          m[e] = top;
-          any[e] = true;
-        }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float w = __expf(ml[y][e].x - m[e]);
-          l[e] = fmaf(ml[y][e].y, w, l[e]);
-#pragma unroll
-          for (int x = 0; x < V; ++x) o[e][x] = fmaf(v[y][e][x], w, o[e][x]);
-        }
+        for (int e = 0; e < 4; ++e) chains[e].template add<4>(ml[e], v[e]);
       }
-    }
-    if constexpr (WARPS == 1) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (e >= heads) continue;
-        const size_t row = (size_t)b * p.Hq + hg.h0 + g0 + e;
-#pragma unroll
-        for (int x = 0; x < V; ++x)
-          static_cast<T*>(p.o)[row * D + lane * V + x] = (T)(l[e] == 0.f ? 0.f : o[e][x] / l[e]);
-        if (lane == 0) p.lse[row] = l[e] == 0.f ? -INFINITY : m[e] + logf(l[e]);
-      }
-    } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
 #pragma unroll
-        for (int x = 0; x < V; ++x) buf[(warp * 4 + e) * D + lane * V + x] = o[e][x];
+        for (int x = 0; x < V; ++x) buf[(warp * 4 + e) * D + lane * V + x] = chains[e].o[x];
         if (lane == 0) {
-          sbuf[warp * 4 + e] = any[e] ? m[e] : -INFINITY;
-          sbuf[16 + warp * 4 + e] = l[e];
+          sbuf[warp * 4 + e] = chains[e].any ? chains[e].m : -INFINITY;
+          sbuf[16 + warp * 4 + e] = chains[e].l;
         }
       }
       named_bar_sync(bar, 128);
       if (warp < heads) {  // a head a warp
         float y[V], sum, top;
         merge_warps<D>(buf, sbuf, sbuf + 16, warp, lane, y, &sum, &top);
-        const size_t row = (size_t)b * p.Hq + hg.h0 + g0 + warp;
-#pragma unroll
-        for (int x = 0; x < V; ++x)
-          static_cast<T*>(p.o)[row * D + lane * V + x] = (T)(sum == 0.f ? 0.f : y[x] / sum);
-        if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
+        write_row<T, V>(p, (size_t)b * p.Hq + hg.h0 + g0 + warp, lane, y, sum, top);
       }
       named_bar_sync(bar, 128);
     }

@@ -10,6 +10,7 @@ import pytest
 import torch
 
 from kv_cache_utils import EPS32
+from soft_capped_attention_gb300 import capattn as ca
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +111,48 @@ def test_pieces_left_by_other_ctas_are_all_read(lib, shape):
         got = p.run(lib, 0)
         assert torch.equal(got[0].view(torch.int32), want[0].view(torch.int32))
         assert torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_a_join_has_the_same_bits_whoever_makes_it(lib, shape):
+    """One warp (a group's last CTA, which has more to do) or four (the others)."""
+    for seed in range(5):
+        p = Parts(*shape, seed=1000 * seed + sum(shape))
+        one, four = p.run(lib, 1), p.run(lib, 4)
+        assert torch.equal(one[0].view(torch.int32), four[0].view(torch.int32))
+        assert torch.equal(one[1], four[1])
+
+
+@pytest.mark.parametrize("lens, Hq, Hkv, D, page, window", [
+    ([2050 + 409 * i for i in range(16)], 32, 8, 128, 64, 0),
+    ([130_977], 32, 8, 128, 64, 0),
+    ([9000, 300, 20_000], 5, 1, 64, 32, 6000),
+], ids=["batch", "long", "window"])
+def test_split_decodes_repeat_their_bits_while_other_work_runs(lens, Hq, Hkv, D, page, window):
+    """Another stream's kernels hold some of the SMs for some of the time, so that now one
+    CTA comes last to a group and now another."""
+    from soft_capped_attention_gb300 import kv_cache as kv
+    g = torch.Generator(device="cuda").manual_seed(Hq)
+    used = [-(-n // page) for n in lens]
+    table = torch.full((len(lens), max(used)), -1, dtype=torch.int32)
+    order, at = torch.randperm(sum(used)).to(torch.int32), 0
+    for b, n in enumerate(used):
+        table[b, :n] = order[at:at + n]
+        at += n
+    k, v = (torch.randn(sum(used), Hkv, page, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    start = torch.rand(len(lens), Hkv, max(used) * page, generator=g, device="cuda")
+    cache = kv.KVCache(k, v, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), weights=start.clone())
+    q = torch.randn(len(lens), Hq, D, generator=g, device="cuda").bfloat16()
+    ap = ca.AttnParams(sm_scale=1 / math.sqrt(D), cap_method="soft_sign", cap=20.0, causal=True, window_len=window)
+    want = [x.clone() for x in kv.cache_decode(q, cache, ap, accumulate=True)] + [cache.weights.clone()]
+    side, x = torch.cuda.Stream(), torch.randn(700, 700, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(60):
+        with torch.cuda.stream(side):
+            for _ in range(i % 7):
+                torch.mm(x, x)
+        cache.weights.copy_(start)
+        o, lse = kv.cache_decode(q, cache, ap, accumulate=True)
+        assert torch.equal(o.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
+        assert torch.equal(cache.weights, want[2])
+    assert cache.status() == (0, 0)
