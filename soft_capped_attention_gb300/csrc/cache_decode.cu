@@ -50,7 +50,8 @@ struct Smem {
   float half[PARTS > 1 ? GM : 1][64];  // D = 64: outputs of the second half of the threads
   float lsum[32];
   int flag;
-  // the join's 4 x 4 x D floats: no tile is in flight at a piece's end
+  // the join's 4 x 4 x D floats: no tile is in flight at a piece's end (every copy that a
+  // piece starts belongs to one of its tiles, and the last one waits for all)
   __device__ float* join() { return reinterpret_cast<float*>(&k[0][0][0]); }
   static_assert(2 * TK * ROW * sizeof(T) >= 16 * D * sizeof(float), "the join's buffer");
 };
@@ -112,7 +113,7 @@ decode_simt_kernel(CacheParams p) {
     }
 #pragma unroll
     for (int g = 0; g < GM; ++g) acc[g] = 0.f;
-    load(0);
+    if (n > 0) load(0);  // a piece may be a group's first unit alone, or an empty sequence
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
       if (i + 1 < n) {
