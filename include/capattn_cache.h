@@ -41,10 +41,11 @@
  *
  * Status bits that these calls add (capattn_device_status returns
  * CAPATTN_ERR_DEVICE_DATA): 32 = a length outside [0, max_len]; 64 = a page
- * outside [0, num_pages); 128 = cu_new decreases or a sequence has more new rows
- * than lens[b]; 256 = rows of capattn_key_weights outside 0 <= lo <= hi <= L.
- * Nothing outside the caller's buffers is read or written then; the results of
- * that sequence are unspecified.
+ * outside [0, num_pages); 128 = cu_new decreases or leaves [0, n_rows] or a
+ * sequence has more new rows than lens[b]; 256 = rows of capattn_key_weights
+ * outside 0 <= lo <= hi <= L.  Nothing outside the caller's buffers is read or
+ * written then; the results of that sequence (after a bad cu_new: of every sequence
+ * that the call gives rows) are unspecified.
  */
 #ifndef CAPATTN_CACHE_H_
 #define CAPATTN_CACHE_H_
@@ -91,8 +92,8 @@ size_t capattn_cache_workspace_bytes(const capattn_cache_config* cfg, int call);
  * r * row_stride elements (rows of a fused projection need no copy; the stride
  * is a multiple of 16 bytes and at least Hkv * D).  cu_new [B + 1] int32,
  * nullable: the rows of sequence b are cu_new[b] .. cu_new[b + 1] - 1; NULL: row b
- * is the one new token of sequence b (n_rows == B).  Rows at or behind cu_new[B]
- * are ignored.  The n new rows of sequence b go to slots lens[b] - n .. lens[b] - 1.
+ * is the one new token of sequence b (n_rows == B).  Rows before cu_new[0] and at or
+ * behind cu_new[B] are ignored; with n_rows == 0 the call does nothing.  The n new rows of sequence b go to slots lens[b] - n .. lens[b] - 1.
  * With weights, the new slots' weights become 0; with pos, their positions
  * qpos[b] - n + 1 .. qpos[b].
  */

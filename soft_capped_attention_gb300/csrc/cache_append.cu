@@ -66,6 +66,12 @@ append_kernel(CacheParams p, int rows, int vpr, int vph_shift) {
   pdl_wait();
   const int r0 = blockIdx.x * rows;
   const int n = min(rows, p.n_rows - r0);
+  // cu_new itself, shared out over the grid's threads
+  if (p.cu_new)
+    for (long long b = (long long)blockIdx.x * kThreads + threadIdx.x; b < p.B; b += (long long)gridDim.x * kThreads) {
+      const int from = p.cu_new[b], to = p.cu_new[b + 1];
+      if (from > to || from < 0 || to > p.n_rows) atomicOr(p.status, kStatusBadNewRowsBit);
+    }
   if (threadIdx.x < n) places[threadIdx.x] = place_of(p, r0 + threadIdx.x);
   __syncthreads();
   const uint4* kn = static_cast<const uint4*>(p.k_new);

@@ -14,7 +14,7 @@ namespace capattn {
 // Status bits of the cache's calls (beside those of status_bits.h).
 constexpr uint32_t kStatusBadLensBit = 32u;     // a length outside [0, max_len]
 constexpr uint32_t kStatusBadPageBit = 64u;     // a page outside [0, num_pages)
-constexpr uint32_t kStatusBadNewRowsBit = 128u; // cu_new decreases, or more new rows than lens
+constexpr uint32_t kStatusBadNewRowsBit = 128u; // cu_new decreases or leaves [0, n_rows], or more new rows than lens
 constexpr uint32_t kStatusBadRowsBit = 256u;    // rows outside 0 <= lo <= hi <= L
 
 // Constants of a cap in the forms of cache_math.cuh, for raw scores X = <q, k>.
