@@ -120,7 +120,7 @@ select_kernel(CacheParams p, int parts) {
   int n = p.lens[b];
   if (n < 0 || n > p.max_len) {
     if (threadIdx.x == 0) atomicOr(p.status, kStatusBadLensBit);
-    n = n < 0 ? 0 : p.max_len;
+    n = n < 0 ? 0 : p.budget;  // nothing moves: the table behind the tokens may name anyone's pages
   }
   const size_t base = (size_t)row * p.max_len;
   RowKeys keys;
