@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include "cache_internal.h"
+#include "near_tanh.h"
 #include "softmax_elem.cuh"
 
 namespace capattn {
@@ -34,26 +35,6 @@ capattn_status check_config(const capattn_cache_config* c) {
   // units of work of a decode (64-key tiles) and (sequence, head) rows are 32-bit too
   if ((int64_t)c->B * c->Hq * (max_len_of(*c) / 32 + 4) > (1ll << 31) - 1) return CAPATTN_ERR_UNSUPPORTED;
   return CAPATTN_OK;
-}
-
-// tanh(u) = u (a0 + a1 w + a2 w^2), w = u^2, for |u| <= kNearTanh: tanh(u) / u
-// interpolated at the three Chebyshev nodes of w in [0, kNearTanh^2] (error 3e-8 of
-// tanh(u) / u), then with both scales folded in: cap tanh(in X) = X (c0 + z (c1 + z c2)),
-// z = X^2.
-constexpr double kNearTanh = 0.2;
-void near_tanh_fit(double cap, double in, float c[3]) {
-  const double pi = 3.14159265358979323846, half = 0.5 * kNearTanh * kNearTanh;
-  double w[3], f[3];
-  for (int i = 0; i < 3; ++i) {
-    w[i] = half * (1.0 + cos((2 * i + 1) * pi / 6.0));
-    f[i] = tanh(sqrt(w[i])) / sqrt(w[i]);
-  }
-  // Newton's divided differences, multiplied out
-  const double d01 = (f[1] - f[0]) / (w[1] - w[0]), d12 = (f[2] - f[1]) / (w[2] - w[1]);
-  const double d012 = (d12 - d01) / (w[2] - w[0]);
-  const double a[3] = {f[0] - d01 * w[0] + d012 * w[0] * w[1], d01 - d012 * (w[0] + w[1]), d012};
-  double s = cap * in;
-  for (int i = 0; i < 3; ++i, s *= in * in) c[i] = (float)(a[i] * s);
 }
 
 ExactCap exact_cap_of(int method, float cap_in, float alpha, float beta, float sm_scale, int* active) {
