@@ -422,6 +422,7 @@ def key_weights(q, k, lse, ap: AttnParams, temp=None, seg=None, bounds=None, row
     op = _want(out, "out", (B, Hkv, W), torch.float32, dev)
     if workspace is None:
         workspace = new_key_weights_workspace(q, k, ap)
+    _want(workspace, "workspace", workspace.shape, torch.uint8, dev)
     st = lib().capattn_key_weights(ref, qp, kp, lp, tp, sp, bp, rp, op, W, workspace.data_ptr(), workspace.numel(), s)
     _ca._check(st, "capattn_key_weights")
     return out
