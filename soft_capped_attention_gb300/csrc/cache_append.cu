@@ -6,8 +6,8 @@
 // finds the sequence (binary search), checks slot and page, and leaves the row's
 // place in shared memory; then all threads copy 16-byte vectors, a head's D
 // values being one contiguous run on both sides.  Bound by memory: prompts of 18,438
-// tokens x 16 heads (303 MB in and out) take 48.7 us, 6.2 TB/s, 91 % of the measured
-// copy rate; a decoding step's 32 rows take 2.4 us, a launch.
+// tokens x 16 heads (303 MB in and out) take 49.2 us, 6.2 TB/s, 91 % of the measured
+// copy rate; a decoding step's 32 rows take 2.1 us, a launch.
 #include "cache_internal.h"
 
 namespace capattn {

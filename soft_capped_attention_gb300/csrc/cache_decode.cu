@@ -8,7 +8,9 @@
 // O likewise.
 //   fp32 stays on the CUDA cores (a TF32 product keeps 11 bits of q and k).  Memory
 // bounds a group of one head (4 sequences of 16,000 keys x 8 heads, D = 128, 524 MB:
-// 97 us, 5.4 TB/s), the products a larger one (4 heads: 125 us, 16 heads: 385 us).
+// 95 us, 5.5 TB/s); a larger one is bound by reading the tile from shared memory once a
+// head, by eight warps an SM (4 heads: 125 us, 16 heads: 356 us, of which the products
+// alone would take 56: the shared-memory pipe is 66 % busy, the FMA pipe 20 %).
 #include "cache_internal.h"
 #include "cache_math.cuh"
 #include "cache_sched.cuh"

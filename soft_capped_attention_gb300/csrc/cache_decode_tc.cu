@@ -4,9 +4,11 @@
 // KV head against 4 D G operations, so memory does at any group size G of up to
 // 16; the kernel's task is to keep the loads in flight.  Measured: 130,977 keys of 8
 // heads (D = 128, 537 MB) in 85 us, 6.3 TB/s, 93 % of the measured copy rate; 32 users
-// of 1024 to 3968 keys (82 MB) in 16 us, 5.1 TB/s; 64 sequences in a window of 1024
+// of 1024 to 3968 keys (82 MB) in 23 us, 3.6 TB/s (16 us when the last call has left
+// them in L2); 64 sequences in a window of 1024
 // (240 MB) in 45 us, 5.3 TB/s (of a consumer warp's 80,000 cycles 34,000 compute,
-// 32,000 wait for memory and 14,000 are the starts, ends and joins of its pieces).  The CUDA-core form of the fp32 kernel took 230, 47 and 120 us.  A persistent grid, two
+// 32,000 wait for memory and 14,000 are the starts, ends and joins of its pieces).  The
+// CUDA-core form of the fp32 kernel took 230, 47 (from L2) and 120 us.  A persistent grid, two
 // CTAs an SM, takes equal shares of 64-key tiles (cache_sched.cuh).  In each CTA
 // one warp fills a ring of shared-memory stages by TMA (a tile's pages are boxes
 // of up to a tile's rows x 64 columns in the 128-byte swizzle) and four warps compute,

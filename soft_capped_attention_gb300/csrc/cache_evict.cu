@@ -20,9 +20,10 @@
 // last pass over the keys lists the slots.  What follows from the lists (the rows' pages,
 // the copies, the moved tokens' weights and positions) is the second kernel's, over
 // all SMs.
-//   Measured: 8 rows of 130,977 tokens cut to 16,384 take 38.4 us (about 17 of them
-// selection, 20 the 117 MB of rows that move), 128 rows of 2049 to 4096 cut to 2048
-// take 24.6 us.  With the slots shared out in one run a CTA instead of two, the CTA
+//   Measured: 8 rows of 130,977 tokens cut to 16,384 take 43 us (about 21 of them
+// selection, 22 the 117 MB of rows that move), 128 rows of 2049 to 4096 cut to 2048
+// take 28.5 us; 38.4 and 24.6 when the last call has left part of them in L2, as in what
+// follows.  With the slots shared out in one run a CTA instead of two, the CTA
 // below the budget had all the freed ones to list (and 44.6 us, with three exchanges
 // of counts).  Clusters of 16 CTAs took 59 us against 46 (a GPC places few of them at
 // once), one CTA a row 640 us.  1024 threads a CTA, copies of the first histogram and

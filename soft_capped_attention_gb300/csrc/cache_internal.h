@@ -86,7 +86,7 @@ struct CacheParams {
   ExactCap cap;
 };
 
-// Heads a decode CTA handles at once (the rows of one tensor-core tile).
+// Heads a decode CTA handles at once (the columns of two tensor-core tiles).
 constexpr int kDecodeHeads = 16;
 // Most CTAs of the persistent decode (bounds its partial results).
 constexpr int kDecodeMaxCtas = 152 * 4;

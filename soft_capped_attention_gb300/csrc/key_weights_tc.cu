@@ -18,10 +18,11 @@
 // 512 on the MUFU pipe (32 a clock and SM), the cap's polynomial and the sums 640
 // (tanh near zero; 5 products a pair at 128 a clock) to 1150 (alsc with
 // temperatures).  Measured are about 1400 cycles a step on a long prompt (8192 rows,
-// 32 heads, tanh: 322 us, 854 TFLOP/s at 2 D a live pair), about half of the issue
-// slots used, and about 12 us of launches and first loads (two prompts of 2048 x 16
-// heads: 32.1 us in all; 4096 rows x 32 heads in a window of 1024 with alsc and
-// temperatures: 70.3 us).
+// 32 heads, tanh: 322 us, 854 TFLOP/s at 2 D a live pair), with about half of the issue
+// slots used (the elementwise warps wait for tensor memory and for one another at a
+// piece's end), and about 12 us of launches and first loads (two prompts of 2048 x 16
+// heads: 32.6 us in all; 4096 rows x 32 heads in a window of 1024 with alsc and
+// temperatures: 72.3 us; 32.1 and 70.3 with inputs in L2, as in what follows).
 //   Tried: the steps of a key tile cut over clusters of up to 8 CTAs instead of the
 // persistent shares (58 us for the two prompts: two steps a CTA, mostly prologue);
 // constants loaded by the TMA warp (40 us: the MMAs waited for it); one step for all

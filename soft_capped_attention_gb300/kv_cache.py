@@ -163,8 +163,9 @@ class KVCache:
     them are the caller's; the cache adds one workspace, which grows to what its
     calls need.  Calls that may overlap on the GPU (two streams, two captured
     graphs) need a KVCache each (the tensors may be the same); keep a KVCache until
-    the work that it enqueued on other streams has finished.  The calls are for
-    serving: they record no gradients."""
+    the work that it enqueued on other streams has finished, and as long as a graph
+    that captured its calls is replayed.  The calls are for serving: they record no
+    gradients."""
 
     def __init__(self, k, v, table, lens, weights=None, pos=None, qpos=None):
         if k.dim() != 4 or table.dim() != 2:
@@ -243,7 +244,8 @@ class KVCache:
                 _want(self.qpos, "qpos", (self.B,), torch.int32, self.device))
 
     def status(self, stream=None) -> tuple[int, int]:
-        """Synchronises; returns (status, raw bits) of the calls so far and clears them."""
+        """Synchronises `stream` (the current one); returns (status, raw bits) of the calls so
+        far, on other streams of those that have finished, and clears them."""
         status, raw = 0, 0
         with _on(self.device, stream):
             for w in self._workspaces:
