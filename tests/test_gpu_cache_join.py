@@ -156,3 +156,27 @@ def test_split_decodes_repeat_their_bits_while_other_work_runs(lens, Hq, Hkv, D,
         assert torch.equal(o.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse, want[1])
         assert torch.equal(cache.weights, want[2])
     assert cache.status() == (0, 0)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_pieces_with_nan_and_infinity_join_alike(lib, shape):
+    """A piece of NaN scores only has no maximum but a NaN sum; one with an infinite score
+    an infinite maximum and NaN; an output may be a negative zero."""
+    D, groups, pieces, heads = shape
+    p = Parts(*shape, seed=7 + sum(shape))
+    g = torch.Generator().manual_seed(3)
+    kind = torch.rand(SLOTS, HEADS, generator=g)
+    m, l, o = p.m.clone(), p.l.clone(), p.o.clone()
+    no_max, top, zero = kind < 0.02, (kind >= 0.02) & (kind < 0.04), (kind >= 0.04) & (kind < 0.3)
+    m[no_max], l[no_max], o[no_max] = -math.inf, math.nan, math.nan
+    m[top], l[top], o[top] = math.inf, math.nan, math.nan
+    o[zero] = -0.0
+    p.ml.copy_(torch.stack([m, l], -1))
+    p.parts.copy_(o)
+    one, left, four = p.run(lib, 1), p.run(lib, 0), p.run(lib, 4)
+    for x, y, z in zip(one, left, four):
+        assert torch.equal(x.view(torch.int32), z.view(torch.int32)) and torch.equal(y.view(torch.int32), z.view(torch.int32))
+    for i in range(groups):
+        slots = [2 * c + ((i & 1) if c == i * pieces else 0) for c in range(i * pieces, (i + 1) * pieces)]
+        bad = (no_max | top)[slots, :heads].any(0)
+        assert torch.equal(torch.isnan(four[1][i]).cpu(), bad) and torch.equal(torch.isnan(four[0][i]).all(-1).cpu(), bad)
