@@ -37,6 +37,8 @@ capattn_status check_config(const capattn_cache_config* c) {
   return CAPATTN_OK;
 }
 
+}  // namespace
+
 ExactCap exact_cap_of(int method, float cap_in, float alpha, float beta, float sm_scale, int* active) {
   ExactCap k;
   memset(&k, 0, sizeof(k));
@@ -80,6 +82,8 @@ ExactCap exact_cap_of(int method, float cap_in, float alpha, float beta, float s
   }
   return k;
 }
+
+namespace {
 
 CacheWorkspace layout(const capattn_cache_config& c, int call) {
   CacheWorkspace w;

@@ -115,6 +115,9 @@ struct KeyWeightsParams {
 };
 constexpr int kWeightCtas = 152;  // CTAs of the persistent bf16 kernel
 
+// Constants of a configuration's cap; *active: the method in force (none without a cap).
+ExactCap exact_cap_of(int method, float cap, float alpha, float beta, float sm_scale, int* active);
+
 // Raises a kernel's dynamic shared memory limit, once per device (`done`: a bit a device).
 inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
   if (bytes <= 48 * 1024) return cudaSuccess;

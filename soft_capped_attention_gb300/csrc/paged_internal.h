@@ -1,0 +1,71 @@
+// Internal interfaces of the steps with many new tokens (capattn_paged.h).
+#pragma once
+
+#include "../../include/capattn_paged.h"
+#include "cache_internal.h"
+
+namespace capattn {
+
+// Status bits of these calls (beside those of cache_internal.h).
+constexpr uint32_t kStatusBadParentBit = 512u;
+constexpr uint32_t kStatusBadPlanBit = 1024u;
+constexpr uint32_t kStatusBadPathBit = 2048u;
+
+// Rows of attention whose result has to be formed once more, by itself: a flag and a
+// ticket in the workspace's header, behind the counters; both are zero between calls.
+constexpr size_t kRedoOff = kCacheHeaderBytes - 64;
+static_assert(kCountersOff + kDecodeMaxCtas * sizeof(uint32_t) <= kRedoOff, "header too small");
+
+struct PagedParams {
+  CacheParams c;               // shapes, cache, q, temp, o, lse, status, counters, cap
+  const int32_t* cu_new;
+  int32_t n_rows;
+  const int32_t* parents;      // or null: a prompt
+  uint32_t* redo;              // flag, ticket
+  // query tiles: `tokens` tokens of `heads` query heads of one KV head, parts per KV head
+  int32_t tokens, heads, parts;  // parts * heads >= G
+  int32_t ctas;                // most CTAs of the persistent grid
+  int32_t min_units;           // least units a CTA takes
+  // partial results of split query tiles: slot s has rows [s * rows, (s + 1) * rows)
+  float* part_o;               // [slots][rows][D]
+  float2* part_ml;             // [slots][rows]
+  uint8_t* part_bad;           // [slots][rows][4]
+};
+
+// Slots of partial results: two a CTA.
+constexpr int kAttendCtas = 152;       // bf16: one CTA an SM, tiles of 128 rows
+constexpr int kAttendSimtCtas = 304;   // fp32: two an SM, tiles of 64 rows
+constexpr int kAttendPartRows = 2 * kAttendCtas * 128;
+static_assert(2 * kAttendSimtCtas * 64 <= kAttendPartRows && kAttendSimtCtas <= kDecodeMaxCtas, "partial results");
+
+struct PlanParams {
+  const int32_t* n_new;
+  int32_t* table;
+  const int32_t *lens, *qpos, *held, *n_free;
+  int32_t* free_pages;
+  int32_t *lens_out, *qpos_out, *held_out, *n_free_out;
+  int32_t n_rows;
+  int32_t* cu_new;
+  int64_t* slots;
+  int32_t* positions;
+  int32_t B, page_size, page_shift, max_pages, num_pages, max_len;
+  int4* seqs;                  // [B] workspace, for more sequences than shared memory holds
+  uint32_t* status;
+};
+
+struct AcceptParams {
+  CacheParams c;
+  const int32_t* cu_new;
+  int32_t n_rows;
+  const int32_t *tokens, *predicted, *parents;
+  int32_t width;
+  int32_t *path, *count, *next;
+  int32_t *lens_out, *qpos_out;
+};
+
+cudaError_t launch_paged_attend_simt(const PagedParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_paged_redo(const PagedParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t s);
+cudaError_t launch_paged_accept(const AcceptParams& p, int dtype, cudaStream_t s);
+
+}  // namespace capattn

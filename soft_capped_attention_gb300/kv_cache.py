@@ -150,6 +150,7 @@ class _Plan:
         self.ref = ctypes.byref(cfg)
         self.bytes = [cache_workspace_bytes(cfg, c) for c in range(4)]
         self.lse_like = None  # a tensor of lse's shape, which new ones are made like
+        self.paged = None      # workspace bytes of the calls in paged.py
 
 
 class KVCache:
@@ -210,7 +211,9 @@ class KVCache:
         """The cache's workspace (its address and bytes), at least as large as `call` needs.  A larger call's
         first use adds a larger one (so make that call once before a graph is
         captured); the earlier ones stay, since captured graphs may hold them."""
-        n = plan.bytes[call]
+        return self._room(plan.bytes[call])
+
+    def _room(self, n: int) -> tuple[int, int]:
         if self._workspace_bytes < n:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("the cache's workspace would grow during a graph capture: "
