@@ -489,16 +489,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 // 2-D map over the cache's rows [num_pages * Hkv * page_size][D]: boxes of 64
 // columns x the rows a tile has of a page, 128-byte swizzle.
 cudaError_t make_rows_map(CUtensorMap* map, const void* base, const CacheParams& p, int tile) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return cudaErrorNotSupported;
-  cuuint64_t dims[2] = {(cuuint64_t)p.D, (cuuint64_t)p.num_pages * p.Hkv * p.page_size};
-  cuuint64_t strides[1] = {(cuuint64_t)p.D * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)(p.page_size < tile ? p.page_size : tile)};
-  cuuint32_t es[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  const cuuint64_t dims[2] = {(cuuint64_t)p.D, (cuuint64_t)p.num_pages * p.Hkv * p.page_size};
+  const cuuint64_t strides[1] = {(cuuint64_t)p.D * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)(p.page_size < tile ? p.page_size : tile)};
+  return encode_bf16_map(map, base, 2, dims, strides, box);
 }
 
 template <int D, int METHOD, int NT>
