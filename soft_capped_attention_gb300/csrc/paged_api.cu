@@ -107,7 +107,7 @@ capattn_status capattn_paged_attend(const capattn_cache_config* cfg, const void*
   p.part_ml = reinterpret_cast<float2*>(base + w.ml_off);
   p.part_bad = reinterpret_cast<uint8_t*>(base + w.bad_off);
   p.part_o = reinterpret_cast<float*>(base + w.o_off);
-  cudaError_t e = launch_paged_attend_simt(p, cfg->dtype, stream);
+  cudaError_t e = cfg->dtype == CAPATTN_BF16 ? launch_paged_attend_tc(p, stream) : launch_paged_attend_simt(p, stream);
   if (e == cudaSuccess) e = launch_paged_redo(p, cfg->dtype, stream);
   return of(e);
 }

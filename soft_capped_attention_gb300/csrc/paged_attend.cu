@@ -1,5 +1,5 @@
-// Attention of many new tokens per sequence over the paged cache on the CUDA cores, and
-// the rows that are formed once more.
+// Attention of many new tokens per sequence over the paged cache on the CUDA cores (fp32), and
+// the rows that are formed once more (both types).
 //
 // Per query tile (tokens x query heads of one KV head, 64 rows) and 64 slots, with a
 // running reference m (log2 units):
@@ -36,13 +36,7 @@ struct SimtSmem {
   int last;
 };
 
-// Four consecutive elements as floats.
 __device__ __forceinline__ float4 load4(const float* x) { return *reinterpret_cast<const float4*>(x); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* x) {
-  const uint2 u = *reinterpret_cast<const uint2*>(x);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xFFFF0000u));
-}
 
 // Row of the cache that holds a slot of sequence b (a bad page is flagged and read as page 0).
 __device__ __forceinline__ size_t cache_row(const CacheParams& c, int b, int g, int slot) {
@@ -207,11 +201,7 @@ paged_simt_kernel(PagedParams p) {
         for (int w = 0; w < OC / 4; ++w) {
           const float v[4] = {none ? 0.f : o[y][4 * w] * inv, none ? 0.f : o[y][4 * w + 1] * inv,
                               none ? 0.f : o[y][4 * w + 2] * inv, none ? 0.f : o[y][4 * w + 3] * inv};
-          T* dst = static_cast<T*>(c.o) + row * D + 64 * w + 4 * tx;
-          if constexpr (sizeof(T) == 2)
-            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-          else
-            *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+          store_values(static_cast<T*>(c.o) + row * D + 64 * w + 4 * tx, v);
         }
         if (tx == 0) {
           if (bad) ask_redo(p);
@@ -360,14 +350,21 @@ cudaError_t run_redo(const PagedParams& p, cudaStream_t s) {
   return launch_pdl(paged_redo_kernel<T, D, METHOD>, dim3(kAttendCtas), dim3(128), 0, s, p);
 }
 
+template <typename T, int D, int METHOD>
+cudaError_t run(const PagedParams& p, bool redo, cudaStream_t s) {
+  if constexpr (sizeof(T) == 4) {
+    if (!redo) return run_simt<T, D, METHOD>(p, s);
+  }
+  return run_redo<T, D, METHOD>(p, s);
+}
+
 template <typename T, int D>
 cudaError_t run_cap(const PagedParams& p, bool redo, cudaStream_t s) {
   switch (p.c.method) {
-    case CAPATTN_CAP_TANH: return redo ? run_redo<T, D, CAPATTN_CAP_TANH>(p, s) : run_simt<T, D, CAPATTN_CAP_TANH>(p, s);
-    case CAPATTN_CAP_SOFT_SIGN:
-      return redo ? run_redo<T, D, CAPATTN_CAP_SOFT_SIGN>(p, s) : run_simt<T, D, CAPATTN_CAP_SOFT_SIGN>(p, s);
-    case CAPATTN_CAP_ALSC: return redo ? run_redo<T, D, CAPATTN_CAP_ALSC>(p, s) : run_simt<T, D, CAPATTN_CAP_ALSC>(p, s);
-    default: return redo ? run_redo<T, D, CAPATTN_CAP_NONE>(p, s) : run_simt<T, D, CAPATTN_CAP_NONE>(p, s);
+    case CAPATTN_CAP_TANH: return run<T, D, CAPATTN_CAP_TANH>(p, redo, s);
+    case CAPATTN_CAP_SOFT_SIGN: return run<T, D, CAPATTN_CAP_SOFT_SIGN>(p, redo, s);
+    case CAPATTN_CAP_ALSC: return run<T, D, CAPATTN_CAP_ALSC>(p, redo, s);
+    default: return run<T, D, CAPATTN_CAP_NONE>(p, redo, s);
   }
 }
 
@@ -378,14 +375,14 @@ cudaError_t run_dim(const PagedParams& p, bool redo, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_paged_attend_simt(const PagedParams& p0, int dtype, cudaStream_t s) {
+cudaError_t launch_paged_attend_simt(const PagedParams& p0, cudaStream_t s) {
   PagedParams p = p0;
   p.parts = (p.c.G + BM - 1) / BM;
   p.heads = (p.c.G + p.parts - 1) / p.parts;
   p.tokens = BM / p.heads;
   p.ctas = kAttendSimtCtas;
   p.min_units = 4;
-  return dtype == CAPATTN_BF16 ? run_dim<__nv_bfloat16>(p, false, s) : run_dim<float>(p, false, s);
+  return run_dim<float>(p, false, s);
 }
 
 cudaError_t launch_paged_redo(const PagedParams& p, int dtype, cudaStream_t s) {

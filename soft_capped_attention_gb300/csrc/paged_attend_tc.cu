@@ -1,0 +1,663 @@
+// Attention of many new tokens per sequence over the paged cache on the 5th-generation
+// tensor cores (bf16).
+//
+// Per query tile (tokens x query heads of one KV head, up to 128 rows) and 128 slots:
+//   S = Q K^T, x = log2(e) temp cap(sm_scale S), P = 2^(x - m), l += sum P, O += P V.
+// One CTA per SM takes an equal share of all steps (paged_sched.cuh); the query heads of a
+// group lie in one tile, so a key is read once for all of them, and a tile of a prompt
+// spans few tokens, which wastes little of its causal edge.
+//
+// The reference m of a row's exponentials is fixed before its scores are seen, so no step
+// looks for a maximum and the four threads of a row exchange nothing but l at the end:
+//   with a cap, |x| is bounded and m = max(0, bound - 100) (0 for all usual caps, which
+//   also makes x - m exact); without one, m comes from the first step's scores (0 while
+//   they are within 2^+-40).
+// That holds for logits within about 2^100 above m; a row whose sum leaves [2^-80, inf),
+// and one that met NaN or infinity in a slot that is not live for it (0 times them), gets
+// NaN for its lse and is formed once more by paged_redo_kernel.
+//
+// Warp roles (20 warps):
+//   warp 19      walks the CTA's pieces into a ring of four slots and loads their Q (two
+//                buffers); warps 0 and 18 follow and load K and V, a page (or 128 rows of
+//                one) a box, into two-stage rings; V's rows without a token are zeroed (0
+//                times what they hold must be 0);
+//   warp 1       TMEM allocator and MMA issuer: S_0 S_1 | PV_0 S_2 | PV_1 S_3 | ..., O of
+//                piece k in accumulator k & 1;
+//   warps 2..17  softmax, four threads a row, 32 slots each: one TMEM load (which gives the
+//                largest |S| too, for the choice of the cap's polynomial), one store of P.
+//                A piece's O leaves after the next piece's first step, when its last P V has
+//                completed.
+// TMEM (512 columns): S [0, 128) and [128, 256), O [256, 256 + D) and [384, 384 + D).
+// P is rounded to bf16 (at most half a step of o's own type, and the sum l is of the
+// unrounded values): a second product for its low half would cost as much as the first.
+#include <float.h>
+
+#include "fwd_common.cuh"
+#include "paged_out.cuh"
+#include "tma_maps.h"
+
+namespace capattn {
+namespace {
+
+using fwdtc::BM;
+using fwdtc::BN;
+using fwdtc::SLAB;
+using fwdtc::tile_bytes;
+
+constexpr int KST = 2;    // K stages
+constexpr int VST = 2;    // V stages
+constexpr int NSLOT = 4;  // pieces known ahead
+constexpr int kSoftmaxWarps = 16;
+constexpr int NTHREADS = 640;
+constexpr float kLeastSum = 0x1p-80f;
+// two Q tiles, KST K tiles, VST V tiles, the sums [2][4][128] and the first step's maxima
+template <int HD>
+constexpr int smem_bytes() { return (2 + KST + VST) * tile_bytes<HD>() + 2 * 4096 + 1024; }
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Values that an asynchronous TMEM load delivers: nothing that uses them moves before the
+// wait that this follows.
+template <int N>
+__device__ __forceinline__ void settled(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) asm volatile("" : "+r"(v[e]));
+}
+
+// O += P V, P packed at the start of each 32 columns of its score buffer.
+template <int HD>
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pt, uint64_t dV, uint32_t acc0) {
+  constexpr uint32_t idesc = idesc_bf16(BM, HD, 0, 1);
+#pragma unroll
+  for (int ks = 0; ks < BN / 16; ++ks)
+    mma_ts(d, pt + 32 * (ks >> 1) + 8 * (ks & 1), desc_add(dV, ks * 2048), idesc, (acc0 || ks > 0) ? 1u : 0u);
+}
+
+// x = log2(e) temp cap(sm_scale X) of one row as X Q: the cap's polynomial near zero times
+// the row's factor.
+template <int METHOD>
+struct RowPoly {
+  static constexpr int N = METHOD == CAPATTN_CAP_TANH ? 3 : METHOD == CAPATTN_CAP_ALSC ? 7 : 1;
+  F2 c[N];
+  __device__ __forceinline__ void set(const ExactCap& k, float mul) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float x = METHOD == CAPATTN_CAP_TANH ? k.near.c[i] : METHOD == CAPATTN_CAP_ALSC ? k.poly[i] : k.sm_scale;
+      c[i] = f2(x * mul, x * mul);
+    }
+  }
+  __device__ __forceinline__ F2 eval(F2 X) const {
+    const F2 z = METHOD == CAPATTN_CAP_TANH ? f2_mul(X, X) : X;
+    F2 q = c[N - 1];
+#pragma unroll
+    for (int i = N - 2; i >= 0; --i) q = f2_fma(q, z, c[i]);
+    return q;
+  }
+};
+
+// How a step's scores are capped: by the row's polynomial, by tanh's longer one, one by one.
+enum { kNear, kWide, kOneByOne };
+
+// 32 columns of P, packed to bf16; returns their sum.
+template <int METHOD, int LEVEL, bool MASKED>
+__device__ __forceinline__ float p_columns(const uint32_t (&v)[32], uint32_t (&pk)[16], const RowPoly<METHOD>& poly,
+                                           float mul, float add, uint32_t live, const ExactCap& k) {
+  const F2 add2 = f2(add, add), mul2 = f2(mul, mul);
+  F2 acc = f2(0.f, 0.f);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const F2 X = f2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+    F2 y;
+    if constexpr (LEVEL == kNear) {
+      y = f2_fma(X, poly.eval(X), add2);
+    } else if constexpr (LEVEL == kWide) {
+      y = f2_fma(poly_cap2<METHOD>(X, k), mul2, add2);
+    } else {
+      y = f2_fma(f2(any_cap<METHOD>(__uint_as_float(v[2 * e]), k), any_cap<METHOD>(__uint_as_float(v[2 * e + 1]), k)),
+                 mul2, add2);
+    }
+    float a, b;
+    f2_split(y, a, b);
+    a = ex2_approx(a);
+    b = ex2_approx(b);
+    if constexpr (MASKED) {
+      if (!(live & (1u << (2 * e)))) a = 0.f;
+      if (!(live & (2u << (2 * e)))) b = 0.f;
+    }
+    acc = f2_add(acc, f2(a, b));
+    pk[e] = pack_bf16x2(a, b);
+  }
+  float a, b;
+  f2_split(acc, a, b);
+  return a + b;
+}
+
+template <int METHOD, bool MASKED>
+__device__ __forceinline__ float p_step(const uint32_t (&v)[32], uint32_t (&pk)[16], const RowPoly<METHOD>& poly,
+                                        float mul, float add, uint32_t live, float top, const ExactCap& k) {
+  if constexpr (METHOD == CAPATTN_CAP_NONE) return p_columns<METHOD, kNear, MASKED>(v, pk, poly, mul, add, live, k);
+  if constexpr (METHOD == CAPATTN_CAP_SOFT_SIGN) return p_columns<METHOD, kOneByOne, MASKED>(v, pk, poly, mul, add, live, k);
+  if constexpr (METHOD == CAPATTN_CAP_TANH) {
+    if (__all_sync(0xFFFFFFFFu, top <= k.near.xmax)) return p_columns<METHOD, kNear, MASKED>(v, pk, poly, mul, add, live, k);
+    if (__all_sync(0xFFFFFFFFu, top <= k.xmax)) return p_columns<METHOD, kWide, MASKED>(v, pk, poly, mul, add, live, k);
+  }
+  if constexpr (METHOD == CAPATTN_CAP_ALSC) {
+    if (__all_sync(0xFFFFFFFFu, top <= k.xmax)) return p_columns<METHOD, kNear, MASKED>(v, pk, poly, mul, add, live, k);
+  }
+  return p_columns<METHOD, kOneByOne, MASKED>(v, pk, poly, mul, add, live, k);
+}
+
+// The largest x of a row: |cap| times its factor's size.
+template <int METHOD>
+__device__ __forceinline__ float largest_x(const ExactCap& k, float mul) {
+  if constexpr (METHOD == CAPATTN_CAP_ALSC) return fmaxf(mul * k.alsc.out * k.alsc.one_minus_sb, -mul * k.alsc.out * k.alsc.sb);
+  return fabsf(mul * k.cap);
+}
+
+template <int METHOD, int HD>
+__global__ void __launch_bounds__(NTHREADS, 1)
+paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                const __grid_constant__ CUtensorMap mv, const PagedParams p) {
+  constexpr int TILE = tile_bytes<HD>();
+  constexpr int NSLAB = HD / 64;
+  constexpr int OQ = HD / 4;  // O columns of a thread
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * 2 + 2 * KST + 2 * VST + 4 * 2 + 2 * NSLOT + 4 + 4 + 4];
+  __shared__ Piece items[NSLOT];
+  __shared__ ScheduleMem s_sched;
+  __shared__ uint32_t s_bad[2][4][4];  // piece parity, quarter, rows / 32
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag, s_last;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const CacheParams& c = p.c;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sQ = base;                     // buffer x at + x * TILE
+  const uint32_t sK = base + 2 * TILE;          // stage s at + s * TILE
+  const uint32_t sV = base + (2 + KST) * TILE;  // stage s at + s * TILE
+  float* sums = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + (2 + KST + VST) * TILE);
+  float* tops = sums + 2 * 4 * BM;
+
+  const uint32_t bar_qfull = smem_u32(&bars[0]);     // + 8 x
+  const uint32_t bar_qempty = bar_qfull + 16;        // + 8 x: the piece's last S complete
+  const uint32_t bar_kfull = bar_qempty + 16;        // + 8 s
+  const uint32_t bar_kempty = bar_kfull + 8 * KST;   // + 8 s
+  const uint32_t bar_vfull = bar_kempty + 8 * KST;   // + 8 s
+  const uint32_t bar_vempty = bar_vfull + 8 * VST;   // + 8 s
+  const uint32_t bar_sfull = bar_vempty + 8 * VST;   // + 8 x: S in buffer x complete
+  const uint32_t bar_pfull = bar_sfull + 16;         // + 8 x: P in buffer x written (16 warps)
+  const uint32_t bar_ofull = bar_pfull + 16;         // + 8 x: the piece's last P V complete
+  const uint32_t bar_oempty = bar_ofull + 16;        // + 8 x: O read by the 16 softmax warps
+  const uint32_t bar_ifull = bar_oempty + 16;        // + 8 s: piece slot written
+  const uint32_t bar_iempty = bar_ifull + 8 * NSLOT; // + 8 s: piece done with (19 warps)
+  const uint32_t bar_rows = bar_iempty + 8 * NSLOT;  // + 8 x: the four quarters of rows 32 x .. met (drain)
+  const uint32_t bar_tops = bar_rows + 32;           // + 8 x: the same, first step without a cap
+  const uint32_t bar_vfix = bar_tops + 32;           // V rows that get zeros have landed
+  const uint32_t bar_parts = bar_vfix + 8;           // partial results written (16 warps)
+  const uint32_t bar_last = bar_parts + 8;           // s_last written
+  const uint32_t bar_final = bar_last + 8;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar_qfull + 8 * x, 1);
+      mbar_init(bar_qempty + 8 * x, 1);
+      mbar_init(bar_sfull + 8 * x, 1);
+      mbar_init(bar_pfull + 8 * x, kSoftmaxWarps);
+      mbar_init(bar_ofull + 8 * x, 1);
+      mbar_init(bar_oempty + 8 * x, kSoftmaxWarps);
+    }
+    for (int s = 0; s < KST; ++s) {
+      mbar_init(bar_kfull + 8 * s, 1);
+      mbar_init(bar_kempty + 8 * s, 1);
+    }
+    for (int s = 0; s < VST; ++s) {
+      mbar_init(bar_vfull + 8 * s, 1);
+      mbar_init(bar_vempty + 8 * s, 1);
+    }
+    for (int s = 0; s < NSLOT; ++s) {
+      mbar_init(bar_ifull + 8 * s, 1);
+      mbar_init(bar_iempty + 8 * s, 3 + kSoftmaxWarps);
+    }
+    for (int x = 0; x < 4; ++x) {
+      mbar_init(bar_rows + 8 * x, 4);
+      mbar_init(bar_tops + 8 * x, 4);
+    }
+    mbar_init(bar_vfix, 1);
+    mbar_init(bar_parts, kSoftmaxWarps);
+    mbar_init(bar_last, 1);
+    mbar_init(bar_final, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), 512);
+    tmem_relinquish();
+  }
+  // the setup above overlaps the previous kernel's tail; global memory only after it
+  pdl_trigger();
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  schedule<BN>(p, NTHREADS, s_sched);
+
+  // The next piece (k-th) as every role but the walker reads it.
+  auto wait_piece = [&](int k) -> bool {
+    return mbar_wait_warp(bar_ifull + 8 * (k % NSLOT), (k / NSLOT) & 1, c.status, &abort_flag) && items[k % NSLOT].steps > 0;
+  };
+  auto done_with = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_iempty + 8 * (k % NSLOT));
+  };
+
+  if (warp == 19) {
+    // ------------------------------------------------------------ pieces and Q
+    const bool leader = elect_one_sync();
+    if (leader) tma_prefetch_desc(&mq);
+    __syncwarp();
+    const uint32_t bytes = (uint32_t)(p.heads * p.tokens) * 128u * NSLAB;
+    PieceWalk<BN> walk(p, s_sched, lane);
+    int k = 0, loaded = 0;
+    for (;; ++k) {
+      const Piece x = walk.next(p);
+      if (k >= NSLOT && !mbar_wait_warp(bar_iempty + 8 * (k % NSLOT), (k / NSLOT - 1) & 1, c.status, &abort_flag)) break;
+      if (lane == 0) {
+        items[k % NSLOT] = x;
+        mbar_arrive(bar_ifull + 8 * (k % NSLOT));
+      }
+      __syncwarp();
+      if (x.steps < 0) break;
+      const int y = k & 1;
+      if (k >= 2 && !mbar_wait_warp(bar_qempty + 8 * y, ((k >> 1) - 1) & 1, c.status, &abort_flag)) break;
+      if (leader) {
+        const int g = x.part / p.parts, head0 = g * c.G + (x.part - g * p.parts) * p.heads;
+        mbar_expect_tx(bar_qfull + 8 * y, bytes);
+        for (int sl = 0; sl < NSLAB; ++sl)
+          tma_load_3d(sQ + y * TILE + sl * SLAB, &mq, bar_qfull + 8 * y, 64 * sl, head0, x.row0 + x.i0);
+      }
+      loaded = k + 1;
+      __syncwarp();
+    }
+    // (on an early exit the copies in flight land before the CTA ends)
+    if (leader)
+      for (int x = loaded > 2 ? loaded - 2 : 0; x < loaded; ++x) drain_wait(bar_qfull + 8 * (x & 1), (x >> 1) & 1);
+    __syncwarp();
+  } else if (warp == 0 || warp == 18) {
+    // ------------------------------------------------------------ K (warp 0) and V (warp 18)
+    const bool values = warp == 18;
+    const CUtensorMap* map = values ? &mv : &mk;
+    const int rows = min(BN, c.page_size), boxes = BN / rows;  // rows of a box, boxes of a step (one a lane)
+    const uint32_t box_bytes = (uint32_t)rows * 128u * NSLAB;
+    const uint32_t tiles = values ? sV : sK, full0 = values ? bar_vfull : bar_kfull, empty0 = values ? bar_vempty : bar_kempty;
+    const int stages = values ? VST : KST;
+    if (lane == 0) tma_prefetch_desc(map);
+    int j = 0, fixes = 0;
+    bool ok = true;
+    for (int k = 0; ok && wait_piece(k); ++k) {
+      const Piece& x = items[k % NSLOT];
+      const int g = x.part / p.parts, len = x.len, first = x.first, tile0 = x.tile0, steps = x.steps;
+      const int32_t* table = c.table + (size_t)x.b * c.max_pages;
+      done_with(k);
+      // The page of this lane's box of a step, as read; looked at a step later.
+      constexpr int kNoBox = INT_MIN;
+      auto page_at = [&](int t) {
+        const int slot = t * BN + lane * rows;
+        return lane >= boxes || slot >= len || slot + rows <= first ? kNoBox : table[slot >> c.page_shift];
+      };
+      int page = page_at(tile0);
+      for (int i = 0; i < steps; ++i, ++j) {
+        const int t = tile0 + i, next = i + 1 < steps ? page_at(t + 1) : kNoBox;
+        const int s = j % stages, u = j / stages;
+        if (u > 0 && !mbar_wait_warp(empty0 + 8 * s, (u - 1) & 1, c.status, &abort_flag)) {
+          ok = false;
+          break;
+        }
+        // rows without a token: [0, lo) and [hi, 128)
+        const int lo = first > t * BN ? (first - t * BN) / rows * rows : 0, hi = min(BN, len - t * BN);
+        const bool fix = values && (lo > 0 || hi < BN);
+        const uint32_t bar = fix ? bar_vfix : full0 + 8 * s, dst = tiles + s * TILE;
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, page != kNoBox));
+        if (lane == 0) mbar_expect_tx(bar, n * box_bytes);
+        __syncwarp();
+        if (page != kNoBox) {
+          if (page < 0 || page >= c.num_pages) {  // flagged, and read as page 0
+            atomicOr(c.status, kStatusBadPageBit);
+            page = 0;
+          }
+          const int row = (page * c.Hkv + g) * c.page_size + ((t * BN + lane * rows) & (c.page_size - 1));
+#pragma unroll
+          for (int sl = 0; sl < NSLAB; ++sl) tma_load_2d(dst + sl * SLAB + lane * rows * 128, map, bar, 64 * sl, row);
+        }
+        __syncwarp();
+        if (fix) {
+          if (!mbar_wait_warp(bar_vfix, fixes & 1, c.status, &abort_flag)) {
+            ok = false;
+            break;
+          }
+          ++fixes;
+          for (int r = lane >> 3; r < BN; r += 4) {
+            if (r >= lo && r < hi) continue;
+#pragma unroll
+            for (int sl = 0; sl < NSLAB; ++sl)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + sl * SLAB + r * 128 + (lane & 7) * 16), "r"(0)
+                           : "memory");
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full0 + 8 * s);
+        }
+        page = next;
+      }
+    }
+    if (lane == 0) {
+      if (!ok && values) drain_wait(bar_vfix, fixes & 1);  // (a wait that gave up: its copies may still come)
+      for (int x = j > stages ? j - stages : 0; x < j; ++x) drain_wait(full0 + 8 * (x % stages), (x / stages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const bool leader = elect_one_sync();
+    const uint64_t dQ = smem_desc(sQ, 16, 1024);
+    const uint64_t dK = smem_desc(sK, 16, 1024);
+    const uint64_t dV = smem_desc(sV, SLAB, 1024);
+    int g0 = 0;  // steps issued so far (ring and score-buffer position)
+    for (int k = 0; wait_piece(k); ++k) {
+      const int n = items[k % NSLOT].steps, x = k & 1;
+      done_with(k);
+      const uint64_t dQx = desc_add(dQ, (uint32_t)(x * TILE));
+      // S of the piece's step i (global step g0 + i) into score buffer (g0 + i) & 1
+      auto issue_scores = [&](int i) -> bool {
+        const int gg = g0 + i, s = gg % KST;
+        if (!mbar_wait_warp(bar_kfull + 8 * s, (gg / KST) & 1, c.status, &abort_flag)) return false;
+        tc_fence_after();
+        if (leader) {
+          fwdtc::issue_s<HD>(tmem + 128u * (uint32_t)(gg & 1), dQx, desc_add(dK, (uint32_t)(s * TILE)));
+          mma_commit(bar_sfull + 8 * (gg & 1));
+          mma_commit(bar_kempty + 8 * s);
+        }
+        __syncwarp();
+        return true;
+      };
+      bool ok = mbar_wait_warp(bar_qfull + 8 * x, (k >> 1) & 1, c.status, &abort_flag) && issue_scores(0);
+      if (ok && n > 1) ok = issue_scores(1);
+      // the piece's O accumulator has been read out since the piece before the last
+      if (ok && k >= 2) ok = mbar_wait_warp(bar_oempty + 8 * x, ((k >> 1) - 1) & 1, c.status, &abort_flag);
+      for (int i = 0; ok && i < n; ++i) {
+        const int gg = g0 + i, xb = gg & 1, s = gg % VST;
+        if (!mbar_wait_warp(bar_pfull + 8 * xb, (gg >> 1) & 1, c.status, &abort_flag) ||
+            !mbar_wait_warp(bar_vfull + 8 * s, (gg / VST) & 1, c.status, &abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (leader) {
+          issue_pv<HD>(tmem + 256u + 128u * (uint32_t)x, tmem + 128u * (uint32_t)xb, desc_add(dV, (uint32_t)(s * TILE)),
+                       i > 0 ? 1u : 0u);
+          mma_commit(bar_vempty + 8 * s);
+        }
+        __syncwarp();
+        // S of step i + 2 overwrites P_i's buffer after PV_i (in-order MMAs)
+        if (i + 2 < n && !issue_scores(i + 2)) {
+          ok = false;
+          break;
+        }
+      }
+      if (!ok) break;
+      g0 += n;
+      if (leader) {
+        mma_commit(bar_ofull + 8 * x);   // the piece's O is complete
+        mma_commit(bar_qempty + 8 * x);  // and its Q no longer read
+      }
+      __syncwarp();
+    }
+    // (warp 1 re-checks this commit before it frees TMEM)
+    if (leader) mma_commit(bar_final);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax and results
+    const int cq = (warp - 2) >> 2;   // slots [32 cq, 32 cq + 32) of each step
+    const int quad = warp & 3;        // rows [32 quad, 32 quad + 32): the TMEM lanes it may access
+    const int r = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t s_quarter = tmem + lane_off + 32u * (uint32_t)cq;  // + 128 x: score buffer x
+    RowPoly<METHOD> poly;
+    int g = 0;        // steps so far
+    int splits = 0;   // pieces of shared tiles so far
+    float m_prev = 0.f;  // reference of the piece whose O is still to leave
+
+    // The results of piece k: O out of its accumulator, normalised or as a partial result.
+    auto drain = [&](int k) -> bool {
+      const Piece& x = items[k % NSLOT];
+      const int xx = k & 1, gk = x.part / p.parts, h0 = (x.part - gk * p.parts) * p.heads;
+      const int heads = min(p.heads, c.G - h0), tok = r / heads;
+      const bool valid = r < x.count * heads;
+      const size_t row = (size_t)(x.row0 + x.i0 + tok) * c.Hq + gk * c.G + h0 + (r - tok * heads);
+      if (!mbar_wait_warp(bar_ofull + 8 * xx, (k >> 1) & 1, c.status, &abort_flag)) return false;
+      tc_fence_after();
+      const uint32_t ob = tmem + lane_off + 256u + 128u * (uint32_t)xx + (uint32_t)(OQ * cq);
+      uint32_t o[OQ];
+#pragma unroll
+      for (int h = 0; h < OQ / 16; ++h) tmem_ld16(ob + 16u * h, *reinterpret_cast<uint32_t(*)[16]>(&o[16 * h]));
+      tmem_wait_ld();
+      settled(o);
+      tc_fence_before();
+      float zero = 0.f;  // NaN once an output is not finite
+#pragma unroll
+      for (int e = 0; e < OQ; ++e) zero = fmaf(__uint_as_float(o[e]), 0.f, zero);
+      const uint32_t bad_here = __ballot_sync(0xFFFFFFFFu, zero != 0.f);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar_oempty + 8 * xx);
+        s_bad[xx][cq][quad] = bad_here;
+        mbar_arrive(bar_rows + 8 * quad);
+      }
+      // (the sums were written before, by the same warps)
+      if (!mbar_wait_warp(bar_rows + 8 * quad, k & 1, c.status, &abort_flag)) return false;
+      float l = 0.f;
+      uint32_t bad_rows = 0u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        l += sums[(xx * 4 + e) * BM + r];
+        bad_rows |= s_bad[xx][e][quad];
+      }
+      const bool none = l == 0.f;  // no live slot
+      const bool bad = !none && (((bad_rows >> lane) & 1u) || !(l >= kLeastSum) || !(l < INFINITY));
+      if (x.whole) {
+        const float inv = none ? 0.f : 1.f / l;
+        if (valid) {
+          float y[OQ];
+#pragma unroll
+          for (int e = 0; e < OQ; ++e) y[e] = none ? 0.f : __uint_as_float(o[e]) * inv;
+          store_values(static_cast<__nv_bfloat16*>(c.o) + row * HD + OQ * cq, y);
+          if (cq == 0) {
+            if (bad) ask_redo(p);
+            c.lse[row] = bad ? kNaN32 : none ? -INFINITY : (m_prev + log2f(l)) * kLn2;
+          }
+        }
+        done_with(k);
+        return true;
+      }
+      if (valid) {
+        const size_t at = (size_t)x.slot * BM + r;
+        float y[OQ];
+#pragma unroll
+        for (int e = 0; e < OQ; ++e) y[e] = __uint_as_float(o[e]);
+        store_values(p.part_o + at * HD + OQ * cq, y);
+        if (cq == 0) {
+          p.part_ml[at] = make_float2(m_prev, l);
+          reinterpret_cast<uint32_t*>(p.part_bad)[at] = bad ? 1u : 0u;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_parts);
+      if (warp == 2) {
+        if (!mbar_wait_warp(bar_parts, splits & 1, c.status, &abort_flag)) return false;
+        if (lane == 0) {
+          s_last = count_tile_piece(p, x) ? 1 : 0;
+          mbar_arrive(bar_last);
+        }
+        __syncwarp();
+      }
+      if (!mbar_wait_warp(bar_last, splits & 1, c.status, &abort_flag)) return false;
+      ++splits;
+      if (s_last && valid) join_row<__nv_bfloat16, HD, BM>(p, x, r, cq, row);
+      done_with(k);
+      return true;
+    };
+
+    int k = 0;
+    for (;; ++k) {
+      if (!wait_piece(k)) break;
+      const Piece& x = items[k % NSLOT];
+      const int n = x.steps, tile0 = x.tile0;
+      float m = 0.f, mul;
+      RowMask mask;
+      bool valid;
+      {
+        const int gk = x.part / p.parts, h0 = (x.part - gk * p.parts) * p.heads, heads = min(p.heads, c.G - h0);
+        valid = r < x.count * heads;
+        const int i = x.i0 + r / heads;
+        mul = (valid && c.temp ? c.temp[x.row0 + i] : 1.f) * kL2E;
+        const SeqShape sh = {x.row0, x.n, x.len, x.base};
+        mask = valid ? row_mask(p, x.b, gk, sh, i) : dead_row();
+      }
+      const bool block = __any_sync(0xFFFFFFFFu, valid);  // the warp has rows at all
+      poly.set(c.cap, mul);
+      if constexpr (METHOD != CAPATTN_CAP_NONE) m = fmaxf(0.f, largest_x<METHOD>(c.cap, mul) - 100.f);
+      float lsum = 0.f;
+      bool seen = false;
+      // one step: this quarter's P over its scores, handed to the issuer
+      auto step = [&](int i) -> bool {
+        const int gg = g + i, c0 = (tile0 + i) * BN + 32 * cq;
+        const uint32_t sb = s_quarter + 128u * (uint32_t)(gg & 1);
+        if (!mbar_wait_warp(bar_sfull + 8 * (gg & 1), (gg >> 1) & 1, c.status, &abort_flag)) return false;
+        if (block) {
+          tc_fence_after();
+          uint32_t v[32], pk[16];
+          float top = tmem_ld32_absmax(sb, v);
+          const bool full = __all_sync(0xFFFFFFFFu, !valid || all_live(mask, c0, 32));
+          uint32_t live = 0xFFFFFFFFu;
+          if (!full) live = live_slots(p, mask, c0);
+          tmem_wait_ld();
+          settled(v);
+          asm volatile("" : "+f"(top));
+          if (!valid) top = 0.f;
+          if constexpr (METHOD == CAPATTN_CAP_NONE) {
+            if (i == 0) {  // the reference, from the live scores of all four quarters
+              float best = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if ((live >> e) & 1u) best = fmaxf(best, __uint_as_float(v[e]) * (c.sm_scale * mul));
+              float* t = tops + (k & 1) * 4 * BM;
+              t[cq * BM + r] = best;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar_tops + 8 * quad);
+              if (!mbar_wait_warp(bar_tops + 8 * quad, k & 1, c.status, &abort_flag)) return false;
+              best = fmaxf(fmaxf(t[r], t[BM + r]), fmaxf(t[2 * BM + r], t[3 * BM + r]));
+              m = best == -INFINITY || fabsf(best) <= 40.f ? 0.f : best;
+            }
+          }
+          if (full) {
+            lsum += p_step<METHOD, false>(v, pk, poly, mul, -m, live, top, c.cap);
+            seen = true;
+          } else if (__any_sync(0xFFFFFFFFu, live != 0u)) {
+            lsum += p_step<METHOD, true>(v, pk, poly, mul, -m, live, top, c.cap);
+            seen = seen || live != 0u;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = 0u;
+          }
+          __syncwarp();
+          tmem_st16(sb, pk);
+          tmem_wait_st();
+          tc_fence_before();
+        } else if (METHOD == CAPATTN_CAP_NONE && i == 0) {
+          if (lane == 0) mbar_arrive(bar_tops + 8 * quad);
+          if (!mbar_wait_warp(bar_tops + 8 * quad, k & 1, c.status, &abort_flag)) return false;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_pfull + 8 * (gg & 1));
+        return true;
+      };
+      bool ok = step(0);
+      // the previous piece's O, once this piece's first P is handed over (its last P V has
+      // completed meanwhile)
+      if (ok && k > 0) ok = drain(k - 1);
+      for (int i = 1; ok && i < n; ++i) ok = step(i);
+      if (!ok) break;
+      g += n;
+      // l: 0 without a live slot, something positive with one
+      sums[((k & 1) * 4 + cq) * BM + r] = !seen ? 0.f : lsum == 0.f ? FLT_MIN : lsum;
+      m_prev = m;
+    }
+    // after the last piece (and not after a wait that gave up)
+    if (k > 0 && __all_sync(0xFFFFFFFFu, abort_flag == 0)) drain(k - 1);
+  }
+  __syncwarp();  // every warp reaches the CTA barrier converged
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    // Every MMA has completed before TMEM is released (bounded non-suspending poll).
+    if (lane == 0) mbar_poll(bar_final, 0);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int METHOD, int HD>
+cudaError_t run_tc(const PagedParams& p, cudaStream_t s) {
+  const CacheParams& c = p.c;
+  CUtensorMap mq, mk, mv;
+  // q: a box is a tile's heads of its tokens; rows past the last token read as zero
+  const cuuint64_t qd[3] = {(cuuint64_t)HD, (cuuint64_t)c.Hq, (cuuint64_t)p.n_rows};
+  const cuuint64_t qs[2] = {(cuuint64_t)HD * 2, (cuuint64_t)c.q_stride * 2};
+  const cuuint32_t qb[3] = {64, (cuuint32_t)p.heads, (cuuint32_t)p.tokens};
+  // pages: a box is a page's rows of one head, at most a step's
+  const cuuint64_t kd[2] = {(cuuint64_t)HD, (cuuint64_t)c.num_pages * c.Hkv * c.page_size};
+  const cuuint64_t ks[1] = {(cuuint64_t)HD * 2};
+  const cuuint32_t kb[2] = {64, (cuuint32_t)(c.page_size < BN ? c.page_size : BN)};
+  cudaError_t e = encode_bf16_map(&mq, c.q, 3, qd, qs, qb);
+  if (e == cudaSuccess) e = encode_bf16_map(&mk, c.k, 2, kd, ks, kb);
+  if (e == cudaSuccess) e = encode_bf16_map(&mv, c.v, 2, kd, ks, kb);
+  auto* kern = paged_tc_kernel<METHOD, HD>;
+  static std::atomic<uint64_t> done{0};
+  if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(kern), smem_bytes<HD>(), done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(p.ctas), dim3(NTHREADS), smem_bytes<HD>(), s, mq, mk, mv, p);
+}
+
+template <int METHOD>
+struct PagedTcLaunch {
+  static cudaError_t run(const PagedParams& p, cudaStream_t s) {
+    return p.c.D == 64 ? run_tc<METHOD, 64>(p, s) : run_tc<METHOD, 128>(p, s);
+  }
+};
+
+}  // namespace
+
+cudaError_t launch_paged_attend_tc(const PagedParams& p0, cudaStream_t s) {
+  PagedParams p = p0;
+  p.parts = (p.c.G + BM - 1) / BM;
+  p.heads = (p.c.G + p.parts - 1) / p.parts;
+  p.tokens = BM / p.heads;
+  p.ctas = kAttendCtas;
+  p.min_units = 4;
+  return dispatch_cap<PagedTcLaunch>(p.c.method, p, s);
+}
+
+}  // namespace capattn

@@ -63,7 +63,8 @@ struct AcceptParams {
   int32_t *lens_out, *qpos_out;
 };
 
-cudaError_t launch_paged_attend_simt(const PagedParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_paged_attend_tc(const PagedParams& p, cudaStream_t s);  // bf16
+cudaError_t launch_paged_attend_simt(const PagedParams& p, cudaStream_t s);  // fp32
 cudaError_t launch_paged_redo(const PagedParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t s);
 cudaError_t launch_paged_accept(const AcceptParams& p, int dtype, cudaStream_t s);
