@@ -11,7 +11,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 struct PagedWorkspace {
-  size_t ml_off, bad_off, o_off, seqs_off, total;
+  size_t ml_off, bad_off, records_off, o_off, seqs_off, total;
 };
 PagedWorkspace layout(const capattn_cache_config& c, int call) {
   PagedWorkspace w;
@@ -21,7 +21,9 @@ PagedWorkspace layout(const capattn_cache_config& c, int call) {
     w.ml_off = at;
     at = up256(at + (size_t)kAttendPartRows * sizeof(float2));
     w.bad_off = at;
-    at = up256(at + (size_t)kAttendPartRows * 4);
+    at = up256(at + (size_t)kAttendPartRows * sizeof(uint32_t));
+    w.records_off = at;
+    at = up256(at + (size_t)kAttendSimtCtas * sizeof(Piece));
     w.o_off = at;
     at = up256(at + (size_t)kAttendPartRows * c.D * sizeof(float));
   } else if (call == CAPATTN_PAGED_PLAN) {
@@ -105,10 +107,18 @@ capattn_status capattn_paged_attend(const capattn_cache_config* cfg, const void*
   char* base = static_cast<char*>(workspace);
   p.redo = reinterpret_cast<uint32_t*>(base + kRedoOff);
   p.part_ml = reinterpret_cast<float2*>(base + w.ml_off);
-  p.part_bad = reinterpret_cast<uint8_t*>(base + w.bad_off);
+  p.part_bad = reinterpret_cast<uint32_t*>(base + w.bad_off);
+  p.records = reinterpret_cast<Piece*>(base + w.records_off);
   p.part_o = reinterpret_cast<float*>(base + w.o_off);
+  // query tiles, as both kernels of the call see them
+  const int rows = cfg->dtype == CAPATTN_BF16 ? kAttendRows : kAttendSimtRows;
+  p.parts = (c.G + rows - 1) / rows;
+  p.heads = (c.G + p.parts - 1) / p.parts;
+  p.tokens = rows / p.heads;
+  p.ctas = cfg->dtype == CAPATTN_BF16 ? kAttendCtas : kAttendSimtCtas;
+  p.min_units = 4;
   cudaError_t e = cfg->dtype == CAPATTN_BF16 ? launch_paged_attend_tc(p, stream) : launch_paged_attend_simt(p, stream);
-  if (e == cudaSuccess) e = launch_paged_redo(p, cfg->dtype, stream);
+  if (e == cudaSuccess) e = launch_paged_finish(p, cfg->dtype, stream);
   return of(e);
 }
 

@@ -1,5 +1,4 @@
-// Attention of many new tokens per sequence over the paged cache on the CUDA cores (fp32), and
-// the rows that are formed once more (both types).
+// Attention of many new tokens per sequence over the paged cache on the CUDA cores (fp32).
 //
 // Per query tile (tokens x query heads of one KV head, 64 rows) and 64 slots, with a
 // running reference m (log2 units):
@@ -16,7 +15,7 @@
 namespace capattn {
 namespace {
 
-constexpr int BM = 64;
+constexpr int BM = kAttendSimtRows;
 constexpr int TK = 64;
 constexpr int kThreads = 256;
 
@@ -33,20 +32,9 @@ struct SimtSmem {
   uint32_t live[BM][TK / 32];
   Piece piece;
   ScheduleMem sched;
-  int last;
 };
 
 __device__ __forceinline__ float4 load4(const float* x) { return *reinterpret_cast<const float4*>(x); }
-
-// Row of the cache that holds a slot of sequence b (a bad page is flagged and read as page 0).
-__device__ __forceinline__ size_t cache_row(const CacheParams& c, int b, int g, int slot) {
-  int page = c.table[(size_t)b * c.max_pages + (slot >> c.page_shift)];
-  if (page < 0 || page >= c.num_pages) {
-    atomicOr(c.status, kStatusBadPageBit);
-    page = 0;
-  }
-  return (((size_t)page * c.Hkv + g) << c.page_shift) + (slot & (c.page_size - 1));
-}
 
 template <typename T, int D, int METHOD>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -64,10 +52,16 @@ paged_simt_kernel(PagedParams p) {
   const CacheParams& c = p.c;
   const T* kc = static_cast<const T*>(c.k);
   const T* vc = static_cast<const T*>(c.v);
+  bool shared = false;
   for (;;) {
     if (warp == 0) {
       const Piece x = walk.next(p);
       if (lane == 0) s.piece = x;
+      if (x.steps > 0 && !x.whole && x.c0 == (int)blockIdx.x) {
+        if (lane == 0) leave_record(p, x);
+        shared = true;
+      }
+      if (x.steps < 0 && !shared && lane == 0) leave_no_record(p);
     }
     __syncthreads();
     const Piece x = s.piece;
@@ -194,8 +188,8 @@ paged_simt_kernel(PagedParams p) {
       // a row without live slots in this piece has l = 0 (and 0 times anything in O)
       const bool none = m[y] == -INFINITY && l[y] == 0.f, bad = !none && (zero != 0.f || !(l[y] < INFINITY));
       if (r >= rows) continue;
+      const size_t row = (size_t)(x.row0 + x.i0 + r / heads) * c.Hq + head0 + r % heads;
       if (x.whole) {
-        const size_t row = (size_t)(x.row0 + x.i0 + r / heads) * c.Hq + head0 + r % heads;
         const float inv = none ? 0.f : 1.f / l[y];
 #pragma unroll
         for (int w = 0; w < OC / 4; ++w) {
@@ -208,185 +202,44 @@ paged_simt_kernel(PagedParams p) {
           c.lse[row] = bad ? kNaN32 : none ? -INFINITY : (m[y] + log2f(l[y])) * kLn2;
         }
       } else {
-        const size_t at = (size_t)x.slot * BM + r;
 #pragma unroll
-        for (int w = 0; w < OC / 4; ++w)
-          *reinterpret_cast<float4*>(p.part_o + at * D + 64 * w + 4 * tx) =
+        for (int w = 0; w < OC / 4; ++w) {
+          const int col = 64 * w + 4 * tx;
+          reinterpret_cast<float4*>(p.part_o)[part_at<D, BM>(x.slot, r, col / (D / 4), col % (D / 4) / 4)] =
               make_float4(o[y][4 * w], o[y][4 * w + 1], o[y][4 * w + 2], o[y][4 * w + 3]);
+        }
         if (tx == 0) {
+          const size_t at = (size_t)x.slot * BM + r;
           p.part_ml[at] = make_float2(m[y], none ? 0.f : l[y]);
-          reinterpret_cast<uint32_t*>(p.part_bad)[at] = bad ? 1u : 0u;
+          p.part_bad[at] = bad ? 1u : 0u;
+          if (x.c0 == (int)blockIdx.x) c.lse[row] = 0.f;  // whatever it held asks for nothing
         }
       }
     }
-    __syncthreads();
-    if (!x.whole) {
-      if (threadIdx.x == 0) s.last = count_tile_piece(p, x);
-      __syncthreads();
-      const int r = threadIdx.x >> 2;
-      if (s.last && r < rows)
-        join_row<T, D, BM>(p, x, r, threadIdx.x & 3, (size_t)(x.row0 + x.i0 + r / heads) * c.Hq + head0 + r % heads);
-    }
+    __syncthreads();  // the next piece's rows
   }
 }
 
-// ---------------------------------------------------------------- rows formed once more
-// A row whose lse is NaN: its sums overflowed or vanished, or something that is not live
-// for it met it in a tile's product (0 times NaN or infinity).  A warp goes over the row's
-// live slots one by one with a running maximum and touches no other; four columns of D a
-// lane.  Most calls have no such row and end at the flag.
-template <typename T, int D, int METHOD>
-__global__ void __launch_bounds__(128)
-paged_redo_kernel(PagedParams p) {
-  constexpr int V = D / 32;
-  pdl_trigger();
-  pdl_wait();
-  if (*reinterpret_cast<volatile uint32_t*>(p.redo) == 0u) return;
-  const CacheParams& c = p.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t all = (int64_t)p.n_rows * c.Hq, warps = (int64_t)gridDim.x * 4;
-  for (int64_t at0 = ((int64_t)blockIdx.x * 4 + warp) * 32; at0 < all; at0 += warps * 32) {
-    const int64_t mine = at0 + lane;
-    const bool asked = mine < all && isnan(__ldcg(c.lse + mine));
-    for (uint32_t left = __ballot_sync(0xFFFFFFFFu, asked); left; left &= left - 1u) {
-      const int64_t at = at0 + __ffs(left) - 1;
-      const int row = (int)(at / c.Hq), h = (int)(at % c.Hq), g = h / c.G;
-      int lo = 0, hi = c.B;  // the first b with cu_new[b + 1] > row
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (p.cu_new[mid + 1] <= row) lo = mid + 1; else hi = mid;
-      }
-      if (lo >= c.B || p.cu_new[lo] > row) continue;  // nobody's
-      const SeqShape s = seq_shape(p, lo);
-      const int i = row - s.row0;
-      if (i < 0 || i >= s.n) continue;
-      const RowMask mask = row_mask(p, lo, g, s, i);
-      const float temp = (c.temp ? c.temp[row] : 1.f) * kL2E;
-      const T* q = static_cast<const T*>(c.q) + (size_t)row * c.q_stride + (size_t)h * D + lane * V;
-      float qv[V], o[V], m = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        qv[e] = (float)q[e];
-        o[e] = 0.f;
-      }
-      const int end = p.parents ? s.base + i + 1 : mask.hi;
-      for (int c0 = mask.lo / 32 * 32; c0 < end; c0 += 32) {
-        uint32_t bits = live_slots(p, mask, c0);
-        while (bits) {
-          // four slots at a time
-          size_t src[4];
-          bool in[4];
-          float kv[4][V], vv[4][V], t[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            in[u] = bits != 0u;
-            src[u] = 0;
-            if (in[u]) {
-              src[u] = cache_row(c, lo, g, c0 + __ffs(bits) - 1) * D + lane * V;
-              bits &= bits - 1u;
-            }
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              kv[u][e] = in[u] ? (float)static_cast<const T*>(c.k)[src[u] + e] : 0.f;
-              vv[u][e] = in[u] ? (float)static_cast<const T*>(c.v)[src[u] + e] : 0.f;
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            t[u] = 0.f;
-#pragma unroll
-            for (int e = 0; e < V; ++e) t[u] = fmaf(qv[e], kv[u][e], t[u]);
-          }
-#pragma unroll
-          for (int w = 16; w; w >>= 1)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) t[u] += __shfl_xor_sync(0xFFFFFFFFu, t[u], w);
-          float top = m;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            t[u] = in[u] ? any_cap<METHOD>(t[u], c.cap) * temp : -INFINITY;
-            top = fmaxf(top, t[u]);
-          }
-          const float ref = top == -INFINITY ? 0.f : top, scale = top == -INFINITY ? 1.f : ex2_approx(m - top);
-          m = top;
-          l *= scale;
-#pragma unroll
-          for (int e = 0; e < V; ++e) o[e] *= scale;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            if (!in[u]) continue;
-            const float w = ex2_approx(t[u] - ref);
-            l += w;
-#pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = fmaf(w, vv[u][e], o[e]);
-          }
-        }
-      }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-      for (int e = 0; e < V; ++e) static_cast<T*>(c.o)[(size_t)at * D + lane * V + e] = (T)(l == 0.f ? 0.f : o[e] * inv);
-      if (lane == 0) c.lse[at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
-    }
-  }
-  // the last CTA clears the flag for the next call
-  __syncthreads();
-  if (threadIdx.x == 0 && atomicAdd(p.redo + 1, 1u) == gridDim.x - 1) {
-    p.redo[0] = 0u;
-    p.redo[1] = 0u;
-  }
-}
-
-template <typename T, int D, int METHOD>
-cudaError_t run_simt(const PagedParams& p, cudaStream_t s) {
-  auto* k = paged_simt_kernel<T, D, METHOD>;
+template <int D, int METHOD>
+cudaError_t launch(const PagedParams& p, cudaStream_t s) {
+  auto* k = paged_simt_kernel<float, D, METHOD>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), sizeof(SimtSmem<D>), done);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, dim3(p.ctas), dim3(kThreads), sizeof(SimtSmem<D>), s, p);
 }
 
-template <typename T, int D, int METHOD>
-cudaError_t run_redo(const PagedParams& p, cudaStream_t s) {
-  return launch_pdl(paged_redo_kernel<T, D, METHOD>, dim3(kAttendCtas), dim3(128), 0, s, p);
-}
-
-template <typename T, int D, int METHOD>
-cudaError_t run(const PagedParams& p, bool redo, cudaStream_t s) {
-  if constexpr (sizeof(T) == 4) {
-    if (!redo) return run_simt<T, D, METHOD>(p, s);
+template <int METHOD>
+struct PagedSimtLaunch {
+  static cudaError_t run(const PagedParams& p, cudaStream_t s) {
+    return p.c.D == 64 ? launch<64, METHOD>(p, s) : launch<128, METHOD>(p, s);
   }
-  return run_redo<T, D, METHOD>(p, s);
-}
-
-template <typename T, int D>
-cudaError_t run_cap(const PagedParams& p, bool redo, cudaStream_t s) {
-  switch (p.c.method) {
-    case CAPATTN_CAP_TANH: return run<T, D, CAPATTN_CAP_TANH>(p, redo, s);
-    case CAPATTN_CAP_SOFT_SIGN: return run<T, D, CAPATTN_CAP_SOFT_SIGN>(p, redo, s);
-    case CAPATTN_CAP_ALSC: return run<T, D, CAPATTN_CAP_ALSC>(p, redo, s);
-    default: return run<T, D, CAPATTN_CAP_NONE>(p, redo, s);
-  }
-}
-
-template <typename T>
-cudaError_t run_dim(const PagedParams& p, bool redo, cudaStream_t s) {
-  return p.c.D == 64 ? run_cap<T, 64>(p, redo, s) : run_cap<T, 128>(p, redo, s);
-}
+};
 
 }  // namespace
 
-cudaError_t launch_paged_attend_simt(const PagedParams& p0, cudaStream_t s) {
-  PagedParams p = p0;
-  p.parts = (p.c.G + BM - 1) / BM;
-  p.heads = (p.c.G + p.parts - 1) / p.parts;
-  p.tokens = BM / p.heads;
-  p.ctas = kAttendSimtCtas;
-  p.min_units = 4;
-  return run_dim<float>(p, false, s);
-}
-
-cudaError_t launch_paged_redo(const PagedParams& p, int dtype, cudaStream_t s) {
-  return dtype == CAPATTN_BF16 ? run_dim<__nv_bfloat16>(p, true, s) : run_dim<float>(p, true, s);
+cudaError_t launch_paged_attend_simt(const PagedParams& p, cudaStream_t s) {
+  return dispatch_cap<PagedSimtLaunch>(p.c.method, p, s);
 }
 
 }  // namespace capattn

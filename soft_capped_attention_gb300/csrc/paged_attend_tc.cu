@@ -14,7 +14,7 @@
 //   they are within 2^+-40).
 // That holds for logits within about 2^100 above m; a row whose sum leaves [2^-80, inf),
 // and one that met NaN or infinity in a slot that is not live for it (0 times them), gets
-// NaN for its lse and is formed once more by paged_redo_kernel.
+// NaN for its lse and is formed once more by paged_finish_kernel.
 //
 // Warp roles (20 warps):
 //   warp 19      walks the CTA's pieces into a ring of four slots and loads their Q (two
@@ -39,11 +39,11 @@
 namespace capattn {
 namespace {
 
-using fwdtc::BM;
 using fwdtc::BN;
 using fwdtc::SLAB;
 using fwdtc::tile_bytes;
 
+constexpr int BM = kAttendRows;
 constexpr int KST = 2;    // K stages
 constexpr int VST = 2;    // V stages
 constexpr int NSLOT = 4;  // pieces known ahead
@@ -175,12 +175,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   constexpr int NSLAB = HD / 64;
   constexpr int OQ = HD / 4;  // O columns of a thread
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * 2 + 2 * KST + 2 * VST + 4 * 2 + 2 * NSLOT + 4 + 4 + 4];
+  __shared__ __align__(8) uint64_t bars[2 * 2 + 2 * KST + 2 * VST + 4 * 2 + 2 * NSLOT + 4 + 4 + 2];
   __shared__ Piece items[NSLOT];
   __shared__ ScheduleMem s_sched;
   __shared__ uint32_t s_bad[2][4][4];  // piece parity, quarter, rows / 32
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag, s_last;
+  __shared__ int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheParams& c = p.c;
@@ -206,9 +206,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   const uint32_t bar_rows = bar_iempty + 8 * NSLOT;  // + 8 x: the four quarters of rows 32 x .. met (drain)
   const uint32_t bar_tops = bar_rows + 32;           // + 8 x: the same, first step without a cap
   const uint32_t bar_vfix = bar_tops + 32;           // V rows that get zeros have landed
-  const uint32_t bar_parts = bar_vfix + 8;           // partial results written (16 warps)
-  const uint32_t bar_last = bar_parts + 8;           // s_last written
-  const uint32_t bar_final = bar_last + 8;
+  const uint32_t bar_final = bar_vfix + 8;
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
@@ -237,8 +235,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       mbar_init(bar_tops + 8 * x, 4);
     }
     mbar_init(bar_vfix, 1);
-    mbar_init(bar_parts, kSoftmaxWarps);
-    mbar_init(bar_last, 1);
     mbar_init(bar_final, 1);
     fence_mbar_init();
   }
@@ -272,8 +268,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
     const uint32_t bytes = (uint32_t)(p.heads * p.tokens) * 128u * NSLAB;
     PieceWalk<BN> walk(p, s_sched, lane);
     int k = 0, loaded = 0;
+    bool shared = false;
     for (;; ++k) {
       const Piece x = walk.next(p);
+      if (x.steps > 0 && !x.whole && x.c0 == (int)blockIdx.x) {
+        if (lane == 0) leave_record(p, x);
+        shared = true;
+      }
       if (k >= NSLOT && !mbar_wait_warp(bar_iempty + 8 * (k % NSLOT), (k / NSLOT - 1) & 1, c.status, &abort_flag)) break;
       if (lane == 0) {
         items[k % NSLOT] = x;
@@ -292,6 +293,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       loaded = k + 1;
       __syncwarp();
     }
+    if (!shared && lane == 0) leave_no_record(p);
     // (on an early exit the copies in flight land before the CTA ends)
     if (leader)
       for (int x = loaded > 2 ? loaded - 2 : 0; x < loaded; ++x) drain_wait(bar_qfull + 8 * (x & 1), (x >> 1) & 1);
@@ -436,7 +438,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
     const uint32_t s_quarter = tmem + lane_off + 32u * (uint32_t)cq;  // + 128 x: score buffer x
     RowPoly<METHOD> poly;
     int g = 0;        // steps so far
-    int splits = 0;   // pieces of shared tiles so far
     float m_prev = 0.f;  // reference of the piece whose O is still to leave
 
     // The results of piece k: O out of its accumulator, normalised or as a partial result.
@@ -492,29 +493,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
         return true;
       }
       if (valid) {
-        const size_t at = (size_t)x.slot * BM + r;
-        float y[OQ];
 #pragma unroll
-        for (int e = 0; e < OQ; ++e) y[e] = __uint_as_float(o[e]);
-        store_values(p.part_o + at * HD + OQ * cq, y);
+        for (int e = 0; e < OQ / 4; ++e)
+          reinterpret_cast<uint4*>(p.part_o)[part_at<HD, BM>(x.slot, r, cq, e)] =
+              make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         if (cq == 0) {
+          const size_t at = (size_t)x.slot * BM + r;
           p.part_ml[at] = make_float2(m_prev, l);
-          reinterpret_cast<uint32_t*>(p.part_bad)[at] = bad ? 1u : 0u;
+          p.part_bad[at] = bad ? 1u : 0u;
+          if (x.c0 == (int)blockIdx.x) c.lse[row] = 0.f;  // whatever it held asks for nothing
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_parts);
-      if (warp == 2) {
-        if (!mbar_wait_warp(bar_parts, splits & 1, c.status, &abort_flag)) return false;
-        if (lane == 0) {
-          s_last = count_tile_piece(p, x) ? 1 : 0;
-          mbar_arrive(bar_last);
-        }
-        __syncwarp();
-      }
-      if (!mbar_wait_warp(bar_last, splits & 1, c.status, &abort_flag)) return false;
-      ++splits;
-      if (s_last && valid) join_row<__nv_bfloat16, HD, BM>(p, x, r, cq, row);
       done_with(k);
       return true;
     };
@@ -650,13 +639,7 @@ struct PagedTcLaunch {
 
 }  // namespace
 
-cudaError_t launch_paged_attend_tc(const PagedParams& p0, cudaStream_t s) {
-  PagedParams p = p0;
-  p.parts = (p.c.G + BM - 1) / BM;
-  p.heads = (p.c.G + p.parts - 1) / p.parts;
-  p.tokens = BM / p.heads;
-  p.ctas = kAttendCtas;
-  p.min_units = 4;
+cudaError_t launch_paged_attend_tc(const PagedParams& p, cudaStream_t s) {
   return dispatch_cap<PagedTcLaunch>(p.c.method, p, s);
 }
 

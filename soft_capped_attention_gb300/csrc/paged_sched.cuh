@@ -7,8 +7,8 @@
 // Units are numbered by sequence, KV head (part), tile, step, and each CTA takes an equal
 // run of them, so that causal tiles of unequal length, long caches with few new tokens
 // and batches of unequal sequences all end together.  A tile that several CTAs share
-// leaves partial results, which the CTA that ends last adds up in the order of their
-// CTAs (found by a counter that returns to zero).
+// leaves partial results, which a second kernel adds up in the order of their CTAs
+// (paged_finish.cu).
 //
 // Where no tile has more than kWholeSteps steps, units are whole tiles: joining costs more.
 //
@@ -124,17 +124,6 @@ struct Shares {
   }
 };
 
-// What one CTA does of one query tile.
-struct Piece {
-  int32_t b, part;         // sequence, part of the heads (KV head * parts + x)
-  int32_t row0, n, base, len;
-  int32_t i0, count;       // tokens [i0, i0 + count)
-  int32_t tile0, steps;    // its steps' first TK slots; steps < 0: there are no more pieces
-  int32_t first;           // first slot that the tile needs
-  int32_t whole;
-  int32_t slot;            // of its partial results
-  int32_t c0, c1, late;    // CTAs that share the tile; whether it begins inside c0's range
-};
 __device__ __forceinline__ int piece_slot(const Piece& x, int c) { return 2 * c + (c == x.c0 ? x.late : 0); }
 
 struct ScheduleMem {
@@ -310,6 +299,16 @@ struct PieceWalk {
     u = end;  // (never reached)
   }
 };
+
+// Row of the cache that holds a slot of sequence b (a bad page is flagged and read as page 0).
+__device__ __forceinline__ size_t cache_row(const CacheParams& c, int b, int g, int slot) {
+  int page = c.table[(size_t)b * c.max_pages + (slot >> c.page_shift)];
+  if (page < 0 || page >= c.num_pages) {
+    atomicOr(c.status, kStatusBadPageBit);
+    page = 0;
+  }
+  return (((size_t)page * c.Hkv + g) << c.page_shift) + (slot & (c.page_size - 1));
+}
 
 // ---------------------------------------------------------------- live slots of a row
 struct RowMask {
