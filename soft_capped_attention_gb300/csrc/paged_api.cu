@@ -116,7 +116,7 @@ capattn_status capattn_paged_attend(const capattn_cache_config* cfg, const void*
   p.heads = (c.G + p.parts - 1) / p.parts;
   p.tokens = rows / p.heads;
   p.ctas = cfg->dtype == CAPATTN_BF16 ? kAttendCtas : kAttendSimtCtas;
-  p.min_units = 4;
+  p.min_units = 2;
   cudaError_t e = cfg->dtype == CAPATTN_BF16 ? launch_paged_attend_tc(p, stream) : launch_paged_attend_simt(p, stream);
   if (e == cudaSuccess) e = launch_paged_finish(p, cfg->dtype, stream);
   return of(e);

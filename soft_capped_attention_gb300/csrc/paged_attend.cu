@@ -47,8 +47,9 @@ paged_simt_kernel(PagedParams p) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   pdl_trigger();
   pdl_wait();
-  schedule<TK>(p, kThreads, s.sched);
-  PieceWalk<TK> walk(p, s.sched, lane);
+  const bool few = p.c.B <= kWarpSeqs;
+  if (!few) schedule_by_cta<TK>(p, kThreads, s.sched);
+  PieceWalk<TK> walk(p, few ? schedule_by_warp<TK>(p, lane) : s.sched.out, lane);  // (used by warp 0)
   const CacheParams& c = p.c;
   const T* kc = static_cast<const T*>(c.k);
   const T* vc = static_cast<const T*>(c.v);

@@ -249,7 +249,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  schedule<BN>(p, NTHREADS, s_sched);
+  const bool few = c.B <= kWarpSeqs;
+  if (!few) schedule_by_cta<BN>(p, NTHREADS, s_sched);
 
   // The next piece (k-th) as every role but the walker reads it.
   auto wait_piece = [&](int k) -> bool {
@@ -266,7 +267,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
     if (leader) tma_prefetch_desc(&mq);
     __syncwarp();
     const uint32_t bytes = (uint32_t)(p.heads * p.tokens) * 128u * NSLAB;
-    PieceWalk<BN> walk(p, s_sched, lane);
+    PieceWalk<BN> walk(p, few ? schedule_by_warp<BN>(p, lane) : s_sched.out, lane);
     int k = 0, loaded = 0;
     bool shared = false;
     for (;; ++k) {

@@ -1,20 +1,23 @@
 // What attention of many new tokens leaves to be done: query tiles that several CTAs shared
 // are added up, and rows whose result cannot be trusted are formed once more.
 //
-// A CTA a (CTA of the attention, 32 rows): if a shared tile begins there, two groups of eight
-// warps take every other piece each (a warp an eighth of the columns, a lane a row) and the
-// groups are added in order, so the result does not depend on scheduling.  Joining in the
+// A CTA takes 32 rows of a shared tile at a time.  Where few CTAs share it (prompts: two), its
+// eight warps are the four quarters of the columns, twice: every other piece each.  Where many
+// do (a long cache's few tokens), it takes one quarter, a warp every eighth piece.  The warps'
+// sums are added in order, so the result does not depend on scheduling.  Joining in the
 // attention kernel, by the CTA that ended last, left 151 SMs idle meanwhile.
 #include <cuda_bf16.h>
 
+#include "cache_sched.cuh"
 #include "paged_out.cuh"
 
 namespace capattn {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kGroups = 2;
-constexpr int kParts = 8;  // of the columns, a warp each
+constexpr int kGroups = 8;  // warps
+constexpr int kThreads = 32 * kGroups;
+constexpr int kCtas = 304;
+static_assert(kAttendSimtCtas <= 2 * kThreads, "two records a thread");
 
 // One row, over its live slots alone, with a running maximum: a warp, D / 32 columns a lane.
 template <typename T, int D, int METHOD>
@@ -120,82 +123,123 @@ struct Sum {
   }
 };
 
-template <int D>
-constexpr int smem_bytes() { return (kGroups - 1) * 32 * kParts * (D / kParts + 3) * (int)sizeof(float); }
+constexpr int kManyPieces = 5;  // from here on a quarter of the columns a CTA
+
+// What GROUPS warps left of columns [first, first + V) of a row, warps w0, w0 + stride, ..
+template <int V, int GROUPS, int WIDTH>
+__device__ __forceinline__ Sum<V> add_groups(const float (&part)[kGroups][WIDTH][32], int w0, int stride, int first, int lane) {
+  Sum<V> sum;
+#pragma unroll
+  for (int k = 0; k < GROUPS; ++k) {
+    const int w = w0 + k * stride;
+    float v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = part[w][first + e][lane];
+    sum.add(part[w][WIDTH - 3][lane], part[w][WIDTH - 2][lane], v, part[w][WIDTH - 1][lane] != 0.f);
+  }
+  return sum;
+}
 
 template <typename T, int D, int METHOD, int ROWS>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_finish_kernel(PagedParams p) {
-  constexpr int N = D / kParts, W = 32 * kParts;
-  extern __shared__ float smem[];  // [group - 1][value][W threads]
+  constexpr int N = D / 4;
+  __shared__ float part[kGroups][N + 3][32];
+  __shared__ int s_sums[kGroups], s_record, s_in;
   const CacheParams& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   pdl_wait();
-  const int from = blockIdx.x / (ROWS / 32), block = blockIdx.x % (ROWS / 32);
-  const Piece x = p.records[from];
-  const int g = x.part / p.parts, h0 = (x.part - g * p.parts) * p.heads;
-  const int heads = min(p.heads, c.G - h0);
-  if (x.steps > 0 && 32 * block < x.count * heads) {  // (the same for all threads)
-    const int part = warp & (kParts - 1), group = warp / kParts, at = threadIdx.x & (W - 1);
-    const int r = 32 * block + lane;
+  // The blocks of work of each record, two records a thread, and their sums.
+  auto blocks_of = [&](int i) -> int {
+    if (i >= p.ctas || p.records[i].steps < 0) return 0;
+    const int g = p.records[i].part / p.parts, h0 = (p.records[i].part - g * p.parts) * p.heads;
+    const bool many = p.records[i].c1 - p.records[i].c0 + 1 >= kManyPieces;
+    return (p.records[i].count * min(p.heads, c.G - h0) + 31) / 32 * (many ? 4 : 1);
+  };
+  const int n0 = blocks_of(2 * threadIdx.x), n1 = blocks_of(2 * threadIdx.x + 1);
+  const int up = lane_scan(n0 + n1, lane);
+  if (lane == 31) s_sums[warp] = up;
+  __syncthreads();
+  int before = up - n0 - n1, all = 0;
+#pragma unroll
+  for (int w = 0; w < kGroups; ++w) {
+    if (w < warp) before += s_sums[w];
+    all += s_sums[w];
+  }
+  for (int block = blockIdx.x; block < all; block += gridDim.x) {
+    if (block >= before && block < before + n0 + n1) {
+      const bool second = block >= before + n0;
+      s_record = 2 * threadIdx.x + (second ? 1 : 0);
+      s_in = block - before - (second ? n0 : 0);
+    }
+    __syncthreads();
+    const Piece x = p.records[s_record];
+    const bool many = x.c1 - x.c0 + 1 >= kManyPieces;
+    const int cq = many ? s_in & 3 : warp & 3, r = 32 * (many ? s_in >> 2 : s_in) + lane;
+    const int group = many ? warp : warp >> 2, groups = many ? kGroups : kGroups / 4;
+    const int g = x.part / p.parts, h0 = (x.part - g * p.parts) * p.heads, heads = min(p.heads, c.G - h0);
     Sum<N> sum;
 #pragma unroll 2
-    for (int k = x.c0 + group; k <= x.c1; k += kGroups) {
+    for (int k = x.c0 + group; k <= x.c1; k += groups) {
       const int slot = piece_slot(x, k);
       const float2 ml = __ldcg(p.part_ml + (size_t)slot * ROWS + r);
       const bool bad = __ldcg(p.part_bad + (size_t)slot * ROWS + r) != 0u;
       float v[N];
 #pragma unroll
       for (int e = 0; e < N / 4; ++e) {
-        const float4 f = __ldcg(reinterpret_cast<const float4*>(p.part_o) + part_at<D, ROWS>(slot, r, part >> 1, (part & 1) * (N / 4) + e));
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(p.part_o) + part_at<D, ROWS>(slot, r, cq, e));
         v[4 * e] = f.x; v[4 * e + 1] = f.y; v[4 * e + 2] = f.z; v[4 * e + 3] = f.w;
       }
       sum.add(ml.x, ml.y, v, bad);
     }
-    if (group > 0) {
-      float* to = smem + (group - 1) * W * (N + 3) + at;
 #pragma unroll
-      for (int e = 0; e < N; ++e) to[e * W] = sum.o[e];
-      to[N * W] = sum.m;
-      to[(N + 1) * W] = sum.l;
-      to[(N + 2) * W] = sum.bad ? 1.f : 0.f;
-    }
+    for (int e = 0; e < N; ++e) part[warp][e][lane] = sum.o[e];
+    part[warp][N][lane] = sum.m;
+    part[warp][N + 1][lane] = sum.l;
+    part[warp][N + 2][lane] = sum.bad ? 1.f : 0.f;
     __syncthreads();
-    if (group == 0) {
-#pragma unroll 1
-      for (int k = 0; k < kGroups - 1; ++k) {
-        const float* src = smem + k * W * (N + 3) + at;
-        float v[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = src[e * W];
-        sum.add(src[N * W], src[(N + 1) * W], v, src[(N + 2) * W] != 0.f);
-      }
-      const bool valid = r < x.count * heads;
-      const int tok = x.row0 + x.i0 + r / heads, head = g * c.G + h0 + r % heads;
-      const size_t row = (size_t)tok * c.Hq + head;
-      const bool none = sum.l == 0.f, bad = valid && !none && (sum.bad || !(sum.l < INFINITY));
+    const bool valid = r < x.count * heads;
+    const int tok = x.row0 + x.i0 + r / heads, head = g * c.G + h0 + r % heads;
+    const size_t row = (size_t)tok * c.Hq + head;
+    uint32_t redo = 0u;
+    // columns [at, at + V) of the row, done; the rows that cannot be trusted are left to one warp
+    auto write = [&](const auto& y, int at, bool first) {
+      constexpr int V = sizeof(y.o) / sizeof(float);
+      const bool none = y.l == 0.f, bad = valid && !none && (y.bad || !(y.l < INFINITY));
       if (valid && !bad) {
-        const float inv = none ? 0.f : 1.f / sum.l;
+        const float inv = none ? 0.f : 1.f / y.l;
+        T* to = static_cast<T*>(c.o) + row * D + at;
 #pragma unroll
-        for (int e = 0; e < N; ++e) sum.o[e] *= inv;
-        store_values(static_cast<T*>(c.o) + row * D + part * N, sum.o);
-        if (part == 0) c.lse[row] = none ? -INFINITY : (sum.m + log2f(sum.l)) * kLn2;
-      }
-      if (part == 0)  // (the other warps know of the same rows and leave them alone)
-        for (uint32_t left = __ballot_sync(0xFFFFFFFFu, bad); left; left &= left - 1u) {
-          const int l = __ffs(left) - 1;
-          redo_row<T, D, METHOD>(p, __shfl_sync(0xFFFFFFFFu, tok, l), __shfl_sync(0xFFFFFFFFu, head, l), lane);
+        for (int e = 0; e < V; e += 2) {
+          const float a = y.o[e] * inv, b = y.o[e + 1] * inv;
+          if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(to + e) = pack_bf16x2(a, b);
+          else *reinterpret_cast<float2*>(to + e) = make_float2(a, b);
         }
+        if (first) c.lse[row] = none ? -INFINITY : (y.m + log2f(y.l)) * kLn2;
+      }
+      if (first) redo = __ballot_sync(0xFFFFFFFFu, bad);
+    };
+    if (many) {
+      constexpr int V = N / kGroups;
+      write(add_groups<V, kGroups>(part, 0, 1, V * warp, lane), cq * N + V * warp, cq == 0 && warp == 0);
+    } else {
+      constexpr int V = N / 2;
+      write(add_groups<V, 2>(part, cq, 4, V * group, lane), cq * N + V * group, warp == 0);
     }
+    for (; redo; redo &= redo - 1u) {
+      const int l = __ffs(redo) - 1;
+      redo_row<T, D, METHOD>(p, __shfl_sync(0xFFFFFFFFu, tok, l), __shfl_sync(0xFFFFFFFFu, head, l), lane);
+    }
+    __syncthreads();  // part, s_record and s_in have been read
   }
   // Rows of whole tiles: the flag says whether there are any (a shared tile's that come to NaN
   // meanwhile may be met here too, and give the same again).
   if (*reinterpret_cast<volatile uint32_t*>(p.redo) == 0u) return;
-  const int64_t all = (int64_t)p.n_rows * c.Hq, warps = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t at0 = ((int64_t)blockIdx.x * (kThreads / 32) + warp) * 32; at0 < all; at0 += warps * 32) {
+  const int64_t lses = (int64_t)p.n_rows * c.Hq, warps = (int64_t)gridDim.x * (kThreads / 32);
+  for (int64_t at0 = ((int64_t)blockIdx.x * (kThreads / 32) + warp) * 32; at0 < lses; at0 += warps * 32) {
     const int64_t mine = at0 + lane;
-    const bool asked = mine < all && isnan(__ldcg(c.lse + mine));
+    const bool asked = mine < lses && isnan(__ldcg(c.lse + mine));
     for (uint32_t left = __ballot_sync(0xFFFFFFFFu, asked); left; left &= left - 1u) {
       const int64_t at = at0 + __ffs(left) - 1;
       redo_row<T, D, METHOD>(p, (int)(at / c.Hq), (int)(at % c.Hq), lane);
@@ -211,11 +255,7 @@ paged_finish_kernel(PagedParams p) {
 
 template <typename T, int D, int METHOD, int ROWS>
 cudaError_t launch(const PagedParams& p, cudaStream_t s) {
-  auto* k = paged_finish_kernel<T, D, METHOD, ROWS>;
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem_bytes<D>(), done);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3(p.ctas * (ROWS / 32)), dim3(kThreads), smem_bytes<D>(), s, p);
+  return launch_pdl(paged_finish_kernel<T, D, METHOD, ROWS>, dim3(kCtas), dim3(kThreads), 0, s, p);
 }
 
 template <int METHOD>

@@ -52,26 +52,31 @@ __device__ __forceinline__ SeqShape seq_shape(const PagedParams& p, int b) {
   return s;
 }
 
-// sum of floor((a i + b) / m) over 0 <= i < n; a, b >= 0, m > 0.
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-  int64_t sum = 0;
+// sum of floor((a i + b) / M) over 0 <= i < n; a <= M, M a power of two.  32 bits hold all
+// but the sum: a n and b are at most a sequence's slots (2^30) and a little more.
+template <int M>
+__device__ __forceinline__ uint64_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+  uint64_t sum = (uint64_t)n * (b / M);
+  b %= M;
+  if (a == M) return n ? sum + (uint64_t)n * (n - 1) / 2 : 0;  // (b < M)
+  uint32_t m = M;
   for (;;) {
-    if (a >= m) {
-      sum += n * (n - 1) / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      sum += n * (b / m);
-      b %= m;
-    }
-    const int64_t y = a * n + b;
+    const uint32_t y = a * n + b;
     if (y < m) return sum;
     n = y / m;
     b = y % m;
-    const int64_t t = m;
+    const uint32_t t = m;
     m = a;
     a = t;
+    sum += (uint64_t)n * (n - 1) / 2 * (a / m) + (uint64_t)n * (b / m);
+    a %= m;
+    b %= m;
   }
+}
+
+// x / y where x rarely needs more than 32 bits (a division of 64 is some 100 instructions).
+__device__ __forceinline__ uint64_t quotient(uint64_t x, uint32_t y) {
+  return (x >> 32) == 0 ? (uint64_t)((uint32_t)x / y) : x / y;
 }
 
 template <int TK>
@@ -91,14 +96,14 @@ struct Tiles {
   // Units of the tiles before tile t < count (every one of them has all its tokens).
   static __device__ __forceinline__ int64_t before(const PagedParams& p, const SeqShape& s, int t, bool whole) {
     if (whole || t == 0) return t;
-    int64_t sum = floor_sum(t, TK, p.tokens, (int64_t)s.base + p.tokens + TK - 1) + (int64_t)t * kTileCost;
+    int64_t sum = (int64_t)floor_sum<TK>(t, p.tokens, s.base + p.tokens + TK - 1) + (int64_t)t * kTileCost;
     if (p.c.window_len > 0 && !p.c.pos) {
       const int x0 = s.base - p.c.window_len + 1;
       if (p.parents) {
         sum -= (int64_t)t * (max(0, x0) / TK);
       } else {
         const int skip = x0 < 0 ? (-x0 + p.tokens - 1) / p.tokens : 0;
-        if (t > skip) sum -= floor_sum(t - skip, TK, p.tokens, (int64_t)x0 + (int64_t)skip * p.tokens);
+        if (t > skip) sum -= (int64_t)floor_sum<TK>(t - skip, p.tokens, x0 + skip * p.tokens);
       }
     }
     return sum;
@@ -112,27 +117,23 @@ struct Tiles {
 
 // The units of all sequences, shared out.
 struct Shares {
-  uint64_t units, q, more;  // all; those of a CTA; CTAs that take one more
-  uint32_t ctas;
+  uint64_t units, q;   // all; those of a CTA
+  uint32_t more, ctas; // CTAs that take one more
   bool whole;
   __device__ __forceinline__ uint64_t begin_of(uint32_t c) const {
     return c >= ctas ? units : q * c + (c < more ? c : more);
   }
   __device__ __forceinline__ int cta_of(uint64_t x) const {
     const uint64_t cut = (q + 1) * more;
+    if ((units >> 32) == 0) {
+      const uint32_t y = (uint32_t)x, z = (uint32_t)cut;
+      return (int)(y < z ? y / ((uint32_t)q + 1u) : more + (y - z) / (uint32_t)q);
+    }
     return (int)(x < cut ? x / (q + 1) : more + (x - cut) / q);
   }
 };
 
 __device__ __forceinline__ int piece_slot(const Piece& x, int c) { return 2 * c + (c == x.c0 ? x.late : 0); }
-
-struct ScheduleMem {
-  Shares sh;
-  uint64_t in;      // of the start: units of its sequence before it
-  int32_t b;
-  int32_t longest[32];
-  uint64_t sums[32], tiles[32];
-};
 
 __device__ __forceinline__ uint64_t lane_scan64(uint64_t x, int lane) {
 #pragma unroll
@@ -143,24 +144,96 @@ __device__ __forceinline__ uint64_t lane_scan64(uint64_t x, int lane) {
   return x;
 }
 
-// All threads of the CTA: the shares and where this CTA's range begins, in `m`.
+// The shares, and where this CTA's range begins.
+struct Schedule {
+  Shares sh;
+  int32_t b;        // its first sequence
+  uint64_t in;      // units of that sequence before it
+};
+struct ScheduleMem {
+  Schedule out;
+  int32_t longest[32];
+  uint64_t sums[32], tiles[32];
+};
+
+__device__ __forceinline__ Shares shares_of(const PagedParams& p, uint64_t sum, uint64_t tiles, int longest) {
+  Shares sh;
+  sh.whole = longest <= kWholeSteps;
+  sh.units = (uint64_t)(p.c.Hkv * p.parts) * (sh.whole ? tiles : sum);
+  const uint64_t want = quotient(sh.units, sh.whole ? 1 : p.min_units);
+  sh.ctas = (uint32_t)(want < 1 ? 1 : want < (uint64_t)gridDim.x ? want : gridDim.x);
+  sh.q = quotient(sh.units, sh.ctas);
+  sh.more = (uint32_t)(sh.units - sh.q * sh.ctas);
+  return sh;
+}
+
+// What sequences [b0, b1) have: units, tiles, the most steps of a tile.
 template <int TK>
-__device__ __forceinline__ void schedule(const PagedParams& p, int threads, ScheduleMem& m) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = threads / 32;
-  const int per = (p.c.B + threads - 1) / threads;
-  const int b0 = min(p.c.B, (int)threadIdx.x * per), b1 = min(p.c.B, b0 + per);
-  uint64_t sum = 0, tiles = 0;
-  int longest = 0;
+__device__ __forceinline__ void sum_sequences(const PagedParams& p, int b0, int b1, uint64_t* sum, uint64_t* tiles,
+                                              int* longest) {
+  *sum = *tiles = 0;
+  *longest = 0;
   for (int b = b0; b < b1; ++b) {
     const SeqShape s = seq_shape(p, b);
     const int c = Tiles<TK>::count(p, s);
     if (c == 0) continue;
-    sum += Tiles<TK>::units(p, s, false);
-    tiles += c;
+    *sum += Tiles<TK>::units(p, s, false);
+    *tiles += c;
     // (a windowed tile never has more steps than its window and its tokens span)
-    longest = max(longest, Tiles<TK>::steps(p, s, c - 1));
-    if (c > 1) longest = max(longest, Tiles<TK>::steps(p, s, c - 2));
+    *longest = max(*longest, Tiles<TK>::steps(p, s, c - 1));
+    if (c > 1) *longest = max(*longest, Tiles<TK>::steps(p, s, c - 2));
   }
+}
+
+// The start of range u0, if it lies in sequences [b0, b1), which `at` units come before.
+template <int TK>
+__device__ __forceinline__ bool find_start(const PagedParams& p, const Shares& sh, uint64_t u0, int b0, int b1,
+                                           uint64_t at, uint64_t mine, int* b_out, uint64_t* in_out) {
+  const uint64_t heads = (uint64_t)(p.c.Hkv * p.parts);
+  if (mine == 0 || u0 < heads * at || u0 >= heads * (at + mine)) return false;
+  int b = b0;
+  for (; b + 1 < b1; ++b) {
+    const uint64_t n = Tiles<TK>::units(p, seq_shape(p, b), sh.whole);
+    if (u0 < heads * (at + n)) break;
+    at += n;
+  }
+  *b_out = b;
+  *in_out = u0 - heads * at;
+  return true;
+}
+
+// Batches of at most kWarpSeqs sequences: by one warp alone, which nobody waits for.
+constexpr int kWarpSeqs = 128;
+template <int TK>
+__device__ __forceinline__ Schedule schedule_by_warp(const PagedParams& p, int lane) {
+  const int per = (p.c.B + 31) / 32, b0 = min(p.c.B, lane * per), b1 = min(p.c.B, b0 + per);
+  uint64_t sum, tiles;
+  int longest;
+  sum_sequences<TK>(p, b0, b1, &sum, &tiles, &longest);
+  const uint64_t up_sum = lane_scan64(sum, lane), up_tiles = lane_scan64(tiles, lane);
+  Schedule s;
+  s.sh = shares_of(p, __shfl_sync(0xFFFFFFFFu, up_sum, 31), __shfl_sync(0xFFFFFFFFu, up_tiles, 31),
+                   __reduce_max_sync(0xFFFFFFFFu, longest));
+  int b = 0;
+  uint64_t in = 0;
+  const bool here = find_start<TK>(p, s.sh, s.sh.begin_of(blockIdx.x), b0, b1, s.sh.whole ? up_tiles - tiles : up_sum - sum,
+                                   s.sh.whole ? tiles : sum, &b, &in);
+  const uint32_t mask = __ballot_sync(0xFFFFFFFFu, here);
+  const int from = mask ? __ffs(mask) - 1 : 0;
+  s.b = __shfl_sync(0xFFFFFFFFu, b, from);
+  s.in = __shfl_sync(0xFFFFFFFFu, in, from);
+  return s;
+}
+
+// Larger ones: by all threads of the CTA, into m.out.
+template <int TK>
+__device__ __noinline__ void schedule_by_cta(const PagedParams& p, int threads, ScheduleMem& m) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = threads / 32;
+  const int per = (p.c.B + threads - 1) / threads;
+  const int b0 = min(p.c.B, (int)threadIdx.x * per), b1 = min(p.c.B, b0 + per);
+  uint64_t sum, tiles;
+  int longest;
+  sum_sequences<TK>(p, b0, b1, &sum, &tiles, &longest);
   const uint64_t up_sum = lane_scan64(sum, lane), up_tiles = lane_scan64(tiles, lane);
   longest = __reduce_max_sync(0xFFFFFFFFu, longest);
   if (lane == 31) {
@@ -172,30 +245,15 @@ __device__ __forceinline__ void schedule(const PagedParams& p, int threads, Sche
   const uint64_t ws = lane < warps ? m.sums[lane] : 0, wt = lane < warps ? m.tiles[lane] : 0;
   const uint64_t as = lane_scan64(ws, lane), at = lane_scan64(wt, lane);
   const int top = __reduce_max_sync(0xFFFFFFFFu, lane < warps ? m.longest[lane] : 0);
-  Shares sh;
-  sh.whole = top <= kWholeSteps;
-  const uint64_t heads = (uint64_t)p.c.Hkv * p.parts;
-  sh.units = heads * __shfl_sync(0xFFFFFFFFu, sh.whole ? at : as, 31);
-  const uint64_t least = sh.whole ? 1 : p.min_units;
-  const uint64_t want = sh.units / least;
-  sh.ctas = (uint32_t)(want < 1 ? 1 : want < (uint64_t)gridDim.x ? want : gridDim.x);
-  sh.q = sh.units / sh.ctas;
-  sh.more = sh.units - sh.q * sh.ctas;
-  const uint64_t u0 = sh.begin_of(blockIdx.x);
-  if (threadIdx.x == 0) m.sh = sh;
-  // units before this thread's sequences
-  uint64_t at0 = __shfl_sync(0xFFFFFFFFu, (sh.whole ? at : as) - (sh.whole ? wt : ws), warp) +
-                 (sh.whole ? up_tiles - tiles : up_sum - sum);
-  const uint64_t mine = sh.whole ? tiles : sum;
-  if (mine > 0 && u0 >= heads * at0 && u0 < heads * (at0 + mine)) {
-    int b = b0;
-    for (; b + 1 < b1; ++b) {
-      const uint64_t n = Tiles<TK>::units(p, seq_shape(p, b), sh.whole);
-      if (u0 < heads * (at0 + n)) break;
-      at0 += n;
-    }
-    m.b = b;
-    m.in = u0 - heads * at0;
+  const Shares sh = shares_of(p, __shfl_sync(0xFFFFFFFFu, as, 31), __shfl_sync(0xFFFFFFFFu, at, 31), top);
+  if (threadIdx.x == 0) m.out.sh = sh;
+  const uint64_t before = __shfl_sync(0xFFFFFFFFu, (sh.whole ? at : as) - (sh.whole ? wt : ws), warp) +
+                          (sh.whole ? up_tiles - tiles : up_sum - sum);
+  int b;
+  uint64_t in;
+  if (find_start<TK>(p, sh, sh.begin_of(blockIdx.x), b0, b1, before, sh.whole ? tiles : sum, &b, &in)) {
+    m.out.b = b;
+    m.out.in = in;
   }
   __syncthreads();
 }
@@ -209,7 +267,7 @@ struct PieceWalk {
   int b, part, t, tiles, lane;
   int at;  // units of the tile before u
 
-  __device__ PieceWalk(const PagedParams& p, const ScheduleMem& m, int lane_in) {
+  __device__ PieceWalk(const PagedParams& p, const Schedule& m, int lane_in) {
     lane = lane_in;
     sh = m.sh;
     begin = u = sh.begin_of(blockIdx.x);
@@ -220,7 +278,7 @@ struct PieceWalk {
     s = seq_shape(p, b);
     tiles = Tiles<TK>::count(p, s);
     const uint64_t per = (uint64_t)Tiles<TK>::units(p, s, sh.whole);
-    part = (int)(m.in / per);
+    part = (per >> 32) == 0 ? (int)quotient(m.in, (uint32_t)per) : (int)(m.in / per);
     const int64_t rest = (int64_t)(m.in - per * part);
     int lo = 0, hi = tiles;  // before(lo) <= rest < before(hi)
     while (hi - lo > 1) {
