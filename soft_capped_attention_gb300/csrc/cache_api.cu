@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include "cache_internal.h"
+#include "near_soft_sign.h"
 #include "near_tanh.h"
 #include "softmax_elem.cuh"
 
@@ -57,6 +58,9 @@ ExactCap exact_cap_of(int method, float cap_in, float alpha, float beta, float s
     // usable while the last coefficient is a normal number
     k.near.xmax = fabsf(k.near.c[2]) >= 1e-30f && isfinite(k.near.c[2]) ? (float)(kNearTanh / fabs(in)) : 0.f;
     k.xmax = fabsf(k.poly[4]) >= 1e-30f && isfinite(k.poly[4]) ? (float)(kTanhPolyMaxU / fabs(in)) : 0.f;
+  } else if (*active == CAPATTN_CAP_SOFT_SIGN) {
+    near_soft_sign_fit(cap, sm_scale, k.poly);
+    k.xmax = fabsf(k.poly[6]) >= 1e-30f && isfinite(k.poly[6]) ? (float)(kNearSoftSign * cap / fabs((double)sm_scale)) : 0.f;
   } else if (*active == CAPATTN_CAP_ALSC) {
     const double ab = (double)alpha * (double)beta;
     const double sb = 1.0 / (1.0 + exp(-ab));

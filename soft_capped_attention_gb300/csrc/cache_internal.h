@@ -37,7 +37,8 @@ struct ExactCap {
     NearTanh near;
   };
   // cap(sm_scale X) as a polynomial for |X| <= xmax (0: none): tanh
-  // X (c0 + z (c1 + z (c2 + z (c3 + z c4)))), z = X^2; alsc X (c0 + X (c1 + .. + X c6))
+  // X (c0 + z (c1 + z (c2 + z (c3 + z c4)))), z = X^2; alsc X (c0 + X (c1 + .. + X c6)); soft_sign
+  // the same in |X|
   float poly[7];
   float xmax;
 };

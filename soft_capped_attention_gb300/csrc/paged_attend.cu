@@ -29,6 +29,7 @@ struct SimtSmem {
   float v[TK][D];
   RowMask mask[BM];
   float temp[BM];
+  int row[BM];         // of o and lse, from the tile's first; -1: none
   uint32_t live[BM][TK / 32];
   Piece piece;
   ScheduleMem sched;
@@ -68,20 +69,22 @@ paged_simt_kernel(PagedParams p) {
     const Piece x = s.piece;
     if (x.steps < 0) break;
     const int g = x.part / p.parts, h0 = (x.part - g * p.parts) * p.heads;
-    const int heads = min(p.heads, c.G - h0), rows = x.count * heads;
+    const int heads = min(p.heads, c.G - h0);
     const int head0 = g * c.G + h0;
     if (threadIdx.x < BM) {
-      const int r = threadIdx.x;
+      const int r = threadIdx.x, t = r / p.heads;
       const SeqShape sh = {x.row0, x.n, x.len, x.base};
-      s.mask[r] = r < rows ? row_mask(p, x.b, g, sh, x.i0 + r / heads) : dead_row();
-      s.temp[r] = (r < rows && c.temp ? c.temp[x.row0 + x.i0 + r / heads] : 1.f) * kL2E;
+      const bool valid = t < x.count && r - t * p.heads < heads;
+      s.mask[r] = valid ? row_mask(p, x.b, g, sh, x.i0 + t) : dead_row();
+      s.temp[r] = (valid && c.temp ? c.temp[x.row0 + x.i0 + t] : 1.f) * kL2E;
+      s.row[r] = valid ? t * c.Hq + r - t * p.heads : -1;
     }
     for (int i = threadIdx.x; i < BM * (D / 4); i += kThreads) {
-      const int r = i % BM, d = i / BM * 4;
+      const int r = i % BM, d = i / BM * 4, t = r / p.heads;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < rows)
-        a = load4(static_cast<const T*>(c.q) + (size_t)(x.row0 + x.i0 + r / heads) * c.q_stride +
-                  (size_t)(head0 + r % heads) * D + d);
+      if (t < x.count && r - t * p.heads < heads)
+        a = load4(static_cast<const T*>(c.q) + (size_t)(x.row0 + x.i0 + t) * c.q_stride +
+                  (size_t)(head0 + r - t * p.heads) * D + d);
       s.q[d][r] = a.x;
       s.q[d + 1][r] = a.y;
       s.q[d + 2][r] = a.z;
@@ -188,8 +191,8 @@ paged_simt_kernel(PagedParams p) {
       }
       // a row without live slots in this piece has l = 0 (and 0 times anything in O)
       const bool none = m[y] == -INFINITY && l[y] == 0.f, bad = !none && (zero != 0.f || !(l[y] < INFINITY));
-      if (r >= rows) continue;
-      const size_t row = (size_t)(x.row0 + x.i0 + r / heads) * c.Hq + head0 + r % heads;
+      if (s.row[r] < 0) continue;
+      const size_t row = (size_t)(x.row0 + x.i0) * c.Hq + head0 + s.row[r];
       if (x.whole) {
         const float inv = none ? 0.f : 1.f / l[y];
 #pragma unroll

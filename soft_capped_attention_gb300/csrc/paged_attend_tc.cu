@@ -17,17 +17,21 @@
 // NaN for its lse and is formed once more by paged_finish_kernel.
 //
 // Warp roles (20 warps):
-//   warp 19      walks the CTA's pieces into a ring of four slots and loads their Q (two
-//                buffers); warps 0 and 18 follow and load K and V, a page (or 128 rows of
-//                one) a box, into two-stage rings; V's rows without a token are zeroed (0
-//                times what they hold must be 0);
-//   warp 1       TMEM allocator and MMA issuer: S_0 S_1 | PV_0 S_2 | PV_1 S_3 | ..., O of
-//                piece k in accumulator k & 1;
+//   warp 19      walks the CTA's pieces into a ring of four slots and loads their Q by TMA;
+//                warps 0 and 18 follow and load K and V, a page (or 128 rows of one) a box,
+//                into rings; V's rows without a token are zeroed (0 times what they hold must
+//                be 0);
+//   warp 1       TMEM allocator and MMA issuer: S_0 S_1 | PV_0 S_2 | PV_1 S_3 | ... over the
+//                steps of all pieces, so that a piece's first scores are there when the last
+//                one's end;
 //   warps 2..17  softmax, four threads a row, 32 slots each: one TMEM load (which gives the
-//                largest |S| too, for the choice of the cap's polynomial), one store of P.
-//                A piece's O leaves after the next piece's first step, when its last P V has
-//                completed.
-// TMEM (512 columns): S [0, 128) and [128, 256), O [256, 256 + D) and [384, 384 + D).
+//                largest |S| too, for the choice of the cap's polynomial), one store of P over
+//                the scores.  They copy the next piece's Q into tensor memory after a piece's
+//                first step, and write the last piece's O then, when its last P V has completed.
+// TMEM (512 columns): S / P [0, 128) and [128, 256), O [256, 256 + D), Q [384, 448), [448, 512).
+// What bounds a long prompt is shared memory's 128 bytes a clock: with Q there, S alone took
+// 512 clocks of a step, P V 256 and the copies of K and V 512; with Q in tensor memory S takes
+// 256, and Q's room makes a third stage of K.
 // P is rounded to bf16 (at most half a step of o's own type, and the sum l is of the
 // unrounded values): a second product for its low half would cost as much as the first.
 #include <float.h>
@@ -44,15 +48,19 @@ using fwdtc::SLAB;
 using fwdtc::tile_bytes;
 
 constexpr int BM = kAttendRows;
-constexpr int KST = 2;    // K stages
-constexpr int VST = 2;    // V stages
+// K and V stages
+template <int HD>
+constexpr int kst() { return HD == 64 ? 5 : 3; }
+template <int HD>
+constexpr int vst() { return HD == 64 ? 4 : 2; }
+constexpr uint32_t kOCol = 256, kQCol = 384;  // TMEM columns of O and of Q (+ 64 x: buffer x)
 constexpr int NSLOT = 4;  // pieces known ahead
 constexpr int kSoftmaxWarps = 16;
 constexpr int NTHREADS = 640;
 constexpr float kLeastSum = 0x1p-80f;
-// two Q tiles, KST K tiles, VST V tiles, the sums [2][4][128] and the first step's maxima
+// a Q tile, the K and V tiles, the sums [2][4][128] and the first step's maxima
 template <int HD>
-constexpr int smem_bytes() { return (2 + KST + VST) * tile_bytes<HD>() + 2 * 4096 + 1024; }
+constexpr int smem_bytes() { return (1 + kst<HD>() + vst<HD>()) * tile_bytes<HD>() + 2 * 4096 + 1024; }
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
   asm volatile(
@@ -69,6 +77,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// mbar_wait_warp with all but the first try out of line: the roles' loops run once a step
+// each and fetch their instructions anew, so a wait of 40 of them costs more than a call.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* abort_flag) {
+  return mbar_wait(bar, parity, status, abort_flag);
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* abort_flag) {
+  const bool ok = mbar_try_wait(bar, parity) || wait_long(bar, parity, status, abort_flag);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
 // Values that an asynchronous TMEM load delivers: nothing that uses them moves before the
 // wait that this follows.
 template <int N>
@@ -77,30 +95,53 @@ __device__ __forceinline__ void settled(uint32_t (&v)[N]) {
   for (int e = 0; e < N; ++e) asm volatile("" : "+r"(v[e]));
 }
 
-// O += P V, P packed at the start of each 32 columns of its score buffer.
+// Matrix descriptors whose high word is a constant (128-byte swizzle, rows of 8 x 128 bytes):
+// only the low one, the address, is computed.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo_bytes) { return ((addr >> 4) & 0x3FFFu) | (lbo_bytes >> 4) << 16; }
+
+__device__ __forceinline__ void mma_ts_low(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t go) {
+  asm volatile(
+      "{ .reg .pred p, q; .reg .b64 y; setp.ne.b32 p, %5, 0; setp.ne.b32 q, %6, 0; mov.b64 y, {%2, %3};"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p; }" ::"r"(d), "r"(a), "r"(b), "n"(kDescHigh), "r"(idesc), "r"(acc), "r"(go)
+      : "memory");
+}
+// S = Q K^T (Q packed in D / 2 columns of tensor memory), O += P V (P packed at the start of
+// each 32 columns of its score buffer).
 template <int HD>
-__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pt, uint64_t dV, uint32_t acc0) {
+__device__ __forceinline__ void issue_s(uint32_t d, uint32_t q, uint32_t dK, uint32_t go) {
+  constexpr uint32_t idesc = idesc_bf16(BM, BN, 0, 0);
+#pragma unroll
+  for (int ks = 0; ks < HD / 16; ++ks)
+    mma_ts_low(d, q + 8 * ks, dK + (((ks >> 2) * SLAB + (ks & 3) * 32) >> 4), idesc, ks > 0 ? 1u : 0u, go);
+}
+template <int HD>
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pt, uint32_t dV, uint32_t acc0, uint32_t go) {
   constexpr uint32_t idesc = idesc_bf16(BM, HD, 0, 1);
 #pragma unroll
   for (int ks = 0; ks < BN / 16; ++ks)
-    mma_ts(d, pt + 32 * (ks >> 1) + 8 * (ks & 1), desc_add(dV, ks * 2048), idesc, (acc0 || ks > 0) ? 1u : 0u);
+    mma_ts_low(d, pt + 32 * (ks >> 1) + 8 * (ks & 1), dV + ((ks * 2048) >> 4), idesc, ks > 0 ? 1u : acc0, go);
+}
+__device__ __forceinline__ void commit_if(uint32_t bar, uint32_t go) {
+  asm volatile("{ .reg .pred q; setp.ne.b32 q, %1, 0; @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar), "r"(go) : "memory");
 }
 
 // x = log2(e) temp cap(sm_scale X) of one row as X Q: the cap's polynomial near zero times
 // the row's factor.
 template <int METHOD>
 struct RowPoly {
-  static constexpr int N = METHOD == CAPATTN_CAP_TANH ? 3 : METHOD == CAPATTN_CAP_ALSC ? 7 : 1;
+  static constexpr int N = METHOD == CAPATTN_CAP_TANH ? 3 : METHOD == CAPATTN_CAP_NONE ? 1 : 7;
   F2 c[N];
   __device__ __forceinline__ void set(const ExactCap& k, float mul) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float x = METHOD == CAPATTN_CAP_TANH ? k.near.c[i] : METHOD == CAPATTN_CAP_ALSC ? k.poly[i] : k.sm_scale;
+      const float x = METHOD == CAPATTN_CAP_TANH ? k.near.c[i] : METHOD == CAPATTN_CAP_NONE ? k.sm_scale : k.poly[i];
       c[i] = f2(x * mul, x * mul);
     }
   }
   __device__ __forceinline__ F2 eval(F2 X) const {
-    const F2 z = METHOD == CAPATTN_CAP_TANH ? f2_mul(X, X) : X;
+    F2 z = METHOD == CAPATTN_CAP_TANH ? f2_mul(X, X) : X;
+    if constexpr (METHOD == CAPATTN_CAP_SOFT_SIGN) z.v &= 0x7FFFFFFF7FFFFFFFull;  // |X|
     F2 q = c[N - 1];
 #pragma unroll
     for (int i = N - 2; i >= 0; --i) q = f2_fma(q, z, c[i]);
@@ -145,19 +186,22 @@ __device__ __forceinline__ float p_columns(const uint32_t (&v)[32], uint32_t (&p
   return a + b;
 }
 
-template <int METHOD, bool MASKED>
-__device__ __forceinline__ float p_step(const uint32_t (&v)[32], uint32_t (&pk)[16], const RowPoly<METHOD>& poly,
-                                        float mul, float add, uint32_t live, float top, const ExactCap& k) {
-  if constexpr (METHOD == CAPATTN_CAP_NONE) return p_columns<METHOD, kNear, MASKED>(v, pk, poly, mul, add, live, k);
-  if constexpr (METHOD == CAPATTN_CAP_SOFT_SIGN) return p_columns<METHOD, kOneByOne, MASKED>(v, pk, poly, mul, add, live, k);
+// The columns whose scores leave the row's polynomial: out of line, so that the loop that runs
+// without it stays small.
+template <int METHOD>
+__device__ __noinline__ float p_far(const uint32_t (&v)[32], uint32_t (&pk)[16], float mul, float add, uint32_t live,
+                                    float top, const ExactCap& k) {
+  const RowPoly<METHOD> none{};
   if constexpr (METHOD == CAPATTN_CAP_TANH) {
-    if (__all_sync(0xFFFFFFFFu, top <= k.near.xmax)) return p_columns<METHOD, kNear, MASKED>(v, pk, poly, mul, add, live, k);
-    if (__all_sync(0xFFFFFFFFu, top <= k.xmax)) return p_columns<METHOD, kWide, MASKED>(v, pk, poly, mul, add, live, k);
+    if (__all_sync(0xFFFFFFFFu, top <= k.xmax)) return p_columns<METHOD, kWide, true>(v, pk, none, mul, add, live, k);
   }
-  if constexpr (METHOD == CAPATTN_CAP_ALSC) {
-    if (__all_sync(0xFFFFFFFFu, top <= k.xmax)) return p_columns<METHOD, kNear, MASKED>(v, pk, poly, mul, add, live, k);
-  }
-  return p_columns<METHOD, kOneByOne, MASKED>(v, pk, poly, mul, add, live, k);
+  return p_columns<METHOD, kOneByOne, true>(v, pk, none, mul, add, live, k);
+}
+
+template <int METHOD>
+__device__ __forceinline__ bool is_near(float top, const ExactCap& k) {
+  if constexpr (METHOD == CAPATTN_CAP_NONE) return true;
+  return __all_sync(0xFFFFFFFFu, top <= (METHOD == CAPATTN_CAP_TANH ? k.near.xmax : k.xmax));
 }
 
 // The largest x of a row: |cap| times its factor's size.
@@ -173,9 +217,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
                 const __grid_constant__ CUtensorMap mv, const PagedParams p) {
   constexpr int TILE = tile_bytes<HD>();
   constexpr int NSLAB = HD / 64;
+  constexpr int KST = kst<HD>(), VST = vst<HD>();
   constexpr int OQ = HD / 4;  // O columns of a thread
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * 2 + 2 * KST + 2 * VST + 4 * 2 + 2 * NSLOT + 4 + 4 + 2];
+  __shared__ __align__(8) uint64_t bars[2 + 2 + 2 * KST + 2 * VST + 2 * 2 + 2 + 2 * NSLOT + 4 + 4 + 2];
   __shared__ Piece items[NSLOT];
   __shared__ ScheduleMem s_sched;
   __shared__ uint32_t s_bad[2][4][4];  // piece parity, quarter, rows / 32
@@ -185,23 +230,24 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheParams& c = p.c;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sQ = base;                     // buffer x at + x * TILE
-  const uint32_t sK = base + 2 * TILE;          // stage s at + s * TILE
-  const uint32_t sV = base + (2 + KST) * TILE;  // stage s at + s * TILE
-  float* sums = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + (2 + KST + VST) * TILE);
+  const uint32_t sQ = base;
+  const uint32_t sK = base + TILE;              // stage s at + s * TILE
+  const uint32_t sV = base + (1 + KST) * TILE;  // stage s at + s * TILE
+  float* sums = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + (1 + KST + VST) * TILE);
   float* tops = sums + 2 * 4 * BM;
 
-  const uint32_t bar_qfull = smem_u32(&bars[0]);     // + 8 x
-  const uint32_t bar_qempty = bar_qfull + 16;        // + 8 x: the piece's last S complete
-  const uint32_t bar_kfull = bar_qempty + 16;        // + 8 s
+  const uint32_t bar_qfull = smem_u32(&bars[0]);     // a piece's Q in shared memory
+  const uint32_t bar_qempty = bar_qfull + 8;         // and out of it (16 warps)
+  const uint32_t bar_qready = bar_qempty + 8;        // + 8 x: Q in tensor memory (16 warps)
+  const uint32_t bar_kfull = bar_qready + 16;        // + 8 s
   const uint32_t bar_kempty = bar_kfull + 8 * KST;   // + 8 s
   const uint32_t bar_vfull = bar_kempty + 8 * KST;   // + 8 s
   const uint32_t bar_vempty = bar_vfull + 8 * VST;   // + 8 s
   const uint32_t bar_sfull = bar_vempty + 8 * VST;   // + 8 x: S in buffer x complete
   const uint32_t bar_pfull = bar_sfull + 16;         // + 8 x: P in buffer x written (16 warps)
-  const uint32_t bar_ofull = bar_pfull + 16;         // + 8 x: the piece's last P V complete
-  const uint32_t bar_oempty = bar_ofull + 16;        // + 8 x: O read by the 16 softmax warps
-  const uint32_t bar_ifull = bar_oempty + 16;        // + 8 s: piece slot written
+  const uint32_t bar_ofull = bar_pfull + 16;         // the piece's last P V complete
+  const uint32_t bar_oempty = bar_ofull + 8;         // O read by the 16 softmax warps
+  const uint32_t bar_ifull = bar_oempty + 8;         // + 8 s: piece slot written
   const uint32_t bar_iempty = bar_ifull + 8 * NSLOT; // + 8 s: piece done with (19 warps)
   const uint32_t bar_rows = bar_iempty + 8 * NSLOT;  // + 8 x: the four quarters of rows 32 x .. met (drain)
   const uint32_t bar_tops = bar_rows + 32;           // + 8 x: the same, first step without a cap
@@ -210,14 +256,15 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
+    mbar_init(bar_qfull, 1);
+    mbar_init(bar_qempty, kSoftmaxWarps);
     for (int x = 0; x < 2; ++x) {
-      mbar_init(bar_qfull + 8 * x, 1);
-      mbar_init(bar_qempty + 8 * x, 1);
+      mbar_init(bar_qready + 8 * x, kSoftmaxWarps);
       mbar_init(bar_sfull + 8 * x, 1);
       mbar_init(bar_pfull + 8 * x, kSoftmaxWarps);
-      mbar_init(bar_ofull + 8 * x, 1);
-      mbar_init(bar_oempty + 8 * x, kSoftmaxWarps);
     }
+    mbar_init(bar_ofull, 1);
+    mbar_init(bar_oempty, kSoftmaxWarps);
     for (int s = 0; s < KST; ++s) {
       mbar_init(bar_kfull + 8 * s, 1);
       mbar_init(bar_kempty + 8 * s, 1);
@@ -254,7 +301,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
 
   // The next piece (k-th) as every role but the walker reads it.
   auto wait_piece = [&](int k) -> bool {
-    return mbar_wait_warp(bar_ifull + 8 * (k % NSLOT), (k / NSLOT) & 1, c.status, &abort_flag) && items[k % NSLOT].steps > 0;
+    return wait_warp(bar_ifull + 8 * (k % NSLOT), (k / NSLOT) & 1, c.status, &abort_flag) && items[k % NSLOT].steps > 0;
   };
   auto done_with = [&](int k) {
     __syncwarp();
@@ -276,28 +323,25 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
         if (lane == 0) leave_record(p, x);
         shared = true;
       }
-      if (k >= NSLOT && !mbar_wait_warp(bar_iempty + 8 * (k % NSLOT), (k / NSLOT - 1) & 1, c.status, &abort_flag)) break;
+      if (k >= NSLOT && !wait_warp(bar_iempty + 8 * (k % NSLOT), (k / NSLOT - 1) & 1, c.status, &abort_flag)) break;
       if (lane == 0) {
         items[k % NSLOT] = x;
         mbar_arrive(bar_ifull + 8 * (k % NSLOT));
       }
       __syncwarp();
       if (x.steps < 0) break;
-      const int y = k & 1;
-      if (k >= 2 && !mbar_wait_warp(bar_qempty + 8 * y, ((k >> 1) - 1) & 1, c.status, &abort_flag)) break;
+      if (k >= 1 && !wait_warp(bar_qempty, (k - 1) & 1, c.status, &abort_flag)) break;
       if (leader) {
         const int g = x.part / p.parts, head0 = g * c.G + (x.part - g * p.parts) * p.heads;
-        mbar_expect_tx(bar_qfull + 8 * y, bytes);
-        for (int sl = 0; sl < NSLAB; ++sl)
-          tma_load_3d(sQ + y * TILE + sl * SLAB, &mq, bar_qfull + 8 * y, 64 * sl, head0, x.row0 + x.i0);
+        mbar_expect_tx(bar_qfull, bytes);
+        for (int sl = 0; sl < NSLAB; ++sl) tma_load_3d(sQ + sl * SLAB, &mq, bar_qfull, 64 * sl, head0, x.row0 + x.i0);
       }
       loaded = k + 1;
       __syncwarp();
     }
     if (!shared && lane == 0) leave_no_record(p);
     // (on an early exit the copies in flight land before the CTA ends)
-    if (leader)
-      for (int x = loaded > 2 ? loaded - 2 : 0; x < loaded; ++x) drain_wait(bar_qfull + 8 * (x & 1), (x >> 1) & 1);
+    if (leader && loaded > 0) drain_wait(bar_qfull, (loaded - 1) & 1);
     __syncwarp();
   } else if (warp == 0 || warp == 18) {
     // ------------------------------------------------------------ K (warp 0) and V (warp 18)
@@ -325,7 +369,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       for (int i = 0; i < steps; ++i, ++j) {
         const int t = tile0 + i, next = i + 1 < steps ? page_at(t + 1) : kNoBox;
         const int s = j % stages, u = j / stages;
-        if (u > 0 && !mbar_wait_warp(empty0 + 8 * s, (u - 1) & 1, c.status, &abort_flag)) {
+        if (u > 0 && !wait_warp(empty0 + 8 * s, (u - 1) & 1, c.status, &abort_flag)) {
           ok = false;
           break;
         }
@@ -347,7 +391,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
         }
         __syncwarp();
         if (fix) {
-          if (!mbar_wait_warp(bar_vfix, fixes & 1, c.status, &abort_flag)) {
+          if (!wait_warp(bar_vfix, fixes & 1, c.status, &abort_flag)) {
             ok = false;
             break;
           }
@@ -373,62 +417,65 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    const bool leader = elect_one_sync();
-    const uint64_t dQ = smem_desc(sQ, 16, 1024);
-    const uint64_t dK = smem_desc(sK, 16, 1024);
-    const uint64_t dV = smem_desc(sV, SLAB, 1024);
-    int g0 = 0;  // steps issued so far (ring and score-buffer position)
-    for (int k = 0; wait_piece(k); ++k) {
-      const int n = items[k % NSLOT].steps, x = k & 1;
-      done_with(k);
-      const uint64_t dQx = desc_add(dQ, (uint32_t)(x * TILE));
-      // S of the piece's step i (global step g0 + i) into score buffer (g0 + i) & 1
-      auto issue_scores = [&](int i) -> bool {
-        const int gg = g0 + i, s = gg % KST;
-        if (!mbar_wait_warp(bar_kfull + 8 * s, (gg / KST) & 1, c.status, &abort_flag)) return false;
-        tc_fence_after();
-        if (leader) {
-          fwdtc::issue_s<HD>(tmem + 128u * (uint32_t)(gg & 1), dQx, desc_add(dK, (uint32_t)(s * TILE)));
-          mma_commit(bar_sfull + 8 * (gg & 1));
-          mma_commit(bar_kempty + 8 * s);
-        }
-        __syncwarp();
-        return true;
-      };
-      bool ok = mbar_wait_warp(bar_qfull + 8 * x, (k >> 1) & 1, c.status, &abort_flag) && issue_scores(0);
-      if (ok && n > 1) ok = issue_scores(1);
-      // the piece's O accumulator has been read out since the piece before the last
-      if (ok && k >= 2) ok = mbar_wait_warp(bar_oempty + 8 * x, ((k >> 1) - 1) & 1, c.status, &abort_flag);
-      for (int i = 0; ok && i < n; ++i) {
-        const int gg = g0 + i, xb = gg & 1, s = gg % VST;
-        if (!mbar_wait_warp(bar_pfull + 8 * xb, (gg >> 1) & 1, c.status, &abort_flag) ||
-            !mbar_wait_warp(bar_vfull + 8 * s, (gg / VST) & 1, c.status, &abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (leader) {
-          issue_pv<HD>(tmem + 256u + 128u * (uint32_t)x, tmem + 128u * (uint32_t)xb, desc_add(dV, (uint32_t)(s * TILE)),
-                       i > 0 ? 1u : 0u);
-          mma_commit(bar_vempty + 8 * s);
-        }
-        __syncwarp();
-        // S of step i + 2 overwrites P_i's buffer after PV_i (in-order MMAs)
-        if (i + 2 < n && !issue_scores(i + 2)) {
-          ok = false;
-          break;
-        }
+    const uint32_t leader = elect_one_sync() ? 1u : 0u;
+    const uint32_t dK = desc_low(sK, 16);
+    const uint32_t dV = desc_low(sV, SLAB);
+    int sk = 0, left = 0;                // next S: its piece, the piece's steps still to come (0: not known yet)
+    uint32_t sg = 0, ks = 0, kp = 0;     // next S: its buffer; K stage and its phase
+    // 1: issued, 0: there are no more steps, -1: a wait gave up
+    auto issue_scores = [&]() -> int {
+      if (left == 0) {
+        if (!wait_warp(bar_ifull + 8 * (sk % NSLOT), (sk / NSLOT) & 1, c.status, &abort_flag)) return -1;
+        left = __reduce_max_sync(0xFFFFFFFFu, items[sk % NSLOT].steps);
+        if (left < 0) return 0;
+        if (!wait_warp(bar_qready + 8 * (sk & 1), (sk >> 1) & 1, c.status, &abort_flag)) return -1;
       }
-      if (!ok) break;
-      g0 += n;
-      if (leader) {
-        mma_commit(bar_ofull + 8 * x);   // the piece's O is complete
-        mma_commit(bar_qempty + 8 * x);  // and its Q no longer read
-      }
+      if (!wait_warp(bar_kfull + 8 * ks, kp, c.status, &abort_flag)) return -1;
+      tc_fence_after();
+      issue_s<HD>(tmem + 128u * sg, tmem + kQCol + 64u * (uint32_t)(sk & 1), dK + ks * (TILE >> 4), leader);
+      commit_if(bar_sfull + 8 * sg, leader);
+      commit_if(bar_kempty + 8 * ks, leader);
       __syncwarp();
+      sg ^= 1u;
+      if (++ks == KST) {
+        ks = 0;
+        kp ^= 1u;
+      }
+      if (--left == 0) ++sk;
+      return 1;
+    };
+    int ahead = issue_scores();
+    if (ahead > 0) ahead = issue_scores();
+    uint32_t g = 0, gp = 0, vs = 0, vp = 0;  // next P V: P's buffer, its phase; V stage, its phase
+    for (int k = 0; ahead >= 0 && wait_piece(k); ++k) {
+      const int n = __reduce_max_sync(0xFFFFFFFFu, items[k % NSLOT].steps);
+      bool ok = true;
+      for (int i = 0; i < n; ++i) {
+        ok = wait_warp(bar_pfull + 8 * g, gp, c.status, &abort_flag) && wait_warp(bar_vfull + 8 * vs, vp, c.status, &abort_flag);
+        // O has been read out since the last piece
+        if (ok && i == 0 && k > 0) ok = wait_warp(bar_oempty, (k - 1) & 1, c.status, &abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv<HD>(tmem + kOCol, tmem + 128u * g, dV + vs * (TILE >> 4), i > 0 ? 1u : 0u, leader);
+        commit_if(bar_vempty + 8 * vs, leader);
+        if (i + 1 == n) commit_if(bar_ofull, leader);  // the piece's O is complete
+        __syncwarp();
+        gp ^= g;
+        g ^= 1u;
+        if (++vs == VST) {
+          vs = 0;
+          vp ^= 1u;
+        }
+        // S of the step after the next overwrites this P after its P V (in-order MMAs)
+        if (ahead > 0) ahead = issue_scores();
+        ok = ahead >= 0;
+        if (!ok) break;
+      }
+      done_with(k);
+      if (!ok) break;
     }
     // (warp 1 re-checks this commit before it frees TMEM)
-    if (leader) mma_commit(bar_final);
+    commit_if(bar_final, leader);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax and results
@@ -440,17 +487,51 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
     RowPoly<METHOD> poly;
     int g = 0;        // steps so far
     float m_prev = 0.f;  // reference of the piece whose O is still to leave
+    // this thread's row of a tile: token and head (the box that Q comes in has p.heads heads)
+    const int tok = r / p.heads, hh = r - tok * p.heads;
+    // heads of a piece's part, its first one
+    auto heads_of = [&](const Piece& x, int* g_out, int* head0) -> int {
+      const int gk = p.parts == 1 ? x.part : x.part / p.parts, h0 = (x.part - gk * p.parts) * p.heads;
+      *g_out = gk;
+      *head0 = gk * c.G + h0;
+      return min(p.heads, c.G - h0);
+    };
+    // Q of piece k, out of shared into tensor memory.
+    auto copy_q = [&](int k) -> bool {
+      if (!wait_warp(bar_qfull, k & 1, c.status, &abort_flag)) return false;
+      constexpr int CH = HD / 32;  // 16-byte chunks of a quarter of the row
+      uint32_t q[4 * CH];
+#pragma unroll
+      for (int e = 0; e < CH; ++e) {
+        const int chunk = cq * CH + e;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(q[4 * e]), "=r"(q[4 * e + 1]), "=r"(q[4 * e + 2]), "=r"(q[4 * e + 3])
+                     : "r"(sQ + (chunk >> 3) * SLAB + r * 128 + (((chunk & 7) ^ (r & 7)) << 4))
+                     : "memory");
+      }
+      const uint32_t to = tmem + lane_off + kQCol + 64u * (uint32_t)(k & 1) + (uint32_t)(4 * CH * cq);
+      if constexpr (CH == 4) tmem_st16(to, q);
+      else tmem_st8(to, q);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar_qempty);
+        mbar_arrive(bar_qready + 8 * (k & 1));
+      }
+      return true;
+    };
 
     // The results of piece k: O out of its accumulator, normalised or as a partial result.
     auto drain = [&](int k) -> bool {
       const Piece& x = items[k % NSLOT];
-      const int xx = k & 1, gk = x.part / p.parts, h0 = (x.part - gk * p.parts) * p.heads;
-      const int heads = min(p.heads, c.G - h0), tok = r / heads;
-      const bool valid = r < x.count * heads;
-      const size_t row = (size_t)(x.row0 + x.i0 + tok) * c.Hq + gk * c.G + h0 + (r - tok * heads);
-      if (!mbar_wait_warp(bar_ofull + 8 * xx, (k >> 1) & 1, c.status, &abort_flag)) return false;
+      const int xx = k & 1;
+      int gk, head0;
+      const int heads = heads_of(x, &gk, &head0);
+      const bool valid = tok < x.count && hh < heads;
+      if (!wait_warp(bar_ofull, k & 1, c.status, &abort_flag)) return false;
       tc_fence_after();
-      const uint32_t ob = tmem + lane_off + 256u + 128u * (uint32_t)xx + (uint32_t)(OQ * cq);
+      const uint32_t ob = tmem + lane_off + kOCol + (uint32_t)(OQ * cq);
       uint32_t o[OQ];
 #pragma unroll
       for (int h = 0; h < OQ / 16; ++h) tmem_ld16(ob + 16u * h, *reinterpret_cast<uint32_t(*)[16]>(&o[16 * h]));
@@ -463,12 +544,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       const uint32_t bad_here = __ballot_sync(0xFFFFFFFFu, zero != 0.f);
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar_oempty + 8 * xx);
+        mbar_arrive(bar_oempty);
         s_bad[xx][cq][quad] = bad_here;
         mbar_arrive(bar_rows + 8 * quad);
       }
       // (the sums were written before, by the same warps)
-      if (!mbar_wait_warp(bar_rows + 8 * quad, k & 1, c.status, &abort_flag)) return false;
+      if (!wait_warp(bar_rows + 8 * quad, k & 1, c.status, &abort_flag)) return false;
       float l = 0.f;
       uint32_t bad_rows = 0u;
 #pragma unroll
@@ -478,17 +559,48 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       }
       const bool none = l == 0.f;  // no live slot
       const bool bad = !none && (((bad_rows >> lane) & 1u) || !(l >= kLeastSum) || !(l < INFINITY));
+      const size_t first = (size_t)(x.row0 + x.i0) * c.Hq + head0;  // row of o of the tile's first
+      const size_t row = first + (size_t)tok * c.Hq + hh;
       if (x.whole) {
         const float inv = none ? 0.f : 1.f / l;
-        if (valid) {
-          float y[OQ];
+        // 16-byte chunks of the rows, passed about among four (D = 64: two) lanes so that they
+        // write a row's chunks side by side: 32 lanes with a row each met 32 lines a store
+        constexpr int CH = OQ / 8;
+        uint4 y[CH];
 #pragma unroll
-          for (int e = 0; e < OQ; ++e) y[e] = none ? 0.f : __uint_as_float(o[e]) * inv;
-          store_values(static_cast<__nv_bfloat16*>(c.o) + row * HD + OQ * cq, y);
-          if (cq == 0) {
-            if (bad) ask_redo(p);
-            c.lse[row] = bad ? kNaN32 : none ? -INFINITY : (m_prev + log2f(l)) * kLn2;
+        for (int e = 0; e < CH; ++e) {
+          uint32_t w[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const float a = __uint_as_float(o[8 * e + 2 * z]), b = __uint_as_float(o[8 * e + 2 * z + 1]);
+            w[z] = none ? 0u : pack_bf16x2(a * inv, b * inv);
           }
+          y[e] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+#pragma unroll
+        for (int d = 1; d < CH; d <<= 1) {
+          const bool high = lane & d;
+#pragma unroll
+          for (int e = 0; e < CH; ++e) {
+            if (e & d) continue;
+            uint4 give = high ? y[e] : y[e + d];
+            give.x = __shfl_xor_sync(0xFFFFFFFFu, give.x, d);
+            give.y = __shfl_xor_sync(0xFFFFFFFFu, give.y, d);
+            give.z = __shfl_xor_sync(0xFFFFFFFFu, give.z, d);
+            give.w = __shfl_xor_sync(0xFFFFFFFFu, give.w, d);
+            if (high) y[e] = give; else y[e + d] = give;
+          }
+        }
+        const int where = valid ? tok * c.Hq + hh : -1;
+#pragma unroll
+        for (int e = 0; e < CH; ++e) {
+          const int to = __shfl_sync(0xFFFFFFFFu, where, (lane & ~(CH - 1)) + e);
+          if (to >= 0)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.o) + (first + to) * HD + OQ * cq + 8 * (lane & (CH - 1))) = y[e];
+        }
+        if (valid && cq == 0) {
+          if (bad) ask_redo(p);
+          c.lse[row] = bad ? kNaN32 : none ? -INFINITY : (m_prev + log2f(l)) * kLn2;
         }
         done_with(k);
         return true;
@@ -509,21 +621,30 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       return true;
     };
 
+    // Temperature of this thread's row of piece k (asked for a piece ahead).
+    auto temp_of = [&](int k) -> float {
+      const Piece& x = items[k % NSLOT];
+      return tok < x.count ? __ldg(c.temp + x.row0 + x.i0 + tok) : 1.f;
+    };
+    float temp = 1.f;
     int k = 0;
     for (;; ++k) {
       if (!wait_piece(k)) break;
       const Piece& x = items[k % NSLOT];
       const int n = x.steps, tile0 = x.tile0;
-      float m = 0.f, mul;
-      RowMask mask;
-      bool valid;
-      {
-        const int gk = x.part / p.parts, h0 = (x.part - gk * p.parts) * p.heads, heads = min(p.heads, c.G - h0);
-        valid = r < x.count * heads;
-        const int i = x.i0 + r / heads;
-        mul = (valid && c.temp ? c.temp[x.row0 + i] : 1.f) * kL2E;
+      if (k == 0) {
+        if (!copy_q(0)) break;
+        if (c.temp) temp = temp_of(0);
+      }
+      int gk, head0;
+      const int heads = heads_of(x, &gk, &head0);
+      const bool valid = tok < x.count && hh < heads;
+      const float mul = temp * kL2E;
+      float m = 0.f;
+      RowMask mask = dead_row();
+      if (valid) {
         const SeqShape sh = {x.row0, x.n, x.len, x.base};
-        mask = valid ? row_mask(p, x.b, gk, sh, i) : dead_row();
+        mask = row_mask(p, x.b, gk, sh, x.i0 + tok);
       }
       const bool block = __any_sync(0xFFFFFFFFu, valid);  // the warp has rows at all
       poly.set(c.cap, mul);
@@ -534,7 +655,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       auto step = [&](int i) -> bool {
         const int gg = g + i, c0 = (tile0 + i) * BN + 32 * cq;
         const uint32_t sb = s_quarter + 128u * (uint32_t)(gg & 1);
-        if (!mbar_wait_warp(bar_sfull + 8 * (gg & 1), (gg >> 1) & 1, c.status, &abort_flag)) return false;
+        if (!wait_warp(bar_sfull + 8 * (gg & 1), (gg >> 1) & 1, c.status, &abort_flag)) return false;
         if (block) {
           tc_fence_after();
           uint32_t v[32], pk[16];
@@ -556,20 +677,29 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
               t[cq * BM + r] = best;
               __syncwarp();
               if (lane == 0) mbar_arrive(bar_tops + 8 * quad);
-              if (!mbar_wait_warp(bar_tops + 8 * quad, k & 1, c.status, &abort_flag)) return false;
+              if (!wait_warp(bar_tops + 8 * quad, k & 1, c.status, &abort_flag)) return false;
               best = fmaxf(fmaxf(t[r], t[BM + r]), fmaxf(t[2 * BM + r], t[3 * BM + r]));
               m = best == -INFINITY || fabsf(best) <= 40.f ? 0.f : best;
             }
           }
-          if (full) {
-            lsum += p_step<METHOD, false>(v, pk, poly, mul, -m, live, top, c.cap);
+          if (full && is_near<METHOD>(top, c.cap)) {
+            lsum += p_columns<METHOD, kNear, false>(v, pk, poly, mul, -m, live, c.cap);
             seen = true;
-          } else if (__any_sync(0xFFFFFFFFu, live != 0u)) {
-            lsum += p_step<METHOD, true>(v, pk, poly, mul, -m, live, top, c.cap);
-            seen = seen || live != 0u;
-          } else {
+          } else if (!__any_sync(0xFFFFFFFFu, live != 0u)) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) pk[e] = 0u;
+          } else {
+            if (is_near<METHOD>(top, c.cap)) {
+              lsum += p_columns<METHOD, kNear, true>(v, pk, poly, mul, -m, live, c.cap);
+            } else {
+              uint32_t scores[32], packed[16];  // (copies, which alone have an address)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) scores[e] = v[e];
+              lsum += p_far<METHOD>(scores, packed, mul, -m, live, top, c.cap);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = packed[e];
+            }
+            seen = seen || live != 0u;
           }
           __syncwarp();
           tmem_st16(sb, pk);
@@ -577,7 +707,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
           tc_fence_before();
         } else if (METHOD == CAPATTN_CAP_NONE && i == 0) {
           if (lane == 0) mbar_arrive(bar_tops + 8 * quad);
-          if (!mbar_wait_warp(bar_tops + 8 * quad, k & 1, c.status, &abort_flag)) return false;
+          if (!wait_warp(bar_tops + 8 * quad, k & 1, c.status, &abort_flag)) return false;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_pfull + 8 * (gg & 1));
@@ -587,6 +717,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       // the previous piece's O, once this piece's first P is handed over (its last P V has
       // completed meanwhile)
       if (ok && k > 0) ok = drain(k - 1);
+      if (ok && wait_piece(k + 1)) {
+        ok = copy_q(k + 1);
+        if (c.temp) temp = temp_of(k + 1);
+      }
       for (int i = 1; ok && i < n; ++i) ok = step(i);
       if (!ok) break;
       g += n;

@@ -153,9 +153,8 @@ paged_finish_kernel(PagedParams p) {
   // The blocks of work of each record, two records a thread, and their sums.
   auto blocks_of = [&](int i) -> int {
     if (i >= p.ctas || p.records[i].steps < 0) return 0;
-    const int g = p.records[i].part / p.parts, h0 = (p.records[i].part - g * p.parts) * p.heads;
     const bool many = p.records[i].c1 - p.records[i].c0 + 1 >= kManyPieces;
-    return (p.records[i].count * min(p.heads, c.G - h0) + 31) / 32 * (many ? 4 : 1);
+    return (p.records[i].count * p.heads + 31) / 32 * (many ? 4 : 1);
   };
   const int n0 = blocks_of(2 * threadIdx.x), n1 = blocks_of(2 * threadIdx.x + 1);
   const int up = lane_scan(n0 + n1, lane);
@@ -199,8 +198,9 @@ paged_finish_kernel(PagedParams p) {
     part[warp][N + 1][lane] = sum.l;
     part[warp][N + 2][lane] = sum.bad ? 1.f : 0.f;
     __syncthreads();
-    const bool valid = r < x.count * heads;
-    const int tok = x.row0 + x.i0 + r / heads, head = g * c.G + h0 + r % heads;
+    const int t = r / p.heads, hh = r - t * p.heads;
+    const bool valid = t < x.count && hh < heads;
+    const int tok = x.row0 + x.i0 + t, head = g * c.G + h0 + hh;
     const size_t row = (size_t)tok * c.Hq + head;
     uint32_t redo = 0u;
     // columns [at, at + V) of the row, done; the rows that cannot be trusted are left to one warp

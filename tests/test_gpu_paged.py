@@ -9,6 +9,7 @@ import torch
 
 from kv_cache_utils import Pool
 from paged_ref import Attend, check
+from soft_capped_attention_gb300 import capattn as ca
 from test_gpu_kv_cache import BF16, FP32, params
 
 pytestmark = pytest.mark.gpu
@@ -92,6 +93,7 @@ CASES = [
     ([400, 129], [65, 64], 32, 2, 128, 16, BF16, "none", 0, True, False),
     ([130, 257], [4, 5], 40, 2, 64, 32, BF16, "alsc", 0, True, False),
     ([60, 7], [9, 2], 130, 1, 64, 16, BF16, "tanh50", 0, False, False),
+    ([60, 7], [9, 2], 129, 1, 128, 16, BF16, "tanh50", 0, False, False),   # two unequal parts of a group
     ([600, 70, 9], [100, 70, 9], 17, 1, 128, 16, BF16, "soft_sign", 1, False, False),
     ([2000, 100], [40, 9], 4, 4, 128, 64, BF16, "tanh", 300, True, True),
     ([900, 321], [30, 100], 8, 2, 64, 16, BF16, "alsc", 200, False, True),
@@ -109,6 +111,7 @@ CASES = [
     ([700, 300], [17, 300], 16, 2, 128, 64, FP32, "none", 77, False, True),
     ([4000], [9], 2, 2, 64, 16, FP32, "tanh15", 0, False, False),
     ([60, 7], [9, 2], 70, 1, 128, 16, FP32, "alsc90", 0, False, False),
+    ([60, 7], [9, 2], 65, 1, 64, 16, FP32, "tanh15", 0, True, False),
 ]
 
 
@@ -120,6 +123,15 @@ def test_attend(case, tree):
     got, want = run(pool, new, Hq, params(cap, D, window), dtype, tree, temp, pos, seed=sum(new), first=len(lens) % 3,
                     tail=sum(lens) % 4)
     check(got, want, dtype)
+
+
+@pytest.mark.parametrize("cap,scale", [(20.0, 1.0), (20.0, 3.0), (4.0, 0.3)])
+def test_soft_sign_near_zero(cap, scale):
+    """Scores inside its polynomial's range, across it, and far below the cap."""
+    pool = Pool([700, 90], 2, 128, 16, BF16, 5)
+    ap = ca.AttnParams(sm_scale=1 / math.sqrt(128), cap_method="soft_sign", cap=cap, causal=True)
+    got, want = run(pool, [200, 30], 4, ap, BF16, False, True, seed=3, scale=scale)
+    check(got, want, BF16)
 
 
 @pytest.mark.parametrize("tree", [False, True], ids=["prompt", "tree"])
