@@ -8,7 +8,7 @@
 // spans few tokens, which wastes little of its causal edge.
 //
 // The reference m of a row's exponentials is fixed before its scores are seen, so no step
-// looks for a maximum and the four threads of a row exchange nothing but l at the end:
+// looks for a maximum and a row's threads exchange nothing but l at the end:
 //   with a cap, |x| is bounded and m = max(0, bound - 100) (0 for all usual caps, which
 //   also makes x - m exact); without one, m comes from the first step's scores (0 while
 //   they are within 2^+-40).
@@ -21,17 +21,15 @@
 //                warps 0 and 18 follow and load K and V, a page (or 128 rows of one) a box,
 //                into rings; V's rows without a token are zeroed (0 times what they hold must
 //                be 0);
-//   warp 1       TMEM allocator and MMA issuer: S_0 S_1 | PV_0 S_2 | PV_1 S_3 | ... over the
-//                steps of all pieces, so that a piece's first scores are there when the last
-//                one's end;
-//   warps 2..17  softmax, four threads a row, 32 slots each: one TMEM load (which gives the
-//                largest |S| too, for the choice of the cap's polynomial), one store of P over
-//                the scores.  They copy the next piece's Q into tensor memory after a piece's
-//                first step, and write the last piece's O then, when its last P V has completed.
-// TMEM (512 columns): S / P [0, 128) and [128, 256), O [256, 256 + D), Q [384, 448), [448, 512).
-// What bounds a long prompt is shared memory's 128 bytes a clock: with Q there, S alone took
-// 512 clocks of a step, P V 256 and the copies of K and V 512; with Q in tensor memory S takes
-// 256, and Q's room makes a third stage of K.
+//   warp 1       TMEM allocator and MMA issuer: S_0 S_1 S_2 | PV_0 S_3 | PV_1 S_4 | ... over
+//                the steps of all pieces, so that a piece's first scores are there when the
+//                last one's end;
+//   warps 2..17  softmax, eight for the even steps and eight for the odd ones, two threads a
+//                row, 64 slots each: loads of 32 columns (which give the largest |S| too, for
+//                the choice of the cap's polynomial), P stored over the scores.  With three
+//                score buffers a group finds its next scores ready when it has written P.
+//                Around a piece's first step they write the last piece's O.
+// TMEM (512 columns): S / P [0, 128), [128, 256), [256, 384), O [384, 384 + D).
 // P is rounded to bf16 (at most half a step of o's own type, and the sum l is of the
 // unrounded values): a second product for its low half would cost as much as the first.
 #include <float.h>
@@ -50,17 +48,18 @@ using fwdtc::tile_bytes;
 constexpr int BM = kAttendRows;
 // K and V stages
 template <int HD>
-constexpr int kst() { return HD == 64 ? 5 : 3; }
+constexpr int kst() { return HD == 64 ? 4 : 2; }
 template <int HD>
 constexpr int vst() { return HD == 64 ? 4 : 2; }
-constexpr uint32_t kOCol = 256, kQCol = 384;  // TMEM columns of O and of Q (+ 64 x: buffer x)
-constexpr int NSLOT = 4;  // pieces known ahead
+constexpr uint32_t NSB = 3;       // score buffers
+constexpr uint32_t kOCol = 384;   // TMEM column of O
+constexpr int NSLOT = 8;  // pieces known ahead
 constexpr int kSoftmaxWarps = 16;
 constexpr int NTHREADS = 640;
 constexpr float kLeastSum = 0x1p-80f;
-// a Q tile, the K and V tiles, the sums [2][4][128] and the first step's maxima
+// two Q tiles, the K and V tiles, the sums [2][4][128] and the first step's maxima
 template <int HD>
-constexpr int smem_bytes() { return (1 + kst<HD>() + vst<HD>()) * tile_bytes<HD>() + 2 * 4096 + 1024; }
+constexpr int smem_bytes() { return (2 + kst<HD>() + vst<HD>()) * tile_bytes<HD>() + 2 * 4096 + 1024; }
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
   asm volatile(
@@ -106,14 +105,21 @@ __device__ __forceinline__ void mma_ts_low(uint32_t d, uint32_t a, uint32_t b, u
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p; }" ::"r"(d), "r"(a), "r"(b), "n"(kDescHigh), "r"(idesc), "r"(acc), "r"(go)
       : "memory");
 }
-// S = Q K^T (Q packed in D / 2 columns of tensor memory), O += P V (P packed at the start of
-// each 32 columns of its score buffer).
+__device__ __forceinline__ void mma_ss_low(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t go) {
+  asm volatile(
+      "{ .reg .pred p, q; .reg .b64 x, y; setp.ne.b32 p, %5, 0; setp.ne.b32 q, %6, 0; mov.b64 x, {%1, %3}; mov.b64 y, {%2, %3};"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p; }" ::"r"(d), "r"(a), "r"(b), "n"(kDescHigh), "r"(idesc), "r"(acc), "r"(go)
+      : "memory");
+}
+// S = Q K^T, O += P V (P packed at the start of each 32 columns of its score buffer).
 template <int HD>
-__device__ __forceinline__ void issue_s(uint32_t d, uint32_t q, uint32_t dK, uint32_t go) {
+__device__ __forceinline__ void issue_s(uint32_t d, uint32_t dQ, uint32_t dK, uint32_t go) {
   constexpr uint32_t idesc = idesc_bf16(BM, BN, 0, 0);
 #pragma unroll
-  for (int ks = 0; ks < HD / 16; ++ks)
-    mma_ts_low(d, q + 8 * ks, dK + (((ks >> 2) * SLAB + (ks & 3) * 32) >> 4), idesc, ks > 0 ? 1u : 0u, go);
+  for (int ks = 0; ks < HD / 16; ++ks) {
+    const uint32_t off = ((ks >> 2) * SLAB + (ks & 3) * 32) >> 4;
+    mma_ss_low(d, dQ + off, dK + off, idesc, ks > 0 ? 1u : 0u, go);
+  }
 }
 template <int HD>
 __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pt, uint32_t dV, uint32_t acc0, uint32_t go) {
@@ -220,48 +226,50 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   constexpr int KST = kst<HD>(), VST = vst<HD>();
   constexpr int OQ = HD / 4;  // O columns of a thread
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 + 2 + 2 * KST + 2 * VST + 2 * 2 + 2 + 2 * NSLOT + 4 + 4 + 2];
+  __shared__ __align__(8) uint64_t bars[2 * 2 + 2 * KST + 2 * VST + 2 * NSB + 2 + 2 * NSLOT + 4 + 4 + 2];
   __shared__ Piece items[NSLOT];
   __shared__ ScheduleMem s_sched;
   __shared__ uint32_t s_bad[2][4][4];  // piece parity, quarter, rows / 32
+  __shared__ int s_drained[2][4];      // piece parity, rows / 32: warps that have read their part of O
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheParams& c = p.c;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sQ = base;
-  const uint32_t sK = base + TILE;              // stage s at + s * TILE
-  const uint32_t sV = base + (1 + KST) * TILE;  // stage s at + s * TILE
-  float* sums = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + (1 + KST + VST) * TILE);
+  const uint32_t sQ = base;                     // buffer x at + x * TILE
+  const uint32_t sK = base + 2 * TILE;          // stage s at + s * TILE
+  const uint32_t sV = base + (2 + KST) * TILE;  // stage s at + s * TILE
+  float* sums = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + (2 + KST + VST) * TILE);
   float* tops = sums + 2 * 4 * BM;
 
-  const uint32_t bar_qfull = smem_u32(&bars[0]);     // a piece's Q in shared memory
-  const uint32_t bar_qempty = bar_qfull + 8;         // and out of it (16 warps)
-  const uint32_t bar_qready = bar_qempty + 8;        // + 8 x: Q in tensor memory (16 warps)
-  const uint32_t bar_kfull = bar_qready + 16;        // + 8 s
+  const uint32_t bar_qfull = smem_u32(&bars[0]);     // + 8 x
+  const uint32_t bar_qempty = bar_qfull + 16;        // + 8 x: the piece's last S complete
+  const uint32_t bar_kfull = bar_qempty + 16;        // + 8 s
   const uint32_t bar_kempty = bar_kfull + 8 * KST;   // + 8 s
   const uint32_t bar_vfull = bar_kempty + 8 * KST;   // + 8 s
   const uint32_t bar_vempty = bar_vfull + 8 * VST;   // + 8 s
   const uint32_t bar_sfull = bar_vempty + 8 * VST;   // + 8 x: S in buffer x complete
-  const uint32_t bar_pfull = bar_sfull + 16;         // + 8 x: P in buffer x written (16 warps)
-  const uint32_t bar_ofull = bar_pfull + 16;         // the piece's last P V complete
+  const uint32_t bar_pfull = bar_sfull + 8 * NSB;    // + 8 x: P in buffer x written (8 warps)
+  const uint32_t bar_ofull = bar_pfull + 8 * NSB;        // the piece's last P V complete
   const uint32_t bar_oempty = bar_ofull + 8;         // O read by the 16 softmax warps
   const uint32_t bar_ifull = bar_oempty + 8;         // + 8 s: piece slot written
   const uint32_t bar_iempty = bar_ifull + 8 * NSLOT; // + 8 s: piece done with (19 warps)
-  const uint32_t bar_rows = bar_iempty + 8 * NSLOT;  // + 8 x: the four quarters of rows 32 x .. met (drain)
-  const uint32_t bar_tops = bar_rows + 32;           // + 8 x: the same, first step without a cap
+  const uint32_t bar_sums = bar_iempty + 8 * NSLOT;  // + 8 x: the sums of rows 32 x .. written (4 warps)
+  const uint32_t bar_tops = bar_sums + 32;           // + 8 x: the same, first step without a cap
   const uint32_t bar_vfix = bar_tops + 32;           // V rows that get zeros have landed
   const uint32_t bar_final = bar_vfix + 8;
 
+  if (threadIdx.x < 8) s_drained[threadIdx.x >> 2][threadIdx.x & 3] = 0;
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    mbar_init(bar_qfull, 1);
-    mbar_init(bar_qempty, kSoftmaxWarps);
     for (int x = 0; x < 2; ++x) {
-      mbar_init(bar_qready + 8 * x, kSoftmaxWarps);
+      mbar_init(bar_qfull + 8 * x, 1);
+      mbar_init(bar_qempty + 8 * x, 1);
+    }
+    for (uint32_t x = 0; x < NSB; ++x) {
       mbar_init(bar_sfull + 8 * x, 1);
-      mbar_init(bar_pfull + 8 * x, kSoftmaxWarps);
+      mbar_init(bar_pfull + 8 * x, kSoftmaxWarps / 2);
     }
     mbar_init(bar_ofull, 1);
     mbar_init(bar_oempty, kSoftmaxWarps);
@@ -278,8 +286,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       mbar_init(bar_iempty + 8 * s, 3 + kSoftmaxWarps);
     }
     for (int x = 0; x < 4; ++x) {
-      mbar_init(bar_rows + 8 * x, 4);
-      mbar_init(bar_tops + 8 * x, 4);
+      mbar_init(bar_sums + 8 * x, 4);
+      mbar_init(bar_tops + 8 * x, 2);
     }
     mbar_init(bar_vfix, 1);
     mbar_init(bar_final, 1);
@@ -330,18 +338,21 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       }
       __syncwarp();
       if (x.steps < 0) break;
-      if (k >= 1 && !wait_warp(bar_qempty, (k - 1) & 1, c.status, &abort_flag)) break;
+      const int y = k & 1;
+      if (k >= 2 && !wait_warp(bar_qempty + 8 * y, ((k >> 1) - 1) & 1, c.status, &abort_flag)) break;
       if (leader) {
         const int g = x.part / p.parts, head0 = g * c.G + (x.part - g * p.parts) * p.heads;
-        mbar_expect_tx(bar_qfull, bytes);
-        for (int sl = 0; sl < NSLAB; ++sl) tma_load_3d(sQ + sl * SLAB, &mq, bar_qfull, 64 * sl, head0, x.row0 + x.i0);
+        mbar_expect_tx(bar_qfull + 8 * y, bytes);
+        for (int sl = 0; sl < NSLAB; ++sl)
+          tma_load_3d(sQ + y * TILE + sl * SLAB, &mq, bar_qfull + 8 * y, 64 * sl, head0, x.row0 + x.i0);
       }
       loaded = k + 1;
       __syncwarp();
     }
     if (!shared && lane == 0) leave_no_record(p);
     // (on an early exit the copies in flight land before the CTA ends)
-    if (leader && loaded > 0) drain_wait(bar_qfull, (loaded - 1) & 1);
+    if (leader)
+      for (int x = loaded > 2 ? loaded - 2 : 0; x < loaded; ++x) drain_wait(bar_qfull + 8 * (x & 1), (x >> 1) & 1);
     __syncwarp();
   } else if (warp == 0 || warp == 18) {
     // ------------------------------------------------------------ K (warp 0) and V (warp 18)
@@ -418,6 +429,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t leader = elect_one_sync() ? 1u : 0u;
+    const uint32_t dQ = desc_low(sQ, 16);
     const uint32_t dK = desc_low(sK, 16);
     const uint32_t dV = desc_low(sV, SLAB);
     int sk = 0, left = 0;                // next S: its piece, the piece's steps still to come (0: not known yet)
@@ -428,15 +440,16 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
         if (!wait_warp(bar_ifull + 8 * (sk % NSLOT), (sk / NSLOT) & 1, c.status, &abort_flag)) return -1;
         left = __reduce_max_sync(0xFFFFFFFFu, items[sk % NSLOT].steps);
         if (left < 0) return 0;
-        if (!wait_warp(bar_qready + 8 * (sk & 1), (sk >> 1) & 1, c.status, &abort_flag)) return -1;
+        if (!wait_warp(bar_qfull + 8 * (sk & 1), (sk >> 1) & 1, c.status, &abort_flag)) return -1;
       }
       if (!wait_warp(bar_kfull + 8 * ks, kp, c.status, &abort_flag)) return -1;
       tc_fence_after();
-      issue_s<HD>(tmem + 128u * sg, tmem + kQCol + 64u * (uint32_t)(sk & 1), dK + ks * (TILE >> 4), leader);
+      issue_s<HD>(tmem + 128u * sg, dQ + (uint32_t)(sk & 1) * (TILE >> 4), dK + ks * (TILE >> 4), leader);
       commit_if(bar_sfull + 8 * sg, leader);
       commit_if(bar_kempty + 8 * ks, leader);
+      if (left == 1) commit_if(bar_qempty + 8 * (sk & 1), leader);  // its Q is no longer read
       __syncwarp();
-      sg ^= 1u;
+      sg = sg + 1 == NSB ? 0 : sg + 1;
       if (++ks == KST) {
         ks = 0;
         kp ^= 1u;
@@ -444,8 +457,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       if (--left == 0) ++sk;
       return 1;
     };
-    int ahead = issue_scores();
-    if (ahead > 0) ahead = issue_scores();
+    int ahead = 1;
+    for (uint32_t x = 0; x < NSB && ahead > 0; ++x) ahead = issue_scores();
     uint32_t g = 0, gp = 0, vs = 0, vp = 0;  // next P V: P's buffer, its phase; V stage, its phase
     for (int k = 0; ahead >= 0 && wait_piece(k); ++k) {
       const int n = __reduce_max_sync(0xFFFFFFFFu, items[k % NSLOT].steps);
@@ -460,13 +473,15 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
         commit_if(bar_vempty + 8 * vs, leader);
         if (i + 1 == n) commit_if(bar_ofull, leader);  // the piece's O is complete
         __syncwarp();
-        gp ^= g;
-        g ^= 1u;
+        if (++g == NSB) {
+          g = 0;
+          gp ^= 1u;
+        }
         if (++vs == VST) {
           vs = 0;
           vp ^= 1u;
         }
-        // S of the step after the next overwrites this P after its P V (in-order MMAs)
+        // S of the step three on overwrites this P after its P V (in-order MMAs)
         if (ahead > 0) ahead = issue_scores();
         ok = ahead >= 0;
         if (!ok) break;
@@ -479,11 +494,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax and results
-    const int cq = (warp - 2) >> 2;   // slots [32 cq, 32 cq + 32) of each step
+    const int cq = (warp - 2) >> 2;   // quarter of Q's and O's columns
+    const int group = cq >> 1;        // takes the even or the odd steps,
+    const int half = cq & 1;          // slots [64 half, 64 half + 64) of each
     const int quad = warp & 3;        // rows [32 quad, 32 quad + 32): the TMEM lanes it may access
     const int r = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t s_quarter = tmem + lane_off + 32u * (uint32_t)cq;  // + 128 x: score buffer x
+    const uint32_t s_half = tmem + lane_off + 64u * (uint32_t)half;  // + 128 x: score buffer x
+    uint32_t sb = (uint32_t)group, sp = 0;  // this group's next score buffer, its phase
     RowPoly<METHOD> poly;
     int g = 0;        // steps so far
     float m_prev = 0.f;  // reference of the piece whose O is still to leave
@@ -496,32 +514,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       *head0 = gk * c.G + h0;
       return min(p.heads, c.G - h0);
     };
-    // Q of piece k, out of shared into tensor memory.
-    auto copy_q = [&](int k) -> bool {
-      if (!wait_warp(bar_qfull, k & 1, c.status, &abort_flag)) return false;
-      constexpr int CH = HD / 32;  // 16-byte chunks of a quarter of the row
-      uint32_t q[4 * CH];
-#pragma unroll
-      for (int e = 0; e < CH; ++e) {
-        const int chunk = cq * CH + e;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(q[4 * e]), "=r"(q[4 * e + 1]), "=r"(q[4 * e + 2]), "=r"(q[4 * e + 3])
-                     : "r"(sQ + (chunk >> 3) * SLAB + r * 128 + (((chunk & 7) ^ (r & 7)) << 4))
-                     : "memory");
-      }
-      const uint32_t to = tmem + lane_off + kQCol + 64u * (uint32_t)(k & 1) + (uint32_t)(4 * CH * cq);
-      if constexpr (CH == 4) tmem_st16(to, q);
-      else tmem_st8(to, q);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar_qempty);
-        mbar_arrive(bar_qready + 8 * (k & 1));
-      }
-      return true;
-    };
-
     // The results of piece k: O out of its accumulator, normalised or as a partial result.
     auto drain = [&](int k) -> bool {
       const Piece& x = items[k % NSLOT];
@@ -542,23 +534,30 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
 #pragma unroll
       for (int e = 0; e < OQ; ++e) zero = fmaf(__uint_as_float(o[e]), 0.f, zero);
       const uint32_t bad_here = __ballot_sync(0xFFFFFFFFu, zero != 0.f);
-      __syncwarp();
+      // the last of the four warps of these rows knows what all of them saw
+      int last = 0;
       if (lane == 0) {
         mbar_arrive(bar_oempty);
         s_bad[xx][cq][quad] = bad_here;
-        mbar_arrive(bar_rows + 8 * quad);
+        __threadfence_block();
+        last = atomicAdd(&s_drained[xx][quad], 1) == 3;
+        if (last) s_drained[xx][quad] = 0;
+        __threadfence_block();
       }
-      // (the sums were written before, by the same warps)
-      if (!wait_warp(bar_rows + 8 * quad, k & 1, c.status, &abort_flag)) return false;
+      last = __shfl_sync(0xFFFFFFFFu, last, 0);
+      __syncwarp();
+      if (!wait_warp(bar_sums + 8 * quad, k & 1, c.status, &abort_flag)) return false;
       float l = 0.f;
-      uint32_t bad_rows = 0u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        l += sums[(xx * 4 + e) * BM + r];
-        bad_rows |= s_bad[xx][e][quad];
-      }
+      for (int e = 0; e < 4; ++e) l += sums[(xx * 4 + e) * BM + r];
       const bool none = l == 0.f;  // no live slot
-      const bool bad = !none && (((bad_rows >> lane) & 1u) || !(l >= kLeastSum) || !(l < INFINITY));
+      bool bad = false;
+      if (last) {
+        uint32_t bad_rows = 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bad_rows |= *const_cast<volatile uint32_t*>(&s_bad[xx][e][quad]);
+        bad = !none && (((bad_rows >> lane) & 1u) || !(l >= kLeastSum) || !(l < INFINITY));
+      }
       const size_t first = (size_t)(x.row0 + x.i0) * c.Hq + head0;  // row of o of the tile's first
       const size_t row = first + (size_t)tok * c.Hq + hh;
       if (x.whole) {
@@ -598,7 +597,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
           if (to >= 0)
             *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.o) + (first + to) * HD + OQ * cq + 8 * (lane & (CH - 1))) = y[e];
         }
-        if (valid && cq == 0) {
+        if (valid && last) {
           if (bad) ask_redo(p);
           c.lse[row] = bad ? kNaN32 : none ? -INFINITY : (m_prev + log2f(l)) * kLn2;
         }
@@ -610,7 +609,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
         for (int e = 0; e < OQ / 4; ++e)
           reinterpret_cast<uint4*>(p.part_o)[part_at<HD, BM>(x.slot, r, cq, e)] =
               make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        if (cq == 0) {
+        if (last) {
           const size_t at = (size_t)x.slot * BM + r;
           p.part_ml[at] = make_float2(m_prev, l);
           p.part_bad[at] = bad ? 1u : 0u;
@@ -627,18 +626,16 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       return tok < x.count ? __ldg(c.temp + x.row0 + x.i0 + tok) : 1.f;
     };
     float temp = 1.f;
-    int k = 0;
-    for (;; ++k) {
-      if (!wait_piece(k)) break;
+    for (int k = 0;; ++k) {
+      const bool more = wait_piece(k);
+      // after the last piece only its O is left (and not even that after a wait that gave up)
+      if (!more && (k == 0 || !__all_sync(0xFFFFFFFFu, abort_flag == 0))) break;
       const Piece& x = items[k % NSLOT];
-      const int n = x.steps, tile0 = x.tile0;
-      if (k == 0) {
-        if (!copy_q(0)) break;
-        if (c.temp) temp = temp_of(0);
-      }
+      const int n = more ? x.steps : 0, tile0 = x.tile0;
+      if (c.temp && k == 0) temp = temp_of(0);
       int gk, head0;
       const int heads = heads_of(x, &gk, &head0);
-      const bool valid = tok < x.count && hh < heads;
+      const bool valid = more && tok < x.count && hh < heads;
       const float mul = temp * kL2E;
       float m = 0.f;
       RowMask mask = dead_row();
@@ -651,85 +648,109 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       if constexpr (METHOD != CAPATTN_CAP_NONE) m = fmaxf(0.f, largest_x<METHOD>(c.cap, mul) - 100.f);
       float lsum = 0.f;
       bool seen = false;
-      // one step: this quarter's P over its scores, handed to the issuer
+      // without a cap: the reference, from the live scores of the piece's first step
+      auto reference = [&]() -> bool {
+        const float* t = tops + (k & 1) * 2 * BM;
+        if (!wait_warp(bar_tops + 8 * quad, k & 1, c.status, &abort_flag)) return false;
+        const float best = fmaxf(t[r], t[BM + r]);
+        m = best == -INFINITY || fabsf(best) <= 40.f ? 0.f : best;
+        return true;
+      };
+      // one step: this half's P over its scores, handed to the issuer
       auto step = [&](int i) -> bool {
-        const int gg = g + i, c0 = (tile0 + i) * BN + 32 * cq;
-        const uint32_t sb = s_quarter + 128u * (uint32_t)(gg & 1);
-        if (!wait_warp(bar_sfull + 8 * (gg & 1), (gg >> 1) & 1, c.status, &abort_flag)) return false;
+        const int c0 = (tile0 + i) * BN + 64 * half;
+        if (!wait_warp(bar_sfull + 8 * sb, sp, c.status, &abort_flag)) return false;
+        const uint32_t at_s = s_half + 128u * sb;
         if (block) {
           tc_fence_after();
-          uint32_t v[32], pk[16];
-          float top = tmem_ld32_absmax(sb, v);
-          const bool full = __all_sync(0xFFFFFFFFu, !valid || all_live(mask, c0, 32));
-          uint32_t live = 0xFFFFFFFFu;
-          if (!full) live = live_slots(p, mask, c0);
-          tmem_wait_ld();
-          settled(v);
-          asm volatile("" : "+f"(top));
-          if (!valid) top = 0.f;
-          if constexpr (METHOD == CAPATTN_CAP_NONE) {
-            if (i == 0) {  // the reference, from the live scores of all four quarters
-              float best = -INFINITY;
+          if (METHOD == CAPATTN_CAP_NONE && i == 0) {
+            float best = -INFINITY;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              uint32_t v[32];
+              tmem_ld32(at_s + 32u * h, v);
+              const uint32_t live = valid ? live_slots(p, mask, c0 + 32 * h) : 0u;
+              tmem_wait_ld();
+              settled(v);
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if ((live >> e) & 1u) best = fmaxf(best, __uint_as_float(v[e]) * (c.sm_scale * mul));
-              float* t = tops + (k & 1) * 4 * BM;
-              t[cq * BM + r] = best;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar_tops + 8 * quad);
-              if (!wait_warp(bar_tops + 8 * quad, k & 1, c.status, &abort_flag)) return false;
-              best = fmaxf(fmaxf(t[r], t[BM + r]), fmaxf(t[2 * BM + r], t[3 * BM + r]));
-              m = best == -INFINITY || fabsf(best) <= 40.f ? 0.f : best;
             }
+            tops[((k & 1) * 2 + half) * BM + r] = best;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_tops + 8 * quad);
+            if (!reference()) return false;
           }
-          if (full && is_near<METHOD>(top, c.cap)) {
-            lsum += p_columns<METHOD, kNear, false>(v, pk, poly, mul, -m, live, c.cap);
-            seen = true;
-          } else if (!__any_sync(0xFFFFFFFFu, live != 0u)) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[32], pk[16];
+            float top = tmem_ld32_absmax(at_s + 32u * h, v);
+            const int at = c0 + 32 * h;
+            const bool full = __all_sync(0xFFFFFFFFu, !valid || all_live(mask, at, 32));
+            uint32_t live = 0xFFFFFFFFu;
+            if (!full) live = live_slots(p, mask, at);
+            tmem_wait_ld();
+            settled(v);
+            asm volatile("" : "+f"(top));
+            if (!valid) top = 0.f;
+            if (full && is_near<METHOD>(top, c.cap)) {
+              lsum += p_columns<METHOD, kNear, false>(v, pk, poly, mul, -m, live, c.cap);
+              seen = true;
+            } else if (!__any_sync(0xFFFFFFFFu, live != 0u)) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) pk[e] = 0u;
-          } else {
-            if (is_near<METHOD>(top, c.cap)) {
-              lsum += p_columns<METHOD, kNear, true>(v, pk, poly, mul, -m, live, c.cap);
+              for (int e = 0; e < 16; ++e) pk[e] = 0u;
             } else {
-              uint32_t scores[32], packed[16];  // (copies, which alone have an address)
+              if (is_near<METHOD>(top, c.cap)) {
+                lsum += p_columns<METHOD, kNear, true>(v, pk, poly, mul, -m, live, c.cap);
+              } else {
+                uint32_t scores[32], packed[16];  // (copies, which alone have an address)
 #pragma unroll
-              for (int e = 0; e < 32; ++e) scores[e] = v[e];
-              lsum += p_far<METHOD>(scores, packed, mul, -m, live, top, c.cap);
+                for (int e = 0; e < 32; ++e) scores[e] = v[e];
+                lsum += p_far<METHOD>(scores, packed, mul, -m, live, top, c.cap);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) pk[e] = packed[e];
+                for (int e = 0; e < 16; ++e) pk[e] = packed[e];
+              }
+              seen = seen || live != 0u;
             }
-            seen = seen || live != 0u;
+            __syncwarp();
+            tmem_st16(at_s + 32u * h, pk);
           }
-          __syncwarp();
-          tmem_st16(sb, pk);
           tmem_wait_st();
           tc_fence_before();
         } else if (METHOD == CAPATTN_CAP_NONE && i == 0) {
           if (lane == 0) mbar_arrive(bar_tops + 8 * quad);
-          if (!wait_warp(bar_tops + 8 * quad, k & 1, c.status, &abort_flag)) return false;
+          if (!reference()) return false;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_pfull + 8 * (gg & 1));
+        if (lane == 0) mbar_arrive(bar_pfull + 8 * sb);
+        // every other step: two buffers on
+        sb += 2;
+        if (sb >= NSB) {
+          sb -= NSB;
+          sp ^= 1u;
+        }
         return true;
       };
-      bool ok = step(0);
-      // the previous piece's O, once this piece's first P is handed over (its last P V has
-      // completed meanwhile)
-      if (ok && k > 0) ok = drain(k - 1);
-      if (ok && wait_piece(k + 1)) {
-        ok = copy_q(k + 1);
-        if (c.temp) temp = temp_of(k + 1);
+      // The group of the piece's first step goes on with it, then with the last piece's O (its
+      // last P V, of the other group's step, has completed meanwhile); the other group begins
+      // with that.
+      bool ok = true;
+      for (int i = more && (g & 1) == group ? 0 : -1; ok && i < max(n, 1); i += 2) {
+        if (i >= 0 && i < n) ok = step(i);
+        if (i > 0) continue;
+        if (ok && k > 0) ok = drain(k - 1);
+        if (!more) break;
+        if (c.temp && ok && wait_piece(k + 1)) temp = temp_of(k + 1);
+        if (METHOD == CAPATTN_CAP_NONE && i < 0) ok = ok && reference();
       }
-      for (int i = 1; ok && i < n; ++i) ok = step(i);
-      if (!ok) break;
+      if (!ok || !more) break;
       g += n;
       // l: 0 without a live slot, something positive with one
       sums[((k & 1) * 4 + cq) * BM + r] = !seen ? 0.f : lsum == 0.f ? FLT_MIN : lsum;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_sums + 8 * quad);
       m_prev = m;
     }
-    // after the last piece (and not after a wait that gave up)
-    if (k > 0 && __all_sync(0xFFFFFFFFu, abort_flag == 0)) drain(k - 1);
   }
   __syncwarp();  // every warp reaches the CTA barrier converged
   tc_fence_before();
