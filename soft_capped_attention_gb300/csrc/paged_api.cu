@@ -28,7 +28,7 @@ PagedWorkspace layout(const capattn_cache_config& c, int call) {
     at = up256(at + (size_t)kAttendPartRows * c.D * sizeof(float));
   } else if (call == CAPATTN_PAGED_PLAN) {
     w.seqs_off = at;
-    at = up256(at + 8 * (size_t)c.B * sizeof(int4));  // a copy for each CTA of the cluster
+    at = up256(at + kPlanCopies * (size_t)c.B * 24);
   }
   w.total = at;
   return w;
@@ -144,7 +144,8 @@ capattn_status capattn_paged_plan(const capattn_cache_config* cfg, const int32_t
   p.n_free_out = n_free_out; p.n_rows = n_rows; p.cu_new = cu_new; p.slots = slots; p.positions = positions;
   p.B = c.B; p.page_size = c.page_size; p.page_shift = c.page_shift; p.max_pages = c.max_pages;
   p.num_pages = c.num_pages; p.max_len = c.max_len;
-  p.seqs = reinterpret_cast<int4*>(static_cast<char*>(workspace) + layout(*cfg, CAPATTN_PAGED_PLAN).seqs_off);
+  p.seqs = static_cast<char*>(workspace) + layout(*cfg, CAPATTN_PAGED_PLAN).seqs_off;
+  p.ticket = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kPlanTicketOff);
   p.status = c.status;
   return of(launch_paged_plan(p, stream));
 }

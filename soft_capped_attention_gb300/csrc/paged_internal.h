@@ -14,6 +14,7 @@ constexpr uint32_t kStatusBadPathBit = 2048u;
 // Whether rows of attention have to be formed once more, by themselves: a flag and a ticket in
 // the workspace's header, behind the counters; both are zero between calls.
 constexpr size_t kRedoOff = kCacheHeaderBytes - 64;
+constexpr size_t kPlanTicketOff = kRedoOff + 32;  // CTAs of a plan that have ended
 static_assert(kCountersOff + kDecodeMaxCtas * sizeof(uint32_t) <= kRedoOff, "header too small");
 
 struct Piece;
@@ -54,6 +55,8 @@ constexpr int kAttendSimtRows = 64;
 constexpr int kAttendPartRows = 2 * kAttendCtas * kAttendRows;
 static_assert(2 * kAttendSimtCtas * kAttendSimtRows <= kAttendPartRows, "partial results");
 
+constexpr int kPlanCopies = 8;  // of the sequences' sums in the workspace, 24 bytes each
+
 struct PlanParams {
   const int32_t* n_new;
   int32_t* table;
@@ -65,8 +68,9 @@ struct PlanParams {
   int64_t* slots;
   int32_t* positions;
   int32_t B, page_size, page_shift, max_pages, num_pages, max_len;
-  int4* seqs;                  // [B] workspace, for more sequences than shared memory holds
+  void* seqs;                  // workspace, for more sequences than shared memory holds
   uint32_t* status;
+  uint32_t* ticket;            // zero between calls
 };
 
 struct AcceptParams {

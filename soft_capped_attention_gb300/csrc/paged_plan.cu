@@ -1,40 +1,25 @@
 // The tables and slot maps of a step from request lengths, in one launch.
 //
-// Every CTA of one cluster (or a single CTA, for small steps) goes over all sequences and
-// sums up what they add, give back and need: new tokens, pages, pages.  The cluster meets;
-// if everything fits, pages that come back go on the stack, it meets again (a page may
-// come back and go out in the same step), and missing pages and the new rows' slots are
-// shared out over all threads by binary search in the sums.  Every place is a function of
-// the sums alone, so the result does not depend on scheduling.  Bound by latency: the sums
-// and the two meetings.
-#include <cooperative_groups.h>
-
+// Every CTA goes over all sequences by itself and sums up what they add, give back and need:
+// new tokens, pages, pages.  Everything else is a function of those sums: the k-th page that
+// goes out is the k-th from the top of the stack with this step's returns on it, which is an
+// old entry or, found by the sums again, a page that comes back in this very step; so no CTA
+// waits for another, and the result does not depend on scheduling.  The CTAs share out
+// returning pages, outgoing pages and new rows, each finding its sequence by binary search.
+// Lengths, held pages and the stack's height may be updated in place: the CTA that ends last
+// writes them.  Bound by latency (B = 512, 66,000 rows of slots: the first form, a cluster of
+// eight CTAs that met twice, took 14.8 us).
 #include "paged_internal.h"
 #include "tc_common.cuh"
 
 namespace capattn {
 namespace {
 
-namespace cg = cooperative_groups;
-
-constexpr int kThreads = 1024;
-constexpr int kCluster = 8;
-constexpr int kSmemSeqs = 4096;  // sequences whose sums fit shared memory
-
-// Sums before a sequence and what it has: x rows, y pages back, z pages out; w pages held.
-// After all sequences one more entry holds the totals.
-struct Totals {
-  int64_t rows, back, out;
-};
-
-__device__ __forceinline__ int64_t scan64(int64_t x, int lane) {
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
-    if (lane >= d) x += y;
-  }
-  return x;
-}
+constexpr int kThreads = 512;
+constexpr int kRows = 4;           // rows that a thread has in flight
+constexpr int kCtas = 152;
+constexpr int kSmemSeqs = 4096;    // sequences whose sums fit shared memory
+constexpr int kFewCtas = kPlanCopies;  // CTAs for more than those: their sums lie in the workspace
 
 struct Seq {
   int32_t add, len, held, need;
@@ -52,163 +37,172 @@ __device__ __forceinline__ Seq read_seq(const PlanParams& p, int b) {
   return s;
 }
 
-// The last b of B with sums[b].<part> <= x (the entry that holds item x).
+__device__ __forceinline__ int64_t scan64(int64_t x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// What comes before a sequence (rows, pages back, pages out), the pages that it held, its
+// length behind the step and the pages of that.
+struct Entry {
+  int32_t rows, back, out, held, len, need;
+};
+
+// The entry that holds item x: the last one with at most x before it.
 template <int PART>
-__device__ __forceinline__ int find(const int4* sums, int B, int x) {
-  int lo = 0, hi = B;  // sum(lo) <= x < sum(hi)
+__device__ __forceinline__ int find(const Entry* e, int B, int x) {
+  int lo = 0, hi = B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    const int v = PART == 0 ? sums[mid].x : PART == 1 ? sums[mid].y : sums[mid].z;
+    const int v = PART == 0 ? e[mid].rows : PART == 1 ? e[mid].back : e[mid].out;
     if (v <= x) lo = mid; else hi = mid;
   }
   return lo;
 }
 
-template <bool CLUSTER>
 __global__ void __launch_bounds__(kThreads)
 plan_kernel(PlanParams p) {
-  extern __shared__ int4 smem_sums[];
-  __shared__ int64_t s_sum[3][32];
-  __shared__ int s_bad;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int64_t s_sum[3][kThreads / 32];
+  __shared__ int s_bad, s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = CLUSTER ? (int)blockIdx.x : 0, ctas = CLUSTER ? kCluster : 1;
-  int4* sums = p.B <= kSmemSeqs ? smem_sums : p.seqs + (size_t)rank * p.B;
-  auto meet = [&]() {
-    if constexpr (CLUSTER) cg::this_cluster().sync(); else __syncthreads();
-  };
+  Entry* e = p.B <= kSmemSeqs ? reinterpret_cast<Entry*>(smem) : reinterpret_cast<Entry*>(p.seqs) + (size_t)blockIdx.x * p.B;
   if (tid == 0) s_bad = 0;
   pdl_trigger();
   pdl_wait();
   __syncthreads();
   const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  const int64_t n_free = p.n_free[0];
   int64_t add = 0, back = 0, out = 0;
+  Seq only{};
   for (int b = b0; b < b1; ++b) {
-    const Seq s = read_seq(p, b);
+    const Seq s = only = read_seq(p, b);
     if (s.bad) s_bad = 1;
     add += s.add;
     back += max(0, s.held - s.need);
     out += max(0, s.need - s.held);
   }
-  const int64_t ia = scan64(add, lane), ib = scan64(back, lane), io = scan64(out, lane);
+  int64_t sums[3] = {scan64(add, lane), scan64(back, lane), scan64(out, lane)}, all[3];
   if (lane == 31) {
-    s_sum[0][warp] = ia;
-    s_sum[1][warp] = ib;
-    s_sum[2][warp] = io;
-  }
-  const int64_t n_free = p.n_free[0];
-  __syncthreads();
-  Totals before{ia - add, ib - back, io - out}, all{0, 0, 0};
-  {
-    const int64_t a = scan64(s_sum[0][lane], lane), b = scan64(s_sum[1][lane], lane), o = scan64(s_sum[2][lane], lane);
-    all.rows = __shfl_sync(0xFFFFFFFFu, a, 31);
-    all.back = __shfl_sync(0xFFFFFFFFu, b, 31);
-    all.out = __shfl_sync(0xFFFFFFFFu, o, 31);
-    const int up = max(0, warp - 1);
-    const int64_t wa = __shfl_sync(0xFFFFFFFFu, a, up), wb = __shfl_sync(0xFFFFFFFFu, b, up), wo = __shfl_sync(0xFFFFFFFFu, o, up);
-    if (warp > 0) {
-      before.rows += wa;
-      before.back += wb;
-      before.out += wo;
-    }
-  }
-  const bool ok = !s_bad && all.rows <= p.n_rows && n_free >= 0 && n_free + all.back <= p.num_pages &&
-                  all.out <= n_free + all.back;
-  if (!ok && rank == 0 && tid == 0) atomicOr(p.status, kStatusBadPlanBit);
-  // the sums, and what belongs to the sequences (rank 0's threads keep it over the meeting:
-  // the outputs may be the inputs)
-  for (int b = b0; b < b1; ++b) {
-    const Seq s = read_seq(p, b);
-    if (ok) sums[b] = make_int4((int)before.rows, (int)before.back, (int)before.out, s.held);
-    before.rows += s.add;
-    before.back += max(0, s.held - s.need);
-    before.out += max(0, s.need - s.held);
+#pragma unroll
+    for (int x = 0; x < 3; ++x) s_sum[x][warp] = sums[x];
   }
   __syncthreads();
-  const int threads = ctas * kThreads, me = rank * kThreads + tid;
+#pragma unroll
+  for (int x = 0; x < 3; ++x) {
+    const int64_t w = scan64(lane < kThreads / 32 ? s_sum[x][lane] : 0, lane);
+    all[x] = __shfl_sync(0xFFFFFFFFu, w, 31);
+    const int64_t before = __shfl_sync(0xFFFFFFFFu, w, max(0, warp - 1));
+    if (warp > 0) sums[x] += before;
+  }
+  const bool ok = !s_bad && all[0] <= p.n_rows && n_free >= 0 && n_free + all[1] <= p.num_pages && all[2] <= n_free + all[1];
+  const int threads = gridDim.x * kThreads, me = blockIdx.x * kThreads + tid;
   if (!ok) {
-    // nothing changes; other CTAs may still read what the outputs overwrite with itself
+    // nothing changes: outputs of their own get what the inputs are
+    if (me == 0) atomicOr(p.status, kStatusBadPlanBit);
     for (int b = me; b < p.B; b += threads) {
       if (p.lens_out != p.lens) p.lens_out[b] = p.lens[b];
       if (p.held_out != p.held) p.held_out[b] = p.held[b];
       if (p.qpos && p.qpos_out != p.qpos) p.qpos_out[b] = p.qpos[b];
     }
-    for (int b = me; b <= p.B; b += threads) p.cu_new[b] = 0;
+    for (int64_t b = me; b <= p.B; b += threads) p.cu_new[b] = 0;
     if (me == 0 && p.n_free_out != p.n_free) p.n_free_out[0] = (int)n_free;
-    for (int r = me; r < p.n_rows; r += threads) {
+    for (int64_t r = me; r < p.n_rows; r += threads) {
       if (p.slots) p.slots[r] = -1;
       if (p.positions) p.positions[r] = -1;
     }
     return;
   }
-  // pages that come back
-  const int rows = (int)all.rows, backs = (int)all.back, outs = (int)all.out;
-  for (int k = me; k < backs; k += threads) {
-    const int b = find<1>(sums, p.B, k);
-    const Seq s = read_seq(p, b);
-    p.free_pages[n_free + k] = p.table[(size_t)b * p.max_pages + s.need + (k - sums[b].y)];
+  int64_t at[3] = {sums[0] - add, sums[1] - back, sums[2] - out};
+  for (int b = b0; b < b1; ++b) {
+    const Seq s = per == 1 ? only : read_seq(p, b);
+    e[b] = Entry{(int)at[0], (int)at[1], (int)at[2], s.held, s.len, s.need};
+    at[0] += s.add;
+    at[1] += max(0, s.held - s.need);
+    at[2] += max(0, s.need - s.held);
   }
-  // what the rows need of a sequence is read before the outputs may overwrite it
-  meet();
-  const int top = (int)n_free + backs;
-  for (int k = me; k < outs; k += threads) {
-    const int b = find<2>(sums, p.B, k);
-    p.table[(size_t)b * p.max_pages + sums[b].w + (k - sums[b].z)] = p.free_pages[top - 1 - k];
+  __syncthreads();
+  const int rows = (int)all[0], backs = (int)all[1], outs = (int)all[2], old = (int)n_free, top = old + backs;
+  // The k-th page that comes back, the k-th that goes out.
+  auto returned = [&](int k) -> int {
+    const int b = find<1>(e, p.B, k);
+    return p.table[(size_t)b * p.max_pages + e[b].need + (k - e[b].back)];
+  };
+  auto taken = [&](int k) -> int {
+    const int i = top - 1 - k;
+    return i >= old ? returned(i - old) : p.free_pages[i];
+  };
+  for (int64_t k = me; k < backs; k += threads) p.free_pages[old + k] = returned((int)k);
+  for (int64_t k = me; k < outs; k += threads) {
+    const int b = find<2>(e, p.B, (int)k);
+    p.table[(size_t)b * p.max_pages + e[b].held + ((int)k - e[b].out)] = taken((int)k);
   }
-  for (int r = me; r < p.n_rows; r += threads) {
-    int64_t at = -1;
-    int pos = -1;
-    if (r < rows) {
-      const int b = find<0>(sums, p.B, r);
-      const int4 x = sums[b];
-      const int i = r - x.x;
-      const int slot = p.lens[b] + i, page = slot >> p.page_shift;
-      const int id = page < x.w ? p.table[(size_t)b * p.max_pages + page] : p.free_pages[top - 1 - (x.z + page - x.w)];
-      at = ((int64_t)id << p.page_shift) + (slot & (p.page_size - 1));
-      pos = p.qpos ? p.qpos[b] + 1 + i : slot;
+  for (int64_t r0 = me; r0 < p.n_rows; r0 += (int64_t)threads * kRows) {
+    int slot[kRows], page[kRows], pos[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t r = r0 + (int64_t)u * threads;
+      slot[u] = pos[u] = -1;
+      page[u] = 0;
+      if (r >= rows) continue;
+      const int b = find<0>(e, p.B, (int)r);
+      const int left = (b + 1 < p.B ? e[b + 1].rows : rows) - (int)r;  // this row and those behind it
+      slot[u] = e[b].len - left;
+      const int x = slot[u] >> p.page_shift;
+      page[u] = x < e[b].held ? p.table[(size_t)b * p.max_pages + x] : taken(e[b].out + x - e[b].held);
+      pos[u] = p.qpos ? p.qpos[b] + 1 + ((int)r - e[b].rows) : slot[u];
     }
-    if (p.slots) p.slots[r] = at;
-    if (p.positions) p.positions[r] = pos;
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t r = r0 + (int64_t)u * threads;
+      if (r >= p.n_rows) continue;
+      if (p.slots) p.slots[r] = slot[u] < 0 ? -1 : ((int64_t)page[u] << p.page_shift) + (slot[u] & (p.page_size - 1));
+      if (p.positions) p.positions[r] = pos[u];
+    }
   }
-  meet();  // lens, held and qpos have been read by all
-  for (int b = me; b < p.B; b += threads) {
-    const Seq s = read_seq(p, b);
+  // What may replace its own input: by the CTA that ends last
+  __syncthreads();
+  if (tid == 0) {
+    s_last = 1;
+    if (gridDim.x > 1) {
+      __threadfence();
+      s_last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
+      __threadfence();
+    }
+  }
+  __syncthreads();
+  if (!s_last) return;
+  for (int b = tid; b < p.B; b += kThreads) {
     const int n = p.n_new[b], q = p.qpos ? p.qpos[b] : 0;
-    p.cu_new[b] = sums[b].x;
-    p.lens_out[b] = s.len;
-    p.held_out[b] = s.need;
+    p.cu_new[b] = e[b].rows;
+    p.lens_out[b] = e[b].len;
+    p.held_out[b] = e[b].need;
     if (p.qpos) p.qpos_out[b] = n < 0 ? -1 : q + n;
   }
-  if (me == 0) {
+  if (tid == 0) {
     p.cu_new[p.B] = rows;
     p.n_free_out[0] = top - outs;
+    if (gridDim.x > 1) *p.ticket = 0u;
   }
 }
 
 }  // namespace
 
 cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t s) {
-  const int seqs = p.B <= kSmemSeqs ? p.B : 0;
-  const int bytes = seqs * (int)sizeof(int4);
-  // A step whose rows a CTA's threads write in a few turns needs no cluster.
-  const bool cluster = (int64_t)p.n_rows + p.B > 4 * kThreads;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cluster ? kCluster : 1);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kCluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster ? 2 : 1;
-  auto* k = cluster ? plan_kernel<true> : plan_kernel<false>;
-  static std::atomic<uint64_t> done[2];
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kSmemSeqs * (int)sizeof(int4), done[cluster ? 1 : 0]);
+  const bool small = p.B <= kSmemSeqs;
+  const int bytes = small ? p.B * (int)sizeof(Entry) : 0;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(plan_kernel), kSmemSeqs * (int)sizeof(Entry), done);
   if (e != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, k, p);
+  // a thread's rows in one turn where there are CTAs for it; one CTA needs no ticket
+  const int64_t turn = (int64_t)kThreads * kRows, want = (p.n_rows + turn - 1) / turn;
+  const int64_t most = small ? kCtas : kFewCtas;
+  const int ctas = (int)(want < 1 ? 1 : want < most ? want : most);
+  return launch_pdl(plan_kernel, dim3(ctas), dim3(kThreads), bytes, s, p);
 }
 
 }  // namespace capattn

@@ -100,7 +100,7 @@ def cache_plan(cache: KVCache, pool: PagePool, n_new, rows: int, out=None, want_
     n_free = _want(pool.n_free, "pool.n_free", (1,), i32, dev)
     held = _want(pool.held, "pool.held", (B,), i32, dev)
     _, _, table, lens = cache._tensors()
-    qpos = cache._positions()[1]
+    qpos = None if cache.pos is None else cache._positions()[1]
     if out is None:
         lens_out, qpos_out, held_out, n_free_out = lens, qpos, held, n_free
     else:
@@ -113,12 +113,14 @@ def cache_plan(cache: KVCache, pool: PagePool, n_new, rows: int, out=None, want_
     plan = cache.plan(cache.Hkv)
     ws, ws_bytes = _workspace(cache, plan, CALL_PLAN)
     cu = torch.empty(B + 1, dtype=i32, device=dev)
-    slots = torch.empty(rows, dtype=torch.int64, device=dev) if want_slots else None
-    positions = torch.empty(rows, dtype=i32, device=dev) if want_slots else None
+    slots = positions = None
+    if want_slots:
+        slots, positions = torch.empty(rows, dtype=torch.int64, device=dev), torch.empty(rows, dtype=i32, device=dev)
     st = _lib_handle.capattn_paged_plan(plan.ref, nn, table, lens, qpos, held, free, n_free, lens_out, qpos_out, held_out,
                                         n_free_out, rows, cu.data_ptr(), slots.data_ptr() if want_slots else None,
                                         positions.data_ptr() if want_slots else None, ws, ws_bytes, s)
-    _ca._check(st, "capattn_paged_plan")
+    if st:
+        _ca._check(st, "capattn_paged_plan")
     return cu, slots, positions
 
 
@@ -142,16 +144,16 @@ def cache_attend(q, cache: KVCache, ap: AttnParams, cu_new, parents=None, temp=N
     shape = (N, Hq, cache.D)
     qs = _rows(q, "q", shape, cache.dtype, dev)
     cu = _want(cu_new, "cu_new", (cache.B + 1,), torch.int32, dev)
-    up = _want(parents, "parents", (N,), torch.int32, dev)
-    tp = _want(temp, "temp", (N,), torch.float32, dev)
+    up = None if parents is None else _want(parents, "parents", (N,), torch.int32, dev)
+    tp = None if temp is None else _want(temp, "temp", (N,), torch.float32, dev)
     k, v, table, lens = cache._tensors()
     pos = qpos = None
     if cache.pos is not None:
         pos, qpos = cache._positions()
     plan = cache.plan(Hq, ap)
     if out is None:
-        o = torch.empty(shape, dtype=q.dtype, device=dev)
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+        o = torch.empty_like(q) if qs == Hq * cache.D and q.is_contiguous() else torch.empty(shape, dtype=q.dtype, device=dev)
+        lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
     else:
         o, lse = out
         _want(o, "o", shape, cache.dtype, dev)
@@ -164,12 +166,15 @@ def cache_attend(q, cache: KVCache, ap: AttnParams, cu_new, parents=None, temp=N
     return o, lse
 
 
-def _accept(cache, cu_new, N, tokens, predicted, parents, path, count, nxt, out, s, where):
+def _accept(cache, cu_new, N, tokens, predicted, parents, path, width, count, nxt, out, s):
+    """The call itself, on addresses; raises what it returns."""
     B, dev, i32 = cache.B, cache.device, torch.int32
     cu = _want(cu_new, "cu_new", (B + 1,), i32, dev)
-    weights = _want(cache.weights, "weights", cache._slots, torch.float32, dev)
+    weights = None if cache.weights is None else _want(cache.weights, "weights", cache._slots, torch.float32, dev)
     k, v, table, lens = cache._tensors()
-    pos, qpos = cache._positions()
+    pos = qpos = None
+    if cache.pos is not None:
+        pos, qpos = cache._positions()
     if out is None:
         lens_out, qpos_out = lens, qpos
     else:
@@ -179,10 +184,10 @@ def _accept(cache, cu_new, N, tokens, predicted, parents, path, count, nxt, out,
         qpos_out = _want(out[1], "qpos_out", (B,), i32, dev)
     plan = cache.plan(cache.Hkv)
     ws, ws_bytes = _workspace(cache, plan, CALL_ACCEPT)
-    st = _lib_handle.capattn_paged_accept(plan.ref, cu, N, tokens, predicted, parents, path.shape[1], path.data_ptr(),
-                                          count.data_ptr(), nxt, k, v, table, lens, weights, pos, qpos, lens_out,
-                                          qpos_out, ws, ws_bytes, s)
-    _ca._check(st, where)
+    st = _lib_handle.capattn_paged_accept(plan.ref, cu, N, tokens, predicted, parents, width, path, count, nxt, k, v, table,
+                                          lens, weights, pos, qpos, lens_out, qpos_out, ws, ws_bytes, s)
+    if st:
+        _ca._check(st, "capattn_paged_accept")
 
 
 def cache_verify(cache: KVCache, cu_new, tokens, predicted, parents, width: int, out=None, stream=None):
@@ -195,23 +200,26 @@ def cache_verify(cache: KVCache, cu_new, tokens, predicted, parents, width: int,
     (lens, qpos) (qpos None without positions).  Returns path [B, width] int32 (-1 behind
     its end), count [B] int32 and the next token [B] int32, predicted behind the last
     accepted one (-1 for a sequence without new tokens)."""
-    s = _raw_stream(cache.device, stream)
+    dev, i32 = cache.device, torch.int32
+    s = _raw_stream(dev, stream)
     if s is None:
-        with _on(cache.device, stream):
+        with _on(dev, stream):
             return cache_verify(cache, cu_new, tokens, predicted, parents, width, out)
     if width < 1:
         raise ValueError(f"width has to be at least 1, got {width}")
-    N, i32 = tokens.shape[0], dict(dtype=torch.int32, device=cache.device)
-    t, m, u = (_want(x, n, (N,), torch.int32, cache.device)
-               for x, n in ((tokens, "tokens"), (predicted, "predicted"), (parents, "parents")))
-    path, both = torch.empty((cache.B, width), **i32), torch.empty((2, -(-cache.B // 4) * 4), **i32)
-    count, nxt = both[0, :cache.B], both[1, :cache.B]
-    if N == 0:  # nothing is drafted (an empty tensor has no address that says so)
+    B, rows = cache.B, tokens.shape[:1]
+    t = _want(tokens, "tokens", rows, i32, dev)
+    m = _want(predicted, "predicted", rows, i32, dev)
+    u = _want(parents, "parents", rows, i32, dev)
+    path = torch.empty((B, width), dtype=i32, device=dev)
+    count, nxt = torch.empty(B, dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev)
+    if rows[0] == 0:  # nothing is drafted (an empty tensor has no address that says so)
         path.fill_(-1)
         count.zero_()
-        _accept(cache, cu_new, 0, None, None, None, path, count, None, out, s, "capattn_paged_accept")
-        return path, count, nxt.fill_(-1)
-    _accept(cache, cu_new, N, t, m, u, path, count, nxt.data_ptr(), out, s, "capattn_paged_accept")
+        nxt.fill_(-1)
+        _accept(cache, cu_new, 0, None, None, None, path.data_ptr(), width, count.data_ptr(), None, out, s)
+    else:
+        _accept(cache, cu_new, rows[0], t, m, u, path.data_ptr(), width, count.data_ptr(), nxt.data_ptr(), out, s)
     return path, count, nxt
 
 
@@ -219,12 +227,13 @@ def cache_accept(cache: KVCache, cu_new, path, count, out=None, stream=None):
     """Accepts a path that the caller chose (by sampling, for instance): path [B, width]
     int32, strictly increasing rows of the sequence's new tokens, of which the first count[b]
     (count [B] int32) stay; the rest as in cache_verify."""
-    s = _raw_stream(cache.device, stream)
+    dev, i32 = cache.device, torch.int32
+    s = _raw_stream(dev, stream)
     if s is None:
-        with _on(cache.device, stream):
+        with _on(dev, stream):
             return cache_accept(cache, cu_new, path, count, out)
     if path.dim() != 2 or path.shape[1] < 1:
         raise ValueError("path is [B, width]")
-    _want(path, "path", (cache.B, path.shape[1]), torch.int32, cache.device)
-    _want(count, "count", (cache.B,), torch.int32, cache.device)
-    _accept(cache, cu_new, 2 ** 31 - 1, None, None, None, path, count, None, out, s, "capattn_paged_accept")
+    width = path.shape[1]
+    at = _want(path, "path", (cache.B, width), i32, dev)
+    _accept(cache, cu_new, 2 ** 31 - 1, None, None, None, at, width, _want(count, "count", (cache.B,), i32, dev), None, out, s)
