@@ -25,7 +25,7 @@
 
 namespace capattn {
 
-constexpr int kTileCost = 1;
+constexpr int kTileCost = 2;
 constexpr int kWholeSteps = 2;
 
 struct SeqShape {

@@ -1,6 +1,6 @@
 """The split of attention over many new tokens, as csrc/paged_sched.cuh computes it."""
 
-TILE_COST, WHOLE_STEPS = 1, 2
+TILE_COST, WHOLE_STEPS = 2, 2
 
 
 def floor_sum(n, m, a, b):

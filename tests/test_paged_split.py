@@ -5,7 +5,7 @@ import random
 
 import pytest
 
-from paged_model import Split, floor_sum
+from paged_model import TILE_COST, Split, floor_sum
 
 
 def test_floor_sum():
@@ -34,7 +34,7 @@ def test_pieces(case):
     sp = Split(*case)
     for s, c in enumerate(sp.count):
         if not sp.whole:
-            assert all(sp.before(s, t + 1) - sp.before(s, t) == sp.steps(s, t) + 1 for t in range(c - 1))
+            assert all(sp.before(s, t + 1) - sp.before(s, t) == sp.steps(s, t) + TILE_COST for t in range(c - 1))
         assert all(sp.steps(s, t) >= 1 for t in range(c))
     seen, slots, parts = {}, set(), {}
     for cta in range(min(case[4], sp.ctas + 1)):
