@@ -115,7 +115,7 @@ capattn_status capattn_paged_attend(const capattn_cache_config* cfg, const void*
   p.parts = (c.G + rows - 1) / rows;
   p.heads = (c.G + p.parts - 1) / p.parts;
   p.tokens = rows / p.heads;
-  p.ctas = cfg->dtype == CAPATTN_BF16 ? kAttendCtas : kAttendSimtCtas;
+  p.ctas = cfg->dtype == CAPATTN_FP32 && c.D == 64 ? kAttendSimtCtas : kAttendCtas;
   p.min_units = 2;
   cudaError_t e = cfg->dtype == CAPATTN_BF16 ? launch_paged_attend_tc(p, stream) : launch_paged_attend_simt(p, stream);
   if (e == cudaSuccess) e = launch_paged_finish(p, cfg->dtype, stream);

@@ -4,10 +4,10 @@
 // running reference m (log2 units):
 //   S = Q K^T, x = log2(e) temp cap(sm_scale S), P = 2^(x - m), l += sum P, O += P V.
 // fp32 stays on the CUDA cores: a TF32 product keeps 11 bits of q and k.  256 threads, 4 x 4
-// scores each (16 products for two vectors of shared memory) and 4 x D / 16 outputs; Q and K
-// lie transposed, so that both products read vectors along rows or keys.
-#include <cuda_bf16.h>
-
+// scores each (rows 4 ty .., keys tx + 16 z: 64 products for eight vectors of shared memory
+// along D, whose padded rows spread over the banks) and 4 x D / 16 outputs.  The next step's
+// keys and values come in by cp.async meanwhile, their pages looked up a step before that
+// (loaded when they were needed, through registers, four small prompts took 45 us).
 #include "cache_math.cuh"
 #include "cap_math.cuh"
 #include "paged_out.cuh"
@@ -21,12 +21,13 @@ constexpr int kThreads = 256;
 
 template <int D>
 struct SimtSmem {
-  float q[D][BM];      // transposed
+  static constexpr int ROW = D + 4;  // a row's stride
+  float q[BM][ROW];
   union {
-    float k[D][TK];    // transposed
-    float p[TK * BM];  // once the scores are there: key-major; a key's rows in blocks of 4, rotated by key / 4
-  };
-  float v[TK][D];
+    float k[TK][ROW];
+    float p[TK * BM];  // once the scores are there: key-major; a key's rows in blocks of 4, rotated by key
+  } k[2];
+  float v[2][TK][D];
   RowMask mask[BM];
   float temp[BM];
   int row[BM];         // of o and lse, from the tile's first; -1: none
@@ -35,25 +36,36 @@ struct SimtSmem {
   ScheduleMem sched;
 };
 
-__device__ __forceinline__ float4 load4(const float* x) { return *reinterpret_cast<const float4*>(x); }
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool live) {  // zeros where !live
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
-template <typename T, int D, int METHOD>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int D, int METHOD>
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
 paged_simt_kernel(PagedParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
   using S = SimtSmem<D>;
   S& s = *reinterpret_cast<S*>(raw);
-  constexpr int OC = D / 16;  // output columns of a thread: 4 tx + 64 x
+  constexpr int OC = D / 16;                   // output columns of a thread: 4 tx + 64 w
+  constexpr int CH = D / 4;                    // 16-byte chunks of a row
+  constexpr int NI = TK * CH / kThreads;       // of K (and of V) a thread copies a step
+  constexpr int kNoRow = INT_MIN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int chunk = threadIdx.x % CH * 4, row0 = threadIdx.x / CH;  // rows row0 + it * kThreads / CH
   pdl_trigger();
   pdl_wait();
   const bool few = p.c.B <= kWarpSeqs;
   if (!few) schedule_by_cta<TK>(p, kThreads, s.sched);
   PieceWalk<TK> walk(p, few ? schedule_by_warp<TK>(p, lane) : s.sched.out, lane);  // (used by warp 0)
   const CacheParams& c = p.c;
-  const T* kc = static_cast<const T*>(c.k);
-  const T* vc = static_cast<const T*>(c.v);
+  const float* kc = static_cast<const float*>(c.k);
+  const float* vc = static_cast<const float*>(c.v);
   bool shared = false;
   for (;;) {
     if (warp == 0) {
@@ -71,6 +83,36 @@ paged_simt_kernel(PagedParams p) {
     const int g = x.part / p.parts, h0 = (x.part - g * p.parts) * p.heads;
     const int heads = min(p.heads, c.G - h0);
     const int head0 = g * c.G + h0;
+    // the pages of this thread's rows of a step, as read
+    const int32_t* table = c.table + (size_t)x.b * c.max_pages;
+    int pages[NI];
+    auto look_up = [&](int step) {
+#pragma unroll
+      for (int it = 0; it < NI; ++it) {
+        const int j = (x.tile0 + step) * TK + row0 + it * (kThreads / CH);
+        pages[it] = step < x.steps && j >= x.first && j < x.len ? table[j >> c.page_shift] : kNoRow;
+      }
+    };
+    auto copy = [&](int step) {
+      const int st = step & 1;
+#pragma unroll
+      for (int it = 0; it < NI; ++it) {
+        const int r = row0 + it * (kThreads / CH), j = (x.tile0 + step) * TK + r;
+        const bool live = pages[it] != kNoRow;
+        int page = pages[it];
+        if (live && (page < 0 || page >= c.num_pages)) {  // flagged, and read as page 0
+          atomicOr(c.status, kStatusBadPageBit);
+          page = 0;
+        }
+        const size_t at = live ? ((((size_t)page * c.Hkv + g) << c.page_shift) + (j & (c.page_size - 1))) * D + chunk : 0;
+        copy16(&s.k[st].k[r][chunk], kc + at, live);
+        copy16(&s.v[st][r][chunk], vc + at, live);
+      }
+      copy_commit();
+    };
+    look_up(0);
+    copy(0);
+    look_up(1);
     if (threadIdx.x < BM) {
       const int r = threadIdx.x, t = r / p.heads;
       const SeqShape sh = {x.row0, x.n, x.len, x.base};
@@ -79,16 +121,13 @@ paged_simt_kernel(PagedParams p) {
       s.temp[r] = (valid && c.temp ? c.temp[x.row0 + x.i0 + t] : 1.f) * kL2E;
       s.row[r] = valid ? t * c.Hq + r - t * p.heads : -1;
     }
-    for (int i = threadIdx.x; i < BM * (D / 4); i += kThreads) {
-      const int r = i % BM, d = i / BM * 4, t = r / p.heads;
+    for (int i = threadIdx.x; i < BM * CH; i += kThreads) {
+      const int r = i / CH, d = i % CH * 4, t = r / p.heads;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       if (t < x.count && r - t * p.heads < heads)
-        a = load4(static_cast<const T*>(c.q) + (size_t)(x.row0 + x.i0 + t) * c.q_stride +
-                  (size_t)(head0 + r - t * p.heads) * D + d);
-      s.q[d][r] = a.x;
-      s.q[d + 1][r] = a.y;
-      s.q[d + 2][r] = a.z;
-      s.q[d + 3][r] = a.w;
+        a = *reinterpret_cast<const float4*>(static_cast<const float*>(c.q) + (size_t)(x.row0 + x.i0 + t) * c.q_stride +
+                                             (size_t)(head0 + r - t * p.heads) * D + d);
+      *reinterpret_cast<float4*>(&s.q[r][d]) = a;
     }
     float m[4], l[4], o[4][OC];
 #pragma unroll
@@ -99,21 +138,14 @@ paged_simt_kernel(PagedParams p) {
       for (int e = 0; e < OC; ++e) o[a][e] = 0.f;
     }
     for (int step = 0; step < x.steps; ++step) {
-      const int j0 = (x.tile0 + step) * TK;
-      __syncthreads();  // the last step's products, the row masks
-      for (int i = threadIdx.x; i < TK * (D / 4); i += kThreads) {
-        const int r = i % TK, d = i / TK * 4, j = j0 + r;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        if (j >= x.first && j < x.len) {
-          const size_t at = cache_row(c, x.b, g, j) * D + d;
-          a = load4(kc + at);
-          b = load4(vc + at);
-        }
-        s.k[d][r] = a.x;
-        s.k[d + 1][r] = a.y;
-        s.k[d + 2][r] = a.z;
-        s.k[d + 3][r] = a.w;
-        *reinterpret_cast<float4*>(&s.v[r][d]) = b;
+      const int j0 = (x.tile0 + step) * TK, st = step & 1;
+      __syncthreads();  // the last step's products (their stage is filled again), the row masks
+      if (step + 1 < x.steps) {
+        copy(step + 1);
+        look_up(step + 2);
+        copy_wait<1>();
+      } else {
+        copy_wait<0>();
       }
       if (threadIdx.x < 2 * BM) {
         const int r = threadIdx.x >> 1, half = threadIdx.x & 1, c0 = j0 + 32 * half;
@@ -121,23 +153,31 @@ paged_simt_kernel(PagedParams p) {
       }
       __syncthreads();
       float acc[4][4] = {};
-#pragma unroll 8
-      for (int d = 0; d < D; ++d) {
-        const float4 a = *reinterpret_cast<const float4*>(&s.q[d][4 * ty]), b = *reinterpret_cast<const float4*>(&s.k[d][4 * tx]);
-        const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) a[y] = *reinterpret_cast<const float4*>(&s.q[4 * ty + y][d]);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) b[z] = *reinterpret_cast<const float4*>(&s.k[st].k[tx + 16 * z][d]);
 #pragma unroll
         for (int y = 0; y < 4; ++y)
 #pragma unroll
-          for (int z = 0; z < 4; ++z) acc[y][z] = fmaf(av[y], bv[z], acc[y][z]);
+          for (int z = 0; z < 4; ++z) {
+            acc[y][z] = fmaf(a[y].x, b[z].x, acc[y][z]);
+            acc[y][z] = fmaf(a[y].y, b[z].y, acc[y][z]);
+            acc[y][z] = fmaf(a[y].z, b[z].z, acc[y][z]);
+            acc[y][z] = fmaf(a[y].w, b[z].w, acc[y][z]);
+          }
       }
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        const uint32_t live = s.live[4 * ty + y][tx >> 3] >> (4 * (tx & 7));
         const float temp = s.temp[4 * ty + y];
         float top = -INFINITY;
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
-          acc[y][z] = (live >> z) & 1u ? any_cap<METHOD>(acc[y][z], c.cap) * temp : -INFINITY;
+          const bool live = (s.live[4 * ty + y][z >> 1] >> (tx + 16 * (z & 1))) & 1u;
+          acc[y][z] = live ? any_cap<METHOD>(acc[y][z], c.cap) * temp : -INFINITY;
           top = fmaxf(top, acc[y][z]);
         }
 #pragma unroll
@@ -157,16 +197,16 @@ paged_simt_kernel(PagedParams p) {
       __syncthreads();  // P takes the place of K
 #pragma unroll
       for (int z = 0; z < 4; ++z)
-        *reinterpret_cast<float4*>(&s.p[(4 * tx + z) * BM + 4 * ((ty + tx) & 15)]) =
+        *reinterpret_cast<float4*>(&s.k[st].p[(tx + 16 * z) * BM + 4 * ((ty + tx) & 15)]) =
             make_float4(acc[0][z], acc[1][z], acc[2][z], acc[3][z]);
       __syncthreads();
 #pragma unroll 4
       for (int j = 0; j < TK; ++j) {
-        const float4 a = *reinterpret_cast<const float4*>(&s.p[j * BM + 4 * ((ty + (j >> 2)) & 15)]);
+        const float4 a = *reinterpret_cast<const float4*>(&s.k[st].p[j * BM + 4 * ((ty + j) & 15)]);
         const float av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int w = 0; w < OC / 4; ++w) {
-          const float4 b = *reinterpret_cast<const float4*>(&s.v[j][64 * w + 4 * tx]);
+          const float4 b = *reinterpret_cast<const float4*>(&s.v[st][j][64 * w + 4 * tx]);
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             o[y][4 * w] = fmaf(av[y], b.x, o[y][4 * w]);
@@ -199,7 +239,7 @@ paged_simt_kernel(PagedParams p) {
         for (int w = 0; w < OC / 4; ++w) {
           const float v[4] = {none ? 0.f : o[y][4 * w] * inv, none ? 0.f : o[y][4 * w + 1] * inv,
                               none ? 0.f : o[y][4 * w + 2] * inv, none ? 0.f : o[y][4 * w + 3] * inv};
-          store_values(static_cast<T*>(c.o) + row * D + 64 * w + 4 * tx, v);
+          store_values(static_cast<float*>(c.o) + row * D + 64 * w + 4 * tx, v);
         }
         if (tx == 0) {
           if (bad) ask_redo(p);
@@ -226,7 +266,7 @@ paged_simt_kernel(PagedParams p) {
 
 template <int D, int METHOD>
 cudaError_t launch(const PagedParams& p, cudaStream_t s) {
-  auto* k = paged_simt_kernel<float, D, METHOD>;
+  auto* k = paged_simt_kernel<D, METHOD>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), sizeof(SimtSmem<D>), done);
   if (e != cudaSuccess) return e;

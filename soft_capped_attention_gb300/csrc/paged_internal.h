@@ -50,7 +50,7 @@ struct Piece {
 // Slots of partial results: two a CTA.
 constexpr int kAttendCtas = 152;       // bf16: one CTA an SM, tiles of 128 rows
 constexpr int kAttendRows = 128;
-constexpr int kAttendSimtCtas = 304;   // fp32: two an SM, tiles of 64 rows
+constexpr int kAttendSimtCtas = 304;   // fp32: two an SM at D = 64 (one at D = 128), tiles of 64 rows
 constexpr int kAttendSimtRows = 64;
 constexpr int kAttendPartRows = 2 * kAttendCtas * kAttendRows;
 static_assert(2 * kAttendSimtCtas * kAttendSimtRows <= kAttendPartRows, "partial results");
