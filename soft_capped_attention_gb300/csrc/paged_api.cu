@@ -99,8 +99,9 @@ capattn_status capattn_paged_attend(const capattn_cache_config* cfg, const void*
   c.cap = exact_cap_of(cfg->cap_method, cfg->cap, cfg->alpha, cfg->beta, cfg->sm_scale, &c.method);
   c.q = q; c.q_stride = q_row_stride; c.k = const_cast<void*>(k_cache); c.v = const_cast<void*>(v_cache);
   c.table = table; c.lens = lens; c.temp = temp; c.o = o; c.lse = lse;
-  // positions matter to a window only
+  // positions matter to a window only, and without them one that every sequence fits into is none
   c.pos = cfg->window_len > 0 ? const_cast<int32_t*>(pos) : nullptr;
+  if (!pos && c.window_len > c.max_len) c.window_len = 0;
   c.qpos = qpos;
   p.cu_new = cu_new; p.n_rows = n_rows; p.parents = parents;
   const PagedWorkspace w = layout(*cfg, CAPATTN_PAGED_ATTEND);

@@ -192,22 +192,29 @@ __device__ __forceinline__ float p_columns(const uint32_t (&v)[32], uint32_t (&p
   return a + b;
 }
 
-// The columns whose scores leave the row's polynomial: out of line, so that the loop that runs
-// without it stays small.
-template <int METHOD>
-__device__ __noinline__ float p_far(const uint32_t (&v)[32], uint32_t (&pk)[16], float mul, float add, uint32_t live,
-                                    float top, const ExactCap& k) {
-  const RowPoly<METHOD> none{};
-  if constexpr (METHOD == CAPATTN_CAP_TANH) {
-    if (__all_sync(0xFFFFFFFFu, top <= k.xmax)) return p_columns<METHOD, kWide, true>(v, pk, none, mul, add, live, k);
-  }
-  return p_columns<METHOD, kOneByOne, true>(v, pk, none, mul, add, live, k);
-}
-
 template <int METHOD>
 __device__ __forceinline__ bool is_near(float top, const ExactCap& k) {
   if constexpr (METHOD == CAPATTN_CAP_NONE) return true;
   return __all_sync(0xFFFFFFFFu, top <= (METHOD == CAPATTN_CAP_TANH ? k.near.xmax : k.xmax));
+}
+
+// The columns whose scores leave the row's polynomial: out of line, so that the loop that runs
+// without it stays small.  The scores of slots without a token are of whatever lies there, so
+// the choice is made once more from the live ones: it would change a result's last bit.
+template <int METHOD>
+__device__ __noinline__ float p_far(const uint32_t (&v)[32], uint32_t (&pk)[16], float mul, float add, uint32_t live,
+                                    const ExactCap& k) {
+  RowPoly<METHOD> poly;
+  poly.set(k, mul);
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if ((live >> e) & 1u) top = fmaxf(top, fabsf(__uint_as_float(v[e])));
+  if (is_near<METHOD>(top, k)) return p_columns<METHOD, kNear, true>(v, pk, poly, mul, add, live, k);
+  if constexpr (METHOD == CAPATTN_CAP_TANH) {
+    if (__all_sync(0xFFFFFFFFu, top <= k.xmax)) return p_columns<METHOD, kWide, true>(v, pk, poly, mul, add, live, k);
+  }
+  return p_columns<METHOD, kOneByOne, true>(v, pk, poly, mul, add, live, k);
 }
 
 // The largest x of a row: |cap| times its factor's size.
@@ -706,7 +713,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
                 uint32_t scores[32], packed[16];  // (copies, which alone have an address)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) scores[e] = v[e];
-                lsum += p_far<METHOD>(scores, packed, mul, -m, live, top, c.cap);
+                lsum += p_far<METHOD>(scores, packed, mul, -m, valid ? live : 0u, c.cap);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) pk[e] = packed[e];
               }

@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from kv_cache_utils import Pool
+from kv_cache_utils import CAPS, Pool, method_of
 from paged_ref import Attend, check
 from soft_capped_attention_gb300 import capattn as ca
 from test_gpu_kv_cache import BF16, FP32, params
@@ -155,6 +155,81 @@ def test_large_scores(dtype, cap, scale, tree):
     pool.k[:, :, :, 0] = pool.k[:, :, :, 0].abs() + 1  # (NaN where no token is stays NaN)
     got, want = run(pool, [150, 40], 4, params(cap, 128), dtype, tree, True, seed=9, scale=scale)
     check(got, want, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("cap", ["none", "tanh", "alsc30", "soft_sign"])
+def test_temperatures_of_any_sign_and_size(dtype, cap):
+    """0 (the plain mean), negative ones, tiny and large ones side by side in a tile."""
+    pool = Pool([700, 40], 2, 128, 16, dtype, 3)
+    g = torch.Generator().manual_seed(4)
+    q = torch.randn(190, 4, 128, generator=g).to(dtype)
+    temp = torch.tensor([0.0, -1.0, 1e-3, 1.0, -0.3, 30.0, -20.0, 1e-30])[torch.randint(0, 8, (190,), generator=g)]
+    ap, cu = params(cap, 128), [0, 150, 190]
+    cache = pool.cuda()
+    got = paged().cache_attend(q.cuda(), cache, ap, i32(cu), temp=temp.cuda())
+    check(got, Attend(q, pool.k, pool.v, pool.table, pool.lens, cu, ap, temp=temp), dtype)
+    assert cache.status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 1 << 30, 900])
+@pytest.mark.parametrize("pos", [False, True], ids=["slots", "pos"])
+def test_windows_wider_than_the_cache(dtype, window, pos):
+    pool = Pool([700, 40], 2, 64, 16, dtype, 3)
+    for tree in (False, True):
+        got, want = run(pool, [150, 40], 4, params("tanh15", 64, window), dtype, tree, pos=pos, seed=4)
+        check(got, want, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("scale", [0.0, -0.1])
+@pytest.mark.parametrize("cap", ["none", "tanh50", "alsc30", "soft_sign"])
+def test_scales_of_any_sign(dtype, scale, cap):
+    pool = Pool([300, 40], 2, 128, 16, dtype, 3)
+    c, a, b = CAPS[cap]
+    ap = ca.AttnParams(sm_scale=scale, cap_method=method_of(cap), cap=c, alpha=a, beta=b, causal=True)
+    got, want = run(pool, [50, 40], 4, ap, dtype, False, True, seed=4)
+    check(got, want, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_a_long_chain_of_drafts(dtype):
+    """A tree that is one chain is a prompt, however long."""
+    pool = Pool([700, 650], 2, 64, 16, dtype, 9)
+    new = [600, 650]
+    q = torch.randn(sum(new), 2, 64, generator=pool.gen).to(dtype).cuda()
+    chain = torch.cat([torch.arange(-1, n - 1, dtype=torch.int32) for n in new]).cuda()
+    cache, ap = pool.cuda(), params("tanh", 64, 77)
+    one = paged().cache_attend(q, cache, ap, i32(sums(new)))
+    two = paged().cache_attend(q, cache, ap, i32(sums(new)), parents=chain)
+    want = Attend(q.cpu(), pool.k, pool.v, pool.table, pool.lens, sums(new), ap)
+    check(one, want, dtype)
+    check(two, want, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", ["none", "tanh", "alsc", "soft_sign"])
+def test_what_lies_in_free_slots_changes_no_bit(dtype, D, cap):
+    """Slots behind a sequence's last token, of its page and of pages it has not, hold anything."""
+    pool = Pool([300, 40, 7], 2, D, 64, dtype, 3)
+    q = torch.randn(77, 4, D, generator=torch.Generator().manual_seed(6)).to(dtype).cuda()
+    used = torch.zeros(pool.k.shape[0], pool.page, dtype=torch.bool)
+    for b, L in enumerate(pool.lens):
+        for t in range(L):
+            used[pool.table[b][t // pool.page], t % pool.page] = True
+    cu, up, kept = i32([0, 30, 70, 77]), a_tree([30, 40, 7], torch.Generator().manual_seed(1)).cuda(), []
+    for junk in (0.0, 5.0, 1e4, -3e38, math.inf, math.nan):
+        free = ~used[:, None, :, None].expand_as(pool.k)
+        pool.k[free] = torch.tensor(junk).to(dtype)
+        pool.v[free] = torch.tensor(-junk).to(dtype)
+        cache = pool.cuda()
+        for parents in (None, up):
+            kept.append(paged().cache_attend(q, cache, params(cap, D), cu, parents=parents))
+    for first in range(2):
+        for o, lse in kept[first::2]:
+            assert torch.equal(o, kept[first][0]) and torch.equal(lse, kept[first][1])
 
 
 def test_a_first_tile_far_below_the_rest():

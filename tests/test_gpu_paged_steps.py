@@ -261,3 +261,56 @@ def test_steps_together(dtype, window):
             step([-1, 1, -1, 1], False)
             step([40, 1, 17, 0], False)
     assert cache.status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_a_captured_step(dtype):
+    """Plan, append, attend, verify in one graph: replays give what the same calls give one by one."""
+    B, Hq, Hkv, D, page, max_pages, pages, rows, width = 3, 4, 2, 64, 16, 12, 40, 64, 4
+    g = torch.Generator().manual_seed(8)
+
+    def state():
+        k = torch.zeros(pages, Hkv, page, D, dtype=dtype, device="cuda")
+        cache = kv().KVCache(k, k.clone(), i32([[-1] * max_pages] * B), i32([0] * B), weights=torch.ones(B, Hkv, max_pages * page, device="cuda"))
+        return cache, paged().PagePool.full(cache)
+
+    ap = params("alsc", D)
+    inputs = [[torch.randn(rows, h, D, generator=g).to(dtype).cuda() for h in (Hq, Hkv, Hkv)] +
+              [torch.randint(0, 2, (rows,), generator=g, dtype=torch.int32).cuda() for _ in range(2)] for _ in range(5)]
+    news = [[20, 1, 30], [9, 20, 30], [-1, 0, 7], [33, 5, 1], [1, 1, 1]]
+    trees = [a_tree([max(n, 0) for n in new], g) for new in news]
+    trees = [torch.cat([t, torch.full((rows - len(t),), -1, dtype=torch.int32)]).cuda() for t in trees]
+
+    def step(cache, pool, q, k, v, tokens, says, n_new, up):
+        cu, _, _ = paged().cache_plan(cache, pool, n_new, rows)
+        kv().cache_append(cache, k, v, cu_new=cu)
+        o, lse = paged().cache_attend(q, cache, ap, cu, parents=up, out=(out_o, out_lse))
+        return paged().cache_verify(cache, cu, tokens, says, up, width)
+
+    out_o, out_lse = torch.zeros(rows, Hq, D, dtype=dtype, device="cuda"), torch.zeros(rows, Hq, device="cuda")
+    held = [x.clone() for x in inputs[0]] + [i32(news[0]), trees[0].clone()]
+    one, two = state(), state()
+    warm = state()  # (its workspace is not the others': make theirs before the capture)
+    for x in (two, warm):
+        step(*x, *held)
+    for a, b in zip((two[0].k, two[0].v, two[0].table, two[0].lens, two[0].weights, two[1].free, two[1].n_free, two[1].held),
+                    (one[0].k, one[0].v, one[0].table, one[0].lens, one[0].weights, one[1].free, one[1].n_free, one[1].held)):
+        a.copy_(b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(*two, *held)
+    for x, new, up in zip(inputs, news, trees):
+        out_o.zero_()
+        out_lse.zero_()
+        want = step(*one, *x, i32(new), up)
+        kept = [out_o.clone(), out_lse.clone()]
+        out_o.zero_()
+        out_lse.zero_()
+        for a, b in zip(held, x + [i32(new), up]):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out_o, kept[0]) and torch.equal(out_lse, kept[1])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(one[0].k, two[0].k) and torch.equal(one[0].lens, two[0].lens) and torch.equal(one[1].held, two[1].held)
+    assert one[0].status() == (0, 0) and two[0].status() == (0, 0)
