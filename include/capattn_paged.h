@@ -20,9 +20,10 @@
  * a later plan gives the pages back that the rejected tokens do not need.
  *
  * Status bits that these calls add: 512 = a parent that is not an earlier row of its
- * sequence (nor -1); 1024 = a plan without the pages or rows that it needs, or with a
- * bad stack (nothing was changed); 2048 = a path that does not increase within the
- * sequence's rows, or a bad count.  Bits 32, 64 and 128 as in capattn_cache.h.
+ * sequence (nor -1), or a tree of more than CAPATTN_PAGED_MAX_TREE tokens (its rows stay
+ * as they were); 1024 = a plan without the pages or rows that it needs, or with a bad
+ * stack (nothing was changed); 2048 = a path that does not increase within the sequence's
+ * rows, or a bad count.  Bits 32, 64 and 128 as in capattn_cache.h.
  */
 #ifndef CAPATTN_PAGED_H_
 #define CAPATTN_PAGED_H_
@@ -32,6 +33,12 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/*
+ * Most new tokens of a sequence that come as a tree: a row finds its ancestors by walking up
+ * from itself, which a chain of all its tokens makes a walk of that many steps per 32 slots.
+ */
+#define CAPATTN_PAGED_MAX_TREE 8192
 
 enum { CAPATTN_PAGED_ATTEND = 0, CAPATTN_PAGED_PLAN = 1, CAPATTN_PAGED_ACCEPT = 2 };
 
@@ -56,9 +63,9 @@ size_t capattn_paged_workspace_bytes(const capattn_cache_config* cfg, int call);
  * a new token's position is that of the first new slot plus its depth in the tree.
  * A row without live slots gives o = 0, lse = -inf.
  * q: n_rows rows of [Hq, D], row r at r * q_row_stride elements; o [n_rows, Hq, D];
- * lse [n_rows, Hq] float32; temp [n_rows] float32, nullable (1).  What a slot holds
- * that is not live for a row (NaN, infinities) does not reach that row.  The result
- * does not depend on scheduling: same inputs, same bits.
+ * lse [n_rows, Hq] float32; temp [n_rows] float32, nullable (1); o must not overlap q.
+ * What a slot holds that is not live for a row (NaN, infinities) does not reach that row.
+ * The result does not depend on scheduling: same inputs, same bits.
  */
 capattn_status capattn_paged_attend(const capattn_cache_config* cfg, const void* q, int64_t q_row_stride,
                                     int32_t n_rows, const int32_t* cu_new, const int32_t* parents,

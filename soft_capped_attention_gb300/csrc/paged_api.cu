@@ -90,6 +90,12 @@ capattn_status capattn_paged_attend(const capattn_cache_config* cfg, const void*
   if (!all_aligned({q, cu_new, parents, k_cache, v_cache, table, lens, temp, pos, qpos, o, lse}))
     return CAPATTN_ERR_INVALID_ARG;
   if (n_rows == 0) return CAPATTN_OK;
+  {  // a row may be formed from q once more when o has been written
+    const uintptr_t size = cfg->dtype == CAPATTN_BF16 ? 2 : 4, row = (uintptr_t)cfg->Hq * cfg->D * size;
+    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(o);
+    const uintptr_t q1 = q0 + (uintptr_t)(n_rows - 1) * (uintptr_t)q_row_stride * size + row;
+    if (o0 < q1 && q0 < o0 + (uintptr_t)n_rows * row) return CAPATTN_ERR_INVALID_ARG;
+  }
   PagedParams p;
   memset(&p, 0, sizeof(p));
   p.c = shapes_of(*cfg, workspace);

@@ -43,6 +43,7 @@ __device__ __forceinline__ SeqShape seq_shape(const PagedParams& p, int b) {
   if (s.row0 < 0 || end < s.row0 || end > p.n_rows) bad |= kStatusBadNewRowsBit;
   s.n = bad ? 0 : end - s.row0;
   if (!bad && s.n > s.len) bad |= kStatusBadNewRowsBit;
+  if (p.parents && s.n > CAPATTN_PAGED_MAX_TREE) bad |= kStatusBadParentBit;
   if (bad) {
     atomicOr(p.c.status, bad);
     s.n = 0;

@@ -131,8 +131,8 @@ def cache_attend(q, cache: KVCache, ap: AttnParams, cu_new, parents=None, temp=N
     Row i sees the slots up to its own, or with parents [N] int32 (a row's index within the
     sequence that it continues, less than its own; -1: none) the slots before the new
     tokens, itself and its ancestors; ap's window goes by positions, a drafted token's by
-    its depth.  temp [N] fp32 optional.  Returns (o [N, Hq, D], lse [N, Hq]); out:
-    preallocated (o, lse), of which rows that belong to no sequence are left as they are.
+    its depth.  A tree has at most 8192 tokens.  temp [N] fp32 optional.  Returns (o [N, Hq, D], lse [N, Hq]); out:
+    preallocated (o, lse; o apart from q), of which rows that belong to no sequence are left as they are.
     ap's causal and z_loss_weight play no part."""
     s = _raw_stream(cache.device, stream)
     if s is None:
@@ -207,7 +207,9 @@ def cache_verify(cache: KVCache, cu_new, tokens, predicted, parents, width: int,
             return cache_verify(cache, cu_new, tokens, predicted, parents, width, out)
     if width < 1:
         raise ValueError(f"width has to be at least 1, got {width}")
-    B, rows = cache.B, tokens.shape[:1]
+    B, rows = cache.B, tuple(tokens.shape)
+    if len(rows) != 1:
+        raise ValueError(f"tokens is [N], got {rows}")
     t = _want(tokens, "tokens", rows, i32, dev)
     m = _want(predicted, "predicted", rows, i32, dev)
     u = _want(parents, "parents", rows, i32, dev)

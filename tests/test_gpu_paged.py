@@ -208,6 +208,42 @@ def test_a_long_chain_of_drafts(dtype):
     check(two, want, dtype)
 
 
+@pytest.mark.parametrize("dtype,step", [(BF16, 2.0 ** -8), (FP32, 2.0 ** -20)], ids=["bf16", "fp32"])
+def test_the_longest_tree(dtype, step):
+    """8192 tokens, a chain, which is a prompt: outputs within max |v| times half a step of P and half
+    of o for either call, fp32's sums of 8192 terms within the usual few steps; a longer one is
+    flagged and gives nothing."""
+    n = 8192
+    pool = Pool([n + 1], 1, 64, 16, dtype, 9)
+    q = torch.randn(n + 1, 1, 64, generator=pool.gen).to(dtype).cuda()
+    chain = torch.arange(-1, n, dtype=torch.int32).cuda()
+    cache, ap = pool.cuda(), params("tanh", 64)
+    one = paged().cache_attend(q[:n], cache, ap, i32([0, n]))
+    two = paged().cache_attend(q[:n], cache, ap, i32([0, n]), parents=chain[:n])
+    assert (one[0].double() - two[0].double()).abs().max() <= 4 * step * pool.v.double().nan_to_num(0).abs().max()
+    assert (one[1] - two[1]).abs().max() <= 2 ** -18
+    assert cache.status() == (0, 0)
+    out = torch.full_like(q, 3), torch.full_like(q[:, :, 0], 3, dtype=torch.float32)
+    paged().cache_attend(q, cache, ap, i32([0, n + 1]), parents=chain, out=out)
+    assert all((x == 3).all() for x in out) and cache.status() == (6, 512)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_two_caches_on_two_streams(dtype):
+    """Calls at once, each cache with a workspace of its own."""
+    pools = [Pool([900, 40, 333], 2, 128, 16, dtype, s) for s in (1, 2)]
+    caches, streams = [p.cuda() for p in pools], [torch.cuda.Stream() for _ in pools]
+    q = torch.randn(300, 8, 128, generator=pools[0].gen).to(dtype).cuda()
+    cu, ap = i32([0, 160, 190, 300]), params("alsc30", 128)
+    want = [paged().cache_attend(q, c, ap, cu) for c in caches]
+    torch.cuda.synchronize()
+    got = [[paged().cache_attend(q, c, ap, cu, stream=s) for c, s in zip(caches, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for row in got:
+        for x, y in zip(row, want):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("cap", ["none", "tanh", "alsc", "soft_sign"])

@@ -187,6 +187,56 @@ def test_verify_without_rows():
     assert cache.lens.tolist() == [20, 30] and cache.status() == (0, 0)
 
 
+@pytest.mark.parametrize("shape", [(), (5, 1)], ids=str)
+def test_tokens_of_another_shape_are_refused(shape):
+    cache = Pool([20], 2, 64, 16, BF16, 3).cuda()
+    x = torch.zeros(shape, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="tokens"):
+        paged().cache_verify(cache, i32([0, 0]), x, x, x, 3)
+
+
+@pytest.mark.parametrize("what", ["plan", "longer_plan", "verify", "accept"])
+def test_steps_on_a_given_stream(what):
+    """What the call reads arrives on that stream, late.  (The longer plan needs slots 112 .. 119,
+    which the table has no place for.)"""
+    from test_gpu_kv_cache_streams import late
+    side = torch.cuda.Stream()
+
+    def a_call(stream, work):
+        cache = Pool([100, 50], 2, 64, 16, BF16, 3).cuda()
+        pool = paged().PagePool(torch.arange(cache.num_pages, dtype=torch.int32, device="cuda"), i32([3]), i32([7, 4]))
+        if "plan" in what:
+            given = [i32([12 if what == "plan" else 20, -1])]
+        elif what == "verify":
+            given = [i32([0, 30, 50])] + [x.cuda() for x in (*a_walk([50], None, torch.Generator().manual_seed(3), vocab=2),
+                                                              a_tree([30, 20], torch.Generator().manual_seed(4)))]
+        else:
+            given = [i32([0, 30, 50]), i32([[0, 4, 9], [3, 19, -1]]), i32([3, 2])]
+        late_ones = [torch.zeros_like(x) for x in given]
+        torch.cuda.synchronize()
+        work(list(zip(late_ones, given)))
+        if "plan" in what:
+            got = paged().cache_plan(cache, pool, late_ones[0], 40, stream=stream)
+        elif what == "verify":
+            got = paged().cache_verify(cache, *late_ones, 4, stream=stream)
+        else:
+            paged().cache_accept(cache, *late_ones, stream=stream)
+            got = ()
+        if stream is not None:
+            stream.synchronize()
+        return [*got, cache.k, cache.v, cache.lens, cache.table, pool.held, pool.n_free, pool.free], cache.status(stream=stream)
+
+    def now(pairs):
+        for a, b in pairs:
+            a.copy_(b)
+
+    want, status = a_call(None, now)
+    got, status2 = a_call(side, lambda pairs: late(side, pairs))
+    assert status == status2 == ((6, 1024) if what == "longer_plan" else (0, 0))
+    assert all(torch.equal(a.nan_to_num(7.0) if a.is_floating_point() else a, b.nan_to_num(7.0) if b.is_floating_point() else b)
+               for a, b in zip(got, want))
+
+
 class Dense:
     """A sequence kept as plain rows, for what a whole run has to give."""
 

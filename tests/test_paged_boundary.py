@@ -69,6 +69,14 @@ def test_attend_refusals(lib, kw, status):
     assert lib.capattn_paged_attend(*args(ATTEND, kw)) == status
 
 
+@pytest.mark.parametrize("shift", [0, 16, 4 * 512 * 2 + 511 * 2 // 16 * 16, -(5 * 512 * 2 - 16)])
+def test_outputs_over_the_queries_are_refused(lib, shift):
+    """512 elements a row (bf16), five rows."""
+    assert cfg().Hq * cfg().D == 512
+    at = (P if isinstance(P, int) else P.value) + (1 << 20)
+    assert lib.capattn_paged_attend(*args(ATTEND, dict(q=at, o=at + shift))) == 1
+
+
 PLAN = dict(cfg=cfg(), n_new=P, table=P, lens=P, qpos=None, held=P, free=P, n_free=P, lens_out=P, qpos_out=None, held_out=P,
             n_free_out=P, rows=5, cu=P, slots=P, positions=P, ws=P, wb=WS)
 
