@@ -5,9 +5,15 @@
 //   S = Q K^T, x = log2(e) temp cap(sm_scale S), P = 2^(x - m), l += sum P, O += P V.
 // fp32 stays on the CUDA cores: a TF32 product keeps 11 bits of q and k.  256 threads, 4 x 4
 // scores each (rows 4 ty .., keys tx + 16 z: 64 products for eight vectors of shared memory
-// along D, whose padded rows spread over the banks) and 4 x D / 16 outputs.  The next step's
-// keys and values come in by cp.async meanwhile, their pages looked up a step before that
-// (loaded when they were needed, through registers, four small prompts took 45 us).
+// along D, whose padded rows spread over the banks) and 4 x D / 16 outputs, all in pairs of
+// fp32 products: of the even and odd columns of a score, of two rows' outputs.  The next
+// step's keys and values come in by cp.async meanwhile, their pages looked up a step before
+// that.  Bound by the products' and shared memory's latencies (FMA pipe 36 %, shared memory's
+// 43 %, issue slots 55 % of the time; 16 warps an SM at D = 64, eight at 128), and at small
+// sizes by the first loads and the finish.  Four prompts of up to 1500 tokens, 16 heads x 64:
+// 271 us (305 with products one at a time, 348 with loads through registers); x 128: 494
+// (538, 647); four prompts of 61 to 333 tokens behind up to 700 others, 4 / 2 heads x 64: 39
+// (42.5, 45).  Loops over D unrolled by 4, 8, 16: 289, 282, 271 and 524, 510, 506.
 #include "cache_math.cuh"
 #include "cap_math.cuh"
 #include "paged_out.cuh"
@@ -129,14 +135,15 @@ paged_simt_kernel(PagedParams p) {
                                              (size_t)(head0 + r - t * p.heads) * D + d);
       *reinterpret_cast<float4*>(&s.q[r][d]) = a;
     }
-    float m[4], l[4], o[4][OC];
+    float m[4], l[4];
+    F2 o2[2][OC];  // rows 4 ty + 2 x and the next
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       m[a] = -INFINITY;
       l[a] = 0.f;
-#pragma unroll
-      for (int e = 0; e < OC; ++e) o[a][e] = 0.f;
     }
+#pragma unroll
+    for (int e = 0; e < OC; ++e) o2[0][e] = o2[1][e] = f2(0.f, 0.f);
     for (int step = 0; step < x.steps; ++step) {
       const int j0 = (x.tile0 + step) * TK, st = step & 1;
       __syncthreads();  // the last step's products (their stage is filled again), the row masks
@@ -152,8 +159,12 @@ paged_simt_kernel(PagedParams p) {
         s.live[r][half] = all_live(s.mask[r], c0, 32) ? 0xFFFFFFFFu : live_slots(p, s.mask[r], c0);
       }
       __syncthreads();
-      float acc[4][4] = {};
-#pragma unroll 4
+      F2 sums[4][4];  // over the even and the odd columns
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+#pragma unroll
+        for (int z = 0; z < 4; ++z) sums[y][z] = f2(0.f, 0.f);
+#pragma unroll 16
       for (int d = 0; d < D; d += 4) {
         float4 a[4], b[4];
 #pragma unroll
@@ -164,12 +175,20 @@ paged_simt_kernel(PagedParams p) {
         for (int y = 0; y < 4; ++y)
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
-            acc[y][z] = fmaf(a[y].x, b[z].x, acc[y][z]);
-            acc[y][z] = fmaf(a[y].y, b[z].y, acc[y][z]);
-            acc[y][z] = fmaf(a[y].z, b[z].z, acc[y][z]);
-            acc[y][z] = fmaf(a[y].w, b[z].w, acc[y][z]);
+            sums[y][z] = f2_fma(f2(a[y].x, a[y].y), f2(b[z].x, b[z].y), sums[y][z]);
+            sums[y][z] = f2_fma(f2(a[y].z, a[y].w), f2(b[z].z, b[z].w), sums[y][z]);
           }
       }
+      float acc[4][4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          float even, odd;
+          f2_split(sums[y][z], even, odd);
+          acc[y][z] = even + odd;
+        }
+      float scales[4];
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const float temp = s.temp[4 * ty + y];
@@ -186,38 +205,47 @@ paged_simt_kernel(PagedParams p) {
         const float scale = top == -INFINITY ? 1.f : ex2_approx(m[y] - top), ref = top == -INFINITY ? 0.f : top;
         m[y] = top;
         l[y] *= scale;
-#pragma unroll
-        for (int e = 0; e < OC; ++e) o[y][e] *= scale;
+        scales[y] = scale;
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           acc[y][z] = ex2_approx(acc[y][z] - ref);
           l[y] += acc[y][z];
         }
       }
+#pragma unroll
+      for (int x2 = 0; x2 < 2; ++x2)
+#pragma unroll
+        for (int e = 0; e < OC; ++e) o2[x2][e] = f2_mul(o2[x2][e], f2(scales[2 * x2], scales[2 * x2 + 1]));
       __syncthreads();  // P takes the place of K
 #pragma unroll
       for (int z = 0; z < 4; ++z)
         *reinterpret_cast<float4*>(&s.k[st].p[(tx + 16 * z) * BM + 4 * ((ty + tx) & 15)]) =
             make_float4(acc[0][z], acc[1][z], acc[2][z], acc[3][z]);
       __syncthreads();
-#pragma unroll 4
+#pragma unroll (D / 16)
       for (int j = 0; j < TK; ++j) {
         const float4 a = *reinterpret_cast<const float4*>(&s.k[st].p[j * BM + 4 * ((ty + j) & 15)]);
-        const float av[4] = {a.x, a.y, a.z, a.w};
+        const F2 a01 = f2(a.x, a.y), a23 = f2(a.z, a.w);
 #pragma unroll
         for (int w = 0; w < OC / 4; ++w) {
           const float4 b = *reinterpret_cast<const float4*>(&s.v[st][j][64 * w + 4 * tx]);
+          const float bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            o[y][4 * w] = fmaf(av[y], b.x, o[y][4 * w]);
-            o[y][4 * w + 1] = fmaf(av[y], b.y, o[y][4 * w + 1]);
-            o[y][4 * w + 2] = fmaf(av[y], b.z, o[y][4 * w + 2]);
-            o[y][4 * w + 3] = fmaf(av[y], b.w, o[y][4 * w + 3]);
+          for (int e = 0; e < 4; ++e) {
+            const F2 b2 = f2(bv[e], bv[e]);
+            o2[0][4 * w + e] = f2_fma(a01, b2, o2[0][4 * w + e]);
+            o2[1][4 * w + e] = f2_fma(a23, b2, o2[1][4 * w + e]);
           }
         }
       }
     }
     // ---------------------------------------------------------- end of a piece
+    float o[4][OC];
+#pragma unroll
+    for (int e = 0; e < OC; ++e) {
+      f2_split(o2[0][e], o[0][e], o[1][e]);
+      f2_split(o2[1][e], o[2][e], o[3][e]);
+    }
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
       const int r = 4 * ty + y;
