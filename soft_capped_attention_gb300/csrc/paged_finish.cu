@@ -150,6 +150,7 @@ paged_finish_kernel(PagedParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   pdl_wait();
+  const bool redo_asked = *reinterpret_cast<volatile uint32_t*>(p.redo) != 0u;  // (by the attention kernel, not here)
   // The blocks of work of each record, two records a thread, and their sums.
   auto blocks_of = [&](int i) -> int {
     if (i >= p.ctas || p.records[i].steps < 0) return 0;
@@ -235,7 +236,7 @@ paged_finish_kernel(PagedParams p) {
   }
   // Rows of whole tiles: the flag says whether there are any (a shared tile's that come to NaN
   // meanwhile may be met here too, and give the same again).
-  if (*reinterpret_cast<volatile uint32_t*>(p.redo) == 0u) return;
+  if (!redo_asked) return;
   const int64_t lses = (int64_t)p.n_rows * c.Hq, warps = (int64_t)gridDim.x * (kThreads / 32);
   for (int64_t at0 = ((int64_t)blockIdx.x * (kThreads / 32) + warp) * 32; at0 < lses; at0 += warps * 32) {
     const int64_t mine = at0 + lane;

@@ -7,8 +7,11 @@
 // waits for another, and the result does not depend on scheduling.  The CTAs share out
 // returning pages, outgoing pages and new rows, each finding its sequence by binary search.
 // Lengths, held pages and the stack's height may be updated in place: the CTA that ends last
-// writes them.  Bound by latency (B = 512, 66,000 rows of slots: the first form, a cluster of
-// eight CTAs that met twice, took 14.8 us).
+// writes them.  Bound by latency: a launch, the lengths, two scans, the searches in shared
+// memory, the pages, the stores.  64 sequences of one new token: 4.8 us; 512 sequences and
+// 66,000 rows: 7.3 (four rows a thread in flight at once 10.8, a cluster of eight CTAs that
+// met twice 14.8); 400,000 rows: 10.9; 6000 sequences: 17.6 (81 with their sums in memory,
+// where those of more than 8192 have to be).  256 threads instead of 512: 4.4, 7.4, but 144.
 #include "paged_internal.h"
 #include "tc_common.cuh"
 
@@ -16,9 +19,8 @@ namespace capattn {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kRows = 4;           // rows that a thread has in flight
 constexpr int kCtas = 152;
-constexpr int kSmemSeqs = 4096;    // sequences whose sums fit shared memory
+constexpr int kSmemSeqs = 8192;    // sequences whose sums fit shared memory
 constexpr int kFewCtas = kPlanCopies;  // CTAs for more than those: their sums lie in the workspace
 
 struct Seq {
@@ -141,28 +143,19 @@ plan_kernel(PlanParams p) {
     const int b = find<2>(e, p.B, (int)k);
     p.table[(size_t)b * p.max_pages + e[b].held + ((int)k - e[b].out)] = taken((int)k);
   }
-  for (int64_t r0 = me; r0 < p.n_rows; r0 += (int64_t)threads * kRows) {
-    int slot[kRows], page[kRows], pos[kRows];
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int64_t r = r0 + (int64_t)u * threads;
-      slot[u] = pos[u] = -1;
-      page[u] = 0;
-      if (r >= rows) continue;
+  for (int64_t r = me; r < p.n_rows; r += threads) {
+    int64_t place = -1;
+    int pos = -1;
+    if (r < rows) {
       const int b = find<0>(e, p.B, (int)r);
       const int left = (b + 1 < p.B ? e[b + 1].rows : rows) - (int)r;  // this row and those behind it
-      slot[u] = e[b].len - left;
-      const int x = slot[u] >> p.page_shift;
-      page[u] = x < e[b].held ? p.table[(size_t)b * p.max_pages + x] : taken(e[b].out + x - e[b].held);
-      pos[u] = p.qpos ? p.qpos[b] + 1 + ((int)r - e[b].rows) : slot[u];
+      const int slot = e[b].len - left, x = slot >> p.page_shift;
+      const int page = x < e[b].held ? p.table[(size_t)b * p.max_pages + x] : taken(e[b].out + x - e[b].held);
+      place = ((int64_t)page << p.page_shift) + (slot & (p.page_size - 1));
+      pos = p.qpos ? p.qpos[b] + 1 + ((int)r - e[b].rows) : slot;
     }
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int64_t r = r0 + (int64_t)u * threads;
-      if (r >= p.n_rows) continue;
-      if (p.slots) p.slots[r] = slot[u] < 0 ? -1 : ((int64_t)page[u] << p.page_shift) + (slot[u] & (p.page_size - 1));
-      if (p.positions) p.positions[r] = pos[u];
-    }
+    if (p.slots) p.slots[r] = place;
+    if (p.positions) p.positions[r] = pos;
   }
   // What may replace its own input: by the CTA that ends last
   __syncthreads();
@@ -198,8 +191,8 @@ cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(plan_kernel), kSmemSeqs * (int)sizeof(Entry), done);
   if (e != cudaSuccess) return e;
-  // a thread's rows in one turn where there are CTAs for it; one CTA needs no ticket
-  const int64_t turn = (int64_t)kThreads * kRows, want = (p.n_rows + turn - 1) / turn;
+  // a row a thread where there are CTAs for it; one CTA needs no ticket
+  const int64_t want = ((int64_t)p.n_rows + kThreads - 1) / kThreads;
   const int64_t most = small ? kCtas : kFewCtas;
   const int ctas = (int)(want < 1 ? 1 : want < most ? want : most);
   return launch_pdl(plan_kernel, dim3(ctas), dim3(kThreads), bytes, s, p);

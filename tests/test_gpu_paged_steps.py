@@ -38,7 +38,7 @@ def a_cache(table, lens, num_pages, page, qpos=None):
 
 
 PLANS = [(1, 16, 8, 1), (2, 8, 3, 1), (5, 64, 4, 9), (64, 16, 20, 1), (64, 16, 20, 40), (700, 32, 6, 50), (1100, 16, 4, 3),
-         (6000, 8, 4, 2), (3, 16, 700, 5000)]
+         (6000, 8, 4, 2), (3, 16, 700, 5000), (9000, 8, 3, 2)]
 
 
 @pytest.mark.parametrize("in_place", [True, False], ids=["in_place", "out"])
