@@ -56,7 +56,6 @@ CacheParams shapes_of(const capattn_cache_config& c, void* ws) {
   p.max_pages = c.max_pages; p.num_pages = c.num_pages; p.max_len = c.max_pages * c.page_size;
   char* base = static_cast<char*>(ws);
   p.status = reinterpret_cast<uint32_t*>(base);
-  p.counters = reinterpret_cast<uint32_t*>(base + kCountersOff);
   return p;
 }
 

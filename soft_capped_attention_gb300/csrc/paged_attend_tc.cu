@@ -17,7 +17,7 @@
 // NaN for its lse and is formed once more by paged_finish_kernel.
 //
 // Warp roles (20 warps):
-//   warp 19      walks the CTA's pieces into a ring of four slots and loads their Q by TMA;
+//   warp 19      walks the CTA's pieces into a ring of eight slots and loads their Q by TMA;
 //                warps 0 and 18 follow and load K and V, a page (or 128 rows of one) a box,
 //                into rings; V's rows without a token are zeroed (0 times what they hold must
 //                be 0);
@@ -32,6 +32,24 @@
 // TMEM (512 columns): S / P [0, 128), [128, 256), [256, 384), O [384, 384 + D).
 // P is rounded to bf16 (at most half a step of o's own type, and the sum l is of the
 // unrounded values): a second product for its low half would cost as much as the first.
+// o's error against 64 bits is 2.3e-3 of its size, 1.7e-3 of it its own rounding.
+//
+// What bounds it: long prompts, the softmax (issue slots 57-59 % used, tensor pipe 40-60 % of
+// the active cycles; no pipe is full, the two groups wait for tensor memory and the issuer in
+// turn); trees and long caches, memory; single small sequences, the chain of lengths, pages,
+// tiles and the join.  A chunk of 4096 tokens behind 12,288, 32 / 8 heads x 128, tanh: 702 us
+// (1370 TFLOP/s; 660 without a cap, 850 soft_sign, 837 alsc); nine prompts of 128 to 3969
+// tokens, 16 / 16 heads, soft_sign: 258 us; four of 4096, 32 / 8 heads, window 1024, alsc,
+// temperatures: 305 us; 64 of 512, 32 / 8 heads, tanh: 272 us; 32 trees of 16 tokens on 916 to
+// 4016, 32 / 8 heads, alsc: 71 us (4.7 TB/s); one of 32 on 131,009: 93 us (5.8 TB/s).
+//
+// What was tried and lost (the chunk's, the nine prompts' or the windowed ones' us): one group
+// of 16 warps for every step (705, 307, 337), with P in tensor memory of its own (876, 353,
+// 394); separate issuers of S and of P V (spills at 80 registers); K and V by one warp (898),
+// pieces by K's warp (645, but 64 short prompts 343) or the issuer's (670, 302); waits for the
+// last P V before P is written (730); 16 columns at a time (alsc 966, 334); the two 32-column
+// halves unrolled (355: the loop outgrows the instruction cache); masked columns out of line
+// (584); MMAs issued in a loop (863) or under a branch of one lane (730).
 #include <float.h>
 
 #include "fwd_common.cuh"

@@ -4,8 +4,10 @@
 // A CTA takes 32 rows of a shared tile at a time.  Where few CTAs share it (prompts: two), its
 // eight warps are the four quarters of the columns, twice: every other piece each.  Where many
 // do (a long cache's few tokens), it takes one quarter, a warp every eighth piece.  The warps'
-// sums are added in order, so the result does not depend on scheduling.  Joining in the
-// attention kernel, by the CTA that ended last, left 151 SMs idle meanwhile.
+// sums are added in order, so the result does not depend on scheduling.  Bound by latency: it
+// starts as attention ends, then records, partial results and the sums' exchange follow one
+// another (4 to 6 us).  Joining in the attention kernel, by the CTA that ended last, left 151
+// SMs idle meanwhile.
 #include <cuda_bf16.h>
 
 #include "cache_sched.cuh"
@@ -123,7 +125,9 @@ struct Sum {
   }
 };
 
-constexpr int kManyPieces = 5;  // from here on a quarter of the columns a CTA
+// From here on a quarter of the columns a CTA (never: a tree of 24 tokens 18.3 us instead of
+// 15.0, one on 131,009 keys 100.6 instead of 93.8; from three pieces on: no different).
+constexpr int kManyPieces = 5;
 
 // What GROUPS warps left of columns [first, first + V) of a row, warps w0, w0 + stride, ..
 template <int V, int GROUPS, int WIDTH>

@@ -12,14 +12,15 @@ constexpr uint32_t kStatusBadPlanBit = 1024u;
 constexpr uint32_t kStatusBadPathBit = 2048u;
 
 // Whether rows of attention have to be formed once more, by themselves: a flag and a ticket in
-// the workspace's header, behind the counters; both are zero between calls.
+// the workspace's header, behind the counters of capattn_cache.h's calls; both are zero
+// between calls.
 constexpr size_t kRedoOff = kCacheHeaderBytes - 64;
 constexpr size_t kPlanTicketOff = kRedoOff + 32;  // CTAs of a plan that have ended
 static_assert(kCountersOff + kDecodeMaxCtas * sizeof(uint32_t) <= kRedoOff, "header too small");
 
 struct Piece;
 struct PagedParams {
-  CacheParams c;               // shapes, cache, q, temp, o, lse, status, counters, cap
+  CacheParams c;               // shapes, cache, q, temp, o, lse, status, cap
   const int32_t* cu_new;
   int32_t n_rows;
   const int32_t* parents;      // or null: a prompt
