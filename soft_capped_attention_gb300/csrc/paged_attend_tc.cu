@@ -32,7 +32,10 @@
 // TMEM (512 columns): S / P [0, 128), [128, 256), [256, 384), O [384, 384 + D).
 // P is rounded to bf16 (at most half a step of o's own type, and the sum l is of the
 // unrounded values): a second product for its low half would cost as much as the first.
-// o's error against 64 bits is 2.3e-3 of its size, 1.7e-3 of it its own rounding.
+// o's error against 64 bits is 2.3e-3 of its size, 1.7e-3 of it its own rounding.  A row of one
+// live slot, whose o is its value, divides by the rounded P (l has its sign set on the way);
+// rounded sums for every row cost the windowed prompts 12 us and gain nothing from some ten
+// slots on.
 //
 // What bounds it: long prompts, the softmax (issue slots 57-59 % used, tensor pipe 40-60 % of
 // the active cycles; no pipe is full, the two groups wait for tensor memory and the issuer in
@@ -49,7 +52,8 @@
 // pieces by K's warp (645, but 64 short prompts 343) or the issuer's (670, 302); waits for the
 // last P V before P is written (730); 16 columns at a time (alsc 966, 334); the two 32-column
 // halves unrolled (355: the loop outgrows the instruction cache); masked columns out of line
-// (584); MMAs issued in a loop (863) or under a branch of one lane (730).
+// (584); MMAs issued in a loop (863) or under a branch of one lane (730); 104 registers for
+// the softmax warps and 64 for the others (spills: 980, 411, 486).
 #include <float.h>
 
 #include "fwd_common.cuh"
@@ -106,6 +110,16 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_
 
 // Values that an asynchronous TMEM load delivers: nothing that uses them moves before the
 // wait that this follows.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
 template <int N>
 __device__ __forceinline__ void settled(uint32_t (&v)[N]) {
 #pragma unroll
@@ -176,14 +190,13 @@ struct RowPoly {
 // How a step's scores are capped: by the row's polynomial, by tanh's longer one, one by one.
 enum { kNear, kWide, kOneByOne };
 
-// 32 columns of P, packed to bf16; returns their sum.
-template <int METHOD, int LEVEL, bool MASKED>
-__device__ __forceinline__ float p_columns(const uint32_t (&v)[32], uint32_t (&pk)[16], const RowPoly<METHOD>& poly,
-                                           float mul, float add, uint32_t live, const ExactCap& k) {
+// N columns of P, packed to bf16; adds their sums (of the even and the odd ones) to acc.
+template <int METHOD, int LEVEL, bool MASKED, int N>
+__device__ __forceinline__ void p_columns(F2& acc, const uint32_t (&v)[N], uint32_t (&pk)[N / 2], const RowPoly<METHOD>& poly,
+                                          float mul, float add, uint32_t live, const ExactCap& k) {
   const F2 add2 = f2(add, add), mul2 = f2(mul, mul);
-  F2 acc = f2(0.f, 0.f);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
+  for (int e = 0; e < N / 2; ++e) {
     const F2 X = f2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
     F2 y;
     if constexpr (LEVEL == kNear) {
@@ -205,6 +218,8 @@ __device__ __forceinline__ float p_columns(const uint32_t (&v)[32], uint32_t (&p
     acc = f2_add(acc, f2(a, b));
     pk[e] = pack_bf16x2(a, b);
   }
+}
+__device__ __forceinline__ float total(F2 acc) {
   float a, b;
   f2_split(acc, a, b);
   return a + b;
@@ -216,23 +231,43 @@ __device__ __forceinline__ bool is_near(float top, const ExactCap& k) {
   return __all_sync(0xFFFFFFFFu, top <= (METHOD == CAPATTN_CAP_TANH ? k.near.xmax : k.xmax));
 }
 
-// The columns whose scores leave the row's polynomial: out of line, so that the loop that runs
-// without it stays small.  The scores of slots without a token are of whatever lies there, so
-// the choice is made once more from the live ones: it would change a result's last bit.
+// 32 columns whose scores leave the row's polynomial, from tensor memory to P in their place;
+// returns their sum.  Out of line, so that the loop that runs without it stays small; it loads
+// the scores once more (handed over, they went through local memory, which the little L1 beside
+// the tiles does not hold: a step took 6 us).  The scores of slots without a token are of
+// whatever lies there, so the choice is made once more from the live ones, for eight columns at
+// a time, and the sum goes in the inline forms' order: a result's last bit would show either.
+// With queries that make scores of sigma 4, 12 and 12 at caps of 50 (tanh), 20 (soft_sign) and 30
+// (alsc), a prompt of 4096 tokens, 32 / 8 heads, takes 276, 247 and 834 us instead of 143 (near);
+// inline these were 231, 232 and 506 but 64 short prompts of small scores 291 instead of 272.
 template <int METHOD>
-__device__ __noinline__ float p_far(const uint32_t (&v)[32], uint32_t (&pk)[16], float mul, float add, uint32_t live,
-                                    const ExactCap& k) {
+__device__ __noinline__ float p_far(uint32_t at, float mul, float add, uint32_t live, const ExactCap& k) {
   RowPoly<METHOD> poly;
   poly.set(k, mul);
-  float top = 0.f;
+  F2 acc = f2(0.f, 0.f);
+#pragma unroll 1
+  for (int e0 = 0; e0 < 32; e0 += 8) {
+    uint32_t v[8], pk[4];
+    tmem_ld8(at + e0, v);
+    tmem_wait_ld();
+    settled(v);
+    const uint32_t mine = live >> e0;
+    float top = 0.f;
 #pragma unroll
-  for (int e = 0; e < 32; ++e)
-    if ((live >> e) & 1u) top = fmaxf(top, fabsf(__uint_as_float(v[e])));
-  if (is_near<METHOD>(top, k)) return p_columns<METHOD, kNear, true>(v, pk, poly, mul, add, live, k);
-  if constexpr (METHOD == CAPATTN_CAP_TANH) {
-    if (__all_sync(0xFFFFFFFFu, top <= k.xmax)) return p_columns<METHOD, kWide, true>(v, pk, poly, mul, add, live, k);
+    for (int e = 0; e < 8; ++e)
+      if ((mine >> e) & 1u) top = fmaxf(top, fabsf(__uint_as_float(v[e])));
+    if (is_near<METHOD>(top, k)) {
+      p_columns<METHOD, kNear, true>(acc, v, pk, poly, mul, add, mine, k);
+    } else if (METHOD == CAPATTN_CAP_TANH && __all_sync(0xFFFFFFFFu, top <= k.xmax)) {
+      p_columns<METHOD, METHOD == CAPATTN_CAP_TANH ? kWide : kOneByOne, true>(acc, v, pk, poly, mul, add, mine, k);
+    } else {
+      p_columns<METHOD, kOneByOne, true>(acc, v, pk, poly, mul, add, mine, k);
+    }
+    __syncwarp();
+    tmem_st4(at + e0 / 2, pk);
+    tmem_wait_st();
   }
-  return p_columns<METHOD, kOneByOne, true>(v, pk, poly, mul, add, live, k);
+  return total(acc);
 }
 
 // The largest x of a row: |cap| times its factor's size.
@@ -575,6 +610,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       float l = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) l += sums[(xx * 4 + e) * BM + r];
+      const float l_o = l < 0.f ? __bfloat162float(__float2bfloat16_rn(-l)) : l;  // of the rounded P
+      l = fabsf(l);
       const bool none = l == 0.f;  // no live slot
       bool bad = false;
       if (last) {
@@ -586,7 +623,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       const size_t first = (size_t)(x.row0 + x.i0) * c.Hq + head0;  // row of o of the tile's first
       const size_t row = first + (size_t)tok * c.Hq + hh;
       if (x.whole) {
-        const float inv = none ? 0.f : 1.f / l;
+        const float inv = none ? 0.f : 1.f / l_o;
         // 16-byte chunks of the rows, passed about among four (D = 64: two) lanes so that they
         // write a row's chunks side by side: 32 lanes with a row each met 32 lines a store
         constexpr int CH = OQ / 8;
@@ -630,10 +667,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
         return true;
       }
       if (valid) {
+        const float scale = l_o == l ? 1.f : l / l_o;
 #pragma unroll
         for (int e = 0; e < OQ / 4; ++e)
-          reinterpret_cast<uint4*>(p.part_o)[part_at<HD, BM>(x.slot, r, cq, e)] =
-              make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          reinterpret_cast<float4*>(p.part_o)[part_at<HD, BM>(x.slot, r, cq, e)] =
+              make_float4(__uint_as_float(o[4 * e]) * scale, __uint_as_float(o[4 * e + 1]) * scale,
+                          __uint_as_float(o[4 * e + 2]) * scale, __uint_as_float(o[4 * e + 3]) * scale);
         if (last) {
           const size_t at = (size_t)x.slot * BM + r;
           p.part_ml[at] = make_float2(m_prev, l);
@@ -719,21 +758,22 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
             asm volatile("" : "+f"(top));
             if (!valid) top = 0.f;
             if (full && is_near<METHOD>(top, c.cap)) {
-              lsum += p_columns<METHOD, kNear, false>(v, pk, poly, mul, -m, live, c.cap);
+              F2 acc = f2(0.f, 0.f);
+              p_columns<METHOD, kNear, false>(acc, v, pk, poly, mul, -m, live, c.cap);
+              lsum += total(acc);
               seen = true;
             } else if (!__any_sync(0xFFFFFFFFu, live != 0u)) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) pk[e] = 0u;
             } else {
-              if (is_near<METHOD>(top, c.cap)) {
-                lsum += p_columns<METHOD, kNear, true>(v, pk, poly, mul, -m, live, c.cap);
+              if (__builtin_expect(is_near<METHOD>(top, c.cap), 1)) {
+                F2 acc = f2(0.f, 0.f);
+                p_columns<METHOD, kNear, true>(acc, v, pk, poly, mul, -m, live, c.cap);
+                lsum += total(acc);
               } else {
-                uint32_t scores[32], packed[16];  // (copies, which alone have an address)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) scores[e] = v[e];
-                lsum += p_far<METHOD>(scores, packed, mul, -m, valid ? live : 0u, c.cap);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) pk[e] = packed[e];
+                lsum += p_far<METHOD>(at_s + 32u * h, mul, -m, valid ? live : 0u, c.cap);
+                seen = seen || live != 0u;
+                continue;
               }
               seen = seen || live != 0u;
             }
@@ -770,8 +810,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       }
       if (!ok || !more) break;
       g += n;
-      // l: 0 without a live slot, something positive with one
-      sums[((k & 1) * 4 + cq) * BM + r] = !seen ? 0.f : lsum == 0.f ? FLT_MIN : lsum;
+      // l: 0 without a live slot, something positive with one, negative where it is the row's only
+      const float l = !seen ? 0.f : lsum == 0.f ? FLT_MIN : lsum;
+      sums[((k & 1) * 4 + cq) * BM + r] = valid && only_one(mask) ? -l : l;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_sums + 8 * quad);
       m_prev = m;

@@ -407,10 +407,12 @@ __device__ __forceinline__ RowMask row_mask(const PagedParams& p, int b, int g, 
     r.node = i;
     r.hi = s.base;
     depth = 0;
+    const int up = parent_of(p, s.row0, i);
     if (W > 0) {
       r.reach = W;
-      for (int x = parent_of(p, s.row0, i); x >= 0; x = parent_of(p, s.row0, x)) ++depth;
+      for (int x = up; x >= 0; x = parent_of(p, s.row0, x)) ++depth;
     }
+    if (up < 0) r.reach = 1;
   }
   r.lo = 0;
   if (W > 0) {
@@ -436,6 +438,11 @@ __device__ __forceinline__ RowMask dead_row() {
 // Whether the row's slots c0 .. c0 + n - 1 are all live without a look at pos or parents.
 __device__ __forceinline__ bool all_live(const RowMask& r, int c0, int n) {
   return r.lo <= c0 && c0 + n <= r.hi && !r.pos;
+}
+
+// Whether the row has one live slot (by pos: not whether it has no more than one).
+__device__ __forceinline__ bool only_one(const RowMask& r) {
+  return r.node < 0 ? r.hi - r.lo == 1 : r.hi <= r.lo && r.reach == 1;
 }
 
 // Bit e: slot c0 + e is live, 32 of them.

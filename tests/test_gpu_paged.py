@@ -208,6 +208,29 @@ def test_a_long_chain_of_drafts(dtype):
     check(two, want, dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", ["none", "tanh", "alsc", "soft_sign"])
+def test_a_single_slot_gives_its_value(dtype, D, cap):
+    """First tokens, windows of one, drafts that continue nothing: o is v, to the bit."""
+    new = [500, 1, 130]
+    pool = Pool(new, 2, D, 16, dtype, 3)
+    q = torch.randn(sum(new), 4, D, generator=torch.Generator().manual_seed(6)).to(dtype).cuda()
+    cache, cu = pool.cuda(), i32(sums(new))
+    v = torch.cat([torch.cat([pool.v[pool.table[b][t // 16], :, t % 16][None] for t in range(n)]) for b, n in enumerate(new)])
+    v = v.repeat_interleave(2, 1).cuda()
+    roots = torch.full((sum(new),), -1, dtype=torch.int32).cuda()
+    chain = torch.cat([torch.arange(-1, n - 1, dtype=torch.int32) for n in new]).cuda()
+    for window, up in ((1, None), (1, chain), (0, roots), (40, roots)):
+        o, lse = paged().cache_attend(q, cache, params(cap, D, window), cu, parents=up)
+        assert torch.equal(o, v), (window, up is None)
+    for up in (None, chain):
+        o, lse = paged().cache_attend(q, cache, params(cap, D), cu, parents=up)
+        first = [0, 500, 501]
+        assert torch.equal(o[first], v[first])
+    assert cache.status() == (0, 0)
+
+
 @pytest.mark.parametrize("dtype,step", [(BF16, 2.0 ** -8), (FP32, 2.0 ** -20)], ids=["bf16", "fp32"])
 def test_the_longest_tree(dtype, step):
     """8192 tokens, a chain, which is a prompt: outputs within max |v| times half a step of P and half
@@ -246,11 +269,12 @@ def test_two_caches_on_two_streams(dtype):
 
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("cap", ["none", "tanh", "alsc", "soft_sign"])
-def test_what_lies_in_free_slots_changes_no_bit(dtype, D, cap):
+@pytest.mark.parametrize("cap,scale", [("none", 1), ("tanh", 1), ("alsc", 1), ("soft_sign", 1), ("tanh15", 1), ("tanh15", 0.02),
+                                       ("tanh50", 3), ("alsc30", 0.01), ("alsc90", 1), ("soft_sign", 0.01)])
+def test_what_lies_in_free_slots_changes_no_bit(dtype, D, cap, scale):
     """Slots behind a sequence's last token, of its page and of pages it has not, hold anything."""
     pool = Pool([300, 40, 7], 2, D, 64, dtype, 3)
-    q = torch.randn(77, 4, D, generator=torch.Generator().manual_seed(6)).to(dtype).cuda()
+    q = (scale * torch.randn(77, 4, D, generator=torch.Generator().manual_seed(6))).to(dtype).cuda()
     used = torch.zeros(pool.k.shape[0], pool.page, dtype=torch.bool)
     for b, L in enumerate(pool.lens):
         for t in range(L):
