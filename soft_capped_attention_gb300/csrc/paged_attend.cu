@@ -265,9 +265,9 @@ paged_simt_kernel(PagedParams p) {
         const float inv = none ? 0.f : 1.f / l[y];
 #pragma unroll
         for (int w = 0; w < OC / 4; ++w) {
-          const float v[4] = {none ? 0.f : o[y][4 * w] * inv, none ? 0.f : o[y][4 * w + 1] * inv,
-                              none ? 0.f : o[y][4 * w + 2] * inv, none ? 0.f : o[y][4 * w + 3] * inv};
-          store_values(static_cast<float*>(c.o) + row * D + 64 * w + 4 * tx, v);
+          *reinterpret_cast<float4*>(static_cast<float*>(c.o) + row * D + 64 * w + 4 * tx) =
+              none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                   : make_float4(o[y][4 * w] * inv, o[y][4 * w + 1] * inv, o[y][4 * w + 2] * inv, o[y][4 * w + 3] * inv);
         }
         if (tx == 0) {
           if (bad) ask_redo(p);

@@ -29,20 +29,6 @@ __device__ __forceinline__ void ask_redo(const PagedParams& p) {
   *reinterpret_cast<volatile uint32_t*>(p.redo) = 1u;  // (every writer writes the same)
 }
 
-// N consecutive values of a row of o.
-template <typename T, int N>
-__device__ __forceinline__ void store_values(T* dst, const float (&y)[N]) {
-  if constexpr (sizeof(T) == 2) {
-#pragma unroll
-    for (int e = 0; e < N; e += 8)
-      *reinterpret_cast<uint4*>(dst + e) = make_uint4(pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]),
-                                                      pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
-  } else {
-#pragma unroll
-    for (int e = 0; e < N; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-  }
-}
-
 // Which shared tile begins in this CTA, if any (x) or none.
 __device__ __forceinline__ void leave_record(const PagedParams& p, const Piece& x) { p.records[blockIdx.x] = x; }
 __device__ __forceinline__ void leave_no_record(const PagedParams& p) { p.records[blockIdx.x].steps = -1; }
