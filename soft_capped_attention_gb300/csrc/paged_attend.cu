@@ -8,8 +8,8 @@
 // along D, whose padded rows spread over the banks) and 4 x D / 16 outputs, all in pairs of
 // fp32 products: of the even and odd columns of a score, of two rows' outputs.  The next
 // step's keys and values come in by cp.async meanwhile, their pages looked up a step before
-// that.  Bound by the products' and shared memory's latencies (FMA pipe 36 %, shared memory's
-// 43 %, issue slots 55 % of the time; 16 warps an SM at D = 64, eight at 128), and at small
+// that.  Bound by shared memory's and the products' latencies (short scoreboard 2.2, wait 1.5
+// stalls an issue; issue slots 44 %, 16 warps an SM at D = 64, eight at 128), and at small
 // sizes by the first loads and the finish.  Four prompts of up to 1500 tokens, 16 heads x 64:
 // 271 us (305 with products one at a time, 348 with loads through registers); x 128: 494
 // (538, 647); four prompts of 61 to 333 tokens behind up to 700 others, 4 / 2 heads x 64: 39
