@@ -286,7 +286,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   constexpr int KST = kst<HD>(), VST = vst<HD>();
   constexpr int OQ = HD / 4;  // O columns of a thread
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * 2 + 2 * KST + 2 * VST + 2 * NSB + 2 + 2 * NSLOT + 4 + 4 + 2];
+  __shared__ __align__(8) uint64_t bars[2 * 2 + 2 * KST + 2 * VST + 2 * NSB + 2 + 2 * NSLOT + 4 + 8 + 2];
   __shared__ Piece items[NSLOT];
   __shared__ ScheduleMem s_sched;
   __shared__ uint32_t s_bad[2][4][4];  // piece parity, quarter, rows / 32
@@ -316,8 +316,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   const uint32_t bar_ifull = bar_oempty + 8;         // + 8 s: piece slot written
   const uint32_t bar_iempty = bar_ifull + 8 * NSLOT; // + 8 s: piece done with (19 warps)
   const uint32_t bar_sums = bar_iempty + 8 * NSLOT;  // + 8 x: the sums of rows 32 x .. written (4 warps)
-  const uint32_t bar_tops = bar_sums + 32;           // + 8 x: the same, first step without a cap
-  const uint32_t bar_vfix = bar_tops + 32;           // V rows that get zeros have landed
+  const uint32_t bar_tops = bar_sums + 32;           // + 8 (2 x + piece parity): first step's maxima without a cap (2 warps)
+  const uint32_t bar_vfix = bar_tops + 64;           // V rows that get zeros have landed
   const uint32_t bar_final = bar_vfix + 8;
 
   if (threadIdx.x < 8) s_drained[threadIdx.x >> 2][threadIdx.x & 3] = 0;
@@ -345,10 +345,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       mbar_init(bar_ifull + 8 * s, 1);
       mbar_init(bar_iempty + 8 * s, 3 + kSoftmaxWarps);
     }
-    for (int x = 0; x < 4; ++x) {
-      mbar_init(bar_sums + 8 * x, 4);
-      mbar_init(bar_tops + 8 * x, 2);
-    }
+    for (int x = 0; x < 4; ++x) mbar_init(bar_sums + 8 * x, 4);
+    for (int x = 0; x < 8; ++x) mbar_init(bar_tops + 8 * x, 2);
     mbar_init(bar_vfix, 1);
     mbar_init(bar_final, 1);
     fence_mbar_init();
@@ -712,10 +710,15 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       if constexpr (METHOD != CAPATTN_CAP_NONE) m = fmaxf(0.f, largest_x<METHOD>(c.cap, mul) - 100.f);
       float lsum = 0.f;
       bool seen = false;
-      // without a cap: the reference, from the live scores of the piece's first step
+      // Without a cap: the reference, from the live scores of the piece's first step.  The two warps
+      // that arrive may do so for piece k + 1 (whose first scores need nothing of piece k's last
+      // step) before the other two have looked at piece k; for k + 2 they may not: they have written
+      // out piece k by then, which takes the sums of all four, given after that look.  So two
+      // barriers in turn, as the maxima have two buffers.
+      const uint32_t bar_top = bar_tops + 8 * (2 * quad + (k & 1));
       auto reference = [&]() -> bool {
         const float* t = tops + (k & 1) * 2 * BM;
-        if (!wait_warp(bar_tops + 8 * quad, k & 1, c.status, &abort_flag)) return false;
+        if (!wait_warp(bar_top, (k >> 1) & 1, c.status, &abort_flag)) return false;
         const float best = fmaxf(t[r], t[BM + r]);
         m = best == -INFINITY || fabsf(best) <= 40.f ? 0.f : best;
         return true;
@@ -742,7 +745,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
             }
             tops[((k & 1) * 2 + half) * BM + r] = best;
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_tops + 8 * quad);
+            if (lane == 0) mbar_arrive(bar_top);
             if (!reference()) return false;
           }
 #pragma unroll 1
@@ -783,7 +786,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
           tmem_wait_st();
           tc_fence_before();
         } else if (METHOD == CAPATTN_CAP_NONE && i == 0) {
-          if (lane == 0) mbar_arrive(bar_tops + 8 * quad);
+          if (lane == 0) mbar_arrive(bar_top);
           if (!reference()) return false;
         }
         __syncwarp();
