@@ -422,7 +422,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
     const int stages = values ? VST : KST;
     if (lane == 0) tma_prefetch_desc(map);
     int j = 0, fixes = 0;
-    bool ok = true;
+    bool ok = true, landing = false;  // landing: copies that bar_vfix counts may be on their way
     for (int k = 0; ok && wait_piece(k); ++k) {
       const Piece& x = items[k % NSLOT];
       const int g = x.part / p.parts, len = x.len, first = x.first, tile0 = x.tile0, steps = x.steps;
@@ -462,6 +462,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
         if (fix) {
           if (!wait_warp(bar_vfix, fixes & 1, c.status, &abort_flag)) {
             ok = false;
+            landing = true;
             break;
           }
           ++fixes;
@@ -480,7 +481,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       }
     }
     if (lane == 0) {
-      if (!ok && values) drain_wait(bar_vfix, fixes & 1);  // (a wait that gave up: its copies may still come)
+      if (landing) drain_wait(bar_vfix, fixes & 1);
       for (int x = j > stages ? j - stages : 0; x < j; ++x) drain_wait(full0 + 8 * (x % stages), (x / stages) & 1);
     }
     __syncwarp();

@@ -50,7 +50,7 @@ class Cta:
     copies of zeroed rows that it issued; "always", whether or not there are any.  gives_up: after
     so many waits one of them runs into its limit."""
 
-    def __init__(self, pieces, HD, rng, tops_by="two", drains="always", gives_up=None):
+    def __init__(self, pieces, HD, rng, tops_by="two", drains="issued", gives_up=None):
         self.pieces, self.rng, self.tops_by, self.drains, self.gives_up = pieces, rng, tops_by, drains, gives_up
         stages = 4 if HD == 64 else 2
         bars = lambda n, count: [Bar(count) for _ in range(n)]  # noqa: E731
@@ -118,14 +118,12 @@ class Cta:
                 bar = self.vfix if fix else full[s]
                 bar.arrive(tx=1)
                 self.copies.append((bar, tiles, s, (k, i)))
-                landing = fix
                 yield None
                 if fix:
                     if not (yield self.vfix, fixes & 1):
-                        ok = False
+                        ok, landing = False, True
                         break
                     fixes += 1
-                    landing = False
                     full[s].arrive()
                 j += 1
             k += 1

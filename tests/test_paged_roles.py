@@ -40,6 +40,23 @@ def test_one_barrier_for_every_exchange_is_too_few():
     assert stuck
 
 
+@pytest.mark.parametrize("drains", ["issued", "always"])
+def test_a_wait_that_gives_up_ends_every_role(drains):
+    """And at once: none waits on its way out for a copy that nobody issued (which takes as long as
+    the wait that gave up)."""
+    rng = random.Random(9)
+    stuck = 0
+    for _ in range(60):
+        cta = Cta(random_pieces(rng, [1, 2, 3], rng.choice(["all", "none"])), rng.choice([64, 128]), rng, drains=drains,
+                  gives_up=rng.randint(1, 900))
+        try:
+            cta.run()
+            assert cta.abort
+        except Stuck:
+            stuck += 1
+    assert (stuck > 0) == (drains == "always")
+
+
 @pytest.mark.parametrize("name", MANY_PIECES)
 def test_the_batches_give_every_cta_many_pieces(name):
     """Of the lengths that they are there for, one after another in the same CTA."""
