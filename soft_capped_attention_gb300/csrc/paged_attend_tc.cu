@@ -9,12 +9,15 @@
 //
 // The reference m of a row's exponentials is fixed before its scores are seen, so no step
 // looks for a maximum and a row's threads exchange nothing but l at the end:
-//   with a cap, |x| is bounded and m = max(0, bound - 100) (0 for all usual caps, which
-//   also makes x - m exact); without one, m comes from the first step's scores (0 while
-//   they are within 2^+-40).
+//   with a cap, |x| is bounded and m = min(max(0, bound - 100), 40) (0 for all usual caps,
+//   which also makes x - m exact), which serves rows whose largest x is between -40 and 160;
+//   without one, and with one so wide that rows may lie elsewhere (is_wide_cap: a kernel of
+//   its own, since the exchange costs the others 1 to 10 %), m comes from the live scores of
+//   the piece's first step (0 while the largest is within 2^+-40).
 // That holds for logits within about 2^100 above m; a row whose sum leaves [2^-80, inf),
 // and one that met NaN or infinity in a slot that is not live for it (0 times them), gets
-// NaN for its lse and is formed once more by paged_finish_kernel.
+// NaN for its lse and is formed once more by paged_finish_kernel, a warp a row: some 1500
+// times as long (a prompt of 4096 tokens under tanh 300 with m = bound - 100: 213 ms).
 //
 // Warp roles (20 warps):
 //   warp 19      walks the CTA's pieces into a ring of eight slots and loads their Q by TMA;
@@ -270,6 +273,28 @@ __device__ __noinline__ float p_far(uint32_t at, float mul, float add, uint32_t 
   return total(acc);
 }
 
+// The largest live x of 64 columns of a row.  x rises or falls with the score everywhere, so the
+// cap is taken once.
+template <int METHOD>
+__device__ __noinline__ float live_top(uint32_t at, float mul, uint64_t live, const ExactCap& k) {
+  float way = k.sm_scale * mul;
+  if constexpr (METHOD == CAPATTN_CAP_ALSC) way *= k.alsc.a;
+  const float sign = way < 0.f ? -1.f : 1.f;
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[32];
+    tmem_ld32(at + 32u * h, v);
+    const uint32_t mine = (uint32_t)(live >> (32 * h));
+    tmem_wait_ld();
+    settled(v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if ((mine >> e) & 1u) top = fmaxf(top, sign * __uint_as_float(v[e]));
+  }
+  return top == -INFINITY ? top : any_cap<METHOD>(sign * top, k) * mul;
+}
+
 // The largest x of a row: |cap| times its factor's size.
 template <int METHOD>
 __device__ __forceinline__ float largest_x(const ExactCap& k, float mul) {
@@ -277,7 +302,7 @@ __device__ __forceinline__ float largest_x(const ExactCap& k, float mul) {
   return fabsf(mul * k.cap);
 }
 
-template <int METHOD, int HD>
+template <int METHOD, int HD, bool WIDE>
 __global__ void __launch_bounds__(NTHREADS, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                 const __grid_constant__ CUtensorMap mv, const PagedParams p) {
@@ -285,6 +310,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   constexpr int NSLAB = HD / 64;
   constexpr int KST = kst<HD>(), VST = vst<HD>();
   constexpr int OQ = HD / 4;  // O columns of a thread
+  constexpr bool LOOK = METHOD == CAPATTN_CAP_NONE || WIDE;  // the first step's scores give the reference
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * 2 + 2 * KST + 2 * VST + 2 * NSB + 2 + 2 * NSLOT + 4 + 8 + 2];
   __shared__ Piece items[NSLOT];
@@ -316,7 +342,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   const uint32_t bar_ifull = bar_oempty + 8;         // + 8 s: piece slot written
   const uint32_t bar_iempty = bar_ifull + 8 * NSLOT; // + 8 s: piece done with (19 warps)
   const uint32_t bar_sums = bar_iempty + 8 * NSLOT;  // + 8 x: the sums of rows 32 x .. written (4 warps)
-  const uint32_t bar_tops = bar_sums + 32;           // + 8 (2 x + piece parity): first step's maxima without a cap (2 warps)
+  const uint32_t bar_tops = bar_sums + 32;           // + 8 (2 x + piece parity): first step's maxima (2 warps)
   const uint32_t bar_vfix = bar_tops + 64;           // V rows that get zeros have landed
   const uint32_t bar_final = bar_vfix + 8;
 
@@ -708,11 +734,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       }
       const bool block = __any_sync(0xFFFFFFFFu, valid);  // the warp has rows at all
       poly.set(c.cap, mul);
-      if constexpr (METHOD != CAPATTN_CAP_NONE) m = fmaxf(0.f, largest_x<METHOD>(c.cap, mul) - 100.f);
+      if constexpr (!LOOK) m = fminf(fmaxf(0.f, largest_x<METHOD>(c.cap, mul) - 100.f), 40.f);
       float lsum = 0.f;
       bool seen = false;
-      // Without a cap: the reference, from the live scores of the piece's first step.  The two warps
-      // that arrive may do so for piece k + 1 (whose first scores need nothing of piece k's last
+      // The reference from the live scores of the piece's first step.  The two warps that arrive may do so for piece k + 1 (whose first scores need nothing of piece k's last
       // step) before the other two have looked at piece k; for k + 2 they may not: they have written
       // out piece k by then, which takes the sums of all four, given after that look.  So two
       // barriers in turn, as the maxima have two buffers.
@@ -731,18 +756,25 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
         const uint32_t at_s = s_half + 128u * sb;
         if (block) {
           tc_fence_after();
-          if (METHOD == CAPATTN_CAP_NONE && i == 0) {
+          if (LOOK && i == 0) {
             float best = -INFINITY;
+            if constexpr (METHOD == CAPATTN_CAP_NONE) {
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              uint32_t v[32];
-              tmem_ld32(at_s + 32u * h, v);
-              const uint32_t live = valid ? live_slots(p, mask, c0 + 32 * h) : 0u;
-              tmem_wait_ld();
-              settled(v);
+              for (int h = 0; h < 2; ++h) {
+                uint32_t v[32];
+                tmem_ld32(at_s + 32u * h, v);
+                const uint32_t live = valid ? live_slots(p, mask, c0 + 32 * h) : 0u;
+                tmem_wait_ld();
+                settled(v);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if ((live >> e) & 1u) best = fmaxf(best, __uint_as_float(v[e]) * (c.sm_scale * mul));
+                for (int e = 0; e < 32; ++e)
+                  if ((live >> e) & 1u) best = fmaxf(best, __uint_as_float(v[e]) * (c.sm_scale * mul));
+              }
+            } else {
+              uint64_t live = 0;
+              if (valid) live = live_slots(p, mask, c0) | (uint64_t)live_slots(p, mask, c0 + 32) << 32;
+              __syncwarp();
+              best = live_top<METHOD>(at_s, mul, live, c.cap);
             }
             tops[((k & 1) * 2 + half) * BM + r] = best;
             __syncwarp();
@@ -786,7 +818,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
           }
           tmem_wait_st();
           tc_fence_before();
-        } else if (METHOD == CAPATTN_CAP_NONE && i == 0) {
+        } else if (LOOK && i == 0) {
           if (lane == 0) mbar_arrive(bar_top);
           if (!reference()) return false;
         }
@@ -810,7 +842,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
         if (ok && k > 0) ok = drain(k - 1);
         if (!more) break;
         if (c.temp && ok && wait_piece(k + 1)) temp = temp_of(k + 1);
-        if (METHOD == CAPATTN_CAP_NONE && i < 0) ok = ok && reference();
+        if (LOOK && i < 0) ok = ok && reference();
       }
       if (!ok || !more) break;
       g += n;
@@ -834,7 +866,16 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
   }
 }
 
-template <int METHOD, int HD>
+// Whether a cap alone, at temperature 1, bounds x by more than 120 (tanh 83): the fixed reference
+// then lies far above ordinary scores, or far below the bound.  (Temperatures are in device
+// memory: they widen the rows' bounds, not this.)
+bool is_wide_cap(const CacheParams& c) {
+  if (c.method == CAPATTN_CAP_NONE) return false;
+  const float top = c.method == CAPATTN_CAP_ALSC ? c.cap.alsc.out * c.cap.alsc.one_minus_sb : c.cap.cap;
+  return !(top * kL2E <= 120.f);
+}
+
+template <int METHOD, int HD, bool WIDE>
 cudaError_t run_tc(const PagedParams& p, cudaStream_t s) {
   const CacheParams& c = p.c;
   CUtensorMap mq, mk, mv;
@@ -849,7 +890,7 @@ cudaError_t run_tc(const PagedParams& p, cudaStream_t s) {
   cudaError_t e = encode_bf16_map(&mq, c.q, 3, qd, qs, qb);
   if (e == cudaSuccess) e = encode_bf16_map(&mk, c.k, 2, kd, ks, kb);
   if (e == cudaSuccess) e = encode_bf16_map(&mv, c.v, 2, kd, ks, kb);
-  auto* kern = paged_tc_kernel<METHOD, HD>;
+  auto* kern = paged_tc_kernel<METHOD, HD, WIDE>;
   static std::atomic<uint64_t> done{0};
   if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(kern), smem_bytes<HD>(), done);
   if (e != cudaSuccess) return e;
@@ -859,7 +900,9 @@ cudaError_t run_tc(const PagedParams& p, cudaStream_t s) {
 template <int METHOD>
 struct PagedTcLaunch {
   static cudaError_t run(const PagedParams& p, cudaStream_t s) {
-    return p.c.D == 64 ? run_tc<METHOD, 64>(p, s) : run_tc<METHOD, 128>(p, s);
+    if constexpr (METHOD != CAPATTN_CAP_NONE)
+      if (is_wide_cap(p.c)) return p.c.D == 64 ? run_tc<METHOD, 64, true>(p, s) : run_tc<METHOD, 128, true>(p, s);
+    return p.c.D == 64 ? run_tc<METHOD, 64, false>(p, s) : run_tc<METHOD, 128, false>(p, s);
   }
 };
 
