@@ -11,9 +11,11 @@
 // looks for a maximum and a row's threads exchange nothing but l at the end:
 //   with a cap, |x| is bounded and m = min(max(0, bound - 100), 40) (0 for all usual caps,
 //   which also makes x - m exact), which serves rows whose largest x is between -40 and 160;
-//   without one, and with one so wide that rows may lie elsewhere (is_wide_cap: a kernel of
-//   its own, since the exchange costs the others 1 to 10 %), m comes from the live scores of
-//   the piece's first step (0 while the largest is within 2^+-40).
+//   without one, and with one so wide that rows may lie elsewhere (is_wide_cap), m comes from
+//   the live scores of the piece's first step (0 while the largest is within 2^+-40).  Wide
+//   caps have a kernel of their own, since the exchange of a row's largest score among its warps
+//   costs 2 to 3 us a piece: tanh 300 and 50 take 155 and 137 us (a prompt of 4096 tokens, 32 / 8
+//   heads), 418 and 268 (64 of 512); in the ordinary kernel, not used, it cost 1 to 10 %.
 // That holds for logits within about 2^100 above m; a row whose sum leaves [2^-80, inf),
 // and one that met NaN or infinity in a slot that is not live for it (0 times them), gets
 // NaN for its lse and is formed once more by paged_finish_kernel, a warp a row: some 1500
@@ -273,13 +275,8 @@ __device__ __noinline__ float p_far(uint32_t at, float mul, float add, uint32_t 
   return total(acc);
 }
 
-// The largest live x of 64 columns of a row.  x rises or falls with the score everywhere, so the
-// cap is taken once.
-template <int METHOD>
-__device__ __noinline__ float live_top(uint32_t at, float mul, uint64_t live, const ExactCap& k) {
-  float way = k.sm_scale * mul;
-  if constexpr (METHOD == CAPATTN_CAP_ALSC) way *= k.alsc.a;
-  const float sign = way < 0.f ? -1.f : 1.f;
+// The largest live score (sign 1) or the smallest one's negative (-1) of 64 columns of a row.
+__device__ __noinline__ float live_top(uint32_t at, float sign, uint64_t live) {
   float top = -INFINITY;
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
@@ -292,7 +289,7 @@ __device__ __noinline__ float live_top(uint32_t at, float mul, uint64_t live, co
     for (int e = 0; e < 32; ++e)
       if ((mine >> e) & 1u) top = fmaxf(top, sign * __uint_as_float(v[e]));
   }
-  return top == -INFINITY ? top : any_cap<METHOD>(sign * top, k) * mul;
+  return top;
 }
 
 // The largest x of a row: |cap| times its factor's size.
@@ -774,7 +771,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
               uint64_t live = 0;
               if (valid) live = live_slots(p, mask, c0) | (uint64_t)live_slots(p, mask, c0 + 32) << 32;
               __syncwarp();
-              best = live_top<METHOD>(at_s, mul, live, c.cap);
+              // x rises or falls with the score everywhere, so the cap is taken once
+              const float way = METHOD == CAPATTN_CAP_ALSC ? c.sm_scale * mul * c.cap.alsc.a : c.sm_scale * mul;
+              const float sign = way < 0.f ? -1.f : 1.f, top = live_top(at_s, sign, live);
+              if (top > -INFINITY) best = any_cap<METHOD>(sign * top, c.cap) * mul;
             }
             tops[((k & 1) * 2 + half) * BM + r] = best;
             __syncwarp();
