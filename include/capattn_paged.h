@@ -77,7 +77,7 @@ capattn_status capattn_paged_attend(const capattn_cache_config* cfg, const void*
 /*
  * The tables and slot maps of a step.  n_new [B] int32: tokens that each sequence is
  * about to get; negative: the sequence ends (length 0).  held [B] int32: pages that
- * sequence b owns, table[b][0 .. held[b]).  free_pages [num_pages] int32, n_free [1]: a
+ * sequence b owns, table[b][0 .. held[b]), at least those of its lens[b] tokens.  free_pages [num_pages] int32, n_free [1]: a
  * stack of the pages that nobody owns, free_pages[0 .. n_free).
  *   lens_out = lens + n_new (0 for one that ends), qpos_out = qpos + n_new (-1);
  *   held_out = ceil(lens_out / page_size): the pages behind that go on the stack, in the
@@ -88,12 +88,14 @@ capattn_status capattn_paged_attend(const capattn_cache_config* cfg, const void*
  *   slots % page_size; positions [n_rows] int32 (nullable): its position (the slot, or
  *   with qpos qpos[b] + 1 + i); -1 in both behind the last new token.
  * Either everything is done or, when the stack holds too few pages, a sequence would
- * outgrow max_len, the new tokens do not fit n_rows or held or the stack are out of
- * range, nothing: the status word says so, the outputs are what the inputs were, cu_new
+ * outgrow max_len, the new tokens do not fit n_rows or held (also one that does not reach
+ * lens) or the stack are out of range, nothing: the status word says so, the outputs are what the inputs were, cu_new
  * is 0 and slots and positions are -1.  lens_out, qpos_out, held_out and n_free_out may
  * be lens, qpos, held and n_free; other overlaps are not allowed.  qpos and qpos_out
  * come together or are both NULL.  Table entries behind held_out are left as they were.
- * Pages that several sequences share must not be counted in held.
+ * Sequences that share pages (a common prefix) cannot be planned: counted in held they would
+ * be given back while others read them, and held names the front of the table, so they cannot
+ * be left out (such a held is refused as above).
  */
 capattn_status capattn_paged_plan(const capattn_cache_config* cfg, const int32_t* n_new, int32_t* table,
                                   const int32_t* lens, const int32_t* qpos, const int32_t* held,

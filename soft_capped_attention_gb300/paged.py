@@ -65,8 +65,9 @@ class PagePool:
     """The pages of a cache that no sequence owns, and how many each sequence does.
 
     free [num_pages] int32, n_free [1] int32: a stack, free[:n_free]; held [B] int32: the
-    pages of sequence b, table[b, :held[b]].  All of them are the caller's.  Pages that
-    several sequences share are not counted in held."""
+    pages of sequence b, table[b, :held[b]], at least those of its lens[b] tokens.  All of
+    them are the caller's.  Sequences that share pages (a common prefix) cannot be planned:
+    each page belongs to one sequence or to the stack."""
 
     def __init__(self, free, n_free, held):
         self.free, self.n_free, self.held = free, n_free, held
