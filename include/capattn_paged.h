@@ -116,6 +116,9 @@ capattn_status capattn_paged_plan(const capattn_cache_config* cfg, const int32_t
  * the first row c with parents[c] == i and tokens[c] == predicted[i], up to `width` tokens;
  * path is -1 behind count, next [B] int32 (nullable) is predicted of the last accepted row
  * (-1, and count 0, for a sequence without new tokens).
+ * A sequence with wrong data (lengths, rows, a path, a page that a row would leave or enter)
+ * stays as it is: nothing of it moves, lens_out = lens, qpos_out = qpos; with tokens its path is
+ * -1, count 0 and next -1.
  * lens_out and qpos_out may be lens and qpos.  The pages of the new tokens belong to one
  * sequence.
  */
