@@ -65,6 +65,8 @@ size_t capattn_paged_workspace_bytes(const capattn_cache_config* cfg, int call);
  * q: n_rows rows of [Hq, D], row r at r * q_row_stride elements; o [n_rows, Hq, D];
  * lse [n_rows, Hq] float32; temp [n_rows] float32, nullable (1); o must not overlap q.
  * What a slot holds that is not live for a row (NaN, infinities) does not reach that row.
+ * bf16: P enters the product with V as one bf16 (capattn_cache_decode keeps two): o is off by
+ * 2.3e-3 of its size, 1.7e-3 of it its own rounding.
  * The result does not depend on scheduling: same inputs, same bits.
  */
 capattn_status capattn_paged_attend(const capattn_cache_config* cfg, const void* q, int64_t q_row_stride,

@@ -1,6 +1,6 @@
 // Acceptance of a drafted path: a CTA a sequence walks the tree (one warp, 32 candidates at
-// a time) or checks the given path, looks up the pages of all rows that move, and moves the path's keys and values to the front of
-// the new slots.  A row goes to a slot at or before its own and behind every earlier row's
+// a time) or checks the given path, looks up the pages of all rows that move, and moves the
+// path's keys and values to the front of the new slots.  A row goes to a slot at or before its own and behind every earlier row's
 // source, so a chunk of rows is loaded whole before any of it is stored, and chunks follow
 // one another without more ado.  Bound by latency: the walk's dependent reads (from shared
 // memory) and one round trip of the rows.  One tree of 25 tokens: 3.2 us; 128 of 33 (8 heads

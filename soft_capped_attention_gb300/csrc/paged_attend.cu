@@ -3,7 +3,8 @@
 // Per query tile (tokens x query heads of one KV head, 64 rows) and 64 slots, with a
 // running reference m (log2 units):
 //   S = Q K^T, x = log2(e) temp cap(sm_scale S), P = 2^(x - m), l += sum P, O += P V.
-// fp32 stays on the CUDA cores: a TF32 product keeps 11 bits of q and k.  256 threads, 4 x 4
+// fp32 stays on the CUDA cores: a TF32 product keeps 11 bits of q and k (three of split operands
+// would keep them all; not tried).  256 threads, 4 x 4
 // scores each (rows 4 ty .., keys tx + 16 z: 64 products for eight vectors of shared memory
 // along D, whose padded rows spread over the banks) and 4 x D / 16 outputs, all in pairs of
 // fp32 products: of the even and odd columns of a score, of two rows' outputs.  The next
