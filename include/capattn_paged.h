@@ -21,8 +21,8 @@
  *
  * Status bits that these calls add: 512 = a parent that is not an earlier row of its
  * sequence (nor -1), or a tree of more than CAPATTN_PAGED_MAX_TREE tokens (its rows stay
- * as they were); 1024 = a plan without the pages or rows that it needs, or with a bad
- * stack (nothing was changed); 2048 = a path that does not increase within the sequence's
+ * as they were); 1024 = a plan without the pages or rows that it needs, or with bad lengths,
+ * held pages or stack (nothing was changed); 2048 = a path that does not increase within the sequence's
  * rows, or a bad count.  Bits 32, 64 and 128 as in capattn_cache.h.
  */
 #ifndef CAPATTN_PAGED_H_

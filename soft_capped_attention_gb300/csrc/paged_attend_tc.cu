@@ -734,10 +734,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ 
       if constexpr (!LOOK) m = fminf(fmaxf(0.f, largest_x<METHOD>(c.cap, mul) - 100.f), 40.f);
       float lsum = 0.f;
       bool seen = false;
-      // The reference from the live scores of the piece's first step.  The two warps that arrive may do so for piece k + 1 (whose first scores need nothing of piece k's last
-      // step) before the other two have looked at piece k; for k + 2 they may not: they have written
-      // out piece k by then, which takes the sums of all four, given after that look.  So two
-      // barriers in turn, as the maxima have two buffers.
+      // The reference from the live scores of the piece's first step.  The two warps that arrive may
+      // do so for piece k + 1 (whose first scores need nothing of piece k's last step) before the
+      // other two have looked at piece k; for k + 2 they may not: they have written out piece k by
+      // then, which takes the sums of all four, given after that look.  So two barriers in turn, as
+      // the maxima have two buffers.
       const uint32_t bar_top = bar_tops + 8 * (2 * quad + (k & 1));
       auto reference = [&]() -> bool {
         const float* t = tops + (k & 1) * 2 * BM;

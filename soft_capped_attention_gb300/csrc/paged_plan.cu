@@ -35,7 +35,7 @@ __device__ __forceinline__ Seq read_seq(const PlanParams& p, int b) {
   const int64_t after = n < 0 ? 0 : (int64_t)len + n;
   s.bad = s.held < 0 || s.held > p.max_pages || after > p.max_len || len < 0 || len > p.max_len;
   // a sequence owns the pages of all its tokens: others would be taken for missing and replaced
-  s.bad = s.bad || s.held < (len + p.page_size - 1) >> p.page_shift;
+  s.bad = s.bad || s.held < (int)(((int64_t)len + p.page_size - 1) >> p.page_shift);
   s.len = s.bad ? 0 : (int)after;
   s.need = (s.len + p.page_size - 1) >> p.page_shift;
   return s;
