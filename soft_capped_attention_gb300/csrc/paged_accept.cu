@@ -3,7 +3,7 @@
 // path's keys and values to the front of the new slots.  A row goes to a slot at or before its own and behind every earlier row's
 // source, so a chunk of rows is loaded whole before any of it is stored, and chunks follow
 // one another without more ado.  Bound by latency: the walk's dependent reads (from shared
-// memory) and one round trip of the rows.  One tree of 25 tokens: 3.2 us; 128 of 33 (8 heads
+// memory) and one round trip of the rows.  One tree of 25 tokens: 3.5 us; 128 of 33 (8 heads
 // x 128, bf16, paths of up to 9): 5.3 us.
 #include "paged_internal.h"
 #include "tc_common.cuh"

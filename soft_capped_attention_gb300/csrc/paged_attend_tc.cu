@@ -48,7 +48,7 @@
 // tiles and the join.  A chunk of 4096 tokens behind 12,288, 32 / 8 heads x 128, tanh: 702 us
 // (1370 TFLOP/s; 660 without a cap, 850 soft_sign, 837 alsc); nine prompts of 128 to 3969
 // tokens, 16 / 16 heads, soft_sign: 258 us; four of 4096, 32 / 8 heads, window 1024, alsc,
-// temperatures: 305 us; 64 of 512, 32 / 8 heads, tanh: 272 us; 32 trees of 16 tokens on 916 to
+// temperatures: 308 us; 64 of 512, 32 / 8 heads, tanh: 272 us; 32 trees of 16 tokens on 916 to
 // 4016, 32 / 8 heads, alsc: 71 us (4.7 TB/s); one of 32 on 131,009: 93 us (5.8 TB/s).
 //
 // What was tried and lost (the chunk's, the nine prompts' or the windowed ones' us): one group

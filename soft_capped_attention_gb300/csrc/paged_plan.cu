@@ -9,7 +9,7 @@
 // Lengths, held pages and the stack's height may be updated in place: the CTA that ends last
 // writes them.  Bound by latency: a launch, the lengths, two scans, the searches in shared
 // memory, the pages, the stores.  64 sequences of one new token: 4.8 us; 512 sequences and
-// 66,000 rows: 7.3 (four rows a thread in flight at once 10.8, a cluster of eight CTAs that
+// 66,000 rows: 7.5 (four rows a thread in flight at once 10.8, a cluster of eight CTAs that
 // met twice 14.8); 400,000 rows: 10.9; 6000 sequences: 17.6 (81 with their sums in memory,
 // where those of more than 8192 have to be).  256 threads instead of 512: 4.4, 7.4, but 144.
 #include "paged_internal.h"
